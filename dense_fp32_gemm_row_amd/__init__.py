@@ -8,11 +8,12 @@ so the seeded input generators in ``workloads`` stay usable without a GPU.
 
 from __future__ import annotations
 
-__all__ = ["gemm", "gemm_f32", "gemm_f32_variant", "gemm_f32_strerror", "workloads"]
+__all__ = ["gemm", "gemm_f32", "gemm_f32_variant", "gemm_f32_strerror", "Mxfp4", "mxfp4_quantize",
+           "mxfp4_quantize_both", "mxfp4_dequantize", "gemm_mxfp4", "gemm_mxfp4_weight", "workloads"]
 
 
 def __getattr__(name):
-    if name in ("gemm", "gemm_f32", "gemm_f32_variant", "gemm_f32_strerror"):
+    if name in __all__ and name != "workloads":
         from . import binding
 
         return getattr(binding, name)

@@ -1,4 +1,5 @@
-"""ctypes binding of libgemm_f32.so (declared in include/gemm_f32.h).
+"""ctypes binding of libgemm_f32.so (declared in include/gemm_f32.h and
+include/gemm_mxfp4.h).
 
 Argument marshalling only: every step of the product runs in the HIP
 kernels behind the C ABI.  PyTorch provides device memory and streams; it
@@ -7,7 +8,9 @@ calls raise.
 
 Functions with the C names take raw integers (sizes, device addresses,
 leading dimensions, a hipStream_t address) and return the C status code.
-``gemm`` is the tensor-level convenience used by tests and the benchmark.
+``gemm`` is the tensor-level convenience used by tests and the benchmark;
+``Mxfp4`` and the functions below it are the same for matrices held in
+microscaled 4-bit floating point.
 """
 
 from __future__ import annotations
@@ -101,6 +104,21 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
                                   ctypes.POINTER(_int), ctypes.POINTER(_int)]
     lib.gemm_f32_abi_version.restype = _int
     lib.gemm_f32_abi_version.argtypes = []
+    lib.gemm_mxfp4_quantize.restype = _int
+    lib.gemm_mxfp4_quantize.argtypes = [_i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp]
+    lib.gemm_mxfp4_dequantize.restype = _int
+    lib.gemm_mxfp4_dequantize.argtypes = [_i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp]
+    lib.gemm_mxfp4.restype = _int
+    lib.gemm_mxfp4.argtypes = [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp]
+    lib.gemm_mxfp4_workspace_size.restype = _i64
+    lib.gemm_mxfp4_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
+    lib.gemm_mxfp4_weight.restype = _int
+    lib.gemm_mxfp4_weight.argtypes = [_int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp,
+                                      _i64, _i64, _vp, _i64, _vp]
+    lib.gemm_mxfp4_weight_workspace_size.restype = _i64
+    lib.gemm_mxfp4_weight_workspace_size.argtypes = [_int, _i64, _i64, _i64, _i64]
+    lib.gemm_mxfp4_abi_version.restype = _int
+    lib.gemm_mxfp4_abi_version.argtypes = []
     _LIB = lib
     return lib
 
@@ -362,3 +380,279 @@ def gemm_batched(A, B, out=None, *, variant: int | str | None = None, config: in
     A or B may be an expanded tensor with batch stride 0, and either may be
     a batch of transposed views)."""
     return _call(A, B, out, variant, config, stream, batched=True)
+
+
+# ---- microscaled 4-bit floating point (include/gemm_mxfp4.h) ----------------
+
+MXFP4_BLOCK = 32  # values that share a scale
+
+
+class Mxfp4Matrix(ctypes.Structure):
+    """gemm_mxfp4_matrix of the C header."""
+
+    _fields_ = [("codes", _vp), ("ld_codes", _i64), ("stride_codes", _i64),
+                ("scales", _vp), ("ld_scales", _i64), ("stride_scales", _i64)]
+
+
+def _matrix_arg(m):
+    return None if m is None else ctypes.byref(m)
+
+
+def gemm_mxfp4_quantize(batch, rows, cols, X, ldx, sX, Q, QT, stream=None) -> int:
+    return load().gemm_mxfp4_quantize(batch, rows, cols, X, ldx, sX, _matrix_arg(Q),
+                                      _matrix_arg(QT), stream)
+
+
+def gemm_mxfp4_dequantize(batch, rows, cols, Q, Y, ldy, sY, stream=None) -> int:
+    return load().gemm_mxfp4_dequantize(batch, rows, cols, _matrix_arg(Q), Y, ldy, sY, stream)
+
+
+def gemm_mxfp4_product(batch, M, N, K, A, B, C, ldc, sC, workspace=None, workspace_bytes=0,
+                       stream=None) -> int:
+    """The C entry point gemm_mxfp4 (that name is the tensor-level call here)."""
+    return load().gemm_mxfp4(batch, M, N, K, _matrix_arg(A), _matrix_arg(B), C, ldc, sC,
+                             workspace, workspace_bytes, stream)
+
+
+def gemm_mxfp4_workspace_size(batch, M, N, K) -> int:
+    return load().gemm_mxfp4_workspace_size(batch, M, N, K)
+
+
+def gemm_mxfp4_weight_product(opW, batch, M, N, K, A, lda, sA, W, C, ldc, sC, workspace=None,
+                              workspace_bytes=0, stream=None) -> int:
+    """The C entry point gemm_mxfp4_weight (that name is the tensor-level call here)."""
+    return load().gemm_mxfp4_weight(opW, batch, M, N, K, A, lda, sA, _matrix_arg(W), C, ldc, sC,
+                                    workspace, workspace_bytes, stream)
+
+
+def gemm_mxfp4_weight_workspace_size(opW, batch, M, N, K) -> int:
+    return load().gemm_mxfp4_weight_workspace_size(opW, batch, M, N, K)
+
+
+def gemm_mxfp4_abi_version() -> int:
+    return load().gemm_mxfp4_abi_version()
+
+
+class Mxfp4:
+    """A matrix (or a batch of them) in microscaled 4-bit floating point:
+    ``codes`` (..., rows, >= 16 ceil(cols / 32)) and ``scales`` (..., rows,
+    >= ceil(cols / 32)), uint8 tensors with unit stride along the last axis,
+    in the layout of include/gemm_mxfp4.h, and the number of columns.  It
+    holds the tensors; their memory is not copied."""
+
+    __slots__ = ("codes", "scales", "cols", "_c")
+
+    def __init__(self, codes, scales, cols: int):
+        import torch
+
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda:
+            raise TypeError("codes and scales must be uint8 GPU tensors")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales are on different devices")
+        cs, ss = codes.shape, scales.shape
+        if len(cs) not in (2, 3) or len(ss) != len(cs) or cs[:-1] != ss[:-1]:
+            raise ValueError(f"codes {tuple(cs)} and scales {tuple(ss)} must be 2-D or 3-D with "
+                             "the same rows")
+        cols = int(cols)
+        nb = (cols + MXFP4_BLOCK - 1) // MXFP4_BLOCK
+        words = (nb + 3) // 4 * 4
+        if cols < 0 or cs[-1] < nb * 16 or ss[-1] < words:
+            raise ValueError(f"{cols} columns need {nb * 16} bytes of codes and {words} of scales "
+                             f"a row, not {cs[-1]} and {ss[-1]}")
+        ct, st = codes.stride(), scales.stride()
+        if (cs[-1] > 1 and ct[-1] != 1) or (ss[-1] > 1 and st[-1] != 1):
+            raise ValueError("codes and scales must have unit stride along the last axis")
+        self.codes, self.scales, self.cols = codes, scales, cols
+        rows = cs[-2]
+        batched = len(cs) == 3
+        self._c = Mxfp4Matrix(codes.data_ptr(), ct[-2] if rows > 1 else cs[-1] // 16 * 16,
+                              ct[0] if batched and cs[0] > 1 else 0,
+                              scales.data_ptr(), st[-2] if rows > 1 else ss[-1] // 4 * 4,
+                              st[0] if batched and cs[0] > 1 else 0)
+
+    @property
+    def shape(self) -> tuple[int, ...]:
+        return (*self.codes.shape[:-1], self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def __repr__(self) -> str:
+        return f"Mxfp4(shape={self.shape}, device={self.device})"
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty for memory that work on ``stream`` (None: the current one)
+    will use: taken from that stream's pool, so that nothing else still uses
+    it, and nothing else gets it before that work is done."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def mxfp4_empty(shape, device="cuda", *, stream=None) -> Mxfp4:
+    """An uninitialised Mxfp4 of ``shape`` (rows, cols) or (batch, rows, cols)."""
+    import torch
+
+    *lead, cols = shape
+    nb = (cols + MXFP4_BLOCK - 1) // MXFP4_BLOCK
+    return Mxfp4(_empty((*lead, nb * 16), torch.uint8, device, stream),
+                 _empty((*lead, (nb + 3) // 4 * 4), torch.uint8, device, stream), cols)
+
+
+def _run_on(device, stream, fn, *args) -> None:
+    """Calls a C entry point with the stream as its last argument, with the
+    tensors' device current, and raises on an error."""
+    import torch
+
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream on {stream.device}, operands on {device}")
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, gemm_f32_last_error())
+
+
+def _float_operand(t, name: str, device=None) -> tuple[int, int, int, int]:
+    """(op, leading dimension, batch stride, batch) of a 2-D or 3-D tensor, as _operand."""
+    dims = t.dim()
+    if dims not in (2, 3):
+        raise TypeError(f"{name} must be a 2-D or 3-D float32 GPU tensor")
+    op, ld, bs = _operand(t, name, dims)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} on {t.device}, other operands on {device}")
+    batch = t.shape[0] if dims == 3 else 1
+    return op, ld, (bs if batch > 1 else 0), batch
+
+
+def _quantize(X, want_rows: bool, want_cols: bool, stream, out, out_t):
+    op, ld, bs, batch = _float_operand(X, "X")
+    if op == OP_T:  # X is the transpose of what is stored: so are its blocks
+        stored = X.transpose(-1, -2)
+        q_cols, q_rows = _quantize(stored, want_cols, want_rows, stream, out_t, out)
+        return q_rows, q_cols
+    lead, (rows, cols) = tuple(X.shape[:-2]), X.shape[-2:]
+    dev = X.device
+
+    def target(q, shape):
+        if q is None:
+            return mxfp4_empty(shape, dev, stream=stream)
+        if q.shape != shape or q.device != dev:
+            raise ValueError(f"out is {q!r}, expected shape {shape} on {dev}")
+        return q
+
+    q = target(out, (*lead, rows, cols)) if want_rows else None
+    qt = target(out_t, (*lead, cols, rows)) if want_cols else None
+    _run_on(dev, stream, load().gemm_mxfp4_quantize, batch, rows, cols, X.data_ptr(), ld, bs,
+            None if q is None else ctypes.byref(q._c), None if qt is None else ctypes.byref(qt._c))
+    return q, qt
+
+
+def mxfp4_quantize(X, out: Mxfp4 | None = None, *, stream=None) -> Mxfp4:
+    """X (2-D or 3-D float32 GPU tensor, row-major or a transposed view of a
+    row-major matrix) rounded to the format, with blocks along its last axis:
+    ``mxfp4_quantize(X)`` for a product that sums over X's columns,
+    ``mxfp4_quantize(X.T)`` for one that sums over its rows."""
+    return _quantize(X, True, False, stream, out, None)[0]
+
+
+def mxfp4_quantize_both(X, out: Mxfp4 | None = None, out_t: Mxfp4 | None = None, *,
+                        stream=None) -> tuple[Mxfp4, Mxfp4]:
+    """(mxfp4_quantize(X), mxfp4_quantize(X.transpose(-1, -2))) in one read of
+    X, as a training step needs them."""
+    return _quantize(X, True, True, stream, out, out_t)
+
+
+def mxfp4_dequantize(q: Mxfp4, out=None, *, stream=None):
+    """The float32 values of ``q``."""
+    import torch
+
+    shape = q.shape
+    if out is None:
+        out = _empty(shape, torch.float32, q.device, stream)
+    elif tuple(out.shape) != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
+    op, ld, bs, batch = _float_operand(out, "out", q.device)
+    if op != OP_N:
+        raise ValueError("out must be row-major")
+    _run_on(q.device, stream, load().gemm_mxfp4_dequantize, batch, shape[-2], shape[-1],
+            ctypes.byref(q._c), out.data_ptr(), ld, bs)
+    return out
+
+
+def _mxfp4_out(out, shape, device, workspace, need: int, stream):
+    """(out, its leading dimension and batch stride, workspace pointer and bytes)."""
+    import torch
+
+    if out is None:
+        out = _empty(shape, torch.float32, device, stream)
+    elif tuple(out.shape) != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
+    op, ld, bs, _ = _float_operand(out, "out", device)
+    if op != OP_N:
+        raise ValueError("out must be row-major")
+    if workspace is None:
+        if need:
+            workspace = _empty(need // 4, torch.float32, device, stream)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    if workspace is None:
+        return out, ld, bs, workspace, None, 0
+    return out, ld, bs, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gemm_mxfp4(A: Mxfp4, B: Mxfp4, out=None, workspace=None, *, stream=None):
+    """``out = A @ B.T`` (float32) with A (M x K) and B (N x K) both in the
+    format, or a batch of such products (3-D; an expanded batch is allowed).
+    ``workspace`` (a GPU tensor of at least gemm_mxfp4_workspace_size bytes)
+    is allocated here when the sizes call for one and None is given.
+    Enqueued on ``stream``, default torch's current stream."""
+    sa, sb = A.shape, B.shape
+    if len(sa) != len(sb) or sa[:-2] != sb[:-2] or sa[-1] != sb[-1]:
+        raise ValueError(f"shape mismatch {sa} x {sb} transposed")
+    device = A.codes.device
+    if B.codes.device != device:
+        raise ValueError(f"A on {device}, B on {B.codes.device}")
+    batch = sa[0] if len(sa) == 3 else 1
+    M, N, K = sa[-2], sb[-2], sa[-1]
+    lib = load()
+    out, ldc, sc, workspace, wp, wb = _mxfp4_out(
+        out, (*sa[:-1], N), device, workspace, lib.gemm_mxfp4_workspace_size(batch, M, N, K),
+        stream)
+    _run_on(device, stream, lib.gemm_mxfp4, batch, M, N, K, ctypes.byref(A._c),
+            ctypes.byref(B._c), out.data_ptr(), ldc, sc, wp, wb)
+    return out
+
+
+def gemm_mxfp4_weight(A, W: Mxfp4, out=None, workspace=None, *, op: int = OP_T, stream=None):
+    """``out = A @ W.T`` (op = OP_T: W is N x K, a stored layer) or ``A @ W``
+    (op = OP_N: W is K x N; with A the gradient of the former's result, the
+    gradient with respect to its activations).  A is a row-major float32 GPU
+    tensor, 2-D, or 3-D with a batch of W; it is not rounded.  ``workspace``
+    and ``stream`` as in gemm_mxfp4."""
+    if op not in (OP_N, OP_T):
+        raise ValueError("op must be OP_N or OP_T")
+    opa, lda, sa, batch = _float_operand(A, "A", W.codes.device)
+    if opa != OP_N:
+        raise ValueError("A must be row-major")
+    M, K = A.shape[-2], A.shape[-1]
+    sw = W.shape
+    N, K2 = (sw[-2], sw[-1]) if op == OP_T else (sw[-1], sw[-2])
+    if K != K2 or A.dim() != len(sw) or tuple(A.shape[:-2]) != tuple(sw[:-2]):
+        raise ValueError(f"shape mismatch {tuple(A.shape)} x {sw}{' transposed' if op == OP_T else ''}")
+    lib = load()
+    out, ldc, sc, workspace, wp, wb = _mxfp4_out(
+        out, (*A.shape[:-1], N), A.device, workspace,
+        lib.gemm_mxfp4_weight_workspace_size(op, batch, M, N, K), stream)
+    _run_on(A.device, stream, lib.gemm_mxfp4_weight, op, batch, M, N, K, A.data_ptr(), lda, sa,
+            ctypes.byref(W._c), out.data_ptr(), ldc, sc, wp, wb)
+    return out

@@ -30,7 +30,8 @@ COMMON_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 
-SOURCES = ["mfma.hip", "mfma16.hip", "mfma_regs.hip", "api.hip", "naive.hip", "lds_tiled.hip", "regblock.hip"]
+SOURCES = ["mfma.hip", "mfma16.hip", "mfma_regs.hip", "api.hip", "naive.hip", "lds_tiled.hip", "regblock.hip",
+           "mxfp4_api.hip", "mxfp4_convert.hip", "mxfp4_product.hip", "mxfp4_weight.hip"]
 
 
 def _compile(src: str, extra: list[str]) -> str:

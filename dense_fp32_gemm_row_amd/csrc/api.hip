@@ -14,17 +14,16 @@
 #include <mutex>
 
 #include "../../include/gemm_f32.h"
+#include "errors.h"
 #include "gemm_internal.h"
 #include "tune_table.inc"
 
 namespace gemm_f32_impl {
-namespace {
 
-thread_local char g_last_error[256] = "";
+static thread_local char g_last_error[256] = "";
 
 void clear_error() { g_last_error[0] = '\0'; }
 
-int fail(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int code, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -32,6 +31,8 @@ int fail(int code, const char *fmt, ...) {
     va_end(ap);
     return code;
 }
+
+namespace {
 
 __global__ __launch_bounds__(256) void zero_fill_kernel(float *__restrict__ C, int M, int N,
                                                         int64_t ldc, int batch, int64_t sc) {
