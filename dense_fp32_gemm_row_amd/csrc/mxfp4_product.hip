@@ -1,7 +1,9 @@
 // C = A B^T with both operands in MXFP4 (include/gemm_mxfp4.h).
 
 #include <algorithm>
+#include <type_traits>
 
+#include "gemm_internal.h"
 #include "mxfp4.h"
 #include "mxfp4_device.h"
 
@@ -9,45 +11,371 @@ namespace gemm_f32_impl {
 namespace mx {
 namespace {
 
-// One wavefront per 32 x 32 tile, operands straight from global memory.  In
-// v_mfma_scale_f32_32x32x64_f8f6f4 lane l holds the codes of row l % 32,
-// block l / 32 of two, and the block's scale byte.
-__global__ __launch_bounds__(256) void product_kernel(Product p, int64_t tiles_m, int64_t tiles_n,
-                                                      int64_t tiles) {
-    const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
-    const int nb = (p.K + kBlock - 1) / kBlock;
-    for (int64_t t = blockIdx.x * int64_t{4} + (threadIdx.x >> 6); t < tiles;
-         t += gridDim.x * int64_t{4}) {
-        const int64_t line = t / tiles_n, b = line / tiles_m;
-        const int64_t n0 = (t - line * tiles_n) * 32, m0 = (line - b * tiles_m) * 32;
-        const int64_t m = min(m0 + row, int64_t{p.M} - 1), n = min(n0 + row, int64_t{p.N} - 1);
-        const uint8_t *A = p.a.codes + b * p.a.sq + m * p.a.ldq;
-        const uint8_t *B = p.b.codes + b * p.b.sq + n * p.b.ldq;
-        const uint8_t *As = p.a.scales + b * p.a.ss + m * p.a.lds;
-        const uint8_t *Bs = p.b.scales + b * p.b.ss + n * p.b.lds;
-        f32x16 acc = {};
-        for (int64_t k = half; k < nb + half; k += 2) {
-            u32x4 x = {}, y = {};
-            int ex = 0, ey = 0;
-            if (k < nb) {
-                x = *reinterpret_cast<const u32x4 *>(A + k * kBlockBytes);
-                y = *reinterpret_cast<const u32x4 *>(B + k * kBlockBytes);
-                ex = As[k];
-                ey = Bs[k];
-            }
-            const i32x8 X = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
-            const i32x8 Y = {(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
-            acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(X, Y, acc, 4, 4, 0, ex, 0, ey);
+typedef __attribute__((address_space(3))) void *lptr_t;
+
+// acc += X Y over one 32 x 32 x 64 step; T selects the byte of the scale words.
+template <int T>
+__device__ __forceinline__ f32x16 mfma_fp4(u32x4 x, u32x4 y, f32x16 acc, uint32_t ex, uint32_t ey) {
+    const i32x8 X = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+    const i32x8 Y = {(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(X, Y, acc, 4, 4, T, (int)ex, T, (int)ey);
+}
+
+// Workgroup barrier after which at most N of this wavefront's most recent
+// vector-memory instructions may be outstanding, and no LDS access is.  The
+// empty asm statements keep memory accesses on their side.
+template <int N>
+__device__ __forceinline__ void wait_older() {
+    static_assert(N >= 0 && N < 64, "vmcnt has 6 bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+    asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void barrier_only() {
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Rows of an operand from a tile's first one, as a buffer: offsets past the
+// operand's last byte, as the rows past an edge make, read as zeros.
+struct Rows {
+    __amdgpu_buffer_rsrc_t rsrc;
+    int ld;
+};
+constexpr int kOutside = static_cast<int>(0x80000000u);  // an offset past every buffer
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0,
+                                             static_cast<int>(min(bytes, int64_t{0x7fffffff})),
+                                             0x00020000);
+}
+__device__ __forceinline__ Rows rows_from(const uint8_t *base, int64_t ld, int first, int rows,
+                                          int row_bytes) {
+    return {buffer_of(base + first * ld, (rows - 1 - first) * ld + row_bytes), static_cast<int>(ld)};
+}
+
+// A tile of WM x WN wavefronts, each FM x FN blocks of 32 x 32.  K runs in
+// stages of 128 (4 blocks of every row), kStages of them (a group: 512 k) in
+// LDS at a time.
+template <int FM, int FN, int WM, int WN>
+struct Tile {
+    static constexpr int BM = FM * WM * 32, BN = FN * WN * 32, R = BM + BN, NW = WM * WN;
+    static constexpr int kStages = 4, kStageBlocks = 4, kRowBytes = kStageBlocks * kBlockBytes;
+    static constexpr int kGroupBlocks = kStages * kStageBlocks;
+    static constexpr int kLoads = R / 16 / NW;                   // a wavefront's code loads per stage
+    static constexpr int kScaleLoads = (R / 64 + NW - 1) / NW;   // ... scale loads per group
+    static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0, "");
+};
+
+// One slice of one product's tile, as a workgroup meets it.
+struct Place {
+    int64_t slice;  // batch * splits + split
+    int m0, n0, g0, g1;
+};
+
+template <class T>
+__device__ __forceinline__ Place place_of(const Product &p, int64_t id, int tiles_m, int tiles_n,
+                                          int groups, int len) {
+    const int per = tiles_m * tiles_n;
+    Place q;
+    q.slice = id / per;
+    int tm, tn;
+    grouped_tile(static_cast<int>(id - q.slice * per), tiles_m, tiles_n, 8, tm, tn);
+    q.m0 = tm * T::BM;
+    q.n0 = tn * T::BN;
+    const int split = static_cast<int>(q.slice % p.splits);
+    q.g0 = split * len;
+    q.g1 = min(q.g0 + len, groups);
+    return q;
+}
+
+// Persistent kernel: a workgroup walks over tiles, and its loads run one
+// group ahead of its products, over the ends of tiles too.
+//
+// In v_mfma_scale_f32_32x32x64_f8f6f4 lane l holds the codes of row l % 32,
+// block l / 32 of two, and that block's scale.  Which two blocks meet in one
+// instruction is free as long as A and B agree: in a stage, lanes 0-31 take
+// blocks 0 and 1, lanes 32-63 blocks 2 and 3, so a lane's scales are one half
+// of the row's scale word.
+//
+// LDS holds a stage's rows as 4 slots of 16 bytes, filled by direct loads
+// (64 lanes x 16 bytes into 1 KiB: 16 rows).  Block b of row r sits in slot
+// b ^ (r / 4 % 4): 16 lanes that read one block of 16 rows then touch every
+// bank once.
+//
+// Order within a stage: the fragments of its second half are read under the
+// products of its first; then a barrier, after which the next stage is in
+// LDS and this one's buffer is free; then the loads one group on and the
+// next stage's first fragments go out under the products of the second half.
+// So neither the barrier nor an LDS read is waited for with idle matrix
+// cores.
+template <int FM, int FN, int WM, int WN, int OCC, bool WHOLE>
+__global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product p, int tiles_m,
+                                                                        int tiles_n, int64_t tiles,
+                                                                        int groups, int len) {
+    using T = Tile<FM, FN, WM, WN>;
+    constexpr int kStageBytes = T::R * T::kRowBytes;
+    __shared__ __align__(1024) uint8_t codes0[kStageBytes];
+    __shared__ __align__(1024) uint8_t codes1[kStageBytes];
+    __shared__ __align__(1024) uint8_t codes2[kStageBytes];
+    __shared__ __align__(1024) uint8_t codes3[kStageBytes];
+    __shared__ __align__(1024) uint32_t scales[2 * T::kStages * T::R];  // [group parity][stage][row]
+
+    const int lane = threadIdx.x & 63, half = lane >> 5, row = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int nb = (p.K + kBlock - 1) / kBlock, words = (nb + 3) / 4;
+    const int64_t grid = gridDim.x;
+
+    // ---- loads: codes one group ahead of the products, scales two ----
+    struct Cursor {
+        int64_t id;
+        int g, g1;
+        Rows a, b;
+    };
+    auto seek = [&](Cursor &c, bool scale) {  // to the start of tile c.id
+        if (c.id >= tiles) {
+            c.g = 0, c.g1 = 0;
+            return;
         }
-        if (n0 + row < p.N) {
-            float *C = p.C + b * p.sc + n0 + row;
+        const Place q = place_of<T>(p, c.id, tiles_m, tiles_n, groups, len);
+        const int64_t b = q.slice / p.splits;
+        c.g = q.g0, c.g1 = q.g1;
+        if (scale) {
+            c.a = rows_from(p.a.scales + b * p.a.ss, p.a.lds, q.m0, p.M, words * 4);
+            c.b = rows_from(p.b.scales + b * p.b.ss, p.b.lds, q.n0, p.N, words * 4);
+        } else {
+            c.a = rows_from(p.a.codes + b * p.a.sq, p.a.ldq, q.m0, p.M, nb * kBlockBytes);
+            c.b = rows_from(p.b.codes + b * p.b.sq, p.b.ldq, q.n0, p.N, nb * kBlockBytes);
+        }
+    };
+    auto advance = [&](Cursor &c, bool scale) {
+        if (++c.g >= c.g1) {
+            c.id += grid;
+            seek(c, scale);
+        }
+    };
+    const int lrow = wave * 16 + (lane >> 2);                // row of a lane's first load
+    const int blk = (lane & 3) ^ ((lane >> 4) & 3);          // block of its slot
+    auto load = [&](const Cursor &c, int stage, uint8_t *codes) {
+        const int block = c.g * T::kGroupBlocks + stage * T::kStageBlocks + blk;
+        const int off = c.g < c.g1 ? min(block, nb - 1) * kBlockBytes : kOutside;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int64_t r = m0 + (i & 3) + 8 * (i >> 2) + 4 * half;
-                if (r < p.M) C[r * p.ldc] = acc[i];
+        for (int j = 0; j < T::kLoads; ++j) {
+            const bool in_a = j * T::NW * 16 < T::BM;
+            const Rows &m = in_a ? c.a : c.b;
+            const int r = j * T::NW * 16 - (in_a ? 0 : T::BM);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(m.rsrc, (lptr_t)(codes + (j * T::NW + wave) * 1024),
+                                                     16, (lrow + r) * m.ld + off, 0, 0, 0);
+        }
+    };
+    // A group's scales, 16 bytes of a row per lane: the cache answers so many
+    // requests a cycle, whatever they carry, and a word per row and stage was
+    // two thirds of all requests.
+    u32x4 held[T::kScaleLoads];
+    auto fetch_scales = [&](const Cursor &c) {
+#pragma unroll
+        for (int j = 0; j < T::kScaleLoads; ++j) {
+            const int r = (j * T::NW + wave) * 64;
+            const Rows &m = r < T::BM ? c.a : c.b;
+            const int at = (r - (r < T::BM ? 0 : T::BM) + lane) * m.ld;
+            const int off = c.g < c.g1 && r < T::R ? 0 : kOutside;
+            if constexpr (WHOLE) {
+                held[j] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(m.rsrc, (at + 16 * c.g) | off, 0, 0));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    held[j][k] = __builtin_amdgcn_raw_buffer_load_b32(
+                        m.rsrc, (at + 4 * min(4 * c.g + k, words - 1)) | off, 0, 0);
             }
         }
+    };
+    // Blocks past the end get scale 2^-127 on both sides: whatever their
+    // codes, such products are below 2^-240 and leave an FP32 sum as it is.
+    int put = lane;  // + group parity x 4 R
+    auto store_scales = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < T::kScaleLoads; ++j) {
+            const int r = (j * T::NW + wave) * 64;
+            if (T::R % (64 * T::NW) && r >= T::R) break;
+#pragma unroll
+            for (int k = 0; k < T::kStages; ++k) {
+                const int valid = min(max(nb - (g * T::kStages + k) * T::kStageBlocks, 0), 4);
+                const uint32_t mask = valid == 4 ? 0xffffffffu : (1u << (8 * valid)) - 1u;
+                scales[put + k * T::R + r] = held[j][k] & mask;
+            }
+        }
+        put = 2 * lane + 4 * T::R - put;
+    };
+
+    // ---- fragments ----
+    // Byte offsets of the lane's two blocks in a stage.  Opaque values keep
+    // the read addresses within reach of the compiler's alias analysis, which
+    // else waits for the loads of other buffers first.
+    const int ra = wm * FM * 32 + row, rb = T::BM + wn * FN * 32 + row;
+    int oa[2], ob[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int slot = ((2 * half + t) ^ ((row >> 2) & 3)) * kBlockBytes;
+        oa[t] = ra * T::kRowBytes + slot;
+        ob[t] = rb * T::kRowBytes + slot;
+        asm volatile("" : "+v"(oa[t]), "+v"(ob[t]));
     }
+    int oea = ra + 4 * T::R, oeb = rb + 4 * T::R;  // group parity x 4 R (turned first by read_scales)
+    asm volatile("" : "+v"(oea), "+v"(oeb), "+v"(put));
+    u32x4 x[2][FM], y[2][FN];
+    uint32_t ea[2][FM], eb[2][FN];  // [stage parity]
+    auto fetch = [&](auto tc, const uint8_t *codes) {
+        constexpr int t = decltype(tc)::value;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            x[t][i] = *reinterpret_cast<const u32x4 *>(codes + oa[t] + 32 * i * T::kRowBytes);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            y[t][j] = *reinterpret_cast<const u32x4 *>(codes + ob[t] + 32 * j * T::kRowBytes);
+    };
+    auto read_scales = [&](auto uc, int stage) {
+        constexpr int u = decltype(uc)::value;
+        if (stage == 0) {  // the next group's
+            oea = 2 * ra + 4 * T::R - oea;
+            oeb = 2 * rb + 4 * T::R - oeb;
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) ea[u][i] = scales[oea + stage * T::R + 32 * i] >> (16 * half);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) eb[u][j] = scales[oeb + stage * T::R + 32 * j] >> (16 * half);
+    };
+
+    f32x16 acc[FM][FN];
+    auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    };
+    auto multiply = [&](auto tc, auto uc) {
+        constexpr int t = decltype(tc)::value, u = decltype(uc)::value;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = mfma_fp4<t>(x[t][i], y[t][j], acc[i][j], ea[u][i], eb[u][j]);
+    };
+    // One load or LDS read between two matrix instructions: issued in a row
+    // they would keep the matrix cores waiting.
+    auto interleave = [&](int loads, int reads) {
+#pragma unroll
+        for (int k = 0; k < FM * FN; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (k < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (k < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        // The sums so far are used here, so their instructions stay ahead.
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) asm volatile("" ::"a"(acc[i][j]));
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    auto store_tile = [&](int64_t id) {
+        const Place q = place_of<T>(p, id, tiles_m, tiles_n, groups, len);
+        const int64_t ldc = p.splits > 1 ? p.N : p.ldc;
+        const float *base = p.splits > 1 ? p.W + q.slice * p.M * ldc : p.C + q.slice * p.sc;
+        const int mw = q.m0 + wm * FM * 32, nw = q.n0 + wn * FN * 32;
+        if (mw >= p.M || nw >= p.N) return;  // nothing of C: the buffer below would have no bytes
+        const __amdgpu_buffer_rsrc_t c =
+            buffer_of(base + mw * ldc + nw, ((p.M - 1 - mw) * ldc + p.N - nw) * 4);
+        const int ld = static_cast<int>(ldc) * 4;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int n = 32 * j + row;
+            const int at = nw + n < p.N ? n * 4 + 4 * half * ld : kOutside;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float v = acc[i][j][r];  // (a bit cast of the element itself takes element 0)
+                    __builtin_amdgcn_raw_buffer_store_b32(
+                        __builtin_bit_cast(uint32_t, v), c,
+                        at + (32 * i + (r & 3) + 8 * (r >> 2)) * ld, 0, 0);
+                }
+        }
+    };
+
+    std::integral_constant<int, 0> c0;
+    std::integral_constant<int, 1> c1;
+
+    // Consecutive tiles go to workgroups of one XCD.
+    int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+    Cursor cc, cs;
+    cc.id = cs.id = id;
+    seek(cc, false);
+    seek(cs, true);
+    fetch_scales(cs);
+    load(cc, 0, codes0);
+    load(cc, 1, codes1);
+    load(cc, 2, codes2);
+    load(cc, 3, codes3);
+    store_scales(cs.g);
+    advance(cs, true);
+    fetch_scales(cs);
+    store_scales(cs.g);
+    advance(cs, true);
+    advance(cc, false);
+    wait_older<0>();
+    barrier_only();
+    fetch(c0, codes0);
+    read_scales(c0, 0);
+
+    constexpr int L = T::kLoads, S = T::kScaleLoads * (WHOLE ? 1 : 4);
+    // Stage `i` of the group: products from `cur`, the next stage in `nxt`.
+#define GEMM_MXFP4_STAGE(i, cur, nxt, u, v)                                          \
+    fetch(c1, cur);                                                                  \
+    multiply(c0, u);                                                                 \
+    interleave(0, FM + FN);                                                          \
+    wait_older<2 * L + (i > 0 ? S : 0)>();                                           \
+    barrier_only();                                                                  \
+    if (i == 3) store_scales(cs.g);                                                  \
+    load(cc, i, cur);                                                                \
+    if (i == 0) fetch_scales(cs);                                                    \
+    fetch(c0, nxt);                                                                  \
+    read_scales(v, (i + 1) % 4);                                                     \
+    multiply(c1, u);                                                                 \
+    interleave(L, FM + FN);
+
+    for (; id < tiles; id += grid) {
+        const Place at = place_of<T>(p, id, tiles_m, tiles_n, groups, len);
+        clear();
+        for (int g = at.g0; g < at.g1; ++g) {
+            GEMM_MXFP4_STAGE(0, codes0, codes1, c0, c1)
+            GEMM_MXFP4_STAGE(1, codes1, codes2, c1, c0)
+            GEMM_MXFP4_STAGE(2, codes2, codes3, c0, c1)
+            GEMM_MXFP4_STAGE(3, codes3, codes0, c1, c0)
+            advance(cc, false);
+            advance(cs, true);
+        }
+        store_tile(id);
+    }
+#undef GEMM_MXFP4_STAGE
+    wait_older<0>();  // no load may land in LDS after the workgroup has ended
+}
+
+template <int FM, int FN, int WM, int WN, int OCC>
+hipError_t launch_tile(const Product &p, hipStream_t stream) {
+    using T = Tile<FM, FN, WM, WN>;
+    const int tm = ceil_div(p.M, T::BM), tn = ceil_div(p.N, T::BN);
+    const int64_t tiles = static_cast<int64_t>(tm) * tn * p.batch * p.splits;
+    const int groups = ceil_div(static_cast<int>(blocks_of(p.K)), T::kGroupBlocks);
+    const int len = ceil_div(groups, p.splits);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 256 * OCC));
+    if (groups * T::kStages * T::kStageBlocks == blocks_of(p.K))
+        product_tile_kernel<FM, FN, WM, WN, OCC, true>
+            <<<grid, T::NW * 64, 0, stream>>>(p, tm, tn, tiles, groups, len);
+    else
+        product_tile_kernel<FM, FN, WM, WN, OCC, false>
+            <<<grid, T::NW * 64, 0, stream>>>(p, tm, tn, tiles, groups, len);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -55,11 +383,7 @@ __global__ __launch_bounds__(256) void product_kernel(Product p, int64_t tiles_m
 int product_splits(int64_t, int64_t, int64_t, int64_t) { return 1; }
 
 hipError_t launch_product(const Product &p, hipStream_t stream) {
-    const int64_t tm = (p.M + int64_t{31}) / 32, tn = (p.N + int64_t{31}) / 32;
-    const int64_t tiles = tm * tn * p.batch;
-    product_kernel<<<static_cast<unsigned>(std::min<int64_t>((tiles + 3) / 4, 1 << 22)), 256, 0,
-                     stream>>>(p, tm, tn, tiles);
-    return hipGetLastError();
+    return launch_tile<4, 4, 2, 2, 1>(p, stream);
 }
 
 }  // namespace mx
