@@ -221,7 +221,8 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
         ob[t] = rb * T::kRowBytes + slot;
         asm volatile("" : "+v"(oa[t]), "+v"(ob[t]));
     }
-    int oea = ra + 4 * T::R, oeb = rb + 4 * T::R;  // group parity x 4 R (turned first by read_scales)
+    // half words of the lane's scales, + group parity x 8 R (read_scales turns it first)
+    int oea = 2 * ra + half + 8 * T::R, oeb = 2 * rb + half + 8 * T::R;
     asm volatile("" : "+v"(oea), "+v"(oeb), "+v"(put));
     u32x4 x[2][FM], y[2][FN];
     uint32_t ea[2][FM], eb[2][FN];  // [stage parity]
@@ -236,14 +237,15 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
     };
     auto read_scales = [&](auto uc, int stage) {
         constexpr int u = decltype(uc)::value;
+        const uint16_t *halves = reinterpret_cast<const uint16_t *>(scales);
         if (stage == 0) {  // the next group's
-            oea = 2 * ra + 4 * T::R - oea;
-            oeb = 2 * rb + 4 * T::R - oeb;
+            oea = 4 * ra + 2 * half + 8 * T::R - oea;
+            oeb = 4 * rb + 2 * half + 8 * T::R - oeb;
         }
 #pragma unroll
-        for (int i = 0; i < FM; ++i) ea[u][i] = scales[oea + stage * T::R + 32 * i] >> (16 * half);
+        for (int i = 0; i < FM; ++i) ea[u][i] = halves[oea + 2 * (stage * T::R + 32 * i)];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) eb[u][j] = scales[oeb + stage * T::R + 32 * j] >> (16 * half);
+        for (int j = 0; j < FN; ++j) eb[u][j] = halves[oeb + 2 * (stage * T::R + 32 * j)];
     };
 
     f32x16 acc[FM][FN];
@@ -258,8 +260,10 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
+            for (int k = 0; k < FN; ++k) {
+                const int j = i & 1 ? FN - 1 - k : k;  // one operand stays from each to the next
                 acc[i][j] = mfma_fp4<t>(x[t][i], y[t][j], acc[i][j], ea[u][i], eb[u][j]);
+            }
     };
     // One load or LDS read between two matrix instructions: issued in a row
     // they would keep the matrix cores waiting.
@@ -267,7 +271,10 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
 #pragma unroll
         for (int k = 0; k < FM * FN; ++k) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            if (k < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (reads > FM * FN / 2 && 2 * k < reads)
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            else if (k < reads)
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             if (k < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
         // The sums so far are used here, so their instructions stay ahead.
@@ -332,15 +339,15 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
     // Stage `i` of the group: products from `cur`, the next stage in `nxt`.
 #define GEMM_MXFP4_STAGE(i, cur, nxt, u, v)                                          \
     fetch(c1, cur);                                                                  \
+    read_scales(v, (i + 1) % 4);                                                     \
     multiply(c0, u);                                                                 \
-    interleave(0, FM + FN);                                                          \
+    interleave(0, 2 * (FM + FN));                                                    \
     wait_older<2 * L + (i > 0 ? S : 0)>();                                           \
     barrier_only();                                                                  \
     if (i == 3) store_scales(cs.g);                                                  \
     load(cc, i, cur);                                                                \
     if (i == 0) fetch_scales(cs);                                                    \
     fetch(c0, nxt);                                                                  \
-    read_scales(v, (i + 1) % 4);                                                     \
     multiply(c1, u);                                                                 \
     interleave(L, FM + FN);
 
