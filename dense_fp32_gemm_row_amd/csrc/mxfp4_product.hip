@@ -1,9 +1,9 @@
 // C = A B^T with both operands in MXFP4 (include/gemm_mxfp4.h).
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
-#include "gemm_internal.h"
 #include "mxfp4.h"
 #include "mxfp4_device.h"
 
@@ -11,46 +11,12 @@ namespace gemm_f32_impl {
 namespace mx {
 namespace {
 
-typedef __attribute__((address_space(3))) void *lptr_t;
-
 // acc += X Y over one 32 x 32 x 64 step; T selects the byte of the scale words.
 template <int T>
 __device__ __forceinline__ f32x16 mfma_fp4(u32x4 x, u32x4 y, f32x16 acc, uint32_t ex, uint32_t ey) {
     const i32x8 X = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
     const i32x8 Y = {(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(X, Y, acc, 4, 4, T, (int)ex, T, (int)ey);
-}
-
-// Workgroup barrier after which at most N of this wavefront's most recent
-// vector-memory instructions may be outstanding, and no LDS access is.  The
-// empty asm statements keep memory accesses on their side.
-template <int N>
-__device__ __forceinline__ void wait_older() {
-    static_assert(N >= 0 && N < 64, "vmcnt has 6 bits");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-    asm volatile("" ::: "memory");
-}
-__device__ __forceinline__ void barrier_only() {
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
-// Rows of an operand from a tile's first one, as a buffer: offsets past the
-// operand's last byte, as the rows past an edge make, read as zeros.
-struct Rows {
-    __amdgpu_buffer_rsrc_t rsrc;
-    int ld;
-};
-constexpr int kOutside = static_cast<int>(0x80000000u);  // an offset past every buffer
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0,
-                                             static_cast<int>(min(bytes, int64_t{0x7fffffff})),
-                                             0x00020000);
-}
-__device__ __forceinline__ Rows rows_from(const uint8_t *base, int64_t ld, int first, int rows,
-                                          int row_bytes) {
-    return {buffer_of(base + first * ld, (rows - 1 - first) * ld + row_bytes), static_cast<int>(ld)};
 }
 
 // A tile of WM x WN wavefronts, each FM x FN blocks of 32 x 32.  K runs in
@@ -65,28 +31,6 @@ struct Tile {
     static constexpr int kScaleLoads = (R / 64 + NW - 1) / NW;   // ... scale loads per group
     static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0, "");
 };
-
-// One slice of one product's tile, as a workgroup meets it.
-struct Place {
-    int64_t slice;  // batch * splits + split
-    int m0, n0, g0, g1;
-};
-
-template <class T>
-__device__ __forceinline__ Place place_of(const Product &p, int64_t id, int tiles_m, int tiles_n,
-                                          int groups, int len) {
-    const int per = tiles_m * tiles_n;
-    Place q;
-    q.slice = id / per;
-    int tm, tn;
-    grouped_tile(static_cast<int>(id - q.slice * per), tiles_m, tiles_n, 8, tm, tn);
-    q.m0 = tm * T::BM;
-    q.n0 = tn * T::BN;
-    const int split = static_cast<int>(q.slice % p.splits);
-    q.g0 = split * len;
-    q.g1 = min(q.g0 + len, groups);
-    return q;
-}
 
 // Persistent kernel: a workgroup walks over tiles, and its loads run one
 // group ahead of its products, over the ends of tiles too.
@@ -137,7 +81,7 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
             c.g = 0, c.g1 = 0;
             return;
         }
-        const Place q = place_of<T>(p, c.id, tiles_m, tiles_n, groups, len);
+        const Place q = place_of<T::BM, T::BN>(p, c.id, tiles_m, tiles_n, groups, len);
         const int64_t b = q.slice / p.splits;
         c.g = q.g0, c.g1 = q.g1;
         if (scale) {
@@ -286,7 +230,7 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
     };
 
     auto store_tile = [&](int64_t id) {
-        const Place q = place_of<T>(p, id, tiles_m, tiles_n, groups, len);
+        const Place q = place_of<T::BM, T::BN>(p, id, tiles_m, tiles_n, groups, len);
         const int64_t ldc = p.splits > 1 ? p.N : p.ldc;
         const float *base = p.splits > 1 ? p.W + q.slice * p.M * ldc : p.C + q.slice * p.sc;
         const int mw = q.m0 + wm * FM * 32, nw = q.n0 + wn * FN * 32;
@@ -352,7 +296,7 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
     interleave(L, FM + FN);
 
     for (; id < tiles; id += grid) {
-        const Place at = place_of<T>(p, id, tiles_m, tiles_n, groups, len);
+        const Place at = place_of<T::BM, T::BN>(p, id, tiles_m, tiles_n, groups, len);
         clear();
         for (int g = at.g0; g < at.g1; ++g) {
             GEMM_MXFP4_STAGE(0, codes0, codes1, c0, c1)
@@ -366,6 +310,88 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
     }
 #undef GEMM_MXFP4_STAGE
     wait_older<0>();  // no load may land in LDS after the workgroup has ended
+}
+
+// Few rows, and operands of any stride: a workgroup of NW wavefronts holds a
+// tile of 32 x 32 NT, its wavefronts take steps of 256 k in turn, straight
+// from global memory, and their sums are added in LDS in a fixed order.  What
+// it waits for is memory: every lane has 64 consecutive bytes of a row of B
+// (and A) on the way per step.
+template <int NT, int NW>
+__global__ __launch_bounds__(NW * 64) void product_rows_kernel(Product p, int64_t tiles_m,
+                                                               int64_t tiles_n, int64_t tiles) {
+    __shared__ __align__(16) float part[NW][NT][16][64];
+    const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int nb = (p.K + kBlock - 1) / kBlock, words = (nb + 3) / 4;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t line = t / tiles_n, b = line / tiles_m;
+        const int64_t n0 = (t - line * tiles_n) * 32 * NT, m0 = (line - b * tiles_m) * 32;
+        const int64_t m = min(m0 + row, int64_t{p.M} - 1);
+        const uint8_t *A = p.a.codes + b * p.a.sq + m * p.a.ldq;
+        const uint8_t *As = p.a.scales + b * p.a.ss + m * p.a.lds;
+        const uint8_t *B[NT], *Bs[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int64_t n = min(n0 + 32 * j + row, int64_t{p.N} - 1);
+            B[j] = p.b.codes + b * p.b.sq + n * p.b.ldq;
+            Bs[j] = p.b.scales + b * p.b.ss + n * p.b.lds;
+        }
+        f32x16 acc[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j] = f32x16{};
+        // lanes 0-31 take blocks 0-3 of a step, lanes 32-63 blocks 4-7: their
+        // scales are one word.  Blocks past the end get scale 2^-127 on both
+        // sides, which leaves an FP32 sum as it is.
+        for (int s = wave; s * 8 < nb; s += NW) {
+            const int first = s * 8 + 4 * half, valid = min(max(nb - first, 0), 4);
+            const uint32_t mask = valid == 4 ? 0xffffffffu : (1u << (8 * valid)) - 1u;
+            const int w = min(first / 4, words - 1) * 4;
+            const uint32_t ea = *reinterpret_cast<const uint32_t *>(As + w) & mask;
+            uint32_t eb[NT];
+            u32x4 x[4], y[NT][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t off = min(first + k, nb - 1) * int64_t{kBlockBytes};
+                x[k] = *reinterpret_cast<const u32x4 *>(A + off);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) y[j][k] = *reinterpret_cast<const u32x4 *>(B[j] + off);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) eb[j] = *reinterpret_cast<const uint32_t *>(Bs[j] + w) & mask;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                acc[j] = mfma_fp4<0>(x[0], y[j][0], acc[j], ea, eb[j]);
+                acc[j] = mfma_fp4<1>(x[1], y[j][1], acc[j], ea, eb[j]);
+                acc[j] = mfma_fp4<2>(x[2], y[j][2], acc[j], ea, eb[j]);
+                acc[j] = mfma_fp4<3>(x[3], y[j][3], acc[j], ea, eb[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) part[wave][j][r][lane] = acc[j][r];
+        __syncthreads();
+        for (int e = threadIdx.x; e < NT * 1024; e += NW * 64) {
+            const int l = e & 63, r = (e >> 6) & 15, j = e >> 10;
+            const int64_t n = n0 + 32 * j + (l & 31), mm = m0 + (r & 3) + 8 * (r >> 2) + 4 * (l >> 5);
+            if (mm >= p.M || n >= p.N) continue;
+            float v = part[0][j][r][l];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) v += part[w][j][r][l];
+            p.C[b * p.sc + mm * p.ldc + n] = v;
+        }
+        __syncthreads();
+    }
+}
+
+template <int NT, int NW>
+hipError_t launch_rows(const Product &p, hipStream_t stream) {
+    const int64_t tm = (p.M + int64_t{31}) / 32, tn = (p.N + int64_t{32 * NT - 1}) / (32 * NT);
+    const int64_t tiles = tm * tn * p.batch;
+    product_rows_kernel<NT, NW><<<static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20)), NW * 64, 0,
+                                  stream>>>(p, tm, tn, tiles);
+    return hipGetLastError();
 }
 
 template <int FM, int FN, int WM, int WN, int OCC>
@@ -385,12 +411,112 @@ hipError_t launch_tile(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Partial sums of the slices of K, added in ascending order.
+template <int V>
+__global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t total) {
+    typedef float vec __attribute__((ext_vector_type(V), aligned(4)));
+    const int64_t plane = static_cast<int64_t>(p.M) * p.N, per_row = p.N / V;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total;
+         e += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t line = e / per_row, j = (e - line * per_row) * V, b = line / p.M, i = line - b * p.M;
+        const float *w = p.W + b * p.splits * plane + i * p.N + j;
+        vec v = *reinterpret_cast<const vec *>(w);
+        for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const vec *>(w + s * plane);
+        *reinterpret_cast<vec *>(p.C + b * p.sc + i * p.ldc + j) = v;
+    }
+}
+
+// Which kernel a product takes: the least predicted time.  The figures are
+// microseconds measured on MI355X: per 512 k of a tile with the chip full
+// (and of a lone tile), per store of a tile, and fixed ones.
+//
+//   256 x 256  4 + rounds (3.95 / 512 k + 10.5), one tile a CU; a lone tile
+//              2.7 / 512 k
+//   128 x 128  4 + rounds (2.25 / 512 k + 8.9), two tiles a CU; a lone tile
+//              1.05 / 512 k
+//   32 x 32    3 + 2.3 / 2048 k and tile of a CU
+//
+// So 8192 x 14336 x 4096 (measured 297 us, against 376 with 128 x 128) and 64
+// x 1024^3 (85 against 107) take the large tile, 1024 x 1024 x 65536 128 x
+// 128 with sliced K (53 + 6 against 143 unsliced and 97 + 6 with the large
+// tile), 256^3 (3.2 against 5.8), 1000 x 1023 x 777 (6.4 against 8.0) and
+// products of few rows 32 x 32.
+enum Kernel { kLarge, kMedium, kRows };
+struct Choice {
+    Kernel kernel;
+    int splits;
+};
+double tile_us(int64_t tiles, double groups, int slots, double each, double lone, double store) {
+    const double full = static_cast<double>(tiles / slots), rem = static_cast<double>(tiles % slots) / slots;
+    double t = 4.0 + full * (each * groups + store);
+    if (rem > 0) t += groups * (lone + (each - lone) * rem * std::sqrt(rem)) + store * rem;
+    return t;
+}
+double large_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits) {
+    return tile_us((M + 255) / 256 * ((N + 255) / 256) * batch * splits,
+                   static_cast<double>((groups + splits - 1) / splits), 256, 3.95, 2.7, 10.5);
+}
+double medium_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits) {
+    return tile_us((M + 127) / 128 * ((N + 127) / 128) * batch * splits,
+                   static_cast<double>((groups + splits - 1) / splits), 512, 2.25, 1.05, 8.9);
+}
+Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
+    const double dm = static_cast<double>(M), dn = static_cast<double>(N), db = static_cast<double>(batch);
+    const double shares = std::max(1.0, ((M + 31) / 32) * double((N + 31) / 32) * db / 256);
+    Choice best{kRows, 1};
+    double t = 3.0 + 2.3 * shares * static_cast<double>(K) / 2048;
+    // tiles are counted in 32 bits on the device
+    if (((dm + 127) / 128) * ((dn + 127) / 128) * db > 1e6 * 1024) return best;
+    const int64_t groups = (blocks_of(K) + 15) / 16;
+    for (int want = 1; want <= most_splits && want * 4 <= groups + 3; want *= 2) {
+        const int s = slices_used(groups, want);
+        const double sum = sum_slices_us(db, dm, dn, s);
+        const double l = large_us(batch, M, N, groups, s) + sum, m = medium_us(batch, M, N, groups, s) + sum;
+        if (l < t) t = l, best = {kLarge, s};
+        if (m < t) t = m, best = {kMedium, s};
+    }
+    return best;
+}
+
+// Whether the rows of a tile, in codes and in C, fit 32-bit offsets.
+bool reaches(const Product &p) {
+    constexpr int64_t kReach = int64_t{1} << 31;
+    const int64_t ld = std::max({p.a.ldq, p.b.ldq, p.a.lds, p.b.lds, std::max(p.ldc, int64_t{p.N}) * 4});
+    return ld < kReach / 512;
+}
+
 }  // namespace
 
-int product_splits(int64_t, int64_t, int64_t, int64_t) { return 1; }
+constexpr int kMostSplits = 64;
 
-hipError_t launch_product(const Product &p, hipStream_t stream) {
-    return launch_tile<4, 4, 2, 2, 1>(p, stream);
+int product_splits(int64_t batch, int64_t M, int64_t N, int64_t K) {
+    return choose(batch, M, N, K, kMostSplits).splits;
+}
+
+hipError_t launch_sum_slices(const Product &p, hipStream_t stream) {
+    const int v = p.N % 4 == 0 ? 4 : 1;
+    const int64_t total = p.batch * p.M * (p.N / v);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + 255) / 256, 8192));
+    if (v == 4)
+        sum_slices_kernel<4><<<grid, 256, 0, stream>>>(p, total);
+    else
+        sum_slices_kernel<1><<<grid, 256, 0, stream>>>(p, total);
+    return hipGetLastError();
+}
+
+hipError_t launch_product(const Product &asked, hipStream_t stream) {
+    Product p = asked;
+    Choice c = choose(p.batch, p.M, p.N, p.K, p.splits > 1 ? kMostSplits : 1);
+    if (!reaches(p)) c = {kRows, 1};
+    p.splits = c.splits;
+    hipError_t err = hipSuccess;
+    switch (c.kernel) {
+        case kLarge: err = launch_tile<4, 4, 2, 2, 1>(p, stream); break;
+        case kMedium: err = launch_tile<2, 2, 2, 2, 2>(p, stream); break;
+        case kRows: err = launch_rows<1, 8>(p, stream); break;
+    }
+    if (err == hipSuccess && p.splits > 1) err = launch_sum_slices(p, stream);
+    return err;
 }
 
 }  // namespace mx

@@ -8,8 +8,9 @@
 // where those run at a sixteenth.
 
 #include <algorithm>
+#include <cmath>
+#include <type_traits>
 
-#include "mxfp4.h"
 #include "mxfp4_device.h"
 
 namespace gemm_f32_impl {
@@ -30,11 +31,11 @@ __device__ __forceinline__ uint32_t pack_high(uint32_t lo, uint32_t hi) {
     return (lo >> 16) | (hi & 0xffff0000u);
 }
 
-// One wavefront per 32 x 32 tile.  In v_mfma_f32_32x32x16_bf16 lane l holds
-// 8 consecutive k from 8 (l / 32) of row (column) l % 32.
-template <bool BT>
-__global__ __launch_bounds__(256) void weight_kernel(Product p, int64_t tiles_m, int64_t tiles_n,
-                                                     int64_t tiles) {
+// W as stored, operands of any stride: one wavefront per 32 x 32 tile,
+// straight from global memory.  In v_mfma_f32_32x32x16_bf16 lane l holds 8
+// consecutive k from 8 (l / 32) of row (column) l % 32.
+__global__ __launch_bounds__(256) void weight_any_kernel(Product p, int64_t tiles_m, int64_t tiles_n,
+                                                         int64_t tiles) {
     const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
     for (int64_t t = blockIdx.x * int64_t{4} + (threadIdx.x >> 6); t < tiles;
          t += gridDim.x * int64_t{4}) {
@@ -42,43 +43,28 @@ __global__ __launch_bounds__(256) void weight_kernel(Product p, int64_t tiles_m,
         const int64_t n0 = (t - line * tiles_n) * 32, m0 = (line - b * tiles_m) * 32;
         const int64_t m = min(m0 + row, int64_t{p.M} - 1), n = min(n0 + row, int64_t{p.N} - 1);
         const float *A = p.x + b * p.sx + m * p.ldx;
-        const uint8_t *W = p.b.codes + b * p.b.sq;
-        const uint8_t *S = p.b.scales + b * p.b.ss;
+        const uint8_t *W = p.b.codes + b * p.b.sq + n / 2;
+        const uint8_t *S = p.b.scales + b * p.b.ss + n / kBlock;
         f32x16 acc = {};
         for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
             const int64_t k = k0 + 8 * half;
             uint32_t a[3][8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                split3(k + i < p.K ? A[k + i] : 0.0f, a[0][i], a[1][i], a[2][i]);
             u32x4 w = {};
-            if (BT) {
-                if (k < p.K) {
-                    const uint32_t c = *reinterpret_cast<const uint32_t *>(W + n * p.b.ldq + k / 2);
-                    const float s = scale_of(S[n * p.b.lds + k / kBlock]);
-                    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
-                    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
-                    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
-                    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
-                }
-            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (k + i >= p.K) continue;
-                    const uint32_t c = W[(k + i) * p.b.ldq + n / 2] >> (4 * (n & 1)) & 15;
-                    const float s = scale_of(S[(k + i) * p.b.lds + n / kBlock]);
-                    const uint32_t v = __builtin_bit_cast(
-                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
-                    w[i / 2] |= (v & 0xffffu) << (16 * (i & 1));
-                }
+            for (int i = 0; i < 8; ++i) {
+                split3(k + i < p.K ? A[k + i] : 0.0f, a[0][i], a[1][i], a[2][i]);
+                if (k + i >= p.K) continue;
+                const uint32_t c = W[(k + i) * p.b.ldq] >> (4 * (n & 1)) & 15;
+                const uint32_t v = __builtin_bit_cast(
+                    uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale_of(S[(k + i) * p.b.lds]), 0));
+                w[i / 2] |= (v & 0xffffu) << (16 * (i & 1));
             }
 #pragma unroll
             for (int s = 2; s >= 0; --s) {
                 const u32x4 x = {pack_high(a[s][0], a[s][1]), pack_high(a[s][2], a[s][3]),
                                  pack_high(a[s][4], a[s][5]), pack_high(a[s][6], a[s][7])};
                 acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x),
-                                                              __builtin_bit_cast(bf16x8, w), acc, 0,
-                                                              0, 0);
+                                                              __builtin_bit_cast(bf16x8, w), acc, 0, 0, 0);
             }
         }
         if (n0 + row < p.N) {
@@ -92,19 +78,637 @@ __global__ __launch_bounds__(256) void weight_kernel(Product p, int64_t tiles_m,
     }
 }
 
-}  // namespace
+// W transposed, few rows of A, and operands of any stride: a workgroup of 8
+// wavefronts holds a tile of 16 x 16 NT, its wavefronts take steps of 128 k
+// in turn, straight from global memory, and their sums are added in LDS in a
+// fixed order.  In v_mfma_f32_16x16x32_bf16 lane l holds 8 k of row (column)
+// l % 16; here lane group l / 16 takes block l / 16 of a step, 8 of its k in
+// each of 4 instructions, so a lane's codes are 16 bytes in a row of W and
+// its part of A 128 bytes.  Reading W is the work; splitting A is repeated for
+// every 16 NT columns.
+constexpr int kRowsWaves = 8;
+template <int NT>
+__global__ __launch_bounds__(64 * kRowsWaves) void weight_rows_kernel(Product p, int64_t tiles_m,
+                                                                      int64_t tiles_n, int64_t tiles) {
+    __shared__ __align__(16) float sums[kRowsWaves][NT][4][64];
+    const int lane = threadIdx.x & 63, row = lane & 15, group = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int nb = (p.K + kBlock - 1) / kBlock;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t line = t / tiles_n, b = line / tiles_m;
+        const int64_t n0 = (t - line * tiles_n) * 16 * NT, m0 = (line - b * tiles_m) * 16;
+        const float *A = p.x + b * p.sx + min(m0 + row, int64_t{p.M} - 1) * p.ldx;
+        const uint8_t *W[NT], *S[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int64_t n = min(n0 + 16 * j + row, int64_t{p.N} - 1);
+            W[j] = p.b.codes + b * p.b.sq + n * p.b.ldq;
+            S[j] = p.b.scales + b * p.b.ss + n * p.b.lds;
+        }
+        f32x4 acc[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = wave; s * 4 < nb; s += kRowsWaves) {
+            const int block = s * 4 + group;
+            const int64_t held = min(block, nb - 1);
+            u32x4 w[NT];
+            float e[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                w[j] = *reinterpret_cast<const u32x4 *>(W[j] + held * kBlockBytes);
+                e[j] = scale_of(S[j][held]);
+            }
+            f32x4 a[8];
+            const int64_t k = block * int64_t{kBlock};
+            if (s * 4 * kBlock + 4 * kBlock <= p.K) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const float4u *>(A + k + 4 * i);
+            } else {  // A past K is zero, so what W holds there does not matter
+#pragma unroll
+                for (int i = 0; i < 32; ++i) a[i / 4][i % 4] = k + i < p.K ? A[k + i] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h[3][8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) split3(a[2 * i + q / 4][q % 4], h[0][q], h[1][q], h[2][q]);
+                u32x4 x[3];
+#pragma unroll
+                for (int c = 0; c < 3; ++c)
+                    x[c] = u32x4{pack_high(h[c][0], h[c][1]), pack_high(h[c][2], h[c][3]),
+                                 pack_high(h[c][4], h[c][5]), pack_high(h[c][6], h[c][7])};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint32_t c = w[j][i];
+                    const u32x4 v = {
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e[j], 0)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e[j], 1)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e[j], 2)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e[j], 3))};
+#pragma unroll
+                    for (int q = 2; q >= 0; --q)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, x[q]), __builtin_bit_cast(bf16x8, v), acc[j], 0, 0, 0);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums[wave][j][r][lane] = acc[j][r];
+        __syncthreads();
+        for (int o = threadIdx.x; o < NT * 256; o += 64 * kRowsWaves) {
+            const int l = o & 63, r = (o >> 6) & 3, j = o >> 8;
+            const int64_t n = n0 + 16 * j + (l & 15), m = m0 + 4 * (l >> 4) + r;
+            if (m >= p.M || n >= p.N) continue;
+            float v = sums[0][j][r][l];
+#pragma unroll
+            for (int q = 1; q < kRowsWaves; ++q) v += sums[q][j][r][l];
+            p.C[b * p.sc + m * p.ldc + n] = v;
+        }
+        __syncthreads();
+    }
+}
 
-int weight_splits(bool, int64_t, int64_t, int64_t, int64_t) { return 1; }
+// W transposed, MR (1 or 2) rows of A: FP32 multiply-adds.  A wavefront
+// reads R rows of W, 64 blocks of each (1 KiB) at once, a block per lane; a
+// lane's 32 values of A serve all of them, from LDS, where value quad i of
+// lane l sits at i ^ (l / 2 % 8) so that 16 lanes touch every bank once.  The
+// 64 partial sums of a row are added at the end, in an order that depends on
+// sizes only.  A block costs 16 conversions and 32 MR multiply-adds.
+constexpr int kVectorWaves = 4;
+constexpr int kVectorRows = 2;
+template <int MR>
+__global__ __launch_bounds__(64 * kVectorWaves) void weight_vector_kernel(Product p, int64_t tiles_n,
+                                                                          int64_t tiles) {
+    constexpr int R = kVectorRows;
+    constexpr int kChunk = 64 * kBlock, kThreads = 64 * kVectorWaves;
+    __shared__ __align__(16) float xs[MR][kChunk];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int nb = (p.K + kBlock - 1) / kBlock;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t b = t / tiles_n;
+        const int64_t n0 = ((t - b * tiles_n) * kVectorWaves + wave) * R;
+        const float *A = p.x + b * p.sx;
+        const uint8_t *W[R], *S[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t n = min(n0 + r, int64_t{p.N} - 1);
+            W[r] = p.b.codes + b * p.b.sq + n * p.b.ldq;
+            S[r] = p.b.scales + b * p.b.ss + n * p.b.lds;
+        }
+        float acc[MR][R];
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[m][r] = 0.0f;
+        for (int64_t k0 = 0; k0 < p.K; k0 += kChunk) {
+            const int64_t block = k0 / kBlock + lane;
+            const bool in = block < nb;
+            u32x4 w[R];
+            uint32_t e[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                w[r] = u32x4{0, 0, 0, 0};
+                e[r] = 0;
+                if (in) {
+                    w[r] = *reinterpret_cast<const u32x4 *>(W[r] + block * kBlockBytes);
+                    e[r] = S[r][block];
+                }
+            }
+            __syncthreads();  // the last chunk has been used
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                const float *a = A + min(m, p.M - 1) * p.ldx + k0;
+                for (int i = threadIdx.x; i < kChunk / 4; i += kThreads) {
+                    f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (k0 + 4 * i + 4 <= p.K) {
+                        v = *reinterpret_cast<const float4u *>(a + 4 * i);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 3; ++q)
+                            if (k0 + 4 * i + q < p.K) v[q] = a[4 * i + q];
+                    }
+                    const int l = i >> 3;
+                    *reinterpret_cast<f32x4 *>(&xs[m][l * 32 + ((i & 7) ^ ((l >> 1) & 7)) * 4]) = v;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // 8 values: a word of codes
+                f32x4 v[MR][2];
+#pragma unroll
+                for (int m = 0; m < MR; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        v[m][h] = *reinterpret_cast<const f32x4 *>(
+                            &xs[m][lane * 32 + ((2 * i + h) ^ ((lane >> 1) & 7)) * 4]);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float s = scale_of(e[r]);
+                    const f32x2 c0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r][i], s, 0);
+                    const f32x2 c1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r][i], s, 1);
+                    const f32x2 c2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r][i], s, 2);
+                    const f32x2 c3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r][i], s, 3);
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) {
+                        float u = acc[m][r];
+                        u = fmaf(v[m][0][0], c0[0], u), u = fmaf(v[m][0][1], c0[1], u);
+                        u = fmaf(v[m][0][2], c1[0], u), u = fmaf(v[m][0][3], c1[1], u);
+                        u = fmaf(v[m][1][0], c2[0], u), u = fmaf(v[m][1][1], c2[1], u);
+                        u = fmaf(v[m][1][2], c3[0], u), u = fmaf(v[m][1][3], c3[1], u);
+                        acc[m][r] = u;
+                    }
+                }
+            }
+        }
+        // Each step halves the rows a lane holds: it hands one half to its
+        // partner and adds the other's.
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            int bit = 32;
+#pragma unroll
+            for (int left = R; left > 1; left /= 2, bit /= 2)
+#pragma unroll
+                for (int r = 0; r < left / 2; ++r) {
+                    const bool upper = lane & bit;
+                    const float keep = upper ? acc[m][r + left / 2] : acc[m][r];
+                    const float give = upper ? acc[m][r] : acc[m][r + left / 2];
+                    acc[m][r] = keep + __shfl_xor(give, bit);
+                }
+            float v = acc[m][0];
+#pragma unroll
+            for (int d = bit; d > 0; d /= 2) v += __shfl_xor(v, d);
+            // bit 5 of the lane chose between row halves, bit 4 between
+            // quarters, ...: lane / (64 / R) is the row
+            const int64_t n = n0 + lane / (64 / R);
+            if (lane % (64 / R) == 0 && n < p.N && m < p.M) p.C[b * p.sc + m * p.ldc + n] = v;
+        }
+    }
+}
 
-hipError_t launch_weight(const Product &p, hipStream_t stream) {
+// A tile of 2 x 2 wavefronts, each FM x FN blocks of 32 x 32, K in stages of
+// 32.
+//
+// LDS holds a stage as bf16: the three parts of A's rows and W's columns, 32
+// k (64 bytes: 4 slots of 8 k) a row.  Slot s of row r sits at s ^ (r / 4 % 4):
+// 16 lanes that read one slot of 16 rows touch every bank once.  Column n of
+// W is row n / FN + 64 (n % FN), so that a lane's results of one row of C are
+// FN neighbours and are stored at once.
+//
+// A stage runs in 6 phases, a part of A times 16 k each, the smallest parts
+// first.  Under a phase's products the next phase's operands are read from
+// LDS, and in the first ones the next stage's values, loaded into registers a
+// stage ago, are split (or decoded), written to the other buffer and their
+// registers loaded again.  The one barrier lies before the last phase, under
+// which the next stage's first operands are read.
+template <int FM, int FN, bool BT, bool QUADS, int OCC>
+__global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int tiles_m, int tiles_n,
+                                                               int stages, int len) {
+    constexpr int BM = 64 * FM, BN = 64 * FN, kRow = 64;
+    constexpr int kUnits = BM / 32;           // 4 values of A per lane each
+    constexpr int kWords = BN / 64;           // of codes per lane
+    __shared__ __align__(1024) uint8_t a0[3 * BM * kRow];
+    __shared__ __align__(1024) uint8_t a1[3 * BM * kRow];
+    __shared__ __align__(1024) uint8_t w0[BN * kRow];
+    __shared__ __align__(1024) uint8_t w1[BN * kRow];
+
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, row = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+    const Place at = place_of<BM, BN>(p, xcd_remap(blockIdx.x, gridDim.x), tiles_m, tiles_n, stages, len);
+    const int64_t b = at.slice / p.splits;
+    const int nb = (p.K + kBlock - 1) / kBlock, nbn = (p.N + kBlock - 1) / kBlock;
+
+    // ---- A: 8 lanes along a row, 32 rows a unit ----
+    const __amdgpu_buffer_rsrc_t ar =
+        buffer_of(p.x + b * p.sx + at.m0 * p.ldx, ((p.M - 1 - at.m0) * p.ldx + p.K) * 4);
+    const int lda = static_cast<int>(p.ldx) * 4;
+    const int ak = (tid & 7) * 4, arow = tid >> 3;
+    f32x4 av[kUnits];
+    auto load_a = [&](int u, int s) {
+        const int k = s * 32 + ak, at_row = (arow + 32 * u) * lda;
+        if constexpr (QUADS) {
+            const int off = s < at.g1 && k < p.K ? k * 4 : kOutside;
+            av[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ar, at_row + off, 0, 0));
+        } else {  // four values may end a row, and the operand
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int off = s < at.g1 && k + e < p.K ? (k + e) * 4 : kOutside;
+                av[u][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ar, at_row + off, 0, 0));
+            }
+        }
+    };
+    // k 4 q .. 4 q + 3 of a row: half a slot
+    const int aslot = (((tid & 7) >> 1) ^ ((arow >> 2) & 3)) * 16 + (tid & 1) * 8;
+    auto put_a = [&](int u, uint8_t *dst) {
+        uint32_t h[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            split3(av[u][e], h[0][e], h[1][e], h[2][e]);
+        }
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+            *reinterpret_cast<u32x2 *>(dst + (c * BM + arow + 32 * u) * kRow + aslot) =
+                u32x2{pack_high(h[c][0], h[c][1]), pack_high(h[c][2], h[c][3])};
+    };
+
+    // ---- W ----
+    // Transposed: a lane has (part of) a column's block, kWords words of codes.
+    // As stored: FN columns of 8 rows k.
+    const __amdgpu_buffer_rsrc_t wr =
+        BT ? buffer_of(p.b.codes + b * p.b.sq + at.n0 * p.b.ldq,
+                       (p.N - 1 - at.n0) * p.b.ldq + nb * kBlockBytes)
+           : buffer_of(p.b.codes + b * p.b.sq, (p.K - 1) * p.b.ldq + nbn * kBlockBytes);
+    const __amdgpu_buffer_rsrc_t wsr =
+        BT ? buffer_of(p.b.scales + b * p.b.ss + at.n0 * p.b.lds, (p.N - 1 - at.n0) * p.b.lds + nb)
+           : buffer_of(p.b.scales + b * p.b.ss, (p.K - 1) * p.b.lds + nbn);
+    const int ldq = static_cast<int>(p.b.ldq), lds = static_cast<int>(p.b.lds);
+    uint32_t wc[BT ? kWords : 8], we[BT ? 1 : 8];
+    constexpr int kParts = 4 / FN;  // lanes that share a column's block
+    // transposed: LDS row of the lane, its column
+    const int trow = tid / kParts, tcol = FN * (trow & 63) + (trow >> 6), tpart = tid % kParts;
+    auto load_w = [&](int s) {
+        const bool live = s < at.g1;
+        if constexpr (BT) {
+            const int off = live ? s * kBlockBytes + tpart * kWords * 4 : kOutside;
+            if constexpr (FN == 4) {
+                const u32x4 v = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, tcol * ldq + off, 0, 0));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) wc[i] = v[i];
+            } else {
+                const u32x2 v = __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_raw_buffer_load_b64(wr, tcol * ldq + off, 0, 0));
+                wc[0] = v[0], wc[1] = v[1];
+            }
+            we[0] = __builtin_amdgcn_raw_buffer_load_b8(wsr, tcol * lds + (live ? s : kOutside), 0, 0);
+        } else {
+            const int n = at.n0 + FN * lane;  // first column of the lane
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int k = s * 32 + wave * 8 + i;
+                const bool in = live && k < p.K;
+                const int oc = in ? k * ldq + n / 2 : kOutside, os = in ? k * lds + n / kBlock : kOutside;
+                wc[i] = FN == 4 ? __builtin_amdgcn_raw_buffer_load_b16(wr, oc, 0, 0)
+                                : __builtin_amdgcn_raw_buffer_load_b8(wr, oc, 0, 0);
+                we[i] = __builtin_amdgcn_raw_buffer_load_b8(wsr, os, 0, 0);
+            }
+        }
+    };
+    auto put_w = [&](uint8_t *dst) {
+        if constexpr (BT) {
+            const float e = scale_of(we[0]);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const u32x4 v = {
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 0)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 1)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 2)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 3))};
+                const int slot = (tpart * kWords + i) ^ ((trow >> 2) & 3);
+                *reinterpret_cast<u32x4 *>(dst + trow * kRow + slot * 16) = v;
+            }
+        } else {
+            uint32_t v[8][FN / 2];  // pairs of columns of row k
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float e = scale_of(we[i]);
+                v[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 0));
+                if constexpr (FN == 4)
+                    v[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 1));
+            }
+#pragma unroll
+            for (int c = 0; c < FN; ++c) {
+                u32x4 o;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t lo = v[2 * q][c / 2], hi = v[2 * q + 1][c / 2];
+                    o[q] = c & 1 ? pack_high(lo, hi) : (lo & 0xffffu) | (hi << 16);
+                }
+                const int r = lane + 64 * c, slot = wave ^ ((r >> 2) & 3);
+                *reinterpret_cast<u32x4 *>(dst + r * kRow + slot * 16) = o;
+            }
+        }
+    };
+
+    // ---- products ----
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    u32x4 x[2][FM], y[2][FN];
+    const int ra = (wm * FM * 32 + row) * kRow, rw = (wn * 32 + row) * kRow, sw = (row >> 2) & 3;
+    auto fetch = [&](auto pc, const uint8_t *a, const uint8_t *w) {  // operands of a phase
+        constexpr int ph = decltype(pc)::value, ks = ph / 3, part = 2 - ph % 3;
+        const int slot = ((2 * ks + half) ^ sw) * 16;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            x[ph & 1][i] = *reinterpret_cast<const u32x4 *>(a + part * BM * kRow + ra + 32 * i * kRow + slot);
+        if constexpr (ph % 3 == 0)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                y[ks][j] = *reinterpret_cast<const u32x4 *>(w + rw + 64 * j * kRow + slot);
+    };
+    auto multiply = [&](auto pc) {
+        constexpr int ph = decltype(pc)::value, ks = ph / 3;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int k = 0; k < FN; ++k) {
+                const int j = i & 1 ? FN - 1 - k : k;
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, x[ph & 1][i]), __builtin_bit_cast(bf16x8, y[ks][j]),
+                    acc[i][j], 0, 0, 0);
+            }
+    };
+    // Between two matrix instructions: an LDS read, a few vector instructions
+    // of the splitting, and its writes and loads.
+    auto interleave = [&]() {
+#pragma unroll
+        for (int k = 0; k < FM * FN; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+            __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        // The sums so far are used here, so their instructions stay ahead.
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) asm volatile("" ::"a"(acc[i][j]));
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    constexpr std::integral_constant<int, 0> p0;
+    constexpr std::integral_constant<int, 1> p1;
+    constexpr std::integral_constant<int, 2> p2;
+    constexpr std::integral_constant<int, 3> p3;
+    constexpr std::integral_constant<int, 4> p4;
+    constexpr std::integral_constant<int, 5> p5;
+
+    // Stage s in (a, w); stage s + 1, in registers, goes to (na, nw).
+    auto stage = [&](int s, const uint8_t *a, const uint8_t *w, uint8_t *na, uint8_t *nw) {
+        auto units = [&](int first, int last) {
+#pragma unroll
+            for (int u = first; u < last; ++u) {
+                put_a(u, na);
+                load_a(u, s + 2);
+            }
+        };
+        fetch(p1, a, w);
+        units(0, kUnits / 4);
+        multiply(p0);
+        interleave();
+        fetch(p2, a, w);
+        units(kUnits / 4, kUnits / 2);
+        multiply(p1);
+        interleave();
+        fetch(p3, a, w);
+        units(kUnits / 2, 3 * kUnits / 4);
+        multiply(p2);
+        interleave();
+        fetch(p4, a, w);
+        units(3 * kUnits / 4, kUnits);
+        multiply(p3);
+        interleave();
+        fetch(p5, a, w);
+        put_w(nw);
+        load_w(s + 2);
+        multiply(p4);
+        interleave();
+        wait_older<63>();  // LDS accesses alone
+        barrier_only();
+        fetch(p0, na, nw);
+        multiply(p5);
+        interleave();
+    };
+
+    int s = at.g0;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) load_a(u, s);
+    load_w(s);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        put_a(u, a0);
+        load_a(u, s + 1);
+    }
+    put_w(w0);
+    load_w(s + 1);
+    wait_older<63>();
+    barrier_only();
+    fetch(p0, a0, w0);
+    for (; s < at.g1; s += 2) {
+        stage(s, a0, w0, a1, w1);
+        stage(s + 1, a1, w1, a0, w0);  // past the end: zeros
+    }
+
+    // ---- results: FN neighbours a lane ----
+    const int64_t ldc = p.splits > 1 ? p.N : p.ldc;
+    const float *base = p.splits > 1 ? p.W + at.slice * p.M * ldc : p.C + at.slice * p.sc;
+    const int mw = at.m0 + wm * FM * 32, n = at.n0 + FN * (32 * wn + row);
+    if (mw >= p.M || n >= p.N) return;
+    const __amdgpu_buffer_rsrc_t c = buffer_of(base + mw * ldc, ((p.M - 1 - mw) * ldc + p.N) * 4);
+    const int ld = static_cast<int>(ldc) * 4;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int o = (32 * i + (r & 3) + 8 * (r >> 2) + 4 * half) * ld + n * 4;
+            if (n + FN <= p.N) {
+                if constexpr (FN == 4) {
+                    const f32x4 v{acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), c, o, 0, 0);
+                } else {
+                    const f32x2 v{acc[i][0][r], acc[i][1][r]};
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), c, o, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < FN - 1; ++j) {
+                    const float v = acc[i][j][r];
+                    if (n + j < p.N)
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), c, o + 4 * j, 0, 0);
+                }
+            }
+        }
+}
+
+// Whether a tile's rows (of K rows of W as stored) fit 32-bit offsets.
+bool reaches(const Product &p, int rows_m, int rows_n) {
+    constexpr int64_t kReach = int64_t{1} << 31;
+    const int64_t wrows = p.b_transposed ? rows_n : p.K;
+    return rows_m * p.ldx * 4 < kReach && rows_m * std::max(p.ldc, int64_t{p.N}) * 4 < kReach &&
+           wrows * p.b.ldq < kReach && wrows * p.b.lds < kReach && int64_t{p.K} * 4 < kReach / 2 &&
+           int64_t{p.N} * 4 < kReach / 2;
+}
+
+template <int FM, int FN, int OCC>
+hipError_t launch_tile(const Product &p, hipStream_t stream) {
+    const int tm = ceil_div(p.M, 64 * FM), tn = ceil_div(p.N, 64 * FN);
+    const int stages = static_cast<int>(blocks_of(p.K)), len = ceil_div(stages, p.splits);
+    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(tm) * tn * p.batch * p.splits);
+    const bool quads = p.K % 4 == 0;
+    auto go = [&](auto bt, auto wh) {
+        weight_tile_kernel<FM, FN, decltype(bt)::value, decltype(wh)::value, OCC>
+            <<<grid, 256, 0, stream>>>(p, tm, tn, stages, len);
+    };
+    if (p.b_transposed)
+        quads ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+    else
+        quads ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+    return hipGetLastError();
+}
+
+template <int NT>
+hipError_t launch_rows(const Product &p, hipStream_t stream) {
+    const int64_t tm = (p.M + int64_t{15}) / 16, tn = (p.N + int64_t{16 * NT - 1}) / (16 * NT);
+    const int64_t tiles = tm * tn * p.batch;
+    weight_rows_kernel<NT><<<static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20)), 64 * kRowsWaves, 0,
+                             stream>>>(p, tm, tn, tiles);
+    return hipGetLastError();
+}
+
+template <int MR>
+hipError_t launch_vector(const Product &p, hipStream_t stream) {
+    constexpr int kCols = kVectorWaves * kVectorRows;
+    const int64_t tn = (p.N + int64_t{kCols - 1}) / kCols, tiles = tn * p.batch;
+    weight_vector_kernel<MR><<<static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20)),
+                               64 * kVectorWaves, 0, stream>>>(p, tn, tiles);
+    return hipGetLastError();
+}
+
+hipError_t launch_any(const Product &p, hipStream_t stream) {
     const int64_t tm = (p.M + int64_t{31}) / 32, tn = (p.N + int64_t{31}) / 32;
     const int64_t tiles = tm * tn * p.batch;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((tiles + 3) / 4, 1 << 22));
-    if (p.b_transposed)
-        weight_kernel<true><<<grid, 256, 0, stream>>>(p, tm, tn, tiles);
-    else
-        weight_kernel<false><<<grid, 256, 0, stream>>>(p, tm, tn, tiles);
+    weight_any_kernel<<<static_cast<unsigned>(std::min<int64_t>((tiles + 3) / 4, 1 << 20)), 256, 0, stream>>>(
+        p, tm, tn, tiles);
     return hipGetLastError();
+}
+
+// Which tile a product takes, and how many slices of K: the least predicted
+// time, from microseconds per 32 k measured on MI355X for a lone tile and for
+// a full chip (W transposed / as stored):
+//
+//   256 x 256  one a CU    1.76 / 1.97 lone   2.35 / 2.45 full
+//   128 x 128  two a CU    0.74 / 0.94 lone   1.45 / 1.55 full
+//    64 x 128  four a CU   0.49 / 0.80 lone   1.68 / 1.75 full
+//
+// 4096 x 4096 x 14336 (1021 us, against 1323 and 1471) takes the first, 512 x
+// 4096 x 4096 the last (71 us unsliced, against 98 and 226), and so do 37 rows
+// x 14336 x 4096, in 4 slices of K (30 us, against 63 unsliced).
+struct Choice {
+    int tile;  // 0, 1, 2 as above
+    int splits;
+};
+Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
+    struct Candidate {
+        int bm, bn, slots;
+        double lone[2], full[2];
+    };
+    static constexpr Candidate kTiles[] = {{256, 256, 256, {1.97, 1.76}, {2.45, 2.35}},
+                                           {128, 128, 512, {0.94, 0.74}, {1.55, 1.45}},
+                                           {64, 128, 1024, {0.80, 0.49}, {1.75, 1.68}}};
+    const int64_t stages = blocks_of(K);
+    Choice best{2, 1};
+    double t = 0;
+    for (int want = 1; want <= most_splits && (want == 1 || want * 8 <= stages); want *= 2) {
+        const int s = slices_used(stages, want);
+        const double len = static_cast<double>((stages + s - 1) / s);
+        for (int i = 0; i < 3; ++i) {
+            const Candidate &c = kTiles[i];
+            const double tiles = static_cast<double>((M + c.bm - 1) / c.bm) *
+                                 static_cast<double>((N + c.bn - 1) / c.bn) * static_cast<double>(batch) * s;
+            const double full = std::floor(tiles / c.slots), rem = tiles / c.slots - full;
+            double u = 5.0 + full * len * c.full[bt] +
+                       (rem > 0 ? len * (c.lone[bt] + (c.full[bt] - c.lone[bt]) * rem * std::sqrt(rem)) : 0.0);
+            u += sum_slices_us(static_cast<double>(batch), static_cast<double>(M), static_cast<double>(N), s);
+            if (t == 0 || u < t) t = u, best = {i, s};
+        }
+    }
+    return best;
+}
+
+// Rows of A that W transposed is read for without tiles.
+constexpr int kFewRows = 16;
+
+}  // namespace
+
+int weight_splits(bool b_transposed, int64_t batch, int64_t M, int64_t N, int64_t K) {
+    if (b_transposed && M <= kFewRows) return 1;
+    return choose(b_transposed, batch, M, N, K, 64).splits;
+}
+
+hipError_t launch_weight(const Product &asked, hipStream_t stream) {
+    Product p = asked;
+    const double tiles = static_cast<double>((p.M + 63) / 64) * ((p.N + 127) / 128) * static_cast<double>(p.batch);
+    const bool far = !reaches(p, 256, 256) || tiles > 1e6;  // (a launch has at most 2^32 lanes)
+    if (p.b_transposed && (p.M <= kFewRows || far)) {
+        p.splits = 1;
+        // One and two rows of A cost the vector units less than splitting 16:
+        // a row x 14336 x 4096 8.0 us, against 13.7.  Wide tiles share the
+        // splitting but leave CUs without one: 16 rows x 14336 x 4096 takes
+        // 64 columns a workgroup (18.8 us, against 25 with 32), 16 rows x
+        // 4096 x 4096 16 (8.4, against 10).
+        if (p.M == 1) return launch_vector<1>(p, stream);
+        if (p.M == 2) return launch_vector<2>(p, stream);
+        const int64_t columns = p.N * p.batch * ((p.M + 15) / 16);
+        if (columns >= 200 * 64) return launch_rows<4>(p, stream);
+        return columns >= 200 * 32 ? launch_rows<2>(p, stream) : launch_rows<1>(p, stream);
+    }
+    if (far) {
+        p.splits = 1;
+        return launch_any(p, stream);
+    }
+    const Choice c = choose(p.b_transposed, p.batch, p.M, p.N, p.K, p.splits > 1 ? 64 : 1);
+    p.splits = c.splits;
+    hipError_t err = c.tile == 0   ? launch_tile<4, 4, 1>(p, stream)
+                     : c.tile == 1 ? launch_tile<2, 2, 2>(p, stream)
+                                   : launch_tile<1, 2, 4>(p, stream);
+    if (err == hipSuccess && p.splits > 1) err = launch_sum_slices(p, stream);
+    return err;
 }
 
 }  // namespace mx

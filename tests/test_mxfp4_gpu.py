@@ -633,3 +633,61 @@ def test_concurrent_calls_from_threads():
     for t in threads:
         t.join()
     assert not wrong
+
+
+# ---- large products, against float64 products on the GPU ------------------------------------
+
+def random_on_gpu(rows, cols, seed):
+    """(Mxfp4, its float64 values) of random codes, scales within 2^+-4."""
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    nb = ref.blocks(cols)
+    codes = torch.randint(0, 256, (rows, nb * 16), generator=g, device="cuda", dtype=torch.uint8)
+    if cols % 32:
+        keep = torch.arange(nb * 32, device="cuda") < cols
+        mask = torch.where(keep, 15, 0).view(-1, 2)
+        codes &= (mask[:, 0] | mask[:, 1] << 4).to(torch.uint8)
+    scales = torch.randint(123, 132, (rows, ref.blocks(nb * 8) * 4), generator=g, device="cuda").to(torch.uint8)
+    nib = torch.stack((codes & 15, codes >> 4), -1).view(rows, nb * 32)[:, :cols].long()
+    table = torch.tensor(np.concatenate([ref.ELEMENTS, -ref.ELEMENTS]), device="cuda")
+    v = table[nib] * torch.exp2(scales[:, :nb].double() - 127).repeat_interleave(32, 1)[:, :cols]
+    return b.Mxfp4(codes, scales, cols), v
+
+
+LARGE = [(4133, 4161, 1000), (4096, 4096, 2048), (8200, 2900, 515), (1100, 1024, 40000), (700, 9000, 1568),
+         (2048, 2048, 512)]
+
+
+@pytest.mark.parametrize("shape", LARGE)
+def test_large_products(shape):
+    import torch
+
+    M, N, K = shape
+    log(f"large {shape}")
+    A, a64 = random_on_gpu(M, K, 1)
+    W, w64 = random_on_gpu(N, K, 2)
+    x = torch.randn(M, K, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda") * \
+        torch.exp2(torch.arange(K, device="cuda") % 13 - 6.0)
+    Wn, wn64 = random_on_gpu(K, N, 4)
+    for name, got, p, q, parts in (("product", b.gemm_mxfp4(A, W), a64, w64.t(), 1),
+                                   ("weight T", b.gemm_mxfp4_weight(x, W), x.double(), w64.t(), 3),
+                                   ("weight N", b.gemm_mxfp4_weight(x, Wn, op=b.OP_N), x.double(), wn64, 3)):
+        want, S = p @ q, p.abs() @ q.abs()
+        over = (got.double() - want).abs() - (parts * K / 16 + 8) * ULP * S
+        assert bool(torch.isfinite(got).all()) and float(over.max()) <= 0, (name, float(over.max()))
+
+
+def test_large_batch():
+    import torch
+
+    A, a64 = random_on_gpu(20 * 520, 600, 5)
+    W, w64 = random_on_gpu(20 * 530, 600, 6)
+    A3 = b.Mxfp4(A.codes.view(20, 520, -1), A.scales.view(20, 520, -1), 600)
+    W3 = b.Mxfp4(W.codes.view(20, 530, -1), W.scales.view(20, 530, -1), 600)
+    x = torch.randn(20, 520, 600, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
+    w64 = w64.view(20, 530, 600).transpose(1, 2).contiguous()
+    for got, p, parts in ((b.gemm_mxfp4(A3, W3), a64.view(20, 520, 600), 1),
+                          (b.gemm_mxfp4_weight(x, W3), x.double(), 3)):
+        over = (got.double() - p @ w64).abs() - (parts * 600 / 16 + 8) * ULP * (p.abs() @ w64.abs())
+        assert float(over.max()) <= 0
