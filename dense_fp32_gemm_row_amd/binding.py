@@ -500,8 +500,15 @@ def mxfp4_empty(shape, device="cuda", *, stream=None) -> Mxfp4:
 
     *lead, cols = shape
     nb = (cols + MXFP4_BLOCK - 1) // MXFP4_BLOCK
-    return Mxfp4(_empty((*lead, nb * 16), torch.uint8, device, stream),
-                 _empty((*lead, (nb + 3) // 4 * 4), torch.uint8, device, stream), cols)
+    words = (nb + 3) // 4 * 4
+    codes = _empty((*lead, nb * 16), torch.uint8, device, stream)
+    scales = _empty((*lead, words), torch.uint8, device, stream)
+    q = Mxfp4.__new__(Mxfp4)  # nothing to check
+    q.codes, q.scales, q.cols = codes, scales, cols
+    rows = lead[-1]
+    q._c = Mxfp4Matrix(codes.data_ptr(), nb * 16, rows * nb * 16, scales.data_ptr(), words,
+                       rows * words)
+    return q
 
 
 def _run_on(device, stream, fn, *args) -> None:
@@ -509,15 +516,19 @@ def _run_on(device, stream, fn, *args) -> None:
     tensors' device current, and raises on an error."""
     import torch
 
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        # (the raw handle: a torch.cuda.Stream object costs as much as a launch)
+        sp = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device == device:
+        sp = stream.cuda_stream
+    else:
         raise ValueError(f"stream on {stream.device}, operands on {device}")
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream.cuda_stream)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, sp)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(*args, sp)
     if rc != GEMM_F32_OK:
         raise GemmError(rc, gemm_f32_last_error())
 
@@ -540,7 +551,7 @@ def _quantize(X, want_rows: bool, want_cols: bool, stream, out, out_t):
         stored = X.transpose(-1, -2)
         q_cols, q_rows = _quantize(stored, want_cols, want_rows, stream, out_t, out)
         return q_rows, q_cols
-    lead, (rows, cols) = tuple(X.shape[:-2]), X.shape[-2:]
+    *lead, rows, cols = X.shape
     dev = X.device
 
     def target(q, shape):
@@ -574,17 +585,11 @@ def mxfp4_quantize_both(X, out: Mxfp4 | None = None, out_t: Mxfp4 | None = None,
 
 def mxfp4_dequantize(q: Mxfp4, out=None, *, stream=None):
     """The float32 values of ``q``."""
-    import torch
-
     shape = q.shape
-    if out is None:
-        out = _empty(shape, torch.float32, q.device, stream)
-    elif tuple(out.shape) != shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
-    op, ld, bs, batch = _float_operand(out, "out", q.device)
-    if op != OP_N:
-        raise ValueError("out must be row-major")
-    _run_on(q.device, stream, load().gemm_mxfp4_dequantize, batch, shape[-2], shape[-1],
+    device = q.codes.device
+    out, ld, bs, *_ = _mxfp4_out(out, shape, device, None, 0, stream)
+    batch = shape[0] if len(shape) == 3 else 1
+    _run_on(device, stream, load().gemm_mxfp4_dequantize, batch, shape[-2], shape[-1],
             ctypes.byref(q._c), out.data_ptr(), ld, bs)
     return out
 
@@ -595,19 +600,22 @@ def _mxfp4_out(out, shape, device, workspace, need: int, stream):
 
     if out is None:
         out = _empty(shape, torch.float32, device, stream)
-    elif tuple(out.shape) != shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
-    op, ld, bs, _ = _float_operand(out, "out", device)
-    if op != OP_N:
-        raise ValueError("out must be row-major")
-    if workspace is None:
-        if need:
-            workspace = _empty(need // 4, torch.float32, device, stream)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    if workspace is None:
-        return out, ld, bs, workspace, None, 0
-    return out, ld, bs, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ld = shape[-1] or 1
+        bs = shape[-2] * ld
+    else:
+        if tuple(out.shape) != shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
+        op, ld, bs, _ = _float_operand(out, "out", device)
+        if op != OP_N:
+            raise ValueError("out must be row-major")
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return out, ld, bs, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if need:
+        workspace = _empty(need // 4, torch.float32, device, stream)
+        return out, ld, bs, workspace, workspace.data_ptr(), need
+    return out, ld, bs, None, None, 0
 
 
 def gemm_mxfp4(A: Mxfp4, B: Mxfp4, out=None, workspace=None, *, stream=None):

@@ -93,38 +93,87 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(Quantize p, int lx, 
     }
 }
 
-// Blocks along the columns: a lane holds one column of 32 rows, so nothing
-// is exchanged between lanes and a wavefront reads 256 bytes of every row.
+// Blocks along the columns, and with ROWS along the rows too, in one read: a
+// workgroup takes 128 x 128 values, a wavefront 32 of the rows, a lane 16 of
+// those and 4 columns.  A column's block then lies in two lanes, a row's in
+// 8.  (32 rows a lane need no exchange for a column, but 256 registers: two
+// workgroups a CU, whose reading, converting and writing hardly overlapped.)
+// The codes of 4 blocks of a column meet in LDS so that they leave as 64
+// bytes: 16 at a time, each to a row of its own, would be partial writes of
+// memory's lines.
+template <bool ROWS>
 __global__ __launch_bounds__(256) void quantize_cols_kernel(Quantize p, int64_t tiles_x,
                                                             int64_t tiles_y, int64_t tiles) {
-    const int nb = (p.rows + kBlock - 1) / kBlock, words = (nb + 3) & ~3;
+    constexpr int kSide = 128, kHold = 16;
+    __shared__ __align__(16) uint8_t codes[kSide * 4 * kBlockBytes];  // [column][block, swizzled]
+    __shared__ __align__(4) uint8_t scales[kSide * 4];                // [column][block]
+    const int nbr = (p.rows + kBlock - 1) / kBlock, nbc = (p.cols + kBlock - 1) / kBlock;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, half = lane >> 5, quad = lane & 31;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int64_t line = t / tiles_x, b = line / tiles_y;
-        const int64_t block = line - b * tiles_y;
-        const int64_t c = (t - line * tiles_x) * 256 + threadIdx.x;
-        if (c >= p.cols) continue;
-        const float *X = p.X + b * p.sx + c;
-        float v[kBlock];
-        uint32_t m = 0;
+        const int64_t slab = line - b * tiles_y, c0 = (t - line * tiles_x) * kSide;
+        const int64_t col = c0 + 4 * quad, r0 = slab * kSide + wave * 32 + half * kHold;
+        const float *X = p.X + b * p.sx + col;
+        f32x4 v[kHold];
+        if (col + 4 <= p.cols && r0 + kHold <= p.rows) {
 #pragma unroll
-        for (int k = 0; k < kBlock; ++k) {
-            const int64_t r = block * kBlock + k;
-            v[k] = r < p.rows ? X[r * p.ldx] : 0.0f;
-            m = max(m, magnitude(v[k]));
-        }
-        const uint32_t e = scale_byte(m);
-        u32x4 o;
+            for (int k = 0; k < kHold; ++k) v[k] = *reinterpret_cast<const float4u *>(X + (r0 + k) * p.ldx);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const f32x4 lo{v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]};
-            const f32x4 hi{v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
-            o[k] = codes4(lo, e) | codes4(hi, e) << 16;
+            for (int k = 0; k < kHold; ++k) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[k][i] = r0 + k < p.rows && col + i < p.cols ? X[(r0 + k) * p.ldx + i] : 0.0f;
+            }
         }
-        *reinterpret_cast<u32x4 *>(p.qt.codes + b * p.qt.sq + c * p.qt.ldq + block * kBlockBytes) = o;
-        uint8_t *s = p.qt.scales + b * p.qt.ss + c * p.qt.lds;
-        s[block] = static_cast<uint8_t>(e);
-        if (block == nb - 1)
-            for (int64_t k = nb; k < words; ++k) s[k] = 0;
+        if (ROWS) {
+            const int64_t block = col / kBlock;
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) {
+                const uint32_t m = max8(max(max(magnitude(v[k][0]), magnitude(v[k][1])),
+                                            max(magnitude(v[k][2]), magnitude(v[k][3]))));
+                const uint32_t e = scale_byte(m), c = codes4(v[k], e);
+                const int64_t r = r0 + k;
+                if (r < p.rows && block < ((nbc + 3) & ~3)) {
+                    if (block < nbc)
+                        *reinterpret_cast<uint16_t *>(p.q.codes + b * p.q.sq + r * p.q.ldq + col / 2) =
+                            static_cast<uint16_t>(c);
+                    if ((lane & 7) == 0)
+                        p.q.scales[b * p.q.ss + r * p.q.lds + block] = static_cast<uint8_t>(e);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) m = max(m, magnitude(v[k][i]));
+            m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+            const uint32_t e = scale_byte(m);
+            u32x2 o;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f32x4 lo{v[8 * k][i], v[8 * k + 1][i], v[8 * k + 2][i], v[8 * k + 3][i]};
+                const f32x4 hi{v[8 * k + 4][i], v[8 * k + 5][i], v[8 * k + 6][i], v[8 * k + 7][i]};
+                o[k] = codes4(lo, e) | codes4(hi, e) << 16;
+            }
+            const int c = 4 * quad + i;
+            *reinterpret_cast<u32x2 *>(&codes[(c * 4 + (wave ^ (quad & 3))) * kBlockBytes + 8 * half]) = o;
+            if (half == 0) scales[c * 4 + wave] = static_cast<uint8_t>(e);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSide * 4 / 256; ++i) {
+            const int at = i * 256 + threadIdx.x, c = at >> 2, part = at & 3;
+            const int64_t block = slab * 4 + part;
+            if (c0 + c < p.cols && block < nbr)
+                *reinterpret_cast<u32x4 *>(p.qt.codes + b * p.qt.sq + (c0 + c) * p.qt.ldq + block * kBlockBytes) =
+                    *reinterpret_cast<const u32x4 *>(&codes[(c * 4 + (part ^ (c >> 2 & 3))) * kBlockBytes]);
+        }
+        if (threadIdx.x < kSide && c0 + threadIdx.x < p.cols)
+            *reinterpret_cast<uint32_t *>(p.qt.scales + b * p.qt.ss + (c0 + threadIdx.x) * p.qt.lds + slab * 4) =
+                *reinterpret_cast<const uint32_t *>(&scales[threadIdx.x * 4]);
+        __syncthreads();
     }
 }
 
@@ -191,21 +240,20 @@ Lanes lanes_for(int64_t quads, int64_t rows, int64_t batch) {
 }  // namespace
 
 hipError_t launch_quantize(const Quantize &q, hipStream_t stream) {
-    if (q.along_rows) {
-        const int64_t words = (blocks_of(q.cols) + 3) / 4 * 4;
+    const int64_t words = (blocks_of(q.cols) + 3) / 4 * 4;
+    if (!q.along_cols) {
         const Lanes l = lanes_for(words * 8, q.rows, q.batch);
         quantize_rows_kernel<<<l.grid, 256, 0, stream>>>(q, l.lx, l.tiles_x, l.tiles_y, l.tiles);
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
-    }
-    if (q.along_cols) {
-        const int64_t tx = (q.cols + int64_t{255}) / 256, ty = blocks_of(q.rows);
-        const int64_t tiles = tx * ty * q.batch;
-        quantize_cols_kernel<<<static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 22)), 256, 0,
-                               stream>>>(q, tx, ty, tiles);
         return hipGetLastError();
     }
-    return hipSuccess;
+    const int64_t tx = ((q.along_rows ? words * kBlock : q.cols) + int64_t{127}) / 128;
+    const int64_t ty = (q.rows + int64_t{127}) / 128, tiles = tx * ty * q.batch;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 22));
+    if (q.along_rows)
+        quantize_cols_kernel<true><<<grid, 256, 0, stream>>>(q, tx, ty, tiles);
+    else
+        quantize_cols_kernel<false><<<grid, 256, 0, stream>>>(q, tx, ty, tiles);
+    return hipGetLastError();
 }
 
 hipError_t launch_dequantize(const Dequantize &d, hipStream_t stream) {
