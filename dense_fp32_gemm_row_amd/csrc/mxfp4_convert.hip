@@ -209,7 +209,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(Dequantize p, int lx, i
             float *y = p.Y + b * p.sy + r * p.ldy + col;
             const f32x4 v{lo[0], lo[1], hi[0], hi[1]};
             if (col + 4 <= p.cols) {
-                *reinterpret_cast<float4u *>(y) = v;
+                __builtin_nontemporal_store(v, reinterpret_cast<float4u *>(y));
             } else {
 #pragma unroll
                 for (int k = 0; k < 3; ++k)

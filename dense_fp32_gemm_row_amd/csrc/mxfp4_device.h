@@ -42,6 +42,8 @@ __device__ __forceinline__ void barrier_only() {
     asm volatile("" ::: "memory");
 }
 
+constexpr int kStream = 2;  // cache policy of buffer stores: non-temporal
+
 // A buffer of `bytes` bytes from p: loads past its end give zeros, stores
 // there are dropped.
 constexpr int kOutside = static_cast<int>(0x80000000u);  // an offset past every buffer
@@ -49,6 +51,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0,
                                              static_cast<int>(min(bytes, int64_t{0x7fffffff})),
                                              0x00020000);
+}
+
+// Stores the first min(V, left) of a lane's V (4 or 2) neighbours of a row at
+// byte `at` of the buffer.
+template <int V>
+__device__ __forceinline__ void store_neighbours(const float (&v)[V], __amdgpu_buffer_rsrc_t to, int at,
+                                                 int left) {
+    static_assert(V == 4 || V == 2, "");
+    if (left >= V) {
+        if constexpr (V == 4)
+            __builtin_amdgcn_raw_buffer_store_b128(
+                __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), to, at, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{v[0], v[1]}), to, at, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V - 1; ++j)
+            if (j < left) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[j]), to, at + 4 * j, 0, 0);
+    }
 }
 
 // Rows of an operand from a tile's first one, as a buffer: offsets past the

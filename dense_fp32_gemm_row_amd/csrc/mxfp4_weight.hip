@@ -556,23 +556,10 @@ __global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int ti
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int o = (32 * i + (r & 3) + 8 * (r >> 2) + 4 * half) * ld + n * 4;
-            if (n + FN <= p.N) {
-                if constexpr (FN == 4) {
-                    const f32x4 v{acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), c, o, 0, 0);
-                } else {
-                    const f32x2 v{acc[i][0][r], acc[i][1][r]};
-                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), c, o, 0, 0);
-                }
-            } else {
+            float v[FN];
 #pragma unroll
-                for (int j = 0; j < FN - 1; ++j) {
-                    const float v = acc[i][j][r];
-                    if (n + j < p.N)
-                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), c, o + 4 * j, 0, 0);
-                }
-            }
+            for (int j = 0; j < FN; ++j) v[j] = acc[i][j][r];
+            store_neighbours<FN>(v, c, (32 * i + (r & 3) + 8 * (r >> 2) + 4 * half) * ld + n * 4, p.N - n);
         }
 }
 
