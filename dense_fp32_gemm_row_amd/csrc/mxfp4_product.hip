@@ -52,8 +52,11 @@ struct Tile {
 // next stage's first fragments go out under the products of the second half.
 // So neither the barrier nor an LDS read is waited for with idle matrix
 // cores.
-template <int FM, int FN, int WM, int WN, int OCC, bool WHOLE>
-__global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product p, int tiles_m,
+// A CU holds PER_CU workgroups, which gives every SIMD two wavefronts: with
+// one (4 x 4 blocks each) it idles wherever that one waits, and 8192 x 14336 x
+// 4096 took 293 us instead of 276.
+template <int FM, int FN, int WM, int WN, int PER_CU, bool WHOLE>
+__global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_kernel(Product p, int tiles_m,
                                                                         int tiles_n, int64_t tiles,
                                                                         int groups, int len) {
     using T = Tile<FM, FN, WM, WN>;
@@ -283,16 +286,21 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void product_tile_kernel(Product 
 
     constexpr int L = T::kLoads, S = T::kScaleLoads * (WHOLE ? 1 : 4);
     // Stage `i` of the group: products from `cur`, the next stage in `nxt`.
+    // The wait counts on the order of loads: those of a stage (L) follow its
+    // barrier, the scales (S) lie between the first two, each behind a
+    // scheduling barrier of its own, since the scheduler may turn loads of one
+    // region around.  What stage i + 1 needs was loaded a group ago: two
+    // stages' loads are younger, and past the first barrier the scales'.
 #define GEMM_MXFP4_STAGE(i, cur, nxt, u, v)                                          \
     fetch(c1, cur);                                                                  \
     read_scales(v, (i + 1) % 4);                                                     \
+    if (i == 1) fetch_scales(cs);                                                    \
     multiply(c0, u);                                                                 \
-    interleave(0, 2 * (FM + FN));                                                    \
+    interleave(i == 1 ? S : 0, 2 * (FM + FN));                                       \
     wait_older<2 * L + (i > 0 ? S : 0)>();                                           \
     barrier_only();                                                                  \
     if (i == 3) store_scales(cs.g);                                                  \
     load(cc, i, cur);                                                                \
-    if (i == 0) fetch_scales(cs);                                                    \
     fetch(c0, nxt);                                                                  \
     multiply(c1, u);                                                                 \
     interleave(L, FM + FN);
@@ -396,19 +404,19 @@ hipError_t launch_rows(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int FM, int FN, int WM, int WN, int OCC>
+template <int FM, int FN, int WM, int WN, int PER_CU>
 hipError_t launch_tile(const Product &p, hipStream_t stream) {
     using T = Tile<FM, FN, WM, WN>;
     const int tm = ceil_div(p.M, T::BM), tn = ceil_div(p.N, T::BN);
     const int64_t tiles = static_cast<int64_t>(tm) * tn * p.batch * p.splits;
     const int groups = ceil_div(static_cast<int>(blocks_of(p.K)), T::kGroupBlocks);
     const int len = ceil_div(groups, p.splits);
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 256 * OCC));
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 256 * PER_CU));
     if (groups * T::kStages * T::kStageBlocks == blocks_of(p.K))
-        product_tile_kernel<FM, FN, WM, WN, OCC, true>
+        product_tile_kernel<FM, FN, WM, WN, PER_CU, true>
             <<<grid, T::NW * 64, 0, stream>>>(p, tm, tn, tiles, groups, len);
     else
-        product_tile_kernel<FM, FN, WM, WN, OCC, false>
+        product_tile_kernel<FM, FN, WM, WN, PER_CU, false>
             <<<grid, T::NW * 64, 0, stream>>>(p, tm, tn, tiles, groups, len);
     return hipGetLastError();
 }
@@ -429,18 +437,18 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t tota
 }
 
 // Which kernel a product takes: the least predicted time.  The figures are
-// microseconds measured on MI355X: per 512 k of a tile with the chip full
-// (and of a lone tile), per store of a tile, and fixed ones.
+// microseconds measured on MI355X, per 512 k of a tile and per store of one
+// with the chip full, and for lone tiles:
 //
-//   256 x 256  4 + rounds (3.95 / 512 k + 10.5), one tile a CU; a lone tile
-//              2.7 / 512 k
-//   128 x 128  4 + rounds (2.25 / 512 k + 8.9), two tiles a CU; a lone tile
+//   256 x 256  5 + rounds (3.65 / 512 k + 10.8), one tile a CU; a lone tile
+//              2.6 / 512 k
+//   128 x 128  4 + rounds (2.6 / 512 k + 5), two tiles a CU; a lone tile
 //              1.05 / 512 k
 //   32 x 32    3 + 2.3 / 2048 k and tile of a CU
 //
-// So 8192 x 14336 x 4096 (measured 297 us, against 376 with 128 x 128) and 64
-// x 1024^3 (85 against 107) take the large tile, 1024 x 1024 x 65536 128 x
-// 128 with sliced K (53 + 6 against 143 unsliced and 97 + 6 with the large
+// So 8192 x 14336 x 4096 (276 us, against 367 with 128 x 128) and 64 x 1024^3
+// (72 against 76) take the large tile, 1024 x 1024 x 65536 128 x 128 with
+// sliced K (50 and 8 for the sum, against 143 unsliced and 88 with the large
 // tile), 256^3 (3.2 against 5.8), 1000 x 1023 x 777 (6.4 against 8.0) and
 // products of few rows 32 x 32.
 enum Kernel { kLarge, kMedium, kRows };
@@ -448,19 +456,20 @@ struct Choice {
     Kernel kernel;
     int splits;
 };
-double tile_us(int64_t tiles, double groups, int slots, double each, double lone, double store) {
+double tile_us(int64_t tiles, double groups, int slots, double fixed, double each, double lone,
+               double store) {
     const double full = static_cast<double>(tiles / slots), rem = static_cast<double>(tiles % slots) / slots;
-    double t = 4.0 + full * (each * groups + store);
+    double t = fixed + full * (each * groups + store);
     if (rem > 0) t += groups * (lone + (each - lone) * rem * std::sqrt(rem)) + store * rem;
     return t;
 }
 double large_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits) {
     return tile_us((M + 255) / 256 * ((N + 255) / 256) * batch * splits,
-                   static_cast<double>((groups + splits - 1) / splits), 256, 3.95, 2.7, 10.5);
+                   static_cast<double>((groups + splits - 1) / splits), 256, 5.0, 3.65, 2.6, 10.8);
 }
 double medium_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits) {
     return tile_us((M + 127) / 128 * ((N + 127) / 128) * batch * splits,
-                   static_cast<double>((groups + splits - 1) / splits), 512, 2.25, 1.05, 8.9);
+                   static_cast<double>((groups + splits - 1) / splits), 512, 4.0, 2.6, 1.05, 5.0);
 }
 Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
     const double dm = static_cast<double>(M), dn = static_cast<double>(N), db = static_cast<double>(batch);
@@ -513,7 +522,7 @@ hipError_t launch_product(const Product &asked, hipStream_t stream) {
     p.splits = c.splits;
     hipError_t err = hipSuccess;
     switch (c.kernel) {
-        case kLarge: err = launch_tile<4, 4, 2, 2, 1>(p, stream); break;
+        case kLarge: err = launch_tile<2, 4, 4, 2, 1>(p, stream); break;
         case kMedium: err = launch_tile<2, 2, 2, 2, 2>(p, stream); break;
         case kRows: err = launch_rows<1, 8>(p, stream); break;
     }

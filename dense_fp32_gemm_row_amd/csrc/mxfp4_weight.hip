@@ -305,8 +305,9 @@ __global__ __launch_bounds__(64 * kVectorWaves) void weight_vector_kernel(Produc
 // which the next stage's first operands are read.
 template <int FM, int FN, bool BT, bool QUADS, int OCC>
 __global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int tiles_m, int tiles_n,
-                                                               int stages, int len) {
+                                                               int chunks, int len) {
     constexpr int BM = 64 * FM, BN = 64 * FN, kRow = 64;
+    constexpr int D = FM * FN <= 4 ? 2 : 1;   // stages that loads run ahead: the small tiles' are short
     constexpr int kUnits = BM / 32;           // 4 values of A per lane each
     constexpr int kWords = BN / 64;           // of codes per lane
     __shared__ __align__(1024) uint8_t a0[3 * BM * kRow];
@@ -316,36 +317,38 @@ __global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int ti
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, row = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
-    const Place at = place_of<BM, BN>(p, xcd_remap(blockIdx.x, gridDim.x), tiles_m, tiles_n, stages, len);
+    const Place at = place_of<BM, BN>(p, xcd_remap(blockIdx.x, gridDim.x), tiles_m, tiles_n, chunks, len);
     const int64_t b = at.slice / p.splits;
     const int nb = (p.K + kBlock - 1) / kBlock, nbn = (p.N + kBlock - 1) / kBlock;
+
+    const int s1 = min(at.g1 * 4, nb);  // stages are counted from K's start, 4 a chunk
 
     // ---- A: 8 lanes along a row, 32 rows a unit ----
     const __amdgpu_buffer_rsrc_t ar =
         buffer_of(p.x + b * p.sx + at.m0 * p.ldx, ((p.M - 1 - at.m0) * p.ldx + p.K) * 4);
     const int lda = static_cast<int>(p.ldx) * 4;
     const int ak = (tid & 7) * 4, arow = tid >> 3;
-    f32x4 av[kUnits];
-    auto load_a = [&](int u, int s) {
+    f32x4 av[D][kUnits];
+    auto load_a = [&](int u, int s, int set) {
         const int k = s * 32 + ak, at_row = (arow + 32 * u) * lda;
         if constexpr (QUADS) {
-            const int off = s < at.g1 && k < p.K ? k * 4 : kOutside;
-            av[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ar, at_row + off, 0, 0));
+            const int off = s < s1 && k < p.K ? k * 4 : kOutside;
+            av[set][u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ar, at_row + off, 0, 0));
         } else {  // four values may end a row, and the operand
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int off = s < at.g1 && k + e < p.K ? (k + e) * 4 : kOutside;
-                av[u][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ar, at_row + off, 0, 0));
+                const int off = s < s1 && k + e < p.K ? (k + e) * 4 : kOutside;
+                av[set][u][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ar, at_row + off, 0, 0));
             }
         }
     };
     // k 4 q .. 4 q + 3 of a row: half a slot
     const int aslot = (((tid & 7) >> 1) ^ ((arow >> 2) & 3)) * 16 + (tid & 1) * 8;
-    auto put_a = [&](int u, uint8_t *dst) {
+    auto put_a = [&](int u, uint8_t *dst, int set) {
         uint32_t h[3][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            split3(av[u][e], h[0][e], h[1][e], h[2][e]);
+            split3(av[set][u][e], h[0][e], h[1][e], h[2][e]);
         }
 #pragma unroll
         for (int c = 0; c < 3; ++c)
@@ -361,51 +364,65 @@ __global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int ti
                        (p.N - 1 - at.n0) * p.b.ldq + nb * kBlockBytes)
            : buffer_of(p.b.codes + b * p.b.sq, (p.K - 1) * p.b.ldq + nbn * kBlockBytes);
     const __amdgpu_buffer_rsrc_t wsr =
-        BT ? buffer_of(p.b.scales + b * p.b.ss + at.n0 * p.b.lds, (p.N - 1 - at.n0) * p.b.lds + nb)
+        BT ? buffer_of(p.b.scales + b * p.b.ss + at.n0 * p.b.lds, (p.N - 1 - at.n0) * p.b.lds + (nb + 3) / 4 * 4)
            : buffer_of(p.b.scales + b * p.b.ss, (p.K - 1) * p.b.lds + nbn);
     const int ldq = static_cast<int>(p.b.ldq), lds = static_cast<int>(p.b.lds);
-    uint32_t wc[BT ? kWords : 8], we[BT ? 1 : 8];
+    // Transposed, the codes of 4 stages (64 bytes of a column) are loaded at
+    // once, and their scales as one word: a stage's 16 bytes alone would fetch
+    // the same line from L2 in every stage (128 x 14336 x 4096 ...).
+    uint32_t wc[BT ? 4 * kWords : 8 * D], we[BT ? 1 : 8 * D], wc_next[BT ? 4 * kWords : 1], we_next = 0;
     constexpr int kParts = 4 / FN;  // lanes that share a column's block
     // transposed: LDS row of the lane, its column
     const int trow = tid / kParts, tcol = FN * (trow & 63) + (trow >> 6), tpart = tid % kParts;
-    auto load_w = [&](int s) {
-        const bool live = s < at.g1;
-        if constexpr (BT) {
-            const int off = live ? s * kBlockBytes + tpart * kWords * 4 : kOutside;
+    auto load_group = [&](int g) {  // transposed: stages 4 g .. 4 g + 3
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = 4 * g + i;
+            const int off = s < s1 ? s * kBlockBytes + tpart * kWords * 4 : kOutside;
             if constexpr (FN == 4) {
                 const u32x4 v = __builtin_bit_cast(
                     u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, tcol * ldq + off, 0, 0));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) wc[i] = v[i];
+                for (int q = 0; q < 4; ++q) wc_next[i * 4 + q] = v[q];
             } else {
                 const u32x2 v = __builtin_bit_cast(
                     u32x2, __builtin_amdgcn_raw_buffer_load_b64(wr, tcol * ldq + off, 0, 0));
-                wc[0] = v[0], wc[1] = v[1];
-            }
-            we[0] = __builtin_amdgcn_raw_buffer_load_b8(wsr, tcol * lds + (live ? s : kOutside), 0, 0);
-        } else {
-            const int n = at.n0 + FN * lane;  // first column of the lane
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int k = s * 32 + wave * 8 + i;
-                const bool in = live && k < p.K;
-                const int oc = in ? k * ldq + n / 2 : kOutside, os = in ? k * lds + n / kBlock : kOutside;
-                wc[i] = FN == 4 ? __builtin_amdgcn_raw_buffer_load_b16(wr, oc, 0, 0)
-                                : __builtin_amdgcn_raw_buffer_load_b8(wr, oc, 0, 0);
-                we[i] = __builtin_amdgcn_raw_buffer_load_b8(wsr, os, 0, 0);
+                wc_next[2 * i] = v[0], wc_next[2 * i + 1] = v[1];
             }
         }
+        we_next = __builtin_amdgcn_raw_buffer_load_b32(wsr, tcol * lds + (4 * g < s1 ? 4 * g : kOutside), 0, 0);
     };
-    auto put_w = [&](uint8_t *dst) {
+    auto take_group = [&](int g) {
+#pragma unroll
+        for (int q = 0; q < 4 * kWords; ++q) wc[q] = wc_next[q];
+        const int valid = min(max(s1 - 4 * g, 0), 4);  // past them the word may hold anything
+        we[0] = we_next & (valid == 4 ? 0xffffffffu : (1u << (8 * valid)) - 1u);
+    };
+    auto load_w = [&](int s, int set) {  // as stored: one stage
+        const bool live = s < s1;
+        const int n = at.n0 + FN * lane;  // first column of the lane
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = s * 32 + wave * 8 + i;
+            const bool in = live && k < p.K;
+            const int oc = in ? k * ldq + n / 2 : kOutside, os = in ? k * lds + n / kBlock : kOutside;
+            wc[8 * set + i] = FN == 4 ? __builtin_amdgcn_raw_buffer_load_b16(wr, oc, 0, 0)
+                            : __builtin_amdgcn_raw_buffer_load_b8(wr, oc, 0, 0);
+            we[8 * set + i] = __builtin_amdgcn_raw_buffer_load_b8(wsr, os, 0, 0);
+        }
+    };
+    auto put_w = [&](auto ic, uint8_t *dst) {  // stage ic of 4
+        constexpr int of = decltype(ic)::value;
         if constexpr (BT) {
-            const float e = scale_of(we[0]);
+            const float e = scale_of((we[0] >> (8 * of)) & 255u);
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
+                const uint32_t c = wc[of * kWords + i];
                 const u32x4 v = {
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 0)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 1)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 2)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 3))};
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e, 0)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e, 1)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e, 2)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e, 3))};
                 const int slot = (tpart * kWords + i) ^ ((trow >> 2) & 3);
                 *reinterpret_cast<u32x4 *>(dst + trow * kRow + slot * 16) = v;
             }
@@ -413,10 +430,11 @@ __global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int ti
             uint32_t v[8][FN / 2];  // pairs of columns of row k
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float e = scale_of(we[i]);
-                v[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 0));
+                const uint32_t c = wc[of % D * 8 + i];
+                const float e = scale_of(we[of % D * 8 + i]);
+                v[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e, 0));
                 if constexpr (FN == 4)
-                    v[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wc[i], e, 1));
+                    v[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, e, 1));
             }
 #pragma unroll
             for (int c = 0; c < FN; ++c) {
@@ -489,13 +507,15 @@ __global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int ti
     constexpr std::integral_constant<int, 4> p4;
     constexpr std::integral_constant<int, 5> p5;
 
-    // Stage s in (a, w); stage s + 1, in registers, goes to (na, nw).
-    auto stage = [&](int s, const uint8_t *a, const uint8_t *w, uint8_t *na, uint8_t *nw) {
+    // Stage s (the ic-th of its group) in (a, w); stage s + 1, in registers,
+    // goes to (na, nw).
+    auto stage = [&](auto ic, int s, const uint8_t *a, const uint8_t *w, uint8_t *na, uint8_t *nw) {
+        constexpr int i = decltype(ic)::value;
         auto units = [&](int first, int last) {
 #pragma unroll
             for (int u = first; u < last; ++u) {
-                put_a(u, na);
-                load_a(u, s + 2);
+                put_a(u, na, (i + 1) % D);
+                load_a(u, s + 1 + D, (i + 1) % D);
             }
         };
         fetch(p1, a, w);
@@ -515,8 +535,14 @@ __global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int ti
         multiply(p3);
         interleave();
         fetch(p5, a, w);
-        put_w(nw);
-        load_w(s + 2);
+        put_w(std::integral_constant<int, (i + 1) % 4>{}, nw);
+        if constexpr (!BT) {
+            load_w(s + 1 + D, (i + 1) % D);
+        } else if constexpr (i == 0) {
+            load_group(s / 4 + 1);
+        } else if constexpr (i == 2) {
+            take_group(s / 4 + 1);
+        }
         multiply(p4);
         interleave();
         wait_older<63>();  // LDS accesses alone
@@ -526,23 +552,39 @@ __global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int ti
         interleave();
     };
 
-    int s = at.g0;
+    int s = 4 * at.g0;
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) load_a(u, s);
-    load_w(s);
+    for (int d = 0; d < D; ++d) {
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) load_a(u, s + d, d);
+        if constexpr (!BT) load_w(s + d, d);
+    }
+    if constexpr (BT) {
+        load_group(s / 4);
+        take_group(s / 4);
+    }
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-        put_a(u, a0);
-        load_a(u, s + 1);
+        put_a(u, a0, 0);
+        load_a(u, s + D, 0);
     }
-    put_w(w0);
-    load_w(s + 1);
+    put_w(p0, w0);
+    if constexpr (!BT) load_w(s + D, 0);
     wait_older<63>();
     barrier_only();
     fetch(p0, a0, w0);
-    for (; s < at.g1; s += 2) {
-        stage(s, a0, w0, a1, w1);
-        stage(s + 1, a1, w1, a0, w0);  // past the end: zeros
+    for (; s + 3 < s1; s += 4) {
+        stage(p0, s, a0, w0, a1, w1);
+        stage(p1, s + 1, a1, w1, a0, w0);
+        stage(p2, s + 2, a0, w0, a1, w1);
+        stage(p3, s + 3, a1, w1, a0, w0);
+    }
+    if (s < s1) {
+        stage(p0, s, a0, w0, a1, w1);
+        if (s + 1 < s1) {
+            stage(p1, s + 1, a1, w1, a0, w0);
+            if (s + 2 < s1) stage(p2, s + 2, a0, w0, a1, w1);
+        }
     }
 
     // ---- results: FN neighbours a lane ----
@@ -575,12 +617,12 @@ bool reaches(const Product &p, int rows_m, int rows_n) {
 template <int FM, int FN, int OCC>
 hipError_t launch_tile(const Product &p, hipStream_t stream) {
     const int tm = ceil_div(p.M, 64 * FM), tn = ceil_div(p.N, 64 * FN);
-    const int stages = static_cast<int>(blocks_of(p.K)), len = ceil_div(stages, p.splits);
+    const int chunks = ceil_div(static_cast<int>(blocks_of(p.K)), 4), len = ceil_div(chunks, p.splits);
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(tm) * tn * p.batch * p.splits);
     const bool quads = p.K % 4 == 0;
     auto go = [&](auto bt, auto wh) {
         weight_tile_kernel<FM, FN, decltype(bt)::value, decltype(wh)::value, OCC>
-            <<<grid, 256, 0, stream>>>(p, tm, tn, stages, len);
+            <<<grid, 256, 0, stream>>>(p, tm, tn, chunks, len);
     };
     if (p.b_transposed)
         quads ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
@@ -617,15 +659,16 @@ hipError_t launch_any(const Product &p, hipStream_t stream) {
 
 // Which tile a product takes, and how many slices of K: the least predicted
 // time, from microseconds per 32 k measured on MI355X for a lone tile and for
-// a full chip (W transposed / as stored):
+// a full chip (W transposed / as stored), after 10 that every launch takes:
 //
-//   256 x 256  one a CU    1.76 / 1.97 lone   2.35 / 2.45 full
-//   128 x 128  two a CU    0.74 / 0.94 lone   1.45 / 1.55 full
-//    64 x 128  four a CU   0.49 / 0.80 lone   1.68 / 1.75 full
+//   128 x 256  two a CU     0.91 / 1.10 lone   2.19 / 2.31 full
+//    64 x 256  two a CU     0.56 / 0.75 lone   1.24 / 1.34 full
+//    64 x 128  three a CU   0.42 / 0.60 lone   1.07 / 1.27 full
 //
-// 4096 x 4096 x 14336 (1021 us, against 1323 and 1471) takes the first, 512 x
-// 4096 x 4096 the last (71 us unsliced, against 98 and 226), and so do 37 rows
-// x 14336 x 4096, in 4 slices of K (30 us, against 63 unsliced).
+// 4096 x 4096 x 14336 takes the first (982 us, against 1109 and 1272), 512 x
+// 4096 x 4096 the last (70 us unsliced, against 90 and 128) or the second in
+// 2 slices (58), 37 x 14336 x 4096 the second in 4 (30 us, against 82
+// unsliced).
 struct Choice {
     int tile;  // 0, 1, 2 as above
     int splits;
@@ -635,21 +678,21 @@ Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_
         int bm, bn, slots;
         double lone[2], full[2];
     };
-    static constexpr Candidate kTiles[] = {{256, 256, 256, {1.97, 1.76}, {2.45, 2.35}},
-                                           {128, 128, 512, {0.94, 0.74}, {1.55, 1.45}},
-                                           {64, 128, 1024, {0.80, 0.49}, {1.75, 1.68}}};
-    const int64_t stages = blocks_of(K);
+    static constexpr Candidate kTiles[] = {{128, 256, 512, {1.10, 0.91}, {2.31, 2.19}},
+                                           {64, 256, 512, {0.75, 0.56}, {1.34, 1.24}},
+                                           {64, 128, 768, {0.60, 0.42}, {1.27, 1.07}}};
+    const int64_t chunks = (blocks_of(K) + 3) / 4;
     Choice best{2, 1};
     double t = 0;
-    for (int want = 1; want <= most_splits && (want == 1 || want * 8 <= stages); want *= 2) {
-        const int s = slices_used(stages, want);
-        const double len = static_cast<double>((stages + s - 1) / s);
+    for (int want = 1; want <= most_splits && (want == 1 || want * 2 <= chunks); want *= 2) {
+        const int s = slices_used(chunks, want);
+        const double len = 4.0 * static_cast<double>((chunks + s - 1) / s);
         for (int i = 0; i < 3; ++i) {
             const Candidate &c = kTiles[i];
             const double tiles = static_cast<double>((M + c.bm - 1) / c.bm) *
                                  static_cast<double>((N + c.bn - 1) / c.bn) * static_cast<double>(batch) * s;
             const double full = std::floor(tiles / c.slots), rem = tiles / c.slots - full;
-            double u = 5.0 + full * len * c.full[bt] +
+            double u = 10.0 + full * len * c.full[bt] +
                        (rem > 0 ? len * (c.lone[bt] + (c.full[bt] - c.lone[bt]) * rem * std::sqrt(rem)) : 0.0);
             u += sum_slices_us(static_cast<double>(batch), static_cast<double>(M), static_cast<double>(N), s);
             if (t == 0 || u < t) t = u, best = {i, s};
@@ -671,7 +714,7 @@ int weight_splits(bool b_transposed, int64_t batch, int64_t M, int64_t N, int64_
 hipError_t launch_weight(const Product &asked, hipStream_t stream) {
     Product p = asked;
     const double tiles = static_cast<double>((p.M + 63) / 64) * ((p.N + 127) / 128) * static_cast<double>(p.batch);
-    const bool far = !reaches(p, 256, 256) || tiles > 1e6;  // (a launch has at most 2^32 lanes)
+    const bool far = !reaches(p, 128, 256) || tiles > 1e6;  // (a launch has at most 2^32 lanes)
     if (p.b_transposed && (p.M <= kFewRows || far)) {
         p.splits = 1;
         // One and two rows of A cost the vector units less than splitting 16:
@@ -691,9 +734,9 @@ hipError_t launch_weight(const Product &asked, hipStream_t stream) {
     }
     const Choice c = choose(p.b_transposed, p.batch, p.M, p.N, p.K, p.splits > 1 ? 64 : 1);
     p.splits = c.splits;
-    hipError_t err = c.tile == 0   ? launch_tile<4, 4, 1>(p, stream)
-                     : c.tile == 1 ? launch_tile<2, 2, 2>(p, stream)
-                                   : launch_tile<1, 2, 4>(p, stream);
+    hipError_t err = c.tile == 0   ? launch_tile<2, 4, 2>(p, stream)
+                     : c.tile == 1 ? launch_tile<1, 4, 2>(p, stream)
+                                   : launch_tile<1, 2, 3>(p, stream);
     if (err == hipSuccess && p.splits > 1) err = launch_sum_slices(p, stream);
     return err;
 }
