@@ -41,6 +41,7 @@ _vp = ctypes.c_void_p
 _int = ctypes.c_int
 
 _LIB: ctypes.CDLL | None = None
+_torch = None  # the module, once load() has run
 
 
 class GemmError(RuntimeError):
@@ -51,7 +52,7 @@ class GemmError(RuntimeError):
 
 def load(path: str = LIBRARY) -> ctypes.CDLL:
     """Loads the library (once).  Raises if it has not been built."""
-    global _LIB
+    global _LIB, _torch
     if _LIB is not None:
         return _LIB
     if not os.path.exists(path):
@@ -62,8 +63,9 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     # so the library launches into the same runtime that owns torch's memory
     # and streams.  Loaded the other way round, the process would hold two
     # HIP runtimes and torch's stream handles would be foreign to ours.
-    import torch  # noqa: F401
+    import torch
 
+    _torch = torch
     lib = ctypes.CDLL(path)
     lib.gemm_f32.restype = _int
     lib.gemm_f32.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
@@ -440,39 +442,36 @@ class Mxfp4:
     in the layout of include/gemm_mxfp4.h, and the number of columns.  It
     holds the tensors; their memory is not copied."""
 
-    __slots__ = ("codes", "scales", "cols", "_c")
+    __slots__ = ("codes", "scales", "cols", "shape", "_c")
 
     def __init__(self, codes, scales, cols: int):
-        import torch
-
-        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda:
+        load()
+        if codes.dtype != _torch.uint8 or scales.dtype != _torch.uint8 or not codes.is_cuda:
             raise TypeError("codes and scales must be uint8 GPU tensors")
         if scales.device != codes.device:
             raise ValueError("codes and scales are on different devices")
-        cs, ss = codes.shape, scales.shape
-        if len(cs) not in (2, 3) or len(ss) != len(cs) or cs[:-1] != ss[:-1]:
-            raise ValueError(f"codes {tuple(cs)} and scales {tuple(ss)} must be 2-D or 3-D with "
-                             "the same rows")
+        *lead, cb = codes.shape
+        *lead_s, sb = scales.shape
+        if len(lead) not in (1, 2) or lead_s != lead:
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} must be "
+                             "2-D or 3-D with the same rows")
         cols = int(cols)
         nb = (cols + MXFP4_BLOCK - 1) // MXFP4_BLOCK
         words = (nb + 3) // 4 * 4
-        if cols < 0 or cs[-1] < nb * 16 or ss[-1] < words:
+        if cols < 0 or cb < nb * 16 or sb < words:
             raise ValueError(f"{cols} columns need {nb * 16} bytes of codes and {words} of scales "
-                             f"a row, not {cs[-1]} and {ss[-1]}")
+                             f"a row, not {cb} and {sb}")
         ct, st = codes.stride(), scales.stride()
-        if (cs[-1] > 1 and ct[-1] != 1) or (ss[-1] > 1 and st[-1] != 1):
+        if (cb > 1 and ct[-1] != 1) or (sb > 1 and st[-1] != 1):
             raise ValueError("codes and scales must have unit stride along the last axis")
         self.codes, self.scales, self.cols = codes, scales, cols
-        rows = cs[-2]
-        batched = len(cs) == 3
-        self._c = Mxfp4Matrix(codes.data_ptr(), ct[-2] if rows > 1 else cs[-1] // 16 * 16,
-                              ct[0] if batched and cs[0] > 1 else 0,
-                              scales.data_ptr(), st[-2] if rows > 1 else ss[-1] // 4 * 4,
-                              st[0] if batched and cs[0] > 1 else 0)
-
-    @property
-    def shape(self) -> tuple[int, ...]:
-        return (*self.codes.shape[:-1], self.cols)
+        #: (rows, columns) or (batch, rows, columns)
+        self.shape = (*lead, cols)
+        many, batched = lead[-1] > 1, len(lead) == 2 and lead[0] > 1
+        self._c = Mxfp4Matrix(codes.data_ptr(), ct[-2] if many else cb // 16 * 16,
+                              ct[0] if batched else 0,
+                              scales.data_ptr(), st[-2] if many else sb // 4 * 4,
+                              st[0] if batched else 0)
 
     @property
     def device(self):
@@ -486,25 +485,22 @@ def _empty(shape, dtype, device, stream):
     """torch.empty for memory that work on ``stream`` (None: the current one)
     will use: taken from that stream's pool, so that nothing else still uses
     it, and nothing else gets it before that work is done."""
-    import torch
-
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 def mxfp4_empty(shape, device="cuda", *, stream=None) -> Mxfp4:
     """An uninitialised Mxfp4 of ``shape`` (rows, cols) or (batch, rows, cols)."""
-    import torch
-
+    load()
     *lead, cols = shape
     nb = (cols + MXFP4_BLOCK - 1) // MXFP4_BLOCK
     words = (nb + 3) // 4 * 4
-    codes = _empty((*lead, nb * 16), torch.uint8, device, stream)
-    scales = _empty((*lead, words), torch.uint8, device, stream)
+    codes = _empty((*lead, nb * 16), _torch.uint8, device, stream)
+    scales = _empty((*lead, words), _torch.uint8, device, stream)
     q = Mxfp4.__new__(Mxfp4)  # nothing to check
-    q.codes, q.scales, q.cols = codes, scales, cols
+    q.codes, q.scales, q.cols, q.shape = codes, scales, cols, (*lead, cols)
     rows = lead[-1]
     q._c = Mxfp4Matrix(codes.data_ptr(), nb * 16, rows * nb * 16, scales.data_ptr(), words,
                        rows * words)
@@ -514,20 +510,18 @@ def mxfp4_empty(shape, device="cuda", *, stream=None) -> Mxfp4:
 def _run_on(device, stream, fn, *args) -> None:
     """Calls a C entry point with the stream as its last argument, with the
     tensors' device current, and raises on an error."""
-    import torch
-
     index = device.index
     if stream is None:
         # (the raw handle: a torch.cuda.Stream object costs as much as a launch)
-        sp = torch._C._cuda_getCurrentRawStream(index)
+        sp = _torch._C._cuda_getCurrentRawStream(index)
     elif stream.device == device:
         sp = stream.cuda_stream
     else:
         raise ValueError(f"stream on {stream.device}, operands on {device}")
-    if torch._C._cuda_getDevice() == index:
+    if _torch._C._cuda_getDevice() == index:
         rc = fn(*args, sp)
     else:
-        with torch.cuda.device(device):
+        with _torch.cuda.device(device):
             rc = fn(*args, sp)
     if rc != GEMM_F32_OK:
         raise GemmError(rc, gemm_f32_last_error())
@@ -596,10 +590,8 @@ def mxfp4_dequantize(q: Mxfp4, out=None, *, stream=None):
 
 def _mxfp4_out(out, shape, device, workspace, need: int, stream):
     """(out, its leading dimension and batch stride, workspace pointer and bytes)."""
-    import torch
-
     if out is None:
-        out = _empty(shape, torch.float32, device, stream)
+        out = _empty(shape, _torch.float32, device, stream)
         ld = shape[-1] or 1
         bs = shape[-2] * ld
     else:
@@ -613,7 +605,7 @@ def _mxfp4_out(out, shape, device, workspace, need: int, stream):
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
         return out, ld, bs, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need:
-        workspace = _empty(need // 4, torch.float32, device, stream)
+        workspace = _empty(need // 4, _torch.float32, device, stream)
         return out, ld, bs, workspace, workspace.data_ptr(), need
     return out, ld, bs, None, None, 0
 
