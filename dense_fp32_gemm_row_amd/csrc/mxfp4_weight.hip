@@ -303,8 +303,8 @@ __global__ __launch_bounds__(64 * kVectorWaves) void weight_vector_kernel(Produc
 // stage ago, are split (or decoded), written to the other buffer and their
 // registers loaded again.  The one barrier lies before the last phase, under
 // which the next stage's first operands are read.
-template <int FM, int FN, bool BT, bool QUADS, int OCC>
-__global__ __launch_bounds__(256, OCC) void weight_tile_kernel(Product p, int tiles_m, int tiles_n,
+template <int FM, int FN, bool BT, bool QUADS, int PER_CU>
+__global__ __launch_bounds__(256, PER_CU) void weight_tile_kernel(Product p, int tiles_m, int tiles_n,
                                                                int chunks, int len) {
     constexpr int BM = 64 * FM, BN = 64 * FN, kRow = 64;
     constexpr int D = FM * FN <= 4 ? 2 : 1;   // stages that loads run ahead: the small tiles' are short
@@ -614,14 +614,21 @@ bool reaches(const Product &p, int rows_m, int rows_n) {
            int64_t{p.N} * 4 < kReach / 2;
 }
 
-template <int FM, int FN, int OCC>
+// PER_CU workgroups of a CU, for the registers that a wavefront may take.
+// Where the 128 x 256 tile's do not fit two without spilling dozens (W as
+// stored fits by itself), the compiler is not held to two: with K % 4 != 0
+// and W as stored 4096 x 4096 x 14335 took 1387 us held to them, 1153 so; with
+// W transposed and K % 4 == 0 a few spills cost less than the second
+// workgroup brings (1004 us against 1052).
+template <int FM, int FN, int PER_CU>
 hipError_t launch_tile(const Product &p, hipStream_t stream) {
     const int tm = ceil_div(p.M, 64 * FM), tn = ceil_div(p.N, 64 * FN);
     const int chunks = ceil_div(static_cast<int>(blocks_of(p.K)), 4), len = ceil_div(chunks, p.splits);
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(tm) * tn * p.batch * p.splits);
     const bool quads = p.K % 4 == 0;
     auto go = [&](auto bt, auto wh) {
-        weight_tile_kernel<FM, FN, decltype(bt)::value, decltype(wh)::value, OCC>
+        constexpr bool kFits = FM * FN < 8 || (decltype(bt)::value && decltype(wh)::value);
+        weight_tile_kernel<FM, FN, decltype(bt)::value, decltype(wh)::value, kFits ? PER_CU : 1>
             <<<grid, 256, 0, stream>>>(p, tm, tn, chunks, len);
     };
     if (p.b_transposed)

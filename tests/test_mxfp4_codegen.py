@@ -1,0 +1,96 @@
+"""Code-generation checks of the MXFP4 tiles (CPU only: hipcc cross-compiles
+gfx950 assembly without a GPU).
+
+The product tile's barriers wait until all but the newest N vector-memory
+instructions are done, and N counts on their order: a stage's code loads
+behind its barrier, the scale loads of a group behind the first stage's.  The
+compiler's scheduler may turn loads of one region around, and a scale load
+ahead of a code load makes a wavefront read codes that have not landed.
+"""
+
+from __future__ import annotations
+
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "dense_fp32_gemm_row_amd", "csrc")
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+
+
+@pytest.fixture(scope="module")
+def build(tmp_path_factory):
+    """(assembly, compiler remarks) of the MXFP4 sources."""
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    from concurrent.futures import ThreadPoolExecutor
+
+    tmp = tmp_path_factory.mktemp("asm")
+
+    def one(src):
+        out = tmp / (src + ".s")
+        cmd = [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
+               "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+               "-Rpass-analysis=kernel-resource-usage", "--cuda-device-only", "-S",
+               os.path.join(CSRC, src), "-o", str(out)]
+        res = subprocess.run(cmd, capture_output=True, text=True, timeout=900)
+        assert res.returncode == 0, res.stderr[-2000:]
+        return out.read_text(), res.stderr
+
+    with ThreadPoolExecutor(max_workers=3) as ex:
+        parts = list(ex.map(one, ["mxfp4_product.hip", "mxfp4_weight.hip", "mxfp4_convert.hip"]))
+    return "\n".join(p[0] for p in parts), "\n".join(p[1] for p in parts)
+
+
+def demangled(names):
+    filt = shutil.which("c++filt") or shutil.which("llvm-cxxfilt")
+    assert filt, "c++filt not found"
+    return subprocess.run([filt], input="\n".join(names), capture_output=True, text=True).stdout.splitlines()
+
+
+def arguments(name):
+    return [a.strip() for a in name[name.index("<") + 1:name.index(">")].split(",")]
+
+
+def test_product_tile_waits_count_on_its_load_order(build):
+    kernels = re.findall(r"^(_Z\S*product_tile_kernel\S*):[^\n]*\n(.*?)^\.Lfunc_end", build[0], re.S | re.M)
+    assert len(kernels) == 4
+    for name, body in zip(demangled([k[0] for k in kernels]), (k[1] for k in kernels)):
+        # <FM, FN, WM, WN, workgroups a CU, WHOLE>
+        fm, fn, wm, wn = (int(a) for a in arguments(name)[:4])
+        rows, waves = 32 * (fm * wm + fn * wn), wm * wn
+        code = rows // 16 // waves
+        scale = -(-rows // 64 // waves) * (1 if arguments(name)[5] == "true" else 4)
+        lines = [ln.strip() for ln in body.splitlines()]
+        bars = [i for i, ln in enumerate(lines) if ln.startswith("s_barrier")]
+        assert len(bars) == 5, f"{name}: {len(bars)} barriers"  # one ahead of the loop, four in it
+        for k in range(1, 5):
+            before = [ln for ln in lines[bars[k - 1]:bars[k]] if ln.startswith("s_waitcnt") and "vmcnt" in ln]
+            wait = int(re.search(r"vmcnt\((\d+)\)", before[-1]).group(1))
+            assert wait == 2 * code + (scale if k > 1 else 0), f"{name}: barrier {k} waits for {wait}"
+        for k in range(1, 4):
+            loads = "".join("c" if " lds" in ln else "s" for ln in lines[bars[k]:bars[k + 1]]
+                            if ln.startswith("buffer_load"))
+            assert loads == "c" * code + ("s" * scale if k == 1 else ""), f"{name}: stage {k - 1} loads {loads}"
+            assert not any("vmcnt" in ln for ln in lines[bars[k]:bars[k + 1] - 3] if ln.startswith("s_waitcnt")), name
+
+
+def test_no_kernel_spills_registers(build):
+    """A tile that spills runs at a fraction of its rate.  The one exception
+    was measured: 24 registers of the 128 x 256 FP32 x MXFP4 tile (W
+    transposed), for which a second workgroup fits on a CU."""
+    names = re.findall(r"Function Name: (\S+)", build[1])
+    scratch = [int(x) for x in re.findall(r"ScratchSize \[bytes/lane\]: (\d+)", build[1])]
+    assert len(names) == len(scratch) and len(names) > 20
+    spilled = {n: s for n, s in zip(demangled(names), scratch) if s}
+    allowed = [n for n in spilled if "weight_tile_kernel" in n and
+               (arguments(n) == ["2", "4", "true", "true", "2"] or spilled[n] <= 16)]
+    assert set(spilled) == set(allowed) and all(s <= 160 for s in spilled.values()), spilled
+
+
+def test_no_packed_fp32_instructions(build):
+    assert not re.search(r"\bv_pk_(add|mul|fma)_f32\b", build[0])
