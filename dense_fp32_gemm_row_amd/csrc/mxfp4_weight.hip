@@ -369,7 +369,7 @@ __global__ __launch_bounds__(256, PER_CU) void weight_tile_kernel(Product p, int
     const int ldq = static_cast<int>(p.b.ldq), lds = static_cast<int>(p.b.lds);
     // Transposed, the codes of 4 stages (64 bytes of a column) are loaded at
     // once, and their scales as one word: a stage's 16 bytes alone would fetch
-    // the same line from L2 in every stage (128 x 14336 x 4096 ...).
+    // the same line from L2 in every stage.
     uint32_t wc[BT ? 4 * kWords : 8 * D], we[BT ? 1 : 8 * D], wc_next[BT ? 4 * kWords : 1], we_next = 0;
     constexpr int kParts = 4 / FN;  // lanes that share a column's block
     // transposed: LDS row of the lane, its column
@@ -609,9 +609,9 @@ __global__ __launch_bounds__(256, PER_CU) void weight_tile_kernel(Product p, int
 bool reaches(const Product &p, int rows_m, int rows_n) {
     constexpr int64_t kReach = int64_t{1} << 31;
     const int64_t wrows = p.b_transposed ? rows_n : p.K;
-    return rows_m * p.ldx * 4 < kReach && rows_m * std::max(p.ldc, int64_t{p.N}) * 4 < kReach &&
-           wrows * p.b.ldq < kReach && wrows * p.b.lds < kReach && int64_t{p.K} * 4 < kReach / 2 &&
-           int64_t{p.N} * 4 < kReach / 2;
+    // (a stride may be near 2^60: it is divided into, never multiplied)
+    return p.ldx < kReach / 4 / rows_m && std::max(p.ldc, int64_t{p.N}) < kReach / 4 / rows_m &&
+           std::max(p.b.ldq, p.b.lds) < kReach / wrows && p.K < kReach / 8 && p.N < kReach / 8;
 }
 
 // PER_CU workgroups of a CU, for the registers that a wavefront may take.
@@ -666,11 +666,11 @@ hipError_t launch_any(const Product &p, hipStream_t stream) {
 
 // Which tile a product takes, and how many slices of K: the least predicted
 // time, from microseconds per 32 k measured on MI355X for a lone tile and for
-// a full chip (W transposed / as stored), after 10 that every launch takes:
+// a full chip (W transposed / as stored), after 4.5 that every launch takes:
 //
-//   128 x 256  two a CU     0.91 / 1.10 lone   2.19 / 2.31 full
-//    64 x 256  two a CU     0.56 / 0.75 lone   1.24 / 1.34 full
-//    64 x 128  three a CU   0.42 / 0.60 lone   1.07 / 1.27 full
+//   128 x 256  two a CU     0.95 / 1.24 lone   2.19 / 2.31 full
+//    64 x 256  two a CU     0.58 / 0.82 lone   1.24 / 1.34 full
+//    64 x 128  three a CU   0.45 / 0.69 lone   1.07 / 1.27 full
 //
 // 4096 x 4096 x 14336 takes the first (982 us, against 1109 and 1272), 512 x
 // 4096 x 4096 the last (70 us unsliced, against 90 and 128) or the second in
@@ -685,9 +685,9 @@ Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_
         int bm, bn, slots;
         double lone[2], full[2];
     };
-    static constexpr Candidate kTiles[] = {{128, 256, 512, {1.10, 0.91}, {2.31, 2.19}},
-                                           {64, 256, 512, {0.75, 0.56}, {1.34, 1.24}},
-                                           {64, 128, 768, {0.60, 0.42}, {1.27, 1.07}}};
+    static constexpr Candidate kTiles[] = {{128, 256, 512, {1.24, 0.95}, {2.31, 2.19}},
+                                           {64, 256, 512, {0.82, 0.58}, {1.34, 1.24}},
+                                           {64, 128, 768, {0.69, 0.45}, {1.27, 1.07}}};
     const int64_t chunks = (blocks_of(K) + 3) / 4;
     Choice best{2, 1};
     double t = 0;
@@ -699,7 +699,7 @@ Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_
             const double tiles = static_cast<double>((M + c.bm - 1) / c.bm) *
                                  static_cast<double>((N + c.bn - 1) / c.bn) * static_cast<double>(batch) * s;
             const double full = std::floor(tiles / c.slots), rem = tiles / c.slots - full;
-            double u = 10.0 + full * len * c.full[bt] +
+            double u = 4.5 + full * len * c.full[bt] +
                        (rem > 0 ? len * (c.lone[bt] + (c.full[bt] - c.lone[bt]) * rem * std::sqrt(rem)) : 0.0);
             u += sum_slices_us(static_cast<double>(batch), static_cast<double>(M), static_cast<double>(N), s);
             if (t == 0 || u < t) t = u, best = {i, s};

@@ -440,6 +440,45 @@ def test_far_rows():
     check_product(to_host(out), x.astype(np.float64), w64, K, 3)
 
 
+@pytest.mark.parametrize("op", ["T", "N"])
+def test_one_row_at_the_longest_stride(op):
+    """A lone row's stride is never stepped over, however long it is."""
+    import torch
+
+    rng = np.random.default_rng(13)
+    M, N, K, far = 1, 70, 200, 1 << 57
+    w = ref.random_matrix(rng, (N,) if op == "T" else (K,), K if op == "T" else N)
+    w64 = ref.values(*w, K if op == "T" else N)
+    x = wide_floats(rng, M, K)
+    X, W = to_dev(x), held(*w, K if op == "T" else N)
+    out = torch.full((3, N), 7.0, device="cuda:0")
+    wc = b.Mxfp4Matrix(W.codes.data_ptr(), W.codes.stride(0), 0, W.scales.data_ptr(), W.scales.stride(0), 0)
+    rc = b.gemm_mxfp4_weight_product(b.OP_T if op == "T" else b.OP_N, 1, M, N, K, X.data_ptr(), far, 0, wc,
+                                     out.data_ptr(), far, 0)
+    assert rc == 0
+    torch.cuda.synchronize()
+    check_product(to_host(out[:1]), x.astype(np.float64), w64 if op == "T" else w64.T, K, 3)
+    assert (out[1:] == 7.0).all()
+    if op == "N":
+        return
+    q = b.mxfp4_empty((3, K))
+    q.codes.fill_(9)
+    q.scales.fill_(9)
+    qc = b.Mxfp4Matrix(q.codes.data_ptr(), far, 0, q.scales.data_ptr(), far, 0)
+    back = torch.full((3, K), 7.0, device="cuda:0")
+    assert b.gemm_mxfp4_quantize(1, 1, K, X.data_ptr(), far, 0, qc, None) == 0
+    assert b.gemm_mxfp4_dequantize(1, 1, K, qc, back.data_ptr(), far, 0) == 0
+    assert b.gemm_mxfp4_product(1, 1, N, K, qc, wc, out.data_ptr(), far, 0) == 0
+    torch.cuda.synchronize()
+    codes, scales = ref.quantize(x)
+    assert np.array_equal(to_host(q.codes[:1, : codes.shape[1]]), codes)
+    assert (q.codes[1:] == 9).all() and (q.scales[1:] == 9).all()
+    x64 = ref.values(codes, scales, K)
+    assert np.array_equal(to_host(back[:1]), x64.astype(np.float32)) and (back[1:] == 7.0).all()
+    check_product(to_host(out[:1]), x64, w64, K)
+    assert (out[1:] == 7.0).all()
+
+
 # ---- refusals of the tensor calls ---------------------------------------------------
 
 def test_tensor_refusals():
