@@ -31,50 +31,120 @@ __device__ __forceinline__ uint32_t pack_high(uint32_t lo, uint32_t hi) {
     return (lo >> 16) | (hi & 0xffff0000u);
 }
 
-// W as stored, operands of any stride: one wavefront per 32 x 32 tile,
-// straight from global memory.  In v_mfma_f32_32x32x16_bf16 lane l holds 8
-// consecutive k from 8 (l / 32) of row (column) l % 32.
-__global__ __launch_bounds__(256) void weight_any_kernel(Product p, int64_t tiles_m, int64_t tiles_n,
-                                                         int64_t tiles) {
-    const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
-    for (int64_t t = blockIdx.x * int64_t{4} + (threadIdx.x >> 6); t < tiles;
-         t += gridDim.x * int64_t{4}) {
-        const int64_t line = t / tiles_n, b = line / tiles_m;
-        const int64_t n0 = (t - line * tiles_n) * 32, m0 = (line - b * tiles_m) * 32;
-        const int64_t m = min(m0 + row, int64_t{p.M} - 1), n = min(n0 + row, int64_t{p.N} - 1);
-        const float *A = p.x + b * p.sx + m * p.ldx;
+// W as stored, few rows of A, and operands of any stride: a workgroup of 8
+// wavefronts holds a tile of 16 x 128, its wavefronts take steps of 32 k in
+// turn, straight from global memory, and their sums are added in LDS in a
+// fixed order.  In v_mfma_f32_16x16x32_bf16 lane l holds 8 k, from 8 (l / 16),
+// of row (column) l % 16; here lane l reads those k of 8 neighbouring columns
+// from 8 (l % 16), a word of codes for each, and turns pairs of values of two
+// columns, as W holds them, into pairs of two k.  Neighbouring tiles run on
+// one XCD, whose L2 then fetches lines of W, and of its scales, that tiles
+// share once (16 x 4096 x 14336: 16.9 us, 18.5 without).
+constexpr int kStoredWaves = 8;
+__global__ __launch_bounds__(64 * kStoredWaves) void weight_stored_kernel(Product p, int64_t tiles_m,
+                                                                          int64_t tiles_n, int64_t tiles,
+                                                                          int len) {
+    constexpr int C = 8, NW = kStoredWaves;  // 8 columns: a word of codes
+    __shared__ __align__(16) float sums[NW][C][4][64];
+    const int lane = threadIdx.x & 63, row = lane & 15, group = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int steps = (p.K + kBlock - 1) / kBlock;
+    for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < tiles; t += gridDim.x) {
+        const int64_t line = t / tiles_n, slice = line / tiles_m, b = slice / p.splits;
+        const int64_t n0 = (t - line * tiles_n) * 16 * C, m0 = (line - slice * tiles_m) * 16;
+        const int first = static_cast<int>(slice - b * p.splits) * len, last = min(first + len, steps);
+        // rows and columns past the end repeat the last ones' and are not stored
+        const float *A = p.x + b * p.sx + min(m0 + row, int64_t{p.M} - 1) * p.ldx;
+        const int64_t n = min(n0 + C * row, int64_t{p.N - 1} / C * C);
         const uint8_t *W = p.b.codes + b * p.b.sq + n / 2;
         const uint8_t *S = p.b.scales + b * p.b.ss + n / kBlock;
-        f32x16 acc = {};
-        for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
-            const int64_t k = k0 + 8 * half;
-            uint32_t a[3][8];
-            u32x4 w = {};
+        struct Step {
+            float a[8];
+            uint32_t w[8], e[8];
+        };
+        auto load = [&](int s) {
+            Step v;
+            const int64_t k = s * int64_t{kBlock} + 8 * group;
+            const bool whole = (s + int64_t{1}) * kBlock <= p.K;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                split3(k + i < p.K ? A[k + i] : 0.0f, a[0][i], a[1][i], a[2][i]);
-                if (k + i >= p.K) continue;
-                const uint32_t c = W[(k + i) * p.b.ldq] >> (4 * (n & 1)) & 15;
-                const uint32_t v = __builtin_bit_cast(
-                    uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale_of(S[(k + i) * p.b.lds]), 0));
-                w[i / 2] |= (v & 0xffffu) << (16 * (i & 1));
+            for (int i = 0; i < 8; ++i) {  // A past K is zero, so what W holds there does not matter
+                const int64_t q = whole ? k + i : min(k + i, int64_t{p.K} - 1);
+                v.w[i] = *reinterpret_cast<const uint32_t *>(W + q * p.b.ldq);
+                v.e[i] = S[q * p.b.lds];
             }
+            if (whole) {
 #pragma unroll
-            for (int s = 2; s >= 0; --s) {
-                const u32x4 x = {pack_high(a[s][0], a[s][1]), pack_high(a[s][2], a[s][3]),
-                                 pack_high(a[s][4], a[s][5]), pack_high(a[s][6], a[s][7])};
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x),
-                                                              __builtin_bit_cast(bf16x8, w), acc, 0, 0, 0);
+                for (int i = 0; i < 2; ++i) {
+                    const f32x4 x = *reinterpret_cast<const float4u *>(A + k + 4 * i);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v.a[4 * i + q] = x[q];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v.a[i] = k + i < p.K ? A[k + i] : 0.0f;
+            }
+            return v;
+        };
+        f32x4 acc[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        int s = first + wave;
+        if (s < last) {
+            Step now = load(s);
+            for (; s < last; s += NW) {
+                const Step next = load(min(s + NW, last - 1));
+                uint32_t h[3][8];
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    split3(now.a[i], h[0][i], h[1][i], h[2][i]);
+                    f[i] = scale_of(now.e[i]);
+                }
+                u32x4 x[3];
+#pragma unroll
+                for (int c = 0; c < 3; ++c)
+                    x[c] = u32x4{pack_high(h[c][0], h[c][1]), pack_high(h[c][2], h[c][3]),
+                                 pack_high(h[c][4], h[c][5]), pack_high(h[c][6], h[c][7])};
+                auto pair = [&](auto jc) {  // columns 2 j and 2 j + 1
+                    constexpr int j = decltype(jc)::value;
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
+                                                                now.w[i], f[i], j));
+                    const u32x4 even = {(v[0] & 0xffffu) | (v[1] << 16), (v[2] & 0xffffu) | (v[3] << 16),
+                                        (v[4] & 0xffffu) | (v[5] << 16), (v[6] & 0xffffu) | (v[7] << 16)};
+                    const u32x4 odd = {pack_high(v[0], v[1]), pack_high(v[2], v[3]),
+                                       pack_high(v[4], v[5]), pack_high(v[6], v[7])};
+#pragma unroll
+                    for (int q = 2; q >= 0; --q) {
+                        acc[2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, x[q]), __builtin_bit_cast(bf16x8, even), acc[2 * j], 0, 0, 0);
+                        acc[2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, x[q]), __builtin_bit_cast(bf16x8, odd), acc[2 * j + 1], 0, 0, 0);
+                    }
+                };
+                pair(std::integral_constant<int, 0>{}), pair(std::integral_constant<int, 1>{});
+                pair(std::integral_constant<int, 2>{}), pair(std::integral_constant<int, 3>{});
+                now = next;
             }
         }
-        if (n0 + row < p.N) {
-            float *C = p.C + b * p.sc + n0 + row;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int64_t r = m0 + (i & 3) + 8 * (i >> 2) + 4 * half;
-                if (r < p.M) C[r * p.ldc] = acc[i];
-            }
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums[wave][j][r][lane] = acc[j][r];
+        __syncthreads();
+        float *out = p.splits > 1 ? p.W + slice * p.M * p.N : p.C + b * p.sc;
+        const int64_t ldc = p.splits > 1 ? p.N : p.ldc;
+        for (int o = threadIdx.x; o < C * 256; o += 64 * NW) {
+            const int c = o % (16 * C), r = o / (16 * C), l = c / C + 16 * (r >> 2);
+            if (m0 + r >= p.M || n0 + c >= p.N) continue;
+            float v = sums[0][c % C][r & 3][l];
+#pragma unroll
+            for (int q = 1; q < NW; ++q) v += sums[q][c % C][r & 3][l];
+            out[(m0 + r) * ldc + n0 + c] = v;
         }
+        __syncthreads();
     }
 }
 
@@ -89,14 +159,15 @@ __global__ __launch_bounds__(256) void weight_any_kernel(Product p, int64_t tile
 constexpr int kRowsWaves = 8;
 template <int NT>
 __global__ __launch_bounds__(64 * kRowsWaves) void weight_rows_kernel(Product p, int64_t tiles_m,
-                                                                      int64_t tiles_n, int64_t tiles) {
+                                                                      int64_t tiles_n, int64_t tiles, int len) {
     __shared__ __align__(16) float sums[kRowsWaves][NT][4][64];
     const int lane = threadIdx.x & 63, row = lane & 15, group = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int nb = (p.K + kBlock - 1) / kBlock;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t line = t / tiles_n, b = line / tiles_m;
-        const int64_t n0 = (t - line * tiles_n) * 16 * NT, m0 = (line - b * tiles_m) * 16;
+        const int64_t line = t / tiles_n, slice = line / tiles_m, b = slice / p.splits;
+        const int64_t n0 = (t - line * tiles_n) * 16 * NT, m0 = (line - slice * tiles_m) * 16;
+        const int first = static_cast<int>(slice - b * p.splits) * len, last = min(first + len, (nb + 3) / 4);
         const float *A = p.x + b * p.sx + min(m0 + row, int64_t{p.M} - 1) * p.ldx;
         const uint8_t *W[NT], *S[NT];
 #pragma unroll
@@ -108,7 +179,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void weight_rows_kernel(Product p,
         f32x4 acc[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = wave; s * 4 < nb; s += kRowsWaves) {
+        for (int s = first + wave; s < last; s += kRowsWaves) {
             const int block = s * 4 + group;
             const int64_t held = min(block, nb - 1);
             u32x4 w[NT];
@@ -157,6 +228,8 @@ __global__ __launch_bounds__(64 * kRowsWaves) void weight_rows_kernel(Product p,
 #pragma unroll
             for (int r = 0; r < 4; ++r) sums[wave][j][r][lane] = acc[j][r];
         __syncthreads();
+        float *out = p.splits > 1 ? p.W + slice * p.M * p.N : p.C + b * p.sc;
+        const int64_t ldc = p.splits > 1 ? p.N : p.ldc;
         for (int o = threadIdx.x; o < NT * 256; o += 64 * kRowsWaves) {
             const int l = o & 63, r = (o >> 6) & 3, j = o >> 8;
             const int64_t n = n0 + 16 * j + (l & 15), m = m0 + 4 * (l >> 4) + r;
@@ -164,7 +237,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void weight_rows_kernel(Product p,
             float v = sums[0][j][r][l];
 #pragma unroll
             for (int q = 1; q < kRowsWaves; ++q) v += sums[q][j][r][l];
-            p.C[b * p.sc + m * p.ldc + n] = v;
+            out[m * ldc + n] = v;
         }
         __syncthreads();
     }
@@ -641,9 +714,9 @@ hipError_t launch_tile(const Product &p, hipStream_t stream) {
 template <int NT>
 hipError_t launch_rows(const Product &p, hipStream_t stream) {
     const int64_t tm = (p.M + int64_t{15}) / 16, tn = (p.N + int64_t{16 * NT - 1}) / (16 * NT);
-    const int64_t tiles = tm * tn * p.batch;
+    const int64_t tiles = tm * tn * p.batch * p.splits, steps = (blocks_of(p.K) + 3) / 4;
     weight_rows_kernel<NT><<<static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20)), 64 * kRowsWaves, 0,
-                             stream>>>(p, tm, tn, tiles);
+                             stream>>>(p, tm, tn, tiles, static_cast<int>((steps + p.splits - 1) / p.splits));
     return hipGetLastError();
 }
 
@@ -656,11 +729,12 @@ hipError_t launch_vector(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_any(const Product &p, hipStream_t stream) {
-    const int64_t tm = (p.M + int64_t{31}) / 32, tn = (p.N + int64_t{31}) / 32;
-    const int64_t tiles = tm * tn * p.batch;
-    weight_any_kernel<<<static_cast<unsigned>(std::min<int64_t>((tiles + 3) / 4, 1 << 20)), 256, 0, stream>>>(
-        p, tm, tn, tiles);
+hipError_t launch_stored(const Product &p, hipStream_t stream) {
+    const int64_t tm = (p.M + int64_t{15}) / 16, tn = (p.N + int64_t{127}) / 128;
+    const int64_t tiles = tm * tn * p.batch * p.splits;
+    const int len = static_cast<int>((blocks_of(p.K) + p.splits - 1) / p.splits);
+    weight_stored_kernel<<<static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20)), 64 * kStoredWaves, 0,
+                           stream>>>(p, tm, tn, tiles, len);
     return hipGetLastError();
 }
 
@@ -708,42 +782,83 @@ Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_
     return best;
 }
 
-// Rows of A that W transposed is read for without tiles.
+// Rows of A up to which W is read straight into registers, without tiles.
 constexpr int kFewRows = 16;
+
+// Slices of K for these, W as stored: workgroups for most CUs, and a step of
+// 32 k at least for every wavefront (16 rows x 4096 x 4096: 8 slices 8.6 us,
+// 4 11.0, none 26.8; 16 x 14336 x 4096: 2 slices 18.3 us, 4 the same).
+int stored_splits(int64_t batch, int64_t M, int64_t N, int64_t K) {
+    const double tiles = static_cast<double>((M + 15) / 16) * static_cast<double>((N + 127) / 128) *
+                         static_cast<double>(batch);
+    const int64_t steps = blocks_of(K);
+    int s = 1;
+    while (tiles * s < 200 && steps >= 8 * s) s *= 2;
+    return slices_used(steps, s);
+}
+
+// Columns of a workgroup (16 nt) and slices of K for these, W transposed.
+// Wide tiles share the splitting of A but leave CUs without one: 16 rows x
+// 14336 x 4096 takes 64 columns (19.7 us, against 26 with 32 and 40 with 16),
+// 16 rows x 4096 x 4096 16 (12.5, against 14 and 18).  From 8192 k slices are
+// worth adding their sums: 16 rows x 4096 x 14336 takes 64 columns in 4 slices
+// (21 us, against 37 with 16 columns unsliced), 16 x 512 x 8192 16 columns in 8
+// (9.9, against 20.6); 4 rows x 4096 x 4096 would lose by it (9.7, against 8.9).
+struct FewRows {
+    int nt, splits;
+};
+FewRows few_rows(int64_t batch, int64_t M, int64_t N, int64_t K, bool slices) {
+    constexpr double kEnough = 200;  // workgroups
+    auto tiles = [&](int nt) {
+        return static_cast<double>((M + 15) / 16) * static_cast<double>((N + 16 * nt - 1) / (16 * nt)) *
+               static_cast<double>(batch);
+    };
+    const int64_t steps = (blocks_of(K) + 3) / 4;
+    for (int nt = 4; nt >= 1; nt /= 2) {
+        int s = 1;
+        if (slices && steps >= 64)
+            while (tiles(nt) * s < kEnough && 16 * s <= steps) s *= 2;  // a step at least for every wavefront
+        if (nt == 1 || tiles(nt) * s >= kEnough) return {nt, slices_used(steps, s)};
+    }
+    return {1, 1};
+}
 
 }  // namespace
 
 int weight_splits(bool b_transposed, int64_t batch, int64_t M, int64_t N, int64_t K) {
-    if (b_transposed && M <= kFewRows) return 1;
-    return choose(b_transposed, batch, M, N, K, 64).splits;
+    if (M > kFewRows) return choose(b_transposed, batch, M, N, K, 64).splits;
+    if (!b_transposed) return stored_splits(batch, M, N, K);
+    return M <= 2 ? 1 : few_rows(batch, M, N, K, true).splits;
 }
 
 hipError_t launch_weight(const Product &asked, hipStream_t stream) {
     Product p = asked;
     const double tiles = static_cast<double>((p.M + 63) / 64) * ((p.N + 127) / 128) * static_cast<double>(p.batch);
+    const bool few = p.M <= kFewRows;
     const bool far = !reaches(p, 128, 256) || tiles > 1e6;  // (a launch has at most 2^32 lanes)
-    if (p.b_transposed && (p.M <= kFewRows || far)) {
-        p.splits = 1;
+    const bool slices = p.splits > 1 && (few || !far);
+    p.splits = 1;
+    hipError_t err;
+    if (p.b_transposed && p.M <= 2) {
         // One and two rows of A cost the vector units less than splitting 16:
-        // a row x 14336 x 4096 8.0 us, against 13.7.  Wide tiles share the
-        // splitting but leave CUs without one: 16 rows x 14336 x 4096 takes
-        // 64 columns a workgroup (18.8 us, against 25 with 32), 16 rows x
-        // 4096 x 4096 16 (8.4, against 10).
-        if (p.M == 1) return launch_vector<1>(p, stream);
-        if (p.M == 2) return launch_vector<2>(p, stream);
-        const int64_t columns = p.N * p.batch * ((p.M + 15) / 16);
-        if (columns >= 200 * 64) return launch_rows<4>(p, stream);
-        return columns >= 200 * 32 ? launch_rows<2>(p, stream) : launch_rows<1>(p, stream);
+        // a row x 14336 x 4096 8.0 us, against 13.7.
+        return p.M == 1 ? launch_vector<1>(p, stream) : launch_vector<2>(p, stream);
+    } else if (p.b_transposed && (few || far)) {
+        const FewRows c = few_rows(p.batch, p.M, p.N, p.K, slices);
+        p.splits = c.splits;
+        err = c.nt == 4   ? launch_rows<4>(p, stream)
+              : c.nt == 2 ? launch_rows<2>(p, stream)
+                          : launch_rows<1>(p, stream);
+    } else if (few || far) {
+        if (slices) p.splits = stored_splits(p.batch, p.M, p.N, p.K);
+        err = launch_stored(p, stream);
+    } else {
+        const Choice c = choose(p.b_transposed, p.batch, p.M, p.N, p.K, slices ? 64 : 1);
+        p.splits = c.splits;
+        err = c.tile == 0   ? launch_tile<2, 4, 2>(p, stream)
+              : c.tile == 1 ? launch_tile<1, 4, 2>(p, stream)
+                            : launch_tile<1, 2, 3>(p, stream);
     }
-    if (far) {
-        p.splits = 1;
-        return launch_any(p, stream);
-    }
-    const Choice c = choose(p.b_transposed, p.batch, p.M, p.N, p.K, p.splits > 1 ? 64 : 1);
-    p.splits = c.splits;
-    hipError_t err = c.tile == 0   ? launch_tile<2, 4, 2>(p, stream)
-                     : c.tile == 1 ? launch_tile<1, 4, 2>(p, stream)
-                                   : launch_tile<1, 2, 3>(p, stream);
     if (err == hipSuccess && p.splits > 1) err = launch_sum_slices(p, stream);
     return err;
 }

@@ -403,6 +403,34 @@ def test_long_sums_with_and_without_workspace(shape):
             b.gemm_mxfp4(A, W, out[:M * N].view(M, N), workspace=out)
 
 
+FEW = [(1, 3, 300, 8250), (1, 16, 40, 20001), (1, 5, 1000, 8200), (1, 13, 3500, 8192), (2, 9, 130, 12000),
+       (1, 2, 77, 9000), (1, 16, 2000, 4096)]
+
+
+@pytest.mark.parametrize("op", ["T", "N"])
+@pytest.mark.parametrize("shape", FEW)
+def test_few_rows_with_and_without_workspace(shape, op):
+    import torch
+
+    batch, M, N, K = shape
+    rng = np.random.default_rng(K + N)
+    rows, cols = (N, K) if op == "T" else (K, N)
+    w = ref.random_matrix(rng, (batch, rows), cols)
+    w64 = ref.values(*w, cols)
+    w64 = w64 if op == "T" else np.swapaxes(w64, -1, -2)
+    x = np.stack([wide_floats(rng, M, K) for _ in range(batch)])
+    X, W, code = to_dev(x), held(*w, cols), b.OP_T if op == "T" else b.OP_N
+    need = b.gemm_mxfp4_weight_workspace_size(code, batch, M, N, K)
+    for work in {0, need}:
+        out = torch.full((batch, M + 1, N + 3), 7.0, device="cuda:0")
+        ws = torch.full((work // 4 + 8,), 7.0, device="cuda:0")
+        assert b.gemm_mxfp4_weight_product(code, batch, M, N, K, X.data_ptr(), K, M * K, W._c, out.data_ptr(), N + 3,
+                                           (M + 1) * (N + 3), ws.data_ptr() if work else None, work) == 0
+        torch.cuda.synchronize()
+        check_product(to_host(out[:, :M, :N]), x.astype(np.float64), w64, K, 3, f"workspace {work}")
+        assert (out[:, M:] == 7.0).all() and (out[:, :, N:] == 7.0).all() and (ws[work // 4:] == 7.0).all()
+
+
 def test_far_rows():
     """Rows of codes, of X and of C that lie more than 2^32 bytes apart."""
     import torch
