@@ -13,7 +13,8 @@
 namespace gemm_f32_impl {
 namespace {
 
-constexpr int64_t kSizeMax = 0x7fffffff;
+// The kernels count rows, columns and k in 32 bits, up to the end of the last tile.
+constexpr int64_t kSizeMax = (int64_t{1} << 31) - 1024;
 constexpr int64_t kSpanMax = int64_t{1} << 60;  // bytes that one operand may span
 
 struct Bytes {
@@ -31,7 +32,7 @@ int64_t span(int64_t batch, int64_t stride, int64_t rows, int64_t ld, int64_t ro
 
 int check_size(const char *name, int64_t n) {
     if (n < 0) return fail(GEMM_F32_EINVAL, "negative %s %lld", name, (long long)n);
-    if (n > kSizeMax) return fail(GEMM_F32_EINVAL, "%s=%lld above 2^31-1", name, (long long)n);
+    if (n > kSizeMax) return fail(GEMM_F32_EINVAL, "%s=%lld above 2^31-1024", name, (long long)n);
     return GEMM_F32_OK;
 }
 

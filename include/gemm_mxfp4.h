@@ -24,6 +24,8 @@
  *     16; scales is 4-byte aligned with ld_scales and stride_scales multiples
  *     of 4.  Other layouts are refused.
  *
+ * Sizes (batch, rows, cols, M, N, K) are at most 2^31 - 1024.
+ *
  * Scale bytes 253 and 254 can stand for values beyond FP32's range; a product
  * of such a value is infinite or NaN.
  *
@@ -102,7 +104,8 @@ int gemm_mxfp4_dequantize(int64_t batch, int64_t rows, int64_t cols,
  *   C   M x N, row-major FP32, ldc >= max(1, N), not overlapping A or B
  *
  * Products are exact; they are summed in FP32 on the matrix cores, in an
- * order that depends on sizes only.
+ * order that depends only on the sizes, the row strides and on whether there
+ * is a workspace.
  *
  *   batch        as in gemm_f32_strided_batched (strides of A and B >= 0, 0
  *                reuses one matrix; C's products must not overlap)

@@ -226,3 +226,25 @@ def test_plain_requantizes_to_itself():
     v = ref.values(c, s, 64)
     c2, s2 = ref.quantize(v.astype(np.float32))
     assert np.array_equal(ref.values(c2, s2, 64), v) and np.array_equal(s2[:, :2], s[:, :2])
+
+
+def test_sizes_just_above_the_limit(lib):
+    """Sizes whose last tile would end past what 32 bits count."""
+    n, one = (1 << 31) - 1023, matrix(ldq=1 << 31, lds=1 << 31)
+    calls = [
+        lambda: b.gemm_mxfp4_product(1, 1, 1, n, one, one, 0x500000, 1, 0),
+        lambda: b.gemm_mxfp4_product(1, 1, n, 32, one, one, 0x500000, n, 0),
+        lambda: b.gemm_mxfp4_product(1, n, 1, 32, one, one, 0x500000, 1, 0),
+        lambda: b.gemm_mxfp4_product(n, 1, 1, 32, one, one, 0x500000, 1, 1),
+        lambda: b.gemm_mxfp4_weight_product(b.OP_T, 1, 1, 1, n, 0x600000, n, 0, one, 0x500000, 1, 0),
+        lambda: b.gemm_mxfp4_weight_product(b.OP_N, 1, 1, n, 1, 0x600000, 1, 0, one, 0x500000, n, 0),
+        lambda: b.gemm_mxfp4_quantize(1, 1, n, 0x600000, n, 0, one, None),
+        lambda: b.gemm_mxfp4_quantize(1, n, 1, 0x600000, 1, 0, None, one),
+        lambda: b.gemm_mxfp4_dequantize(1, 1, n, one, 0x600000, n, 0),
+    ]
+    for call in calls:
+        assert call() == b.GEMM_F32_EINVAL
+        assert "above 2^31-1024" in b.gemm_f32_last_error(), b.gemm_f32_last_error()
+    for sizes in ((1, 1, 1, n), (1, n, 1, 1), (n, 1, 1, 1)):
+        assert b.gemm_mxfp4_workspace_size(*sizes) == 0
+        assert b.gemm_mxfp4_weight_workspace_size(b.OP_T, *sizes) == 0

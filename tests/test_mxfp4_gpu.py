@@ -758,3 +758,24 @@ def test_large_batch():
                           (b.gemm_mxfp4_weight(x, W3), x.double(), 3)):
         over = (got.double() - p @ w64).abs() - (parts * 600 / 16 + 8) * ULP * (p.abs() @ w64.abs())
         assert float(over.max()) <= 0
+
+
+def test_longest_rows():
+    """The longest row there may be: 2^31 - 1024 values."""
+    import torch
+
+    K = (1 << 31) - 1024
+    x = torch.zeros(3, K, device="cuda:0")
+    for i in range(3):
+        for v, k in ((1.0, 0), (2.0, K // 2 + 5 * i), (4.0, K - 1 - i)):
+            x[i, k] = v
+    ones = b.mxfp4_empty((2, K))
+    ones.codes.fill_(0x22)
+    ones.scales.fill_(127)
+    want = torch.full((3, 2), 7.0, device="cuda:0")
+    for M in (1, 2, 3):  # sums of powers of two and zeros: exact in any order
+        assert torch.equal(b.gemm_mxfp4_weight(x[:M], ones), want[:M])
+    q = b.mxfp4_quantize(x[2:])
+    assert torch.equal(b.gemm_mxfp4(q, ones), want[:1])
+    assert torch.equal(b.mxfp4_dequantize(q), x[2:])
+    torch.cuda.empty_cache()
