@@ -755,9 +755,9 @@ hipError_t launch_stored(const Product &p, hipStream_t stream) {
 //    64 x 128  three a CU   0.45 / 0.69 lone   1.07 / 1.27 full
 //
 // 4096 x 4096 x 14336 takes the first (982 us, against 1109 and 1272), 512 x
-// 4096 x 4096 the last (70 us unsliced, against 90 and 128) or the second in
-// 2 slices (58), 37 x 14336 x 4096 the second in 4 (30 us, against 82
-// unsliced).
+// 4096 x 4096 the second in 4 slices (55 us, against 61 in 2, 87 unsliced and
+// 70 with the last unsliced), 37 x 14336 x 4096 the second in 8 (34 us, the
+// same in 4, against 82 unsliced).
 struct Choice {
     int tile;  // 0, 1, 2 as above
     int splits;
