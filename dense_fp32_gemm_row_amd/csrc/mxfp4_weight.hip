@@ -746,9 +746,45 @@ hipError_t launch_stored(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Which tile a product takes, and how many slices of K: the least predicted
-// time, from microseconds per 32 k measured on MI355X for a lone tile and for
-// a full chip (W transposed / as stored), after 4.5 that every launch takes:
+// W read straight into registers, 16 rows of A at a time: columns of a
+// workgroup (16 nt) and slices of K, by the least predicted time.  A step of a
+// workgroup's wavefronts (128 k with W transposed, 32 k as stored) takes, in
+// microseconds measured on MI355X with up to 256 workgroups, for r rows of A:
+//
+//   16 columns 0.8 + 0.075 r   32 1.5 + 0.075 r   64 2.3 + 0.075 r   as stored, 128: 1.6
+//
+// and with more of them a fifth above their share of that.
+// So 16 rows x 14336 x 4096 takes 64 columns (19.7 us, against 26 with 32 and
+// 40 with 16), 4 rows x 4096 x 4096 16 (8.9, against 10.3 and 14.2), 16 rows x
+// 4096 x 14336 64 in 4 slices (21, against 37 with 16 unsliced), 16 x 512 x
+// 8192 16 in 8 (9.9, against 20.6); as stored 16 x 4096 x 4096 takes 8 slices
+// (8.6 and 3 for their sum, against 26.8 unsliced).
+struct Direct {
+    int nt, splits;
+    double us;
+};
+Direct direct(bool bt, double batch, double M, double N, int64_t K, bool slices) {
+    const int64_t steps = bt ? (blocks_of(K) + 3) / 4 : blocks_of(K);
+    const double rows = std::ceil(M / 16) * batch, r = std::min(M, 16.0);
+    Direct best{0, 1, 0};
+    for (int nt = bt ? 4 : 8; nt >= (bt ? 1 : 8); nt /= 2) {
+        const double tiles = rows * std::ceil(N / (16 * nt));
+        const double step = !bt ? 1.6 : (nt == 4 ? 2.3 : nt == 2 ? 1.5 : 0.8) + 0.075 * r;
+        for (int want = 1; want == 1 || (slices && want <= 256 && want * 8 <= steps + 7); want *= 2) {
+            const int s = slices_used(steps, want);
+            const double n = static_cast<double>((steps + int64_t{8} * s - 1) / (int64_t{8} * s));
+            double us = 4.5 + n * step * (tiles * s > 256 ? 1.2 * tiles * s / 256 : 1.0);
+            if (s > 1) us += sum_slices_us(batch, M, N, s);
+            if (best.nt == 0 || us < best.us) best = {nt, s, us};
+        }
+    }
+    return best;
+}
+
+// Which kernel a product takes, and how many slices of K: the least predicted
+// time, for tiles from microseconds per 32 k measured on MI355X for a lone
+// tile and for a full chip (W transposed / as stored), after 4.5 that every
+// launch takes:
 //
 //   128 x 256  two a CU     0.95 / 1.24 lone   2.19 / 2.31 full
 //    64 x 256  two a CU     0.58 / 0.82 lone   1.24 / 1.34 full
@@ -757,10 +793,14 @@ hipError_t launch_stored(const Product &p, hipStream_t stream) {
 // 4096 x 4096 x 14336 takes the first (982 us, against 1109 and 1272), 512 x
 // 4096 x 4096 the second in 4 slices (55 us, against 61 in 2, 87 unsliced and
 // 70 with the last unsliced), 37 x 14336 x 4096 the second in 8 (34 us, the
-// same in 4, against 82 unsliced).
+// same in 4, against 82 unsliced).  Up to 16 rows W is always read straight
+// into registers, and beyond where that is quicker: 32 x 4096 x 4096 (14.3 us
+// against 17.4 with tiles, as stored 15.4 against 21.8) and 48 x 1000 x 2000
+// (7.0 against 12.0), but not 48 x 14336 x 4096 (48 against 34).
+constexpr int kDirect = -1;
 struct Choice {
-    int tile;  // 0, 1, 2 as above
-    int splits;
+    int tile;  // 0, 1, 2 as above, or kDirect
+    int splits, nt;
 };
 Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
     struct Candidate {
@@ -770,103 +810,57 @@ Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_
     static constexpr Candidate kTiles[] = {{128, 256, 512, {1.24, 0.95}, {2.31, 2.19}},
                                            {64, 256, 512, {0.82, 0.58}, {1.34, 1.24}},
                                            {64, 128, 768, {0.69, 0.45}, {1.27, 1.07}}};
+    if (bt && M <= 2) return {kDirect, 1, 0};  // a kernel of their own
+    const double db = static_cast<double>(batch), dm = static_cast<double>(M), dn = static_cast<double>(N);
+    const Direct d = direct(bt, db, dm, dn, K, most_splits > 1);
+    Choice best{kDirect, d.splits, d.nt};
+    if (M <= 16) return best;
+    double t = d.us;
     const int64_t chunks = (blocks_of(K) + 3) / 4;
-    Choice best{2, 1};
-    double t = 0;
     for (int want = 1; want <= most_splits && (want == 1 || want * 2 <= chunks); want *= 2) {
         const int s = slices_used(chunks, want);
         const double len = 4.0 * static_cast<double>((chunks + s - 1) / s);
         for (int i = 0; i < 3; ++i) {
             const Candidate &c = kTiles[i];
-            const double tiles = static_cast<double>((M + c.bm - 1) / c.bm) *
-                                 static_cast<double>((N + c.bn - 1) / c.bn) * static_cast<double>(batch) * s;
+            const double tiles = std::ceil(dm / c.bm) * std::ceil(dn / c.bn) * db * s;
             const double full = std::floor(tiles / c.slots), rem = tiles / c.slots - full;
             double u = 4.5 + full * len * c.full[bt] +
                        (rem > 0 ? len * (c.lone[bt] + (c.full[bt] - c.lone[bt]) * rem * std::sqrt(rem)) : 0.0);
-            u += sum_slices_us(static_cast<double>(batch), static_cast<double>(M), static_cast<double>(N), s);
-            if (t == 0 || u < t) t = u, best = {i, s};
+            if (s > 1) u += sum_slices_us(db, dm, dn, s);
+            if (u < t) t = u, best = {i, s, 0};
         }
     }
     return best;
 }
 
-// Rows of A up to which W is read straight into registers, without tiles.
-constexpr int kFewRows = 16;
-
-// Slices of K for these, W as stored: workgroups for most CUs, and a step of
-// 32 k at least for every wavefront (16 rows x 4096 x 4096: 8 slices 8.6 us,
-// 4 11.0, none 26.8; 16 x 14336 x 4096: 2 slices 18.3 us, 4 the same).
-int stored_splits(int64_t batch, int64_t M, int64_t N, int64_t K) {
-    const double tiles = static_cast<double>((M + 15) / 16) * static_cast<double>((N + 127) / 128) *
-                         static_cast<double>(batch);
-    const int64_t steps = blocks_of(K);
-    int s = 1;
-    while (tiles * s < 200 && steps >= 8 * s) s *= 2;
-    return slices_used(steps, s);
-}
-
-// Columns of a workgroup (16 nt) and slices of K for these, W transposed.
-// Wide tiles share the splitting of A but leave CUs without one: 16 rows x
-// 14336 x 4096 takes 64 columns (19.7 us, against 26 with 32 and 40 with 16),
-// 16 rows x 4096 x 4096 16 (12.5, against 14 and 18).  From 8192 k slices are
-// worth adding their sums: 16 rows x 4096 x 14336 takes 64 columns in 4 slices
-// (21 us, against 37 with 16 columns unsliced), 16 x 512 x 8192 16 columns in 8
-// (9.9, against 20.6); 4 rows x 4096 x 4096 would lose by it (9.7, against 8.9).
-struct FewRows {
-    int nt, splits;
-};
-FewRows few_rows(int64_t batch, int64_t M, int64_t N, int64_t K, bool slices) {
-    constexpr double kEnough = 200;  // workgroups
-    auto tiles = [&](int nt) {
-        return static_cast<double>((M + 15) / 16) * static_cast<double>((N + 16 * nt - 1) / (16 * nt)) *
-               static_cast<double>(batch);
-    };
-    const int64_t steps = (blocks_of(K) + 3) / 4;
-    for (int nt = 4; nt >= 1; nt /= 2) {
-        int s = 1;
-        if (slices && steps >= 64)
-            while (tiles(nt) * s < kEnough && 16 * s <= steps) s *= 2;  // a step at least for every wavefront
-        if (nt == 1 || tiles(nt) * s >= kEnough) return {nt, slices_used(steps, s)};
-    }
-    return {1, 1};
-}
-
 }  // namespace
 
 int weight_splits(bool b_transposed, int64_t batch, int64_t M, int64_t N, int64_t K) {
-    if (M > kFewRows) return choose(b_transposed, batch, M, N, K, 64).splits;
-    if (!b_transposed) return stored_splits(batch, M, N, K);
-    return M <= 2 ? 1 : few_rows(batch, M, N, K, true).splits;
+    return choose(b_transposed, batch, M, N, K, 64).splits;
 }
 
 hipError_t launch_weight(const Product &asked, hipStream_t stream) {
     Product p = asked;
+    Choice c = choose(p.b_transposed, p.batch, p.M, p.N, p.K, p.splits > 1 ? 64 : 1);
     const double tiles = static_cast<double>((p.M + 63) / 64) * ((p.N + 127) / 128) * static_cast<double>(p.batch);
-    const bool few = p.M <= kFewRows;
-    const bool far = !reaches(p, 128, 256) || tiles > 1e6;  // (a launch has at most 2^32 lanes)
-    const bool slices = p.splits > 1 && (few || !far);
-    p.splits = 1;
+    if (c.tile != kDirect && (!reaches(p, 128, 256) || tiles > 1e6))  // (a launch has at most 2^32 lanes)
+        c = {kDirect, 1, p.b_transposed ? 4 : 8};
+    p.splits = c.splits;
     hipError_t err;
-    if (p.b_transposed && p.M <= 2) {
+    if (c.tile == kDirect && !p.b_transposed)
+        err = launch_stored(p, stream);
+    else if (c.tile == kDirect && p.M <= 2)
         // One and two rows of A cost the vector units less than splitting 16:
         // a row x 14336 x 4096 8.0 us, against 13.7.
-        return p.M == 1 ? launch_vector<1>(p, stream) : launch_vector<2>(p, stream);
-    } else if (p.b_transposed && (few || far)) {
-        const FewRows c = few_rows(p.batch, p.M, p.N, p.K, slices);
-        p.splits = c.splits;
+        err = p.M == 1 ? launch_vector<1>(p, stream) : launch_vector<2>(p, stream);
+    else if (c.tile == kDirect)
         err = c.nt == 4   ? launch_rows<4>(p, stream)
               : c.nt == 2 ? launch_rows<2>(p, stream)
                           : launch_rows<1>(p, stream);
-    } else if (few || far) {
-        if (slices) p.splits = stored_splits(p.batch, p.M, p.N, p.K);
-        err = launch_stored(p, stream);
-    } else {
-        const Choice c = choose(p.b_transposed, p.batch, p.M, p.N, p.K, slices ? 64 : 1);
-        p.splits = c.splits;
+    else
         err = c.tile == 0   ? launch_tile<2, 4, 2>(p, stream)
               : c.tile == 1 ? launch_tile<1, 4, 2>(p, stream)
                             : launch_tile<1, 2, 3>(p, stream);
-    }
     if (err == hipSuccess && p.splits > 1) err = launch_sum_slices(p, stream);
     return err;
 }

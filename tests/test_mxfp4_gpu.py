@@ -723,7 +723,8 @@ def random_on_gpu(rows, cols, seed):
 
 
 LARGE = [(4133, 4161, 1000), (4096, 4096, 2048), (8200, 2900, 515), (1100, 1024, 40000), (700, 9000, 1568),
-         (2048, 2048, 512)]
+         (2048, 2048, 512), (300, 2050, 1030), (200, 4000, 1029), (511, 1023, 2077), (100, 8193, 1500),
+         (260, 520, 9000), (65, 14000, 1100)]
 
 
 @pytest.mark.parametrize("shape", LARGE)
