@@ -442,7 +442,7 @@ class Mxfp4:
     in the layout of include/gemm_mxfp4.h, and the number of columns.  It
     holds the tensors; their memory is not copied."""
 
-    __slots__ = ("codes", "scales", "cols", "shape", "_c")
+    __slots__ = ("cols", "shape", "device", "_codes", "_scales", "_memory", "_c")
 
     def __init__(self, codes, scales, cols: int):
         load()
@@ -464,7 +464,8 @@ class Mxfp4:
         ct, st = codes.stride(), scales.stride()
         if (cb > 1 and ct[-1] != 1) or (sb > 1 and st[-1] != 1):
             raise ValueError("codes and scales must have unit stride along the last axis")
-        self.codes, self.scales, self.cols = codes, scales, cols
+        self._codes, self._scales, self._memory = codes, scales, None
+        self.cols, self.device = cols, codes.device
         #: (rows, columns) or (batch, rows, columns)
         self.shape = (*lead, cols)
         many, batched = lead[-1] > 1, len(lead) == 2 and lead[0] > 1
@@ -474,21 +475,38 @@ class Mxfp4:
                               st[0] if batched else 0)
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        if self._codes is None:
+            self._split()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._split()
+        return self._scales
+
+    def _split(self) -> None:
+        """The tensors of an mxfp4_empty: its memory is one, codes first."""
+        *lead, rows, _ = self.shape
+        codes, words = self._c.ld_codes, self._c.ld_scales
+        n = (lead[0] if lead else 1) * rows * codes
+        self._codes = self._memory[:n].view(*lead, rows, codes)
+        self._scales = self._memory[n:].view(*lead, rows, words)
 
     def __repr__(self) -> str:
         return f"Mxfp4(shape={self.shape}, device={self.device})"
 
 
-def _empty(shape, dtype, device, stream):
-    """torch.empty for memory that work on ``stream`` (None: the current one)
-    will use: taken from that stream's pool, so that nothing else still uses
-    it, and nothing else gets it before that work is done."""
+def _empty(shape, strides, dtype, device, stream):
+    """torch.empty (the quicker call) for memory that work on ``stream``
+    (None: the current one) will use: taken from that stream's pool, so that
+    nothing else still uses it, and nothing else gets it before that work is
+    done."""
     if stream is None:
-        return _torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty_strided(shape, strides, dtype=dtype, device=device)
     with _torch.cuda.stream(stream):
-        return _torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def mxfp4_empty(shape, device="cuda", *, stream=None) -> Mxfp4:
@@ -497,13 +515,14 @@ def mxfp4_empty(shape, device="cuda", *, stream=None) -> Mxfp4:
     *lead, cols = shape
     nb = (cols + MXFP4_BLOCK - 1) // MXFP4_BLOCK
     words = (nb + 3) // 4 * 4
-    codes = _empty((*lead, nb * 16), _torch.uint8, device, stream)
-    scales = _empty((*lead, words), _torch.uint8, device, stream)
-    q = Mxfp4.__new__(Mxfp4)  # nothing to check
-    q.codes, q.scales, q.cols, q.shape = codes, scales, cols, (*lead, cols)
     rows = lead[-1]
-    q._c = Mxfp4Matrix(codes.data_ptr(), nb * 16, rows * nb * 16, scales.data_ptr(), words,
-                       rows * words)
+    lines = rows if len(lead) == 1 else lead[0] * rows
+    memory = _empty((lines * (nb * 16 + words),), (1,), _torch.uint8, device, stream)
+    q = Mxfp4.__new__(Mxfp4)  # nothing to check
+    q._codes, q._scales, q._memory = None, None, memory
+    q.cols, q.shape, q.device = cols, (*lead, cols), memory.device
+    at = memory.data_ptr()
+    q._c = Mxfp4Matrix(at, nb * 16, rows * nb * 16, at + lines * nb * 16, words, rows * words)
     return q
 
 
@@ -580,7 +599,7 @@ def mxfp4_quantize_both(X, out: Mxfp4 | None = None, out_t: Mxfp4 | None = None,
 def mxfp4_dequantize(q: Mxfp4, out=None, *, stream=None):
     """The float32 values of ``q``."""
     shape = q.shape
-    device = q.codes.device
+    device = q.device
     out, ld, bs, *_ = _mxfp4_out(out, shape, device, None, 0, stream)
     batch = shape[0] if len(shape) == 3 else 1
     _run_on(device, stream, load().gemm_mxfp4_dequantize, batch, shape[-2], shape[-1],
@@ -591,9 +610,9 @@ def mxfp4_dequantize(q: Mxfp4, out=None, *, stream=None):
 def _mxfp4_out(out, shape, device, workspace, need: int, stream):
     """(out, its leading dimension and batch stride, workspace pointer and bytes)."""
     if out is None:
-        out = _empty(shape, _torch.float32, device, stream)
         ld = shape[-1] or 1
         bs = shape[-2] * ld
+        out = _empty(shape, (ld, 1) if len(shape) == 2 else (bs, ld, 1), _torch.float32, device, stream)
     else:
         if tuple(out.shape) != shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
@@ -605,7 +624,7 @@ def _mxfp4_out(out, shape, device, workspace, need: int, stream):
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
         return out, ld, bs, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need:
-        workspace = _empty(need // 4, _torch.float32, device, stream)
+        workspace = _empty((need // 4,), (1,), _torch.float32, device, stream)
         return out, ld, bs, workspace, workspace.data_ptr(), need
     return out, ld, bs, None, None, 0
 
@@ -619,9 +638,9 @@ def gemm_mxfp4(A: Mxfp4, B: Mxfp4, out=None, workspace=None, *, stream=None):
     sa, sb = A.shape, B.shape
     if len(sa) != len(sb) or sa[:-2] != sb[:-2] or sa[-1] != sb[-1]:
         raise ValueError(f"shape mismatch {sa} x {sb} transposed")
-    device = A.codes.device
-    if B.codes.device != device:
-        raise ValueError(f"A on {device}, B on {B.codes.device}")
+    device = A.device
+    if B.device != device:
+        raise ValueError(f"A on {device}, B on {B.device}")
     batch = sa[0] if len(sa) == 3 else 1
     M, N, K = sa[-2], sb[-2], sa[-1]
     lib = load()
@@ -641,18 +660,20 @@ def gemm_mxfp4_weight(A, W: Mxfp4, out=None, workspace=None, *, op: int = OP_T, 
     and ``stream`` as in gemm_mxfp4."""
     if op not in (OP_N, OP_T):
         raise ValueError("op must be OP_N or OP_T")
-    opa, lda, sa, batch = _float_operand(A, "A", W.codes.device)
+    device = W.device
+    opa, lda, sa, batch = _float_operand(A, "A", device)
     if opa != OP_N:
         raise ValueError("A must be row-major")
-    M, K = A.shape[-2], A.shape[-1]
-    sw = W.shape
-    N, K2 = (sw[-2], sw[-1]) if op == OP_T else (sw[-1], sw[-2])
-    if K != K2 or A.dim() != len(sw) or tuple(A.shape[:-2]) != tuple(sw[:-2]):
-        raise ValueError(f"shape mismatch {tuple(A.shape)} x {sw}{' transposed' if op == OP_T else ''}")
+    *lead, M, K = A.shape
+    *lead_w, N, K2 = W.shape
+    if op == OP_N:
+        N, K2 = K2, N
+    if K != K2 or lead != lead_w:
+        raise ValueError(f"shape mismatch {tuple(A.shape)} x {W.shape}{' transposed' if op == OP_T else ''}")
     lib = load()
     out, ldc, sc, workspace, wp, wb = _mxfp4_out(
-        out, (*A.shape[:-1], N), A.device, workspace,
+        out, (*lead, M, N), device, workspace,
         lib.gemm_mxfp4_weight_workspace_size(op, batch, M, N, K), stream)
-    _run_on(A.device, stream, lib.gemm_mxfp4_weight, op, batch, M, N, K, A.data_ptr(), lda, sa,
+    _run_on(device, stream, lib.gemm_mxfp4_weight, op, batch, M, N, K, A.data_ptr(), lda, sa,
             ctypes.byref(W._c), out.data_ptr(), ldc, sc, wp, wb)
     return out

@@ -780,3 +780,24 @@ def test_longest_rows():
     assert torch.equal(b.gemm_mxfp4(q, ones), want[:1])
     assert torch.equal(b.mxfp4_dequantize(q), x[2:])
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("shape", [(3, 100), (2, 3, 100), (1, 1), (0, 64), (3, 0), (0, 2, 40), (2, 0, 40), (2, 5, 0)])
+def test_tensors_of_an_empty(shape):
+    """codes and scales of an mxfp4_empty are its memory, also when asked for
+    after a call has filled it."""
+    import torch
+
+    *lead, cols = shape
+    nb = -(-cols // 32)
+    x = torch.randn(shape, device="cuda:0")
+    q = b.mxfp4_quantize(x)
+    assert q.device == x.device and q.shape == shape
+    assert q.codes.shape == (*lead, nb * 16) and q.scales.shape == (*lead, -(-nb // 4) * 4)
+    again = b.Mxfp4(q.codes, q.scales, cols)
+    assert torch.equal(b.mxfp4_dequantize(again), b.mxfp4_dequantize(q))
+    e = b.mxfp4_empty(shape)
+    e.codes.copy_(q.codes)
+    e.scales.copy_(q.scales)
+    assert torch.equal(b.mxfp4_dequantize(e), b.mxfp4_dequantize(q))
+    assert e.codes.data_ptr() % 16 == 0 and e.scales.data_ptr() % 4 == 0
