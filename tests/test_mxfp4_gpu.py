@@ -469,6 +469,27 @@ def test_far_rows():
 
 
 @pytest.mark.parametrize("op", ["T", "N"])
+def test_tile_sized_products_of_far_rows(op):
+    """Rows of W too far apart for a tile's 32-bit offsets, in a product that tiles would take."""
+    import torch
+
+    rng = np.random.default_rng(17)
+    M, N, K = 3000, 300, 2000
+    rows, cols = (N, K) if op == "T" else (K, N)
+    ld = ((1 << 31) // (256 if op == "T" else K) + 4095) // 16 * 16
+    w = ref.random_matrix(rng, (rows,), cols)
+    far = torch.empty(rows * ld, dtype=torch.uint8, device="cuda:0")
+    codes = far.as_strided((rows, w[0].shape[1]), (ld, 1))
+    scales = far.as_strided((rows, w[1].shape[1]), (ld, 1), 2048)
+    codes.copy_(to_dev(w[0]))
+    scales.copy_(to_dev(w[1]))
+    w64 = ref.values(*w, cols)
+    x = wide_floats(rng, M, K)
+    got = b.gemm_mxfp4_weight(to_dev(x), b.Mxfp4(codes, scales, cols), op=b.OP_T if op == "T" else b.OP_N)
+    check_product(to_host(got), x.astype(np.float64), w64 if op == "T" else w64.T, K, 3)
+
+
+@pytest.mark.parametrize("op", ["T", "N"])
 def test_one_row_at_the_longest_stride(op):
     """A lone row's stride is never stepped over, however long it is."""
     import torch
