@@ -25,9 +25,9 @@ __device__ __forceinline__ f32x16 mfma_fp4(u32x4 x, u32x4 y, f32x16 acc, uint32_
 template <int FM, int FN, int WM, int WN>
 struct Tile {
     static constexpr int BM = FM * WM * 32, BN = FN * WN * 32, R = BM + BN, NW = WM * WN;
-    static constexpr int kStages = 4, kStageBlocks = 4, kRowBytes = kStageBlocks * kBlockBytes;
+    static constexpr int kStages = 4, kStageBlocks = 4, kRowBytes = 2 * kStageBlocks * kBlockBytes;
     static constexpr int kGroupBlocks = kStages * kStageBlocks;
-    static constexpr int kLoads = R / 16 / NW;                   // a wavefront's code loads per stage
+    static constexpr int kLoads = R / 8 / NW;                    // a wavefront's code loads per two stages
     static constexpr int kScaleLoads = (R / 64 + NW - 1) / NW;   // ... scale loads per group
     static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0, "");
 };
@@ -41,36 +41,36 @@ struct Tile {
 // blocks 0 and 1, lanes 32-63 blocks 2 and 3, so a lane's scales are one half
 // of the row's scale word.
 //
-// LDS holds a stage's rows as 4 slots of 16 bytes, filled by direct loads
-// (64 lanes x 16 bytes into 1 KiB: 16 rows).  Block b of row r sits in slot
-// b ^ (r / 4 % 4): 16 lanes that read one block of 16 rows then touch every
-// bank once.
+// LDS holds two stages of a row as 8 slots of 16 bytes, filled by direct
+// loads (64 lanes x 16 bytes into 1 KiB: 8 rows).  That is a line of the
+// caches: loaded a stage at a time, half a line each, L2 had twice the
+// requests, three quarters of what its channels answer (1024 x 1024 x 65536:
+// 60 us so, 48 with whole lines; 4096^3: 49 and 46).  Block b of row r sits in
+// slot b ^ (r / 2 % 8): 16 lanes that read one block of 16 rows then touch
+// every bank once.
 //
 // Order within a stage: the fragments of its second half are read under the
-// products of its first; then a barrier, after which the next stage is in
-// LDS and this one's buffer is free; then the loads one group on and the
-// next stage's first fragments go out under the products of the second half.
-// So neither the barrier nor an LDS read is waited for with idle matrix
-// cores.
+// products of its first.  In every second stage a barrier follows, after
+// which the next two stages are in LDS and these ones' buffer is free, and
+// the loads one group on go out under the products of the second half, as in
+// every stage the next one's first fragments.  So neither the barrier nor an
+// LDS read is waited for with idle matrix cores.
 // A CU holds PER_CU workgroups, which gives every SIMD two wavefronts: with
 // one (4 x 4 blocks each) it idles wherever that one waits, and 8192 x 14336 x
-// 4096 took 293 us instead of 276.
+// 4096 took 293 us instead of 276 (with half lines).
 //
-// 276 us are 3.5 PFLOP/s.  A loop of nothing but these instructions on random
+// 8192 x 14336 x 4096 reaches 3.5 PFLOP/s.  A loop of nothing but these instructions on random
 // codes reaches 5.5, where the card's power holds its clock; of the rest,
-// storing C is little (4096 x 14336 x 8192, half the results, takes 280 us, and
-// workgroups that start at different times, so that some store while others
-// multiply, gain 3%).
+// storing C is little: half the results of as many products (4096 x 14336 x
+// 8192) take as long, and workgroups that start at different times, so that
+// some store while others multiply, gain 3%.
 template <int FM, int FN, int WM, int WN, int PER_CU, bool WHOLE>
 __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_kernel(Product p, int tiles_m,
                                                                         int tiles_n, int64_t tiles,
                                                                         int groups, int len) {
     using T = Tile<FM, FN, WM, WN>;
-    constexpr int kStageBytes = T::R * T::kRowBytes;
-    __shared__ __align__(1024) uint8_t codes0[kStageBytes];
-    __shared__ __align__(1024) uint8_t codes1[kStageBytes];
-    __shared__ __align__(1024) uint8_t codes2[kStageBytes];
-    __shared__ __align__(1024) uint8_t codes3[kStageBytes];
+    __shared__ __align__(1024) uint8_t codes0[T::R * T::kRowBytes];  // stages 0 and 1 of a group
+    __shared__ __align__(1024) uint8_t codes1[T::R * T::kRowBytes];  // 2 and 3
     __shared__ __align__(1024) uint32_t scales[2 * T::kStages * T::R];  // [group parity][stage][row]
 
     const int lane = threadIdx.x & 63, half = lane >> 5, row = lane & 31;
@@ -107,16 +107,16 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
             seek(c, scale);
         }
     };
-    const int lrow = wave * 16 + (lane >> 2);                // row of a lane's first load
-    const int blk = (lane & 3) ^ ((lane >> 4) & 3);          // block of its slot
-    auto load = [&](const Cursor &c, int stage, uint8_t *codes) {
-        const int block = c.g * T::kGroupBlocks + stage * T::kStageBlocks + blk;
+    const int lrow = wave * 8 + (lane >> 3);                 // row of a lane's first load
+    const int blk = (lane & 7) ^ ((lrow >> 1) & 7);          // block of its slot
+    auto load = [&](const Cursor &c, int pair, uint8_t *codes) {
+        const int block = c.g * T::kGroupBlocks + pair * 2 * T::kStageBlocks + blk;
         const int off = c.g < c.g1 ? min(block, nb - 1) * kBlockBytes : kOutside;
 #pragma unroll
         for (int j = 0; j < T::kLoads; ++j) {
-            const bool in_a = j * T::NW * 16 < T::BM;
+            const bool in_a = j * T::NW * 8 < T::BM;
             const Rows &m = in_a ? c.a : c.b;
-            const int r = j * T::NW * 16 - (in_a ? 0 : T::BM);
+            const int r = j * T::NW * 8 - (in_a ? 0 : T::BM);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(m.rsrc, (lptr_t)(codes + (j * T::NW + wave) * 1024),
                                                      16, (lrow + r) * m.ld + off, 0, 0, 0);
         }
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
     int oa[2], ob[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int slot = ((2 * half + t) ^ ((row >> 2) & 3)) * kBlockBytes;
+        const int slot = ((2 * half + t) ^ ((row >> 1) & 7)) * kBlockBytes;
         oa[t] = ra * T::kRowBytes + slot;
         ob[t] = rb * T::kRowBytes + slot;
         asm volatile("" : "+v"(oa[t]), "+v"(ob[t]));
@@ -187,6 +187,8 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             y[t][j] = *reinterpret_cast<const u32x4 *>(codes + ob[t] + 32 * j * T::kRowBytes);
+        oa[t] ^= 4 * kBlockBytes, ob[t] ^= 4 * kBlockBytes;  // the other stage's
+        asm volatile("" : "+v"(oa[t]), "+v"(ob[t]));
     };
     auto read_scales = [&](auto uc, int stage) {
         constexpr int u = decltype(uc)::value;
@@ -228,7 +230,10 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
                 __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
             else if (k < reads)
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            if (k < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            if (loads > FM * FN && 2 * k < loads)
+                __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+            else if (k < loads)
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
         // The sums so far are used here, so their instructions stay ahead.
 #pragma unroll
@@ -277,8 +282,6 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
     fetch_scales(cs);
     load(cc, 0, codes0);
     load(cc, 1, codes1);
-    load(cc, 2, codes2);
-    load(cc, 3, codes3);
     store_scales(cs.g);
     advance(cs, true);
     fetch_scales(cs);
@@ -292,33 +295,36 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
 
     constexpr int L = T::kLoads, S = T::kScaleLoads * (WHOLE ? 1 : 4);
     // Stage `i` of the group: products from `cur`, the next stage in `nxt`.
-    // The wait counts on the order of loads: those of a stage (L) follow its
-    // barrier, the scales (S) lie between the first two, each behind a
-    // scheduling barrier of its own, since the scheduler may turn loads of one
-    // region around.  What stage i + 1 needs was loaded a group ago: two
-    // stages' loads are younger, and past the first barrier the scales'.
+    // The waits count on the order of loads: the scales (S) go out in stage 1
+    // ahead of its barrier, the codes of two stages (L) behind those of stages
+    // 1 and 3, each behind a scheduling barrier of its own, since the scheduler
+    // may turn loads of one region around.  What follows stage 1 was loaded in
+    // the last group's stage 3, and the scales alone are younger; what follows
+    // stage 3 in this group's stage 1, and nothing is.
 #define GEMM_MXFP4_STAGE(i, cur, nxt, u, v)                                          \
     fetch(c1, cur);                                                                  \
     read_scales(v, (i + 1) % 4);                                                     \
     if (i == 1) fetch_scales(cs);                                                    \
     multiply(c0, u);                                                                 \
     interleave(i == 1 ? S : 0, 2 * (FM + FN));                                       \
-    wait_older<2 * L + (i > 0 ? S : 0)>();                                           \
-    barrier_only();                                                                  \
-    if (i == 3) store_scales(cs.g);                                                  \
-    load(cc, i, cur);                                                                \
+    if (i & 1) {                                                                     \
+        wait_older<i == 1 ? S : 0>();                                                \
+        barrier_only();                                                              \
+        if (i == 3) store_scales(cs.g);                                              \
+        load(cc, i / 2, cur);                                                        \
+    }                                                                                \
     fetch(c0, nxt);                                                                  \
     multiply(c1, u);                                                                 \
-    interleave(L, FM + FN);
+    interleave(i & 1 ? L : 0, FM + FN);
 
     for (; id < tiles; id += grid) {
         const Place at = place_of<T::BM, T::BN>(p, id, tiles_m, tiles_n, groups, len);
         clear();
         for (int g = at.g0; g < at.g1; ++g) {
-            GEMM_MXFP4_STAGE(0, codes0, codes1, c0, c1)
-            GEMM_MXFP4_STAGE(1, codes1, codes2, c1, c0)
-            GEMM_MXFP4_STAGE(2, codes2, codes3, c0, c1)
-            GEMM_MXFP4_STAGE(3, codes3, codes0, c1, c0)
+            GEMM_MXFP4_STAGE(0, codes0, codes0, c0, c1)
+            GEMM_MXFP4_STAGE(1, codes0, codes1, c1, c0)
+            GEMM_MXFP4_STAGE(2, codes1, codes1, c0, c1)
+            GEMM_MXFP4_STAGE(3, codes1, codes0, c1, c0)
             advance(cc, false);
             advance(cs, true);
         }
@@ -446,16 +452,15 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t tota
 // microseconds measured on MI355X, per 512 k of a tile and per store of one
 // with the chip full, and for lone tiles:
 //
-//   256 x 256  5 + rounds (3.65 / 512 k + 10.8), one tile a CU; a lone tile
+//   256 x 256  5 + rounds (3.5 / 512 k + 10.8), one tile a CU; a lone tile
 //              2.6 / 512 k
-//   128 x 128  4 + rounds (2.6 / 512 k + 5), two tiles a CU; a lone tile
+//   128 x 128  4 + rounds (2.35 / 512 k + 5), two tiles a CU; a lone tile
 //              1.05 / 512 k
 //   32 x 32    3 + 2.3 / 2048 k and tile of a CU
 //
-// So 8192 x 14336 x 4096 (276 us, against 367 with 128 x 128) and 64 x 1024^3
-// (72 against 76) take the large tile, 1024 x 1024 x 65536 128 x 128 with
-// sliced K (50 and 8 for the sum, against 143 unsliced and 88 with the large
-// tile), 256^3 (3.2 against 5.8), 1000 x 1023 x 777 (6.4 against 8.0) and
+// So 8192 x 14336 x 4096 (275 us, against 318 with 128 x 128) and 64 x 1024^3
+// (72 against 80) take the large tile, 1024 x 1024 x 65536 128 x 128 with
+// sliced K (48 and 8 for the sum, against 55 and 8 with the large tile), 256^3 (3.2 against 5.8), 1000 x 1023 x 777 (6.4 against 8.0) and
 // products of few rows 32 x 32.
 enum Kernel { kLarge, kMedium, kRows };
 struct Choice {
@@ -471,11 +476,11 @@ double tile_us(int64_t tiles, double groups, int slots, double fixed, double eac
 }
 double large_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits) {
     return tile_us((M + 255) / 256 * ((N + 255) / 256) * batch * splits,
-                   static_cast<double>((groups + splits - 1) / splits), 256, 5.0, 3.65, 2.6, 10.8);
+                   static_cast<double>((groups + splits - 1) / splits), 256, 5.0, 3.5, 2.6, 10.8);
 }
 double medium_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits) {
     return tile_us((M + 127) / 128 * ((N + 127) / 128) * batch * splits,
-                   static_cast<double>((groups + splits - 1) / splits), 512, 4.0, 2.6, 1.05, 5.0);
+                   static_cast<double>((groups + splits - 1) / splits), 512, 4.0, 2.35, 1.05, 5.0);
 }
 Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
     const double dm = static_cast<double>(M), dn = static_cast<double>(N), db = static_cast<double>(batch);

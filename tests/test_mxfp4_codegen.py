@@ -2,9 +2,9 @@
 gfx950 assembly without a GPU).
 
 The product tile's barriers wait until all but the newest N vector-memory
-instructions are done, and N counts on their order: a stage's code loads
-behind its barrier, the scale loads of a group behind the first stage's.  The
-compiler's scheduler may turn loads of one region around, and a scale load
+instructions are done, and N counts on their order: the scale loads of a group
+ahead of the first barrier of the loop, the code loads of two stages behind
+each.  The compiler's scheduler may turn loads of one region around, and a scale load
 ahead of a code load makes a wavefront read codes that have not landed.
 """
 
@@ -63,20 +63,21 @@ def test_product_tile_waits_count_on_its_load_order(build):
         # <FM, FN, WM, WN, workgroups a CU, WHOLE>
         fm, fn, wm, wn = (int(a) for a in arguments(name)[:4])
         rows, waves = 32 * (fm * wm + fn * wn), wm * wn
-        code = rows // 16 // waves
+        code = rows // 8 // waves  # of two stages
         scale = -(-rows // 64 // waves) * (1 if arguments(name)[5] == "true" else 4)
         lines = [ln.strip() for ln in body.splitlines()]
         bars = [i for i, ln in enumerate(lines) if ln.startswith("s_barrier")]
-        assert len(bars) == 5, f"{name}: {len(bars)} barriers"  # one ahead of the loop, four in it
-        for k in range(1, 5):
+        assert len(bars) == 3, f"{name}: {len(bars)} barriers"  # one ahead of the loop, two in it
+        for k, want in ((1, scale), (2, 0)):
             before = [ln for ln in lines[bars[k - 1]:bars[k]] if ln.startswith("s_waitcnt") and "vmcnt" in ln]
             wait = int(re.search(r"vmcnt\((\d+)\)", before[-1]).group(1))
-            assert wait == 2 * code + (scale if k > 1 else 0), f"{name}: barrier {k} waits for {wait}"
-        for k in range(1, 4):
-            loads = "".join("c" if " lds" in ln else "s" for ln in lines[bars[k]:bars[k + 1]]
-                            if ln.startswith("buffer_load"))
-            assert loads == "c" * code + ("s" * scale if k == 1 else ""), f"{name}: stage {k - 1} loads {loads}"
-            assert not any("vmcnt" in ln for ln in lines[bars[k]:bars[k + 1] - 3] if ln.startswith("s_waitcnt")), name
+            assert wait == want, f"{name}: barrier {k} waits for {wait}"
+        end = next(i for i in range(bars[2], len(lines)) if lines[i].startswith("buffer_store"))
+        for k, first, last, want in ((0, bars[0], bars[1], "s" * scale), (1, bars[1], bars[2], "c" * code),
+                                     (2, bars[2], end, "c" * code)):
+            loads = "".join("c" if " lds" in ln else "s" for ln in lines[first:last] if ln.startswith("buffer_load"))
+            assert loads == want, f"{name}: after barrier {k} loads {loads}"
+        assert not any("vmcnt" in ln for ln in lines[bars[1]:bars[2] - 3] if ln.startswith("s_waitcnt")), name
 
 
 def test_no_kernel_spills_registers(build):
