@@ -751,9 +751,9 @@ hipError_t launch_stored(const Product &p, hipStream_t stream) {
 // workgroup's wavefronts (128 k with W transposed, 32 k as stored) takes, in
 // microseconds measured on MI355X with up to 256 workgroups, for r rows of A:
 //
-//   16 columns 0.8 + 0.075 r   32 1.5 + 0.075 r   64 2.3 + 0.075 r   as stored, 128: 1.6
+//   16 columns 0.75 + 0.065 r   32 1.4 + 0.065 r   64 2.0 + 0.065 r   as stored, 128: 1.45
 //
-// and with more of them a fifth above their share of that.
+// and with more of them 1.2 times their share of that.
 // So 16 rows x 14336 x 4096 takes 64 columns (19.7 us, against 26 with 32 and
 // 40 with 16), 4 rows x 4096 x 4096 16 (8.9, against 10.3 and 14.2), 16 rows x
 // 4096 x 14336 64 in 4 slices (21, against 37 with 16 unsliced), 16 x 512 x
@@ -769,12 +769,12 @@ Direct direct(bool bt, double batch, double M, double N, int64_t K, bool slices)
     Direct best{0, 1, 0};
     for (int nt = bt ? 4 : 8; nt >= (bt ? 1 : 8); nt /= 2) {
         const double tiles = rows * std::ceil(N / (16 * nt));
-        const double step = !bt ? 1.6 : (nt == 4 ? 2.3 : nt == 2 ? 1.5 : 0.8) + 0.075 * r;
+        const double step = !bt ? 1.45 : (nt == 4 ? 2.0 : nt == 2 ? 1.4 : 0.75) + 0.065 * r;
         for (int want = 1; want == 1 || (slices && want <= 256 && want * 8 <= steps + 7); want *= 2) {
             const int s = slices_used(steps, want);
-            const double n = static_cast<double>((steps + int64_t{8} * s - 1) / (int64_t{8} * s));
-            double us = 4.5 + n * step * (tiles * s > 256 ? 1.2 * tiles * s / 256 : 1.0);
-            if (s > 1) us += sum_slices_us(batch, M, N, s);
+            const double n = static_cast<double>(steps) / (8.0 * s);
+            double us = 4.5 + step * std::max(std::ceil(n), 0.6 * (n + std::ceil(n)) * tiles * s / 256);
+            if (s > 1) us += 1.5 + sum_slices_us(batch, M, N, s);
             if (best.nt == 0 || us < best.us) best = {nt, s, us};
         }
     }
@@ -784,7 +784,7 @@ Direct direct(bool bt, double batch, double M, double N, int64_t K, bool slices)
 // Which kernel a product takes, and how many slices of K: the least predicted
 // time, for tiles from microseconds per 32 k measured on MI355X for a lone
 // tile and for a full chip (W transposed / as stored), after 4.5 that every
-// launch takes:
+// launch takes and 3 that slices lose to their unequal ends:
 //
 //   128 x 256  two a CU     0.95 / 1.24 lone   2.19 / 2.31 full
 //    64 x 256  two a CU     0.58 / 0.82 lone   1.24 / 1.34 full
@@ -826,7 +826,7 @@ Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_
             const double full = std::floor(tiles / c.slots), rem = tiles / c.slots - full;
             double u = 4.5 + full * len * c.full[bt] +
                        (rem > 0 ? len * (c.lone[bt] + (c.full[bt] - c.lone[bt]) * rem * std::sqrt(rem)) : 0.0);
-            if (s > 1) u += sum_slices_us(db, dm, dn, s);
+            if (s > 1) u += 3.0 + sum_slices_us(db, dm, dn, s);
             if (u < t) t = u, best = {i, s, 0};
         }
     }
