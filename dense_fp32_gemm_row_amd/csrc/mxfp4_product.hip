@@ -245,7 +245,10 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
     };
 
     // C is streamed past the caches, which hold A and B (64 products of 1024^3:
-    // 86 us with ordinary stores, 76 so).
+    // 86 us with ordinary stores, 76 so), if its rows are whole lines.  Else
+    // blocks share lines, which L2 has to gather, and a row's blocks are stored
+    // one after the other (8192 x 14335 x 4096: 459 us streamed, 337 with
+    // ordinary stores block by block, 282 row by row).
     auto store_tile = [&](int64_t id) {
         const Place q = place_of<T::BM, T::BN>(p, id, tiles_m, tiles_n, groups, len);
         const int64_t ldc = p.splits > 1 ? p.N : p.ldc;
@@ -255,20 +258,29 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
         const __amdgpu_buffer_rsrc_t c =
             buffer_of(base + mw * ldc + nw, ((p.M - 1 - mw) * ldc + p.N - nw) * 4);
         const int ld = static_cast<int>(ldc) * 4;
+        int at[FN];
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int n = 32 * j + row;
-            const int at = nw + n < p.N ? n * 4 + 4 * half * ld : kOutside;
+            at[j] = nw + n < p.N ? n * 4 + 4 * half * ld : kOutside;
+        }
+        auto store = [&](auto policy) {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float v = acc[i][j][r];  // (a bit cast of the element itself takes element 0)
-                    __builtin_amdgcn_raw_buffer_store_b32(
-                        __builtin_bit_cast(uint32_t, v), c,
-                        at + (32 * i + (r & 3) + 8 * (r >> 2)) * ld, 0, kStream);
-                }
-        }
+                for (int r = 0; r < 16; ++r)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) {
+                        const float v = acc[i][j][r];  // (a bit cast of the element itself takes element 0)
+                        __builtin_amdgcn_raw_buffer_store_b32(
+                            __builtin_bit_cast(uint32_t, v), c,
+                            at[j] + (32 * i + (r & 3) + 8 * (r >> 2)) * ld, 0, decltype(policy)::value);
+                    }
+        };
+        if (ldc % 32 == 0 && reinterpret_cast<uintptr_t>(base) % 128 == 0)
+            store(std::integral_constant<int, kStream>{});
+        else
+            store(std::integral_constant<int, 0>{});
     };
 
     std::integral_constant<int, 0> c0;
@@ -467,7 +479,8 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t tota
 //              2.6 / 512 k
 //   128 x 128  4 + rounds (2.35 / 512 k + 5), two tiles a CU; a lone tile
 //              1.05 / 512 k
-//   32 x 32    3 + 2.3 / 2048 k and tile of a CU
+//   32 x 32    3 + 1 / 2048 k where there are few, up to 1.6 with a tile a CU
+//              and 2.6 with 32 rows of A in it
 //
 // So 8192 x 14336 x 4096 (275 us, against 318 with 128 x 128) and 64 x 1024^3
 // (72 against 80) take the large tile, 1024 x 1024 x 65536 128 x 128 with
@@ -495,9 +508,10 @@ double medium_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits
 }
 Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
     const double dm = static_cast<double>(M), dn = static_cast<double>(N), db = static_cast<double>(batch);
-    const double shares = std::max(1.0, ((M + 31) / 32) * double((N + 31) / 32) * db / 256);
+    const double shares = std::ceil(dm / 32) * std::ceil(dn / 32) * db / 256;
+    const double each = 1.0 + std::min(1.0, shares) * (0.6 + std::min(dm, 32.0) / 32);
     Choice best{kRows, 1};
-    double t = 3.0 + 2.3 * shares * static_cast<double>(K) / 2048;
+    double t = 3.0 + each * std::max(1.0, (shares + std::ceil(shares)) / 2) * static_cast<double>(K) / 2048;
     // tiles are counted in 32 bits on the device
     if (((dm + 127) / 128) * ((dn + 127) / 128) * db > 1e6 * 1024) return best;
     const int64_t groups = (blocks_of(K) + 15) / 16;
