@@ -185,11 +185,11 @@ __global__ __launch_bounds__(256) void quantize_cols_kernel(Quantize p, int64_t 
 // caches if rows are whole lines (8192 x 14336: 102 us with ordinary stores,
 // 77 so; 8192 x 4095: 24.6 with them, 33.3 streamed).  Memory bounds it:
 // 8192 x 4096 in 23.4 us (6.5 TB/s); a row of 4096 2.3 us.
+template <bool LINES>
 __global__ __launch_bounds__(256) void dequantize_kernel(Dequantize p, int lx, int tiles_x,
                                                          int64_t tiles_y, int64_t tiles) {
     const int tx = threadIdx.x & ((1 << lx) - 1), ty = threadIdx.x >> lx;
     const int rows_wg = (256 >> lx) * kRows;
-    const bool lines = p.ldy % 32 == 0 && (reinterpret_cast<uintptr_t>(p.Y) | p.sy * 4) % 128 == 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int64_t line = t / tiles_x;
         const int64_t quad = ((t - line * tiles_x) << lx) + tx;
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(Dequantize p, int lx, i
             float *y = p.Y + b * p.sy + r * p.ldy + col;
             const f32x4 v{lo[0], lo[1], hi[0], hi[1]};
             if (col + 4 <= p.cols) {
-                if (lines)
+                if constexpr (LINES)
                     __builtin_nontemporal_store(v, reinterpret_cast<float4u *>(y));
                 else
                     *reinterpret_cast<float4u *>(y) = v;
@@ -269,7 +269,10 @@ hipError_t launch_quantize(const Quantize &q, hipStream_t stream) {
 
 hipError_t launch_dequantize(const Dequantize &d, hipStream_t stream) {
     const Lanes l = lanes_for((d.cols + int64_t{3}) / 4, d.rows, d.batch);
-    dequantize_kernel<<<l.grid, 256, 0, stream>>>(d, l.lx, l.tiles_x, l.tiles_y, l.tiles);
+    if (d.ldy % 32 == 0 && d.sy % 32 == 0 && reinterpret_cast<uintptr_t>(d.Y) % 128 == 0)
+        dequantize_kernel<true><<<l.grid, 256, 0, stream>>>(d, l.lx, l.tiles_x, l.tiles_y, l.tiles);
+    else
+        dequantize_kernel<false><<<l.grid, 256, 0, stream>>>(d, l.lx, l.tiles_x, l.tiles_y, l.tiles);
     return hipGetLastError();
 }
 
