@@ -512,13 +512,17 @@ def _empty(shape, strides, dtype, device, stream):
 def mxfp4_empty(shape, device="cuda", *, stream=None) -> Mxfp4:
     """An uninitialised Mxfp4 of ``shape`` (rows, cols) or (batch, rows, cols)."""
     load()
+    if len(shape) not in (2, 3) or min(shape) < 0:
+        raise ValueError(f"shape {tuple(shape)} must be (rows, cols) or (batch, rows, cols)")
     *lead, cols = shape
     nb = (cols + MXFP4_BLOCK - 1) // MXFP4_BLOCK
     words = (nb + 3) // 4 * 4
     rows = lead[-1]
     lines = rows if len(lead) == 1 else lead[0] * rows
     memory = _empty((lines * (nb * 16 + words),), (1,), _torch.uint8, device, stream)
-    q = Mxfp4.__new__(Mxfp4)  # nothing to check
+    if not memory.is_cuda:
+        raise TypeError(f"an Mxfp4 lies in GPU memory, not on {memory.device}")
+    q = Mxfp4.__new__(Mxfp4)  # nothing else to check
     q._codes, q._scales, q._memory = None, None, memory
     q.cols, q.shape, q.device = cols, (*lead, cols), memory.device
     at = memory.data_ptr()

@@ -248,3 +248,15 @@ def test_sizes_just_above_the_limit(lib):
     for sizes in ((1, 1, 1, n), (1, n, 1, 1), (n, 1, 1, 1)):
         assert b.gemm_mxfp4_workspace_size(*sizes) == 0
         assert b.gemm_mxfp4_weight_workspace_size(b.OP_T, *sizes) == 0
+
+
+@pytest.mark.parametrize("shape", [(64,), (2, 3, 4, 64), (), (4, -1), (-4, 64), (-2, 4, 64)])
+def test_empty_refuses_shapes_that_no_call_takes(lib, shape):
+    with pytest.raises(ValueError):
+        b.mxfp4_empty(shape, "cuda:0")
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_empty_refuses_other_devices(lib, device):
+    with pytest.raises(TypeError, match="GPU"):
+        b.mxfp4_empty((4, 64), device)
