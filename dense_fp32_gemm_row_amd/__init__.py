@@ -8,8 +8,9 @@ so the seeded input generators in ``workloads`` stay usable without a GPU.
 
 from __future__ import annotations
 
-__all__ = ["gemm", "gemm_f32", "gemm_f32_variant", "gemm_f32_strerror", "Mxfp4", "mxfp4_quantize",
-           "mxfp4_quantize_both", "mxfp4_dequantize", "gemm_mxfp4", "gemm_mxfp4_weight", "workloads"]
+__all__ = ["gemm", "gemm_f32", "gemm_f32_variant", "gemm_f32_strerror", "Mxfp4", "mxfp4_empty",
+           "mxfp4_quantize", "mxfp4_quantize_both", "mxfp4_dequantize", "gemm_mxfp4", "gemm_mxfp4_weight", "OP_N",
+           "OP_T", "workloads"]
 
 
 def __getattr__(name):

@@ -439,8 +439,10 @@ class Mxfp4:
     """A matrix (or a batch of them) in microscaled 4-bit floating point:
     ``codes`` (..., rows, >= 16 ceil(cols / 32)) and ``scales`` (..., rows,
     >= ceil(cols / 32)), uint8 tensors with unit stride along the last axis,
-    in the layout of include/gemm_mxfp4.h, and the number of columns.  It
-    holds the tensors; their memory is not copied."""
+    in the layout of include/gemm_mxfp4.h, and the number of columns.  Codes
+    past ``cols`` in a row's last block of 32 must be zero, which is not
+    checked: the products add them to their sums.  It holds the tensors;
+    their memory is not copied."""
 
     __slots__ = ("cols", "shape", "device", "_codes", "_scales", "_memory", "_c")
 

@@ -260,3 +260,14 @@ def test_empty_refuses_shapes_that_no_call_takes(lib, shape):
 def test_empty_refuses_other_devices(lib, device):
     with pytest.raises(TypeError, match="GPU"):
         b.mxfp4_empty((4, 64), device)
+
+
+def test_package_exports_what_its_calls_take(lib):
+    """`op` of gemm_mxfp4_weight and the `out` of a quantisation, without the binding's own name."""
+    import dense_fp32_gemm_row_amd as pkg
+
+    assert (pkg.OP_N, pkg.OP_T) == (b.OP_N, b.OP_T) and pkg.mxfp4_empty is b.mxfp4_empty
+    for name in set(pkg.__all__) - {"workloads"}:
+        assert getattr(pkg, name) is getattr(b, name)
+    with pytest.raises(AttributeError):
+        pkg.no_such_name
