@@ -19,7 +19,7 @@ def __getattr__(name):
 
         return getattr(binding, name)
     if name == "workloads":
-        from . import workloads
+        from importlib import import_module  # (a `from . import` would come back here)
 
-        return workloads
+        return import_module(".workloads", __name__)
     raise AttributeError(name)

@@ -7,6 +7,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -271,3 +272,10 @@ def test_package_exports_what_its_calls_take(lib):
         assert getattr(pkg, name) is getattr(b, name)
     with pytest.raises(AttributeError):
         pkg.no_such_name
+
+
+def test_package_gives_its_workloads():
+    """In a fresh interpreter: an attribute access must import the module, not ask itself for it."""
+    code = "import dense_fp32_gemm_row_amd as p; assert p.workloads.__name__ == 'dense_fp32_gemm_row_amd.workloads'"
+    run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0, run.stderr[-300:]
