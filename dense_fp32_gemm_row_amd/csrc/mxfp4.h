@@ -6,11 +6,10 @@
 
 #include <cstdint>
 
+#include "mxfp4_choice.h"
+
 namespace gemm_f32_impl {
 namespace mx {
-
-constexpr int kBlock = 32;        // values that share a scale
-constexpr int kBlockBytes = 16;   // their codes
 
 // One matrix (of a batch) in the format; strides in bytes.
 struct View {
@@ -68,19 +67,5 @@ int weight_splits(bool b_transposed, int64_t batch, int64_t M, int64_t N, int64_
 
 // C_b = sum over s < splits of slice [b][s] of p.W, in that order.
 hipError_t launch_sum_slices(const Product &p, hipStream_t);
-// Predicted microseconds of that.
-inline double sum_slices_us(double batch, double M, double N, int splits) {
-    return splits > 1 ? 4.0 + batch * M * N * 4.0 * (splits + 1) / 3.5e6 : 0.0;
-}
-
-// Slices of K of `chunks` chunks each are equally long but for the last: with
-// `want` asked for, the number that is not empty.
-inline int slices_used(int64_t chunks, int64_t want) {
-    const int64_t len = (chunks + want - 1) / want;
-    return static_cast<int>((chunks + len - 1) / len);
-}
-
-inline int64_t blocks_of(int64_t k) { return (k + kBlock - 1) / kBlock; }
-
 }  // namespace mx
 }  // namespace gemm_f32_impl

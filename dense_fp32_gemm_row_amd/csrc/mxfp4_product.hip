@@ -1,7 +1,6 @@
 // C = A B^T with both operands in MXFP4 (include/gemm_mxfp4.h).
 
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -471,73 +470,10 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t tota
     }
 }
 
-// Which kernel a product takes: the least predicted time.  The figures are
-// microseconds measured on MI355X, per 512 k of a tile and per store of one
-// with the chip full, and for lone tiles:
-//
-//   256 x 256  5 + rounds (3.5 / 512 k + 10.8), one tile a CU; a lone tile
-//              2.6 / 512 k
-//   128 x 128  4 + rounds (2.35 / 512 k + 5), two tiles a CU; a lone tile
-//              1.05 / 512 k
-//   32 x 32    3 + 1 / 2048 k where there are few, up to 1.6 with a tile a CU
-//              and 2.6 with 32 rows of A in it
-//
-// So 8192 x 14336 x 4096 (275 us, against 318 with 128 x 128) and 64 x 1024^3
-// (72 against 80) take the large tile, 1024 x 1024 x 65536 128 x 128 with
-// sliced K (48 and 8 for the sum, against 55 and 8 with the large tile), 256^3 (3.2 against 5.8), 1000 x 1023 x 777 (6.4 against 8.0) and
-// products of few rows 32 x 32.
-enum Kernel { kLarge, kMedium, kRows };
-struct Choice {
-    Kernel kernel;
-    int splits;
-};
-double tile_us(int64_t tiles, double groups, int slots, double fixed, double each, double lone,
-               double store) {
-    const double full = static_cast<double>(tiles / slots), rem = static_cast<double>(tiles % slots) / slots;
-    double t = fixed + full * (each * groups + store);
-    if (rem > 0) t += groups * (lone + (each - lone) * rem * std::sqrt(rem)) + store * rem;
-    return t;
-}
-double large_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits) {
-    return tile_us((M + 255) / 256 * ((N + 255) / 256) * batch * splits,
-                   static_cast<double>((groups + splits - 1) / splits), 256, 5.0, 3.5, 2.6, 10.8);
-}
-double medium_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int splits) {
-    return tile_us((M + 127) / 128 * ((N + 127) / 128) * batch * splits,
-                   static_cast<double>((groups + splits - 1) / splits), 512, 4.0, 2.35, 1.05, 5.0);
-}
-Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
-    const double dm = static_cast<double>(M), dn = static_cast<double>(N), db = static_cast<double>(batch);
-    const double shares = std::ceil(dm / 32) * std::ceil(dn / 32) * db / 256;
-    const double each = 1.0 + std::min(1.0, shares) * (0.6 + std::min(dm, 32.0) / 32);
-    Choice best{kRows, 1};
-    double t = 3.0 + each * std::max(1.0, (shares + std::ceil(shares)) / 2) * static_cast<double>(K) / 2048;
-    // tiles are counted in 32 bits on the device
-    if (((dm + 127) / 128) * ((dn + 127) / 128) * db > 1e6 * 1024) return best;
-    const int64_t groups = (blocks_of(K) + 15) / 16;
-    for (int want = 1; want <= most_splits && want * 4 <= groups + 3; want *= 2) {
-        const int s = slices_used(groups, want);
-        const double sum = sum_slices_us(db, dm, dn, s);
-        const double l = large_us(batch, M, N, groups, s) + sum, m = medium_us(batch, M, N, groups, s) + sum;
-        if (l < t) t = l, best = {kLarge, s};
-        if (m < t) t = m, best = {kMedium, s};
-    }
-    return best;
-}
-
-// Whether the rows of a tile, in codes and in C, fit 32-bit offsets.
-bool reaches(const Product &p) {
-    constexpr int64_t kReach = int64_t{1} << 31;
-    const int64_t ld = std::max({p.a.ldq, p.b.ldq, p.a.lds, p.b.lds, std::max(p.ldc, int64_t{p.N}) * 4});
-    return ld < kReach / 512;
-}
-
 }  // namespace
 
-constexpr int kMostSplits = 64;
-
 int product_splits(int64_t batch, int64_t M, int64_t N, int64_t K) {
-    return choose(batch, M, N, K, kMostSplits).splits;
+    return product_choice::choose(batch, M, N, K, kMostSplits).splits;
 }
 
 hipError_t launch_sum_slices(const Product &p, hipStream_t stream) {
@@ -553,8 +489,9 @@ hipError_t launch_sum_slices(const Product &p, hipStream_t stream) {
 
 hipError_t launch_product(const Product &asked, hipStream_t stream) {
     Product p = asked;
+    using namespace product_choice;
     Choice c = choose(p.batch, p.M, p.N, p.K, p.splits > 1 ? kMostSplits : 1);
-    if (!reaches(p)) c = {kRows, 1};
+    if (!reaches(std::max({p.a.ldq, p.b.ldq, p.a.lds, p.b.lds}), std::max(p.ldc, int64_t{p.N}))) c = {kRows, 1};
     p.splits = c.splits;
     hipError_t err = hipSuccess;
     switch (c.kernel) {

@@ -8,7 +8,6 @@
 // where those run at a sixteenth.
 
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "mxfp4_device.h"
@@ -686,15 +685,6 @@ __global__ __launch_bounds__(256, PER_CU) void weight_tile_kernel(Product p, int
         }
 }
 
-// Whether a tile's rows (of K rows of W as stored) fit 32-bit offsets.
-bool reaches(const Product &p, int rows_m, int rows_n) {
-    constexpr int64_t kReach = int64_t{1} << 31;
-    const int64_t wrows = p.b_transposed ? rows_n : p.K;
-    // (a stride may be near 2^60: it is divided into, never multiplied)
-    return p.ldx < kReach / 4 / rows_m && std::max(p.ldc, int64_t{p.N}) < kReach / 4 / rows_m &&
-           std::max(p.b.ldq, p.b.lds) < kReach / wrows && p.K < kReach / 8 && p.N < kReach / 8;
-}
-
 // PER_CU workgroups of a CU, for the registers that a wavefront may take.
 // Where the 128 x 256 tile's do not fit two without spilling dozens (W as
 // stored fits by itself), the compiler is not held to two: with K % 4 != 0
@@ -746,104 +736,18 @@ hipError_t launch_stored(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// W read straight into registers, 16 rows of A at a time: columns of a
-// workgroup (16 nt) and slices of K, by the least predicted time.  A step of a
-// workgroup's wavefronts (128 k with W transposed, 32 k as stored) takes, in
-// microseconds measured on MI355X with up to 256 workgroups, for r rows of A:
-//
-//   16 columns 0.75 + 0.065 r   32 1.4 + 0.065 r   64 2.0 + 0.065 r   as stored, 128: 1.45
-//
-// and with more of them 1.2 times their share of that.
-// So 16 rows x 14336 x 4096 takes 64 columns (19.7 us, against 26 with 32 and
-// 40 with 16), 4 rows x 4096 x 4096 16 (8.9, against 10.3 and 14.2), 16 rows x
-// 4096 x 14336 64 in 4 slices (21, against 37 with 16 unsliced), 16 x 512 x
-// 8192 16 in 8 (9.9, against 20.6); as stored 16 x 4096 x 4096 takes 8 slices
-// (8.6 and 3 for their sum, against 26.8 unsliced).
-struct Direct {
-    int nt, splits;
-    double us;
-};
-Direct direct(bool bt, double batch, double M, double N, int64_t K, bool slices) {
-    const int64_t steps = bt ? (blocks_of(K) + 3) / 4 : blocks_of(K);
-    const double rows = std::ceil(M / 16) * batch, r = std::min(M, 16.0);
-    Direct best{0, 1, 0};
-    for (int nt = bt ? 4 : 8; nt >= (bt ? 1 : 8); nt /= 2) {
-        const double tiles = rows * std::ceil(N / (16 * nt));
-        const double step = !bt ? 1.45 : (nt == 4 ? 2.0 : nt == 2 ? 1.4 : 0.75) + 0.065 * r;
-        for (int want = 1; want == 1 || (slices && want <= 256 && want * 8 <= steps + 7); want *= 2) {
-            const int s = slices_used(steps, want);
-            const double n = static_cast<double>(steps) / (8.0 * s);
-            double us = 4.5 + step * std::max(std::ceil(n), 0.6 * (n + std::ceil(n)) * tiles * s / 256);
-            if (s > 1) us += 1.5 + sum_slices_us(batch, M, N, s);
-            if (best.nt == 0 || us < best.us) best = {nt, s, us};
-        }
-    }
-    return best;
-}
-
-// Which kernel a product takes, and how many slices of K: the least predicted
-// time, for tiles from microseconds per 32 k measured on MI355X for a lone
-// tile and for a full chip (W transposed / as stored), after 4.5 that every
-// launch takes and 3 that slices lose to their unequal ends:
-//
-//   128 x 256  two a CU     0.95 / 1.24 lone   2.19 / 2.31 full
-//    64 x 256  two a CU     0.58 / 0.82 lone   1.24 / 1.34 full
-//    64 x 128  three a CU   0.45 / 0.69 lone   1.07 / 1.27 full
-//
-// 4096 x 4096 x 14336 takes the first (982 us, against 1109 and 1272), 512 x
-// 4096 x 4096 the second in 4 slices (55 us, against 61 in 2, 87 unsliced and
-// 70 with the last unsliced), 37 x 14336 x 4096 the second in 8 (34 us, the
-// same in 4, against 82 unsliced).  Up to 16 rows W is always read straight
-// into registers, and beyond where that is quicker: 32 x 4096 x 4096 (14.3 us
-// against 17.4 with tiles, as stored 15.4 against 21.8) and 48 x 1000 x 2000
-// (7.0 against 12.0), but not 48 x 14336 x 4096 (48 against 34).
-constexpr int kDirect = -1;
-struct Choice {
-    int tile;  // 0, 1, 2 as above, or kDirect
-    int splits, nt;
-};
-Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
-    struct Candidate {
-        int bm, bn, slots;
-        double lone[2], full[2];
-    };
-    static constexpr Candidate kTiles[] = {{128, 256, 512, {1.24, 0.95}, {2.31, 2.19}},
-                                           {64, 256, 512, {0.82, 0.58}, {1.34, 1.24}},
-                                           {64, 128, 768, {0.69, 0.45}, {1.27, 1.07}}};
-    if (bt && M <= 2) return {kDirect, 1, 0};  // a kernel of their own
-    const double db = static_cast<double>(batch), dm = static_cast<double>(M), dn = static_cast<double>(N);
-    const Direct d = direct(bt, db, dm, dn, K, most_splits > 1);
-    Choice best{kDirect, d.splits, d.nt};
-    if (M <= 16) return best;
-    double t = d.us;
-    const int64_t chunks = (blocks_of(K) + 3) / 4;
-    for (int want = 1; want <= most_splits && (want == 1 || want * 2 <= chunks); want *= 2) {
-        const int s = slices_used(chunks, want);
-        const double len = 4.0 * static_cast<double>((chunks + s - 1) / s);
-        for (int i = 0; i < 3; ++i) {
-            const Candidate &c = kTiles[i];
-            const double tiles = std::ceil(dm / c.bm) * std::ceil(dn / c.bn) * db * s;
-            const double full = std::floor(tiles / c.slots), rem = tiles / c.slots - full;
-            double u = 4.5 + full * len * c.full[bt] +
-                       (rem > 0 ? len * (c.lone[bt] + (c.full[bt] - c.lone[bt]) * rem * std::sqrt(rem)) : 0.0);
-            if (s > 1) u += 3.0 + sum_slices_us(db, dm, dn, s);
-            if (u < t) t = u, best = {i, s, 0};
-        }
-    }
-    return best;
-}
-
 }  // namespace
 
 int weight_splits(bool b_transposed, int64_t batch, int64_t M, int64_t N, int64_t K) {
-    return choose(b_transposed, batch, M, N, K, 64).splits;
+    return weight_choice::choose(b_transposed, batch, M, N, K, kMostSplits).splits;
 }
 
 hipError_t launch_weight(const Product &asked, hipStream_t stream) {
     Product p = asked;
-    Choice c = choose(p.b_transposed, p.batch, p.M, p.N, p.K, p.splits > 1 ? 64 : 1);
-    const double tiles = static_cast<double>((p.M + 63) / 64) * ((p.N + 127) / 128) * static_cast<double>(p.batch);
-    if (c.tile != kDirect && (!reaches(p, 128, 256) || tiles > 1e6))  // (a launch has at most 2^32 lanes)
+    using namespace weight_choice;
+    Choice c = choose(p.b_transposed, p.batch, p.M, p.N, p.K, p.splits > 1 ? kMostSplits : 1);
+    if (c.tile != kDirect && !tiles_fit(p.b_transposed, p.batch, p.M, p.N, p.K, p.ldx, std::max(p.b.ldq, p.b.lds),
+                                        std::max(p.ldc, int64_t{p.N})))
         c = {kDirect, 1, p.b_transposed ? 4 : 8};
     p.splits = c.splits;
     hipError_t err;
