@@ -95,3 +95,36 @@ def test_no_kernel_spills_registers(build):
 
 def test_no_packed_fp32_instructions(build):
     assert not re.search(r"\bv_pk_(add|mul|fma)_f32\b", build[0])
+
+
+def test_spills_are_the_documented_ones(build):
+    """24 registers (96 bytes a lane) of one tile, none of any other kernel's."""
+    names = demangled(re.findall(r"Function Name: (\S+)", build[1]))
+    scratch = [int(x) for x in re.findall(r"ScratchSize \[bytes/lane\]: (\d+)", build[1])]
+    for name, n in zip(names, scratch):
+        documented = "weight_tile_kernel" in name and arguments(name) == ["2", "4", "true", "true", "2"]
+        assert n <= (96 if documented else 0), f"{name}: {n} bytes a lane"
+
+
+def test_workgroups_a_cu_that_the_choice_counts_on(build):
+    """Wavefronts a SIMD for which the predicted times were measured."""
+    names = demangled(re.findall(r"Function Name: (\S+)", build[1]))
+    waves = [int(x) for x in re.findall(r"Occupancy \[waves/SIMD\]: (\d+)", build[1])]
+    assert len(names) == len(waves)
+    seen = {}
+    for name, n in zip(names, waves):
+        if "tile_kernel" in name:
+            seen[(re.search(r"\w+_tile_kernel", name).group(0), *arguments(name))] = n
+    # 8 wavefronts of 256 x 256 a CU, and two workgroups of 4 of 128 x 128
+    for whole in ("true", "false"):
+        assert seen["product_tile_kernel", "2", "4", "4", "2", "1", whole] == 2
+        assert seen["product_tile_kernel", "2", "2", "2", "2", "2", whole] == 2
+    # two of 128 x 256 (for which word loads of A leave one, W transposed),
+    # two of 64 x 256, three of 64 x 128
+    for bt in ("true", "false"):
+        for quads in ("true", "false"):
+            fits = "2" if bt == quads == "true" else "1"
+            want = 1 if (bt, quads) == ("true", "false") else 2
+            assert seen["weight_tile_kernel", "2", "4", bt, quads, fits] == want
+            assert seen["weight_tile_kernel", "1", "4", bt, quads, "2"] == 2
+            assert seen["weight_tile_kernel", "1", "2", bt, quads, "3"] == 3
