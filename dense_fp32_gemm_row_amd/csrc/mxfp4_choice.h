@@ -39,11 +39,16 @@ namespace product_choice {
 //   128 x 128  4 + rounds (2.35 / 512 k + 5), two tiles a CU; a lone tile
 //              1.05 / 512 k
 //   32 x 32    3 + 1 / 2048 k where there are few, up to 1.6 with a tile a CU
-//              and 2.6 with 32 rows of A in it
+//              and 2.4 with 32 rows of A in it, 0.5 at least
 //
-// So 8192 x 14336 x 4096 (275 us, against 318 with 128 x 128) and 64 x 1024^3
-// (72 against 80) take the large tile, 1024 x 1024 x 65536 128 x 128 with
-// sliced K (48 and 8 for the sum, against 55 and 8 with the large tile), 256^3 (3.2 against 5.8), 1000 x 1023 x 777 (6.4 against 8.0) and
+// (Products of a few microseconds from a graph: called one by one they wait
+// for their host.)  Over 253 products of up to 4e10 operations that leaves
+// 0.03% on average and 7% at most to the better of 128 x 128 and 32 x 32.
+//
+// So 8192 x 14336 x 4096 (255 to 272 us by card, against 318 with 128 x 128)
+// and 64 x 1024^3 (66 against 80) take the large tile, 1024 x 1024 x 65536 128 x
+// 128 with sliced K (46 and 8 for the sum, against 55 and 8 with the large
+// tile), 256^3 (2.9 against 5.9), 1000 x 1023 x 777 (6.0 against 7.8) and
 // products of few rows 32 x 32.
 enum Kernel { kLarge, kMedium, kRows };
 struct Choice {
@@ -68,9 +73,10 @@ inline double medium_us(int64_t batch, int64_t M, int64_t N, int64_t groups, int
 inline Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
     const double dm = static_cast<double>(M), dn = static_cast<double>(N), db = static_cast<double>(batch);
     const double shares = std::ceil(dm / 32) * std::ceil(dn / 32) * db / 256;
-    const double each = 1.0 + std::min(1.0, shares) * (0.6 + std::min(dm, 32.0) / 32);
+    const double each = 1.0 + std::min(1.0, shares) * (0.6 + 0.8 * std::min(dm, 32.0) / 32);
     Choice best{kRows, 1};
-    double t = 3.0 + each * std::max(1.0, (shares + std::ceil(shares)) / 2) * static_cast<double>(K) / 2048;
+    double t = 3.0 + std::max(1.0, (shares + std::ceil(shares)) / 2) *
+                         std::max(0.5, each * static_cast<double>(K) / 2048);
     // tiles are counted in 32 bits on the device
     if (((dm + 127) / 128) * ((dn + 127) / 128) * db > 1e6 * 1024) return best;
     const int64_t groups = (blocks_of(K) + 15) / 16;
@@ -186,7 +192,8 @@ inline Choice choose(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, in
 // Whether the tiles can run a product: a tile's rows (K rows of W as stored)
 // `ldx` floats apart in A, `ldw` bytes in W and `ldc` floats in C fit 32-bit
 // offsets, and a launch's lanes 2^32.
-inline bool tiles_fit(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int64_t ldc) {
+inline bool tiles_fit(bool bt, int64_t batch, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw,
+                      int64_t ldc) {
     constexpr int64_t kReach = int64_t{1} << 31, kRowsM = 128, kRowsN = 256;
     const int64_t wrows = bt ? kRowsN : K;
     const double tiles = static_cast<double>((M + 63) / 64) * static_cast<double>((N + 127) / 128) *

@@ -19,10 +19,10 @@ PRODUCTS = {
         (3, 646, 1678, 28794): 4,
     },
     "128x128": {
-        (1, 193, 5046, 512): 1,
-        (20, 390, 97, 512): 1,
+        (1, 300, 5046, 512): 1,
+        (20, 500, 97, 512): 1,
         (2, 32, 45, 36352): 15,
-        (1, 483, 2252, 500): 1,
+        (1, 700, 2252, 500): 1,
         (1, 4133, 4161, 1000): 1,
         (9, 97, 944, 1000): 1,
         (1, 37, 33, 29556): 8,

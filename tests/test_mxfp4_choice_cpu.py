@@ -81,6 +81,23 @@ def test_direct_cases_take_no_tile(choose):
     assert [name for name, _ in got] == ["rows" if kind == "P" else "direct" for kind, _ in cases.DIRECT]
 
 
+# microseconds measured in a graph (so that no call waits for its host): tiles of
+# 128 x 128, of 32 x 32
+MEASURED = {(1000, 1023, 777): (7.8, 6.0), (1024, 1024, 777): (7.5, 5.5), (108, 4379, 1761): (9.5, 7.5),
+            (2109, 522, 693): (8.0, 6.5), (1024, 512, 4096): (12.8, 11.4), (128, 4096, 4096): (12.8, 11.4),
+            (221, 3869, 1061): (8.7, 7.9), (511, 1023, 2077): (10.7, 7.7), (256, 256, 256): (5.9, 2.9),
+            (2048, 2048, 512): (8.2, 13.7), (1000, 1000, 4000): (16.1, 24.8), (100, 8193, 1500): (8.7, 10.4),
+            (640, 10496, 128): (10.1, 16.6), (1888, 1760, 128): (7.8, 10.1), (193, 5046, 512): (6.5, 6.2),
+            (1300, 1300, 1000): (8.4, 11.9), (2000, 2000, 500): (8.6, 14.2), (1024, 1024, 1024): (7.4, 7.4)}
+
+
+def test_small_products_take_the_quicker_kernel(choose):
+    """Within 5% of the better of two kernels that were timed."""
+    got = choose([("P", (1, *size)) for size in MEASURED])
+    for (size, (medium, rows)), (name, _) in zip(MEASURED.items(), got):
+        assert {"128x128": medium, "rows": rows}[name] <= 1.05 * min(medium, rows), f"{size} takes {name}"
+
+
 def test_tile_cases_cover_every_compiled_form():
     """Each tile with and without slices and a batch, edges inside a tile, and
     both of its compiled forms (K a multiple of 512, or of 4, and not)."""
