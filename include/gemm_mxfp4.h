@@ -26,12 +26,16 @@
  *
  * Sizes (batch, rows, cols, M, N, K) are at most 2^31 - 1024.
  *
- * Scale bytes 253 and 254 can stand for values beyond FP32's range; a product
- * of such a value is infinite or NaN.
+ * Scale bytes 253 and 254 can stand for values beyond FP32's range.  Read back,
+ * such a value is infinite, and multiplied with FP32 infinite or NaN; a product
+ * of two values in the format is exact, whatever their scales (255 aside), and
+ * infinite only beyond FP32's range.
  *
  * Memory, streams, threads and errors are as in gemm_f32.h: device pointers
  * owned by the caller, nothing allocated, every argument checked before
  * anything is enqueued, results written only inside their rows and columns.
+ * What overlaps is judged by address ranges, from an operand's first byte to the
+ * last of its last row (of the last matrix of a batch).
  * The calls run on the device of `stream` (the current device for NULL).
  */
 #ifndef GEMM_MXFP4_H

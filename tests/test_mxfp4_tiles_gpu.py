@@ -68,7 +68,7 @@ class Matrix:
             byte = byte + exponents.view(1, -1, 1)
         if block_exponents is not None:
             byte = byte + block_exponents.view(1, 1, -1)
-        assert int(byte.min()) >= 0 and int(byte.max()) <= 252
+        assert int(byte.min()) >= 0 and int(byte.max()) <= 254
         scales[..., :nb] = byte.to(torch.uint8)
         self.cols, self.batch, self.rows = cols, batch, rows
         self._power, self._seed = power, seed
@@ -238,12 +238,13 @@ def test_product_tile_nan_blocks(case):
 
 @pytest.mark.parametrize("case", PRODUCT_FEW + [("rows", s) for k, s in cases.DIRECT if k == "P"], ids=cases.ident)
 def test_product_far_exponents(case):
-    """Scale bytes from 2 to 252, one operand's against the other's."""
+    """Scale bytes from 0 to 254, one operand's against the other's: values that
+    FP32 does not hold, with products that it does."""
     tile, size = case
     _, M, N, K = size
     log(f"far exponents {case}")
     nb = ref.blocks(K)
-    t = far_exponents(nb, 123)  # the random part of the scales moves a byte by 2 more
+    t = far_exponents(nb, 125)  # the random part of the scales moves a byte by 2 more
     A, B = Matrix(7, 1, M, K, 2, block_exponents=t), Matrix(8, 1, N, K, 2, block_exponents=-t)
     got = run_product(A.held(False), B.held(False), size, True, "", False)
     exact(got, [(A.values(0), B.values(0).t().contiguous())], 2.0 ** 18, str(case))
