@@ -45,11 +45,11 @@ namespace product_choice {
 // for their host.)  Over 253 products of up to 4e10 operations that leaves
 // 0.03% on average and 7% at most to the better of 128 x 128 and 32 x 32.
 //
-// So 8192 x 14336 x 4096 (255 to 272 us by card, against 318 with 128 x 128)
-// and 64 x 1024^3 (66 against 80) take the large tile, 1024 x 1024 x 65536 128 x
-// 128 with sliced K (46 and 8 for the sum, against 55 and 8 with the large
-// tile), 256^3 (2.9 against 5.9), 1000 x 1023 x 777 (6.0 against 7.8) and
-// products of few rows 32 x 32.
+// So 8192 x 14336 x 4096 (255 us, 284 on a slower card, against 318 with 128 x
+// 128) and 64 x 1024^3 (66, on a slower card 88, against 80) take the large tile,
+// 1024 x 1024 x 65536 128 x 128 with sliced K (46 and 8 for the sum, against 55
+// and 8 with the large tile), 256^3 (2.9 against 5.9), 1000 x 1023 x 777 (6.0
+// against 7.8) and products of few rows 32 x 32.
 enum Kernel { kLarge, kMedium, kRows };
 struct Choice {
     Kernel kernel;
@@ -110,11 +110,11 @@ namespace weight_choice {
 //   16 columns 0.75 + 0.065 r   32 1.4 + 0.065 r   64 2.0 + 0.065 r   as stored, 128: 1.45
 //
 // and with more of them 1.2 times their share of that.
-// So 16 rows x 14336 x 4096 takes 64 columns (19.7 us, against 26 with 32 and
-// 40 with 16), 4 rows x 4096 x 4096 16 (8.9, against 10.3 and 14.2), 16 rows x
+// So 16 rows x 14336 x 4096 takes 64 columns (18.8 us, against 26 with 32 and
+// 40 with 16), 4 rows x 4096 x 4096 16 (8.6, against 10.3 and 14.2), 16 rows x
 // 4096 x 14336 64 in 4 slices (21, against 37 with 16 unsliced), 16 x 512 x
 // 8192 16 in 8 (9.9, against 20.6); as stored 16 x 4096 x 4096 takes 8 slices
-// (8.6 and 3 for their sum, against 26.8 unsliced).
+// (9 and 3 for their sum, against 26.8 unsliced).
 struct Direct {
     int nt, splits;
     double us;
@@ -146,10 +146,14 @@ inline Direct direct(bool bt, double batch, double M, double N, int64_t K, bool 
 //    64 x 256  two a CU     0.58 / 0.82 lone   1.24 / 1.34 full
 //    64 x 128  three a CU   0.45 / 0.69 lone   1.07 / 1.27 full
 //
-// 4096 x 4096 x 14336 takes the first (982 us, against 1109 and 1272), 512 x
-// 4096 x 4096 the second in 4 slices (55 us, against 61 in 2, 87 unsliced and
-// 70 with the last unsliced), 37 x 14336 x 4096 the second in 8 (34 us, the
-// same in 4, against 82 unsliced).  Up to 16 rows W is always read straight
+// (The rates are those of K % 4 == 0: with word loads of A the first tile
+// leaves room for one workgroup a CU, W transposed, which the prediction does
+// not know.  Storing C has no term of its own.)
+//
+// 4096 x 4096 x 14336 takes the first (982 us, 1065 on a slower card, against
+// 1109 and 1272), 512 x 4096 x 4096 the second in 4 slices (55 us, against 61 in
+// 2, 87 unsliced and 70 with the last unsliced), 37 x 14336 x 4096 the second in
+// 8 (26 us and 5 for their sum, the same in 4, against 82 unsliced).  Up to 16 rows W is always read straight
 // into registers, and beyond where that is quicker: 32 x 4096 x 4096 (14.3 us
 // against 17.4 with tiles, as stored 15.4 against 21.8) and 48 x 1000 x 2000
 // (7.0 against 12.0), but not 48 x 14336 x 4096 (48 against 34).

@@ -47,8 +47,8 @@ constexpr int kRows = 4;  // rows in flight per lane
 // Blocks along the rows.  Eight lanes hold a block, four values each, so a
 // wavefront reads 1 KiB of a row at once; `lx` = log2 of the lanes along a
 // row (8 to 256 of the workgroup's 256).  Memory bounds it: 8192 x 4096 in
-// 24.8 us (X in and codes out at 6.1 TB/s, part of X from the last-level
-// cache); a row of 4096 2.5 us, the latency of a launch and a load.
+// 23.2 us (X in and codes out at 6.6 TB/s, part of X from the last-level
+// cache); a row of 4096 2.3 us, the latency of a launch and a load.
 __global__ __launch_bounds__(256) void quantize_rows_kernel(Quantize p, int lx, int tiles_x,
                                                             int64_t tiles_y, int64_t tiles) {
     const int nb = (p.cols + kBlock - 1) / kBlock, words = (nb + 3) & ~3;
@@ -98,13 +98,19 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(Quantize p, int lx, 
 // Blocks along the columns, and with ROWS along the rows too, in one read: a
 // workgroup takes 128 x 128 values, a wavefront 32 of the rows, a lane 16 of
 // those and 4 columns.  A column's block then lies in two lanes, a row's in
-// 8.  (32 rows a lane need no exchange for a column, but 256 registers: two
-// workgroups a CU, whose reading, converting and writing hardly overlapped.)
-// The codes of 4 blocks of a column meet in LDS so that they leave as 64
-// bytes: 16 at a time, each to a row of its own, would be partial writes of
-// memory's lines.  4096 x 4096 in 22.8 us (3.7 TB/s), against 31.8 for one
-// launch along each axis; 1000 x 777 8.7 us, a workgroup's chain of one load,
-// maxima, conversions and stores.
+// 8.  (32 rows a lane would need no exchange for a column, but held 256
+// registers.)  The codes of 4 blocks of a column meet in LDS so that they leave
+// as 64 bytes: 16 at a time, each to a row of its own, would be partial writes
+// of memory's lines.  Lanes conflict where they write there, four to a bank:
+// 960 of a CU's 42,000 cycles at 4096 x 4096.
+//
+// Both ways the kernel takes 194 registers, so a CU holds two workgroups, and
+// waits for memory: 4096 x 4096 in 20.2 us (4.2 TB/s), against 31.8 for one
+// launch along each axis; vector instructions are busy 40% of the time.  Along
+// the columns alone it takes 122, four workgroups a CU: 4096 x 4096 in 14.1 us
+// and 8192 x 4096 in 23.9 (6.4 TB/s, part of X from the last-level cache).
+// 1000 x 777 takes 8.4 us both ways, 6.5 along the columns: a workgroup's
+// chain of one load, maxima, conversions and stores.
 template <bool ROWS>
 __global__ __launch_bounds__(256) void quantize_cols_kernel(Quantize p, int64_t tiles_x,
                                                             int64_t tiles_y, int64_t tiles) {
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(256) void quantize_cols_kernel(Quantize p, int64_t 
 // Four values per lane: 2 bytes of codes in, 16 bytes out, streamed past the
 // caches if rows are whole lines (8192 x 14336: 102 us with ordinary stores,
 // 77 so; 8192 x 4095: 24.6 with them, 33.3 streamed).  Memory bounds it:
-// 8192 x 4096 in 23.4 us (6.5 TB/s); a row of 4096 2.3 us.
+// 8192 x 4096 in 23.9 us (6.4 TB/s); a row of 4096 2.1 us.
 template <bool LINES>
 __global__ __launch_bounds__(256) void dequantize_kernel(Dequantize p, int lx, int tiles_x,
                                                          int64_t tiles_y, int64_t tiles) {

@@ -44,7 +44,7 @@ struct Tile {
 // loads (64 lanes x 16 bytes into 1 KiB: 8 rows).  That is a line of the
 // caches: loaded a stage at a time, half a line each, L2 had twice the
 // requests, three quarters of what its channels answer (1024 x 1024 x 65536:
-// 60 us so, 48 with whole lines; 4096^3: 49 and 46).  Block b of row r sits in
+// 53 us so, 46 with whole lines; 4096^3: 49 and 46).  Block b of row r sits in
 // slot b ^ (r / 2 % 8): 16 lanes that read one block of 16 rows then touch
 // every bank once.
 //
@@ -58,12 +58,19 @@ struct Tile {
 // one (4 x 4 blocks each) it idles wherever that one waits, and 8192 x 14336 x
 // 4096 took 293 us instead of 276 (with half lines).
 //
-// 8192 x 14336 x 4096 reaches 3.5 PFLOP/s on random codes (275 us), 3.8 on the
-// codes of normal values (255).  A loop of nothing but these instructions on random
-// codes reaches 5.5, where the card's power holds its clock; of the rest,
-// storing C is little: half the results of as many products (4096 x 14336 x
-// 8192) take as long, and workgroups that start at different times, so that
-// some store while others multiply, gain 3%.
+// 8192 x 14336 x 4096 takes 255 to 284 us by card on the codes of normal
+// values (3.4 to 3.8 PFLOP/s) and a little longer on random ones.  A loop of
+// nothing but these instructions on random codes reaches 5.5, where the card's
+// power holds its clock; of the rest, storing C is little: half the results of
+// as many products (4096 x 14336 x 8192) take 4% less, and workgroups that
+// start at different times, so that some store while others multiply, gain 3%.
+//
+// 1024 x 1024 x 65536 on 128 x 128 tiles (46 to 48 us) fills no one unit: of a
+// CU's 81,000 cycles the path on which loads return is busy 66,000 (in 26,000 of
+// them it waits for L1 or L2), the one of their addresses 50,000, the matrix
+// cores 33,000 and LDS reads 22,000.  The codes alone need 33,000 cycles of the
+// first at the 64 bytes a cycle that L1 gives; a third of all requests are the
+// 16 bytes of scales a row and group, a line of L1 each.
 template <int FM, int FN, int WM, int WN, int PER_CU, bool WHOLE>
 __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_kernel(Product p, int tiles_m,
                                                                         int tiles_n, int64_t tiles,
@@ -350,7 +357,7 @@ __global__ __launch_bounds__(WM *WN * 64, PER_CU *WM *WN / 4) void product_tile_
 // tile of 32 x 32 NT, its wavefronts take steps of 256 k in turn, straight
 // from global memory, and their sums are added in LDS in a fixed order.  What
 // it waits for is memory: every lane has 64 consecutive bytes of a row of B
-// (and A) on the way per step.  256^3 3.6 us, 1000 x 1023 x 777 7.0 us.
+// (and A) on the way per step.  256^3 3.5 us, 1000 x 1023 x 777 6.8 us.
 template <int NT, int NW>
 __global__ __launch_bounds__(NW * 64) void product_rows_kernel(Product p, int64_t tiles_m,
                                                                int64_t tiles_n, int64_t tiles) {
@@ -447,7 +454,8 @@ hipError_t launch_tile(const Product &p, hipStream_t stream) {
 
 // Partial sums of the slices of K, added in ascending order.  Where they are
 // many and small, a load a time would be waited for a time (64 slices of 64 x
-// 1024: 12 us less with 7 on the way); 8 of 1024 x 1024 take 8.3 us, 4.5 TB/s.
+// 1024: 12 us less with 7 on the way); 8 of 1024 x 1024 take 8.3 to 9.3 us,
+// 4.1 to 4.5 TB/s.
 template <int V>
 __global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t total) {
     typedef float vec __attribute__((ext_vector_type(V), aligned(4)));

@@ -38,7 +38,11 @@ __device__ __forceinline__ uint32_t pack_high(uint32_t lo, uint32_t hi) {
 // from 8 (l % 16), a word of codes for each, and turns pairs of values of two
 // columns, as W holds them, into pairs of two k.  Neighbouring tiles run on
 // one XCD, whose L2 then fetches lines of W, and of its scales, that tiles
-// share once (16 x 4096 x 14336: 16.9 us, 18.5 without).
+// share once (16 x 4096 x 14336: 16.9 us, 18.5 without).  14336 columns x 4096
+// take 16.0 us for a row and 17.7 for 16, W alone, at a copy's rate, 6.6: vector
+// instructions (splitting 16 rows whatever M is, decoding, pairing columns) are
+// busy 65% of the time, and with two wavefronts a SIMD what is left waits for
+// loads, eight words and eight single bytes of scales a step.
 constexpr int kStoredWaves = 8;
 __global__ __launch_bounds__(64 * kStoredWaves) void weight_stored_kernel(Product p, int64_t tiles_m,
                                                                           int64_t tiles_n, int64_t tiles,
@@ -153,9 +157,11 @@ __global__ __launch_bounds__(64 * kStoredWaves) void weight_stored_kernel(Produc
 // fixed order.  In v_mfma_f32_16x16x32_bf16 lane l holds 8 k of row (column)
 // l % 16; here lane group l / 16 takes block l / 16 of a step, 8 of its k in
 // each of 4 instructions, so a lane's codes are 16 bytes in a row of W and
-// its part of A 128 bytes.  Reading and splitting A are repeated for every
-// 16 NT columns, and bound it: 4 rows x 14336 x 4096 take 15.3 us, 16 rows
-// 19.7 (W alone, at a copy's rate, 6.6).
+// its part of A 128 bytes.  Reading A, repeated for every 16 NT columns, bounds
+// it: a lane's 16 bytes at a time lie in lines of their own, and L1 serves about
+// one line a cycle (7.4 million lines at 16 rows x 14336 x 4096, 76% of all
+// cycles, half of them A's; vector instructions are busy 33%).  4 rows x 14336 x
+// 4096 take 15.2 us, 16 rows 18.8 (W alone, at a copy's rate, 6.6).
 constexpr int kRowsWaves = 8;
 template <int NT>
 __global__ __launch_bounds__(64 * kRowsWaves) void weight_rows_kernel(Product p, int64_t tiles_m,
@@ -379,9 +385,9 @@ __global__ __launch_bounds__(64 * kVectorWaves) void weight_vector_kernel(Produc
 // registers loaded again.  The one barrier lies before the last phase, under
 // which the next stage's first operands are read.
 //
-// 4096 x 4096 x 14336, W as stored, takes 1056 us: 456 TFLOP/s, that is 1.37
-// PFLOP/s of bf16 products, where a loop of nothing but them reaches 1.76 on
-// random values.  Splitting and decoding share the issue slots with them: of
+// 4096 x 4096 x 14336, W as stored, takes 1056 us, 1144 on a slower card: 456
+// and 420 TFLOP/s, that is 1.37 and 1.26 PFLOP/s of bf16 products, where a loop
+// of nothing but them reaches 1.76 on random values.  Splitting and decoding share the issue slots with them: of
 // a lone 64 x 128 tile's 0.48 us a stage, 0.27 are theirs.
 template <int FM, int FN, bool BT, bool QUADS, int PER_CU>
 __global__ __launch_bounds__(256, PER_CU) void weight_tile_kernel(Product p, int tiles_m, int tiles_n,
@@ -690,7 +696,9 @@ __global__ __launch_bounds__(256, PER_CU) void weight_tile_kernel(Product p, int
 // stored fits by itself), the compiler is not held to two: with K % 4 != 0
 // and W as stored 4096 x 4096 x 14335 took 1387 us held to them, 1153 so; with
 // W transposed and K % 4 == 0 a few spills cost less than the second
-// workgroup brings (1004 us against 1052).
+// workgroup brings (1004 us against 1052).  With W transposed and K % 4 != 0 the
+// registers left to themselves are 268, one workgroup a CU (4096 x 4096 x 14335:
+// 1180 us, as stored, with two, 1165).
 template <int FM, int FN, int PER_CU>
 hipError_t launch_tile(const Product &p, hipStream_t stream) {
     const int tm = ceil_div(p.M, 64 * FM), tn = ceil_div(p.N, 64 * FN);
@@ -755,7 +763,7 @@ hipError_t launch_weight(const Product &asked, hipStream_t stream) {
         err = launch_stored(p, stream);
     else if (c.tile == kDirect && p.M <= 2)
         // One and two rows of A cost the vector units less than splitting 16:
-        // a row x 14336 x 4096 8.0 us, against 13.7.
+        // a row x 14336 x 4096 8.8 us, against 13.7.
         err = p.M == 1 ? launch_vector<1>(p, stream) : launch_vector<2>(p, stream);
     else if (c.tile == kDirect)
         err = c.nt == 4   ? launch_rows<4>(p, stream)
