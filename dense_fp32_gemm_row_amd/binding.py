@@ -1,5 +1,5 @@
-"""ctypes binding of libgemm_f32.so (declared in include/gemm_f32.h and
-include/gemm_mxfp4.h).
+"""ctypes binding of libgemm_f32.so (declared in include/gemm_f32.h,
+include/gemm_f32_fused.h and include/gemm_mxfp4.h).
 
 Argument marshalling only: every step of the product runs in the HIP
 kernels behind the C ABI.  PyTorch provides device memory and streams; it
@@ -10,7 +10,8 @@ Functions with the C names take raw integers (sizes, device addresses,
 leading dimensions, a hipStream_t address) and return the C status code.
 ``gemm`` is the tensor-level convenience used by tests and the benchmark;
 ``Mxfp4`` and the functions below it are the same for matrices held in
-microscaled 4-bit floating point.
+microscaled 4-bit floating point, ``gemm_fused`` and the functions below it
+for a layer's product with its epilogue, a network's loss, and their gradients.
 """
 
 from __future__ import annotations
@@ -121,6 +122,29 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     lib.gemm_mxfp4_weight_workspace_size.argtypes = [_int, _i64, _i64, _i64, _i64]
     lib.gemm_mxfp4_abi_version.restype = _int
     lib.gemm_mxfp4_abi_version.argtypes = []
+    lib.gemm_f32_fused.restype = _int
+    lib.gemm_f32_fused.argtypes = [_int, _int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64,
+                                   _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp]
+    lib.gemm_f32_fused_workspace_size.restype = _i64
+    lib.gemm_f32_fused_workspace_size.argtypes = [_int, _int, _i64, _i64, _i64, _i64]
+    lib.gemm_f32_fused_grad.restype = _int
+    lib.gemm_f32_fused_grad.argtypes = [_int, _int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _int,
+                                        *[_vp, _i64, _i64] * 5, _vp, _i64, _vp, _i64, _vp]
+    lib.gemm_f32_fused_grad_workspace_size.restype = _i64
+    lib.gemm_f32_fused_grad_workspace_size.argtypes = [_int, _int, _i64, _i64, _i64, _i64, _int,
+                                                       _int, _int, _int]
+    lib.gemm_f32_cross_entropy.restype = _int
+    lib.gemm_f32_cross_entropy.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                           _vp, _vp, _i64, _vp]
+    lib.gemm_f32_cross_entropy_grad.restype = _int
+    lib.gemm_f32_cross_entropy_grad.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                                _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+    for name in ("gemm_f32_cross_entropy_workspace_size", "gemm_f32_cross_entropy_grad_workspace_size",
+                 "gemm_f32_cross_entropy_grad_workspace_least"):
+        getattr(lib, name).restype = _i64
+        getattr(lib, name).argtypes = [_i64, _i64, _i64]
+    lib.gemm_f32_fused_abi_version.restype = _int
+    lib.gemm_f32_fused_abi_version.argtypes = []
     _LIB = lib
     return lib
 
@@ -683,3 +707,289 @@ def gemm_mxfp4_weight(A, W: Mxfp4, out=None, workspace=None, *, op: int = OP_T, 
     _run_on(device, stream, lib.gemm_mxfp4_weight, op, batch, M, N, K, A.data_ptr(), lda, sa,
             ctypes.byref(W._c), out.data_ptr(), ldc, sc, wp, wb)
     return out
+
+
+# ---- a layer with its epilogue, the loss, gradients (include/gemm_f32_fused.h) ----
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # GEMM_F32_ACT_*
+
+
+class Epilogue(ctypes.Structure):
+    """gemm_f32_epilogue of the C header."""
+
+    _fields_ = [("activation", _int), ("bias", _vp), ("stride_bias", _i64),
+                ("residual", _vp), ("ld_residual", _i64), ("stride_residual", _i64),
+                ("pre", _vp), ("ld_pre", _i64), ("stride_pre", _i64)]
+
+
+def gemm_f32_fused(opA, opB, batch, M, N, K, A, lda, sA, B, ldb, sB, epilogue, C, ldc, sC,
+                   workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().gemm_f32_fused(opA, opB, batch, M, N, K, A, lda, sA, B, ldb, sB,
+                                 _matrix_arg(epilogue), C, ldc, sC, workspace, workspace_bytes,
+                                 stream)
+
+
+def gemm_f32_fused_workspace_size(opA, opB, batch, M, N, K) -> int:
+    return load().gemm_f32_fused_workspace_size(opA, opB, batch, M, N, K)
+
+
+def gemm_f32_fused_grad(opA, opB, batch, M, N, K, dC, lddc, sdC, activation, pre, ld_pre, s_pre, A,
+                        lda, sA, B, ldb, sB, dA, ldda, sdA, dB, lddb, sdB, dbias, sdbias,
+                        workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().gemm_f32_fused_grad(opA, opB, batch, M, N, K, dC, lddc, sdC, activation, pre,
+                                      ld_pre, s_pre, A, lda, sA, B, ldb, sB, dA, ldda, sdA, dB, lddb,
+                                      sdB, dbias, sdbias, workspace, workspace_bytes, stream)
+
+
+def gemm_f32_fused_grad_workspace_size(opA, opB, batch, M, N, K, activation, want_dA, want_dB,
+                                       want_dbias) -> int:
+    return load().gemm_f32_fused_grad_workspace_size(opA, opB, batch, M, N, K, activation, want_dA,
+                                                     want_dB, want_dbias)
+
+
+def gemm_f32_cross_entropy(T, V, K, X, ldx, W, ldw, target, ignore_index, loss, lse,
+                           workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().gemm_f32_cross_entropy(T, V, K, X, ldx, W, ldw, target, ignore_index, loss, lse,
+                                         workspace, workspace_bytes, stream)
+
+
+def gemm_f32_cross_entropy_workspace_size(T, V, K) -> int:
+    return load().gemm_f32_cross_entropy_workspace_size(T, V, K)
+
+
+def gemm_f32_cross_entropy_grad(T, V, K, X, ldx, W, ldw, target, ignore_index, grad_loss, loss, lse,
+                                dX, lddx, dW, lddw, workspace=None, workspace_bytes=0,
+                                stream=None) -> int:
+    return load().gemm_f32_cross_entropy_grad(T, V, K, X, ldx, W, ldw, target, ignore_index,
+                                              grad_loss, loss, lse, dX, lddx, dW, lddw, workspace,
+                                              workspace_bytes, stream)
+
+
+def gemm_f32_cross_entropy_grad_workspace_size(T, V, K) -> int:
+    return load().gemm_f32_cross_entropy_grad_workspace_size(T, V, K)
+
+
+def gemm_f32_cross_entropy_grad_workspace_least(T, V, K) -> int:
+    return load().gemm_f32_cross_entropy_grad_workspace_least(T, V, K)
+
+
+def gemm_f32_fused_abi_version() -> int:
+    return load().gemm_f32_fused_abi_version()
+
+
+def _activation(name) -> int:
+    try:
+        return ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation {name!r} is none of {', '.join(ACTIVATIONS)}") from None
+
+
+def _sheet(t, name: str, shape, device) -> tuple[int, int, int]:
+    """(pointer, leading dimension, batch stride) of a row-major tensor of ``shape``."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    op, ld, bs, _ = _float_operand(t, name, device)
+    if op != OP_N:
+        raise ValueError(f"{name} must be row-major")
+    return t.data_ptr(), ld, bs
+
+
+def _vector(t, name: str, shape, device) -> tuple[int, int]:
+    """(pointer, batch stride) of a float32 tensor of ``shape`` (n,) or
+    (batch, n), with unit stride along the last axis."""
+    if t.dtype != _torch.float32 or not t.is_cuda:
+        raise TypeError(f"{name} must be a float32 GPU tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} on {t.device}, other operands on {device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last axis")
+    return t.data_ptr(), t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else 0
+
+
+def _space(workspace, need: int, device, stream):
+    """(workspace, kept alive; its pointer; its bytes)"""
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if need:
+        workspace = _empty(((need + 3) // 4,), (1,), _torch.float32, device, stream)
+        return workspace, workspace.data_ptr(), need
+    return None, None, 0
+
+
+def _pair(A, B):
+    """Checks A and B of a product: (device, leading shape, batch, M, N, K, A's and B's (op, ld, stride))."""
+    load()
+    opa, lda, sa, batch = _float_operand(A, "A")
+    device = A.device
+    opb, ldb, sb, _ = _float_operand(B, "B", device)
+    *lead, M, K = A.shape
+    *lead_b, K2, N = B.shape
+    if K != K2 or lead != lead_b:
+        raise ValueError(f"shape mismatch {tuple(A.shape)} x {tuple(B.shape)}")
+    return device, lead, batch, M, N, K, (opa, lda, sa), (opb, ldb, sb)
+
+
+def gemm_fused(A, B, out=None, *, bias=None, activation: str = "none", residual=None, pre=None,
+               workspace=None, stream=None):
+    """``out = act(A @ B + bias) + residual`` for float32 GPU tensors, 2-D or
+    3-D (a batch of products; A or B may be an expanded tensor).
+
+    A and B may be row-major or transposed views of row-major matrices: a
+    layer stored N x K is ``W.t()``.  ``bias`` is (N,), or (batch, N) for a
+    batch.  ``activation`` is one of ACTIVATIONS.  ``residual`` has out's shape and
+    may be out itself.  ``pre`` (out's shape) receives ``A @ B + bias`` for
+    gemm_fused_grad.  ``workspace`` (a GPU tensor of at least
+    gemm_f32_fused_workspace_size bytes) is allocated here when the sizes call
+    for one and None is given.  Enqueued on ``stream``, default torch's
+    current stream; returns ``out`` without synchronising."""
+    device, lead, batch, M, N, K, (opa, lda, sa), (opb, ldb, sb) = _pair(A, B)
+    kind = _activation(activation)
+    shape = (*lead, M, N)
+    e = None
+    if kind or bias is not None or residual is not None or pre is not None:
+        e = Epilogue(kind)
+        if bias is not None:
+            e.bias, e.stride_bias = _vector(bias, "bias", (batch, N) if bias.dim() == 2 and lead else (N,), device)
+        if residual is not None:
+            e.residual, e.ld_residual, e.stride_residual = _sheet(residual, "residual", shape, device)
+        if pre is not None:
+            e.pre, e.ld_pre, e.stride_pre = _sheet(pre, "pre", shape, device)
+    lib = load()
+    out, ldc, sc, workspace, wp, wb = _mxfp4_out(
+        out, shape, device, workspace, lib.gemm_f32_fused_workspace_size(opa, opb, batch, M, N, K), stream)
+    _run_on(device, stream, lib.gemm_f32_fused, opa, opb, batch, M, N, K, A.data_ptr(), lda, sa,
+            B.data_ptr(), ldb, sb, _matrix_arg(e), out.data_ptr(), ldc, sc, wp, wb)
+    return out
+
+
+def _like(t, op: int, want, name: str, device, stream):
+    """An output laid out as the operand ``t`` of form ``op`` (``want`` True:
+    allocated; a tensor: that one): (tensor, pointer, leading dimension, stride)."""
+    if want is None or want is False:
+        return None, None, 1 << 31, 1 << 59  # not looked at
+    if want is True:
+        *lead, rows, cols = t.shape
+        if op == OP_T:
+            rows, cols = cols, rows
+        ld = max(cols, 1)
+        strides = (rows * ld,) * len(lead) + (ld, 1)
+        new = _empty((*lead, rows, cols), strides, _torch.float32, device, stream)
+        return (new.transpose(-1, -2) if op == OP_T else new), new.data_ptr(), ld, (rows * ld if lead else 0)
+    if tuple(want.shape) != tuple(t.shape):
+        raise ValueError(f"{name} has shape {tuple(want.shape)}, expected {tuple(t.shape)}")
+    stored = want.transpose(-1, -2) if op == OP_T else want
+    got, ld, bs, _ = _float_operand(stored, name, device)
+    if got != OP_N:
+        raise ValueError(f"{name} must be laid out as its operand is "
+                         f"({'a transposed view of a row-major matrix' if op == OP_T else 'row-major'})")
+    return want, stored.data_ptr(), ld, bs
+
+
+def gemm_fused_grad(dC, A, B, *, pre=None, activation: str = "none", dA=True, dB=True, dbias=False,
+                    workspace=None, stream=None):
+    """(dA, dB, dbias): the gradients of ``gemm_fused(A, B, bias=..., activation=activation)``
+    from ``dC``, its result's, and ``pre``, the A @ B + bias that it kept
+    (not needed for "none").  (The residual's gradient is dC.)
+
+    Each of ``dA``, ``dB``, ``dbias`` is True (allocated here, laid out as its
+    operand), a tensor to write, or False (not computed, None returned).  For a batch
+    the gradients are per product, dbias (batch, N).  ``workspace`` (at least
+    gemm_f32_fused_grad_workspace_size bytes) is allocated here when None."""
+    device, lead, batch, M, N, K, (opa, lda, sa), (opb, ldb, sb) = _pair(A, B)
+    kind = _activation(activation)
+    gp, ldg, sg = _sheet(dC, "dC", (*lead, M, N), device)
+    zp, ldz, sz = None, N or 1, 0
+    if kind:
+        if pre is None:
+            raise ValueError(f"the gradient of {activation!r} needs pre")
+        zp, ldz, sz = _sheet(pre, "pre", (*lead, M, N), device)
+    dA, ap, ldda, sda = _like(A, opa, dA, "dA", device, stream)
+    dB, bp, lddb, sdb = _like(B, opb, dB, "dB", device, stream)
+    if dbias is None or dbias is False:
+        dbias, cp, sdc = None, None, 0
+    else:
+        if dbias is True:
+            dbias = _empty((*lead, N), (N, 1) if lead else (1,), _torch.float32, device, stream)
+        cp, sdc = _vector(dbias, "dbias", (*lead, N), device)
+    lib = load()
+    workspace, wp, wb = _space(
+        workspace, lib.gemm_f32_fused_grad_workspace_size(opa, opb, batch, M, N, K, kind, ap is not None,
+                                                          bp is not None, cp is not None), device, stream)
+    _run_on(device, stream, lib.gemm_f32_fused_grad, opa, opb, batch, M, N, K, gp, ldg, sg, kind, zp, ldz, sz,
+            A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, ap, ldda, sda, bp, lddb, sdb, cp, sdc, wp, wb)
+    return dA, dB, dbias
+
+
+def _tokens(X, W, target):
+    """Checks the inputs of the cross entropy: (device, T, V, K, X's and W's leading dimension)."""
+    load()
+    device = X.device
+    if X.dim() != 2 or W.dim() != 2:
+        raise TypeError("X and W must be 2-D float32 GPU tensors")
+    opx, ldx, _, _ = _float_operand(X, "X")
+    opw, ldw, _, _ = _float_operand(W, "W", device)
+    if opx != OP_N or opw != OP_N:
+        raise ValueError("X and W must be row-major")
+    T, K = X.shape
+    V, K2 = W.shape
+    if K != K2:
+        raise ValueError(f"shape mismatch {tuple(X.shape)} x {tuple(W.shape)} transposed")
+    if target.dtype != _torch.int64 or not target.is_cuda:
+        raise TypeError("target must be an int64 GPU tensor")
+    if tuple(target.shape) != (T,):
+        raise ValueError(f"target has shape {tuple(target.shape)}, expected {(T,)}")
+    if target.device != device:
+        raise ValueError(f"target on {target.device}, other operands on {device}")
+    if T > 1 and target.stride(0) != 1:
+        raise ValueError("target must be contiguous")
+    return device, T, V, K, ldx, ldw
+
+
+def _row_out(t, name: str, T: int, device, stream):
+    if t is None:
+        t = _empty((T,), (1,), _torch.float32, device, stream)
+    return t, _vector(t, name, (T,), device)[0]
+
+
+def cross_entropy(X, W, target, *, ignore_index: int = -100, loss=None, lse=None, workspace=None,
+                  stream=None):
+    """(loss, lse) of T tokens over a vocabulary: with ``logits = X @ W.T`` (X
+    T x K, W V x K, row-major float32; never kept), ``lse = logsumexp(logits, 1)``
+    and ``loss[t] = lse[t] - logits[t, target[t]]``, 0 where ``target[t]`` is
+    ``ignore_index``; any other target outside [0, V) gives NaN.  ``loss`` and
+    ``lse`` are written where given; ``workspace`` and ``stream`` as in gemm_fused."""
+    device, T, V, K, ldx, ldw = _tokens(X, W, target)
+    loss, lp = _row_out(loss, "loss", T, device, stream)
+    lse, sp = _row_out(lse, "lse", T, device, stream)
+    lib = load()
+    workspace, wp, wb = _space(workspace, lib.gemm_f32_cross_entropy_workspace_size(T, V, K), device, stream)
+    _run_on(device, stream, lib.gemm_f32_cross_entropy, T, V, K, X.data_ptr(), ldx, W.data_ptr(), ldw,
+            target.data_ptr(), ignore_index, lp, sp, wp, wb)
+    return loss, lse
+
+
+def cross_entropy_grad(X, W, target, grad_loss=None, *, ignore_index: int = -100, dX=True, dW=True,
+                       loss=None, lse=None, workspace=None, stream=None):
+    """(loss, lse, dX, dW): cross_entropy and the gradients of
+    ``(grad_loss * loss).sum()`` (``grad_loss`` (T,), None for ones) with
+    respect to X and W, in three products: one call for a training step.  ``dX`` and ``dW`` are True
+    (allocated here), a row-major tensor to write, or False (not computed).
+    ``workspace`` holds the logits of some tokens at a time: any size from
+    gemm_f32_cross_entropy_grad_workspace_least bytes will do,
+    gemm_f32_cross_entropy_grad_workspace_size (allocated when None) is quickest."""
+    device, T, V, K, ldx, ldw = _tokens(X, W, target)
+    gp = None if grad_loss is None else _vector(grad_loss, "grad_loss", (T,), device)[0]
+    loss, lp = _row_out(loss, "loss", T, device, stream)
+    lse, sp = _row_out(lse, "lse", T, device, stream)
+    dX, xp, lddx, _ = _like(X, OP_N, dX, "dX", device, stream)
+    dW, dwp, lddw, _ = _like(W, OP_N, dW, "dW", device, stream)
+    lib = load()
+    workspace, wp, wb = _space(workspace, lib.gemm_f32_cross_entropy_grad_workspace_size(T, V, K), device,
+                               stream)
+    _run_on(device, stream, lib.gemm_f32_cross_entropy_grad, T, V, K, X.data_ptr(), ldx, W.data_ptr(), ldw,
+            target.data_ptr(), ignore_index, gp, lp, sp, xp, lddx, dwp, lddw, wp, wb)
+    return loss, lse, dX, dW

@@ -1,0 +1,106 @@
+// Internal declarations of the fused operators (include/gemm_f32_fused.h).
+// Nothing here is part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "fused_choice.h"
+
+namespace gemm_f32_impl {
+namespace fused {
+
+typedef float stat2 __attribute__((ext_vector_type(2), aligned(4)));  // (maximum, sum of exponentials)
+
+// One matrix (of a batch); strides in floats.
+struct Operand {
+    const float *p;
+    int64_t ld, stride;
+};
+struct Result {
+    float *p;
+    int64_t ld, stride;
+};
+
+struct Epilogue {
+    int activation;
+    Operand bias;      // ld unused
+    Operand residual;  // p null: none
+    Result pre;        // p null: none
+};
+
+// What the tile kernel does with a tile's sums.
+enum Mode : int {  // of a product
+    kStore = 0,       // the epilogue (or raw slices), stored
+    kStats = 1,       // a maximum and a sum of exponentials per row and 64 columns
+    kStoreStats = 2,  // both; the sums are stored as they are
+};
+
+// C = epilogue(op(A) op(B)); ta: A is stored K x M, tb: B is stored N x K.
+struct Product {
+    int64_t batch;
+    int M, N, K;
+    bool ta, tb;
+    Operand a, b;
+    Epilogue e;
+    Result c;
+    float *slices;  // partial sums [batch][split][M][N], or null
+    int splits;     // slices of K (1: none)
+    // kStats, kStoreStats (no batch, no slices): stats[row * groups + column / 64];
+    // at_target[row] gets the sum in column target[row], where there is one.
+    Mode mode;
+    stat2 *stats;
+    int groups;
+    const int64_t *target;
+    float *at_target;
+    // Where not null, k with target_k[k] == ignore_k take no part in a tile that
+    // is computed again because a sum came out infinite or NaN.
+    const int64_t *target_k;
+    int64_t ignore_k;
+};
+
+hipError_t launch_product(const Product &, hipStream_t);
+
+// The tile kernels, by operand form (fused_nn.hip ...); `tile` as in
+// fused_choice.h.
+hipError_t launch_tile_nn(const Product &, int tile, hipStream_t);
+hipError_t launch_tile_nt(const Product &, int tile, hipStream_t);
+hipError_t launch_tile_tn(const Product &, int tile, hipStream_t);
+hipError_t launch_tile_tt(const Product &, int tile, hipStream_t);
+
+// C = epilogue(sum over the slices, in their order).
+hipError_t launch_sum_slices(const Product &, hipStream_t);
+
+// dZ = dC act'(Z), and the sums of its columns over blocks of rows; either may
+// be absent (dz.p null; partial null).
+struct Slope {
+    int64_t batch;
+    int M, N;
+    int activation;
+    Operand dc, pre;
+    Result dz;
+    float *partial;  // [batch][blocks][N]
+    int blocks, rows;  // rows a block
+    Result dbias;    // ld unused
+};
+hipError_t launch_slope(const Slope &, hipStream_t);
+
+// The rest of the cross entropy: T rows, row t of `stats` in `groups` pieces.
+struct Loss {
+    int T, V;
+    const stat2 *stats;
+    int groups;
+    const float *at_target;
+    const int64_t *target;
+    int64_t ignore;
+    float *loss, *lse;          // loss may be null
+    const float *grad_loss;     // null: ones
+    float *logits;              // launch_probabilities: T x V, in place
+};
+hipError_t launch_loss(const Loss &, hipStream_t);
+// logits = grad_loss (exp(logits - lse) - (v == target)), zero for ignored rows
+hipError_t launch_probabilities(const Loss &, hipStream_t);
+
+}  // namespace fused
+}  // namespace gemm_f32_impl

@@ -1,0 +1,87 @@
+// Device helpers of the fused operators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gemm_f32_fused.h"
+#include "fused.h"
+#include "gemm_internal.h"
+
+namespace gemm_f32_impl {
+namespace fused {
+
+typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));  // 16 bytes at any word
+typedef float float2u __attribute__((ext_vector_type(2), aligned(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kRootHalf = 0.70710678118654752440f;
+constexpr float kRoot2OverPi = 0.79788456080286535588f;
+constexpr float kRootHalfOverPi = 0.39894228040143267794f;  // 1 / sqrt(2 pi)
+constexpr float kCubic = 0.044715f;
+
+// 1 / (1 + exp(-u)), by the exponential that cannot overflow.
+__device__ __forceinline__ float logistic(float u) {
+    const float t = expf(-fabsf(u));
+    return (u < 0.0f ? t : 1.0f) / (1.0f + t);
+}
+
+// (1 + erf(z / sqrt 2)) / 2 as erfc(-z / sqrt 2) / 2: without the difference
+// of two numbers near 1 that loses the left tail.
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-z * kRootHalf); }
+
+// Beyond these |z| the value of a tail is below FP32's range; z itself may be
+// infinite there, and 0 times it would be NaN.
+__device__ __forceinline__ float activate(int kind, float z) {
+    switch (kind) {
+        case GEMM_F32_ACT_RELU: return z < 0.0f ? 0.0f : z;
+        case GEMM_F32_ACT_GELU: return z < -15.0f ? 0.0f : z * normal_cdf(z);
+        // (1 + tanh u) / 2 is the logistic function of 2 u
+        case GEMM_F32_ACT_GELU_TANH:
+            return z < -15.0f ? 0.0f : z * logistic(2.0f * kRoot2OverPi * (z + kCubic * z * z * z));
+        case GEMM_F32_ACT_SILU: return z < -200.0f ? 0.0f : z * logistic(z);
+        default: return z;
+    }
+}
+
+__device__ __forceinline__ float slope(int kind, float z) {
+    switch (kind) {
+        case GEMM_F32_ACT_RELU: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
+        case GEMM_F32_ACT_GELU: {
+            if (fabsf(z) > 15.0f) return z > 0.0f ? 1.0f : 0.0f;
+            return normal_cdf(z) + z * kRootHalfOverPi * expf(-0.5f * z * z);
+        }
+        case GEMM_F32_ACT_GELU_TANH: {
+            if (fabsf(z) > 15.0f) return z > 0.0f ? 1.0f : 0.0f;
+            const float q = logistic(2.0f * kRoot2OverPi * (z + kCubic * z * z * z));
+            return q + z * q * (1.0f - q) * (2.0f * kRoot2OverPi) * (1.0f + 3.0f * kCubic * z * z);
+        }
+        case GEMM_F32_ACT_SILU: {
+            if (fabsf(z) > 200.0f) return z > 0.0f ? 1.0f : 0.0f;
+            const float q = logistic(z);
+            return q + z * q * (1.0f - q);
+        }
+        default: return 1.0f;
+    }
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
+
+// Two running (maximum, sum of exp(x - maximum)) as one.  An empty piece is
+// (-inf, 0).  A maximum of +inf or NaN makes the sum NaN, as the formula does.
+__device__ __forceinline__ void merge_stats(float &m, float &s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    s = s * expf(m - base) + s2 * expf(m2 - base);
+    m = top;
+}
+
+}  // namespace fused
+}  // namespace gemm_f32_impl
