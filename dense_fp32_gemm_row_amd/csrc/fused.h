@@ -45,6 +45,7 @@ struct Product {
     Operand a, b;
     Epilogue e;
     Result c;
+    bool narrow;    // rows of a tile span less than 2^32 bytes 
     float *slices;  // partial sums [batch][split][M][N], or null
     int splits;     // slices of K (1: none)
     // kStats, kStoreStats (no batch, no slices): stats[row * groups + column / 64];
@@ -54,10 +55,10 @@ struct Product {
     int groups;
     const int64_t *target;
     float *at_target;
-    // Where not null, k with target_k[k] == ignore_k take no part in a tile that
-    // is computed again because a sum came out infinite or NaN.
+    // Where not null, k with target_k[k] == ignore (whose factors of A are zero) take
+    // no part in a tile that is computed again because a sum came out infinite or NaN.
     const int64_t *target_k;
-    int64_t ignore_k;
+    int64_t ignore;
 };
 
 hipError_t launch_product(const Product &, hipStream_t);

@@ -291,7 +291,7 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
     fused::Product p = plain_product(1, T, V, K, false, {X, ldx, 0}, true, {W, ldw, 0}, {}, nullptr);
     p.mode = fused::kStats;
     p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * T), p.groups = groups_of(V);
-    p.target = target;
+    p.target = target, p.ignore = ignore_index;
     fused::Loss l{};
     l.T = p.M, l.V = p.N, l.stats = p.stats, l.groups = p.groups, l.at_target = p.at_target;
     l.target = target, l.ignore = ignore_index, l.loss = loss, l.lse = lse != nullptr ? lse : at + T;
@@ -348,7 +348,7 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, V, 0}, nullptr);
             p.mode = fused::kStoreStats;
             p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * n), p.groups = groups_of(V);
-            p.target = target + t0;
+            p.target = target + t0, p.ignore = ignore_index;
             err = run(p, s);
             fused::Loss l{};
             l.T = p.M, l.V = p.N, l.stats = p.stats, l.groups = p.groups, l.at_target = p.at_target;
@@ -363,7 +363,7 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
                                         {dX + t0 * lddx, lddx, 0}, room(n, V)), s);
             if (err == hipSuccess && dW != nullptr) {
                 p = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0}, room(V, n));
-                p.target_k = target + t0, p.ignore_k = ignore_index;
+                p.target_k = target + t0, p.ignore = ignore_index;
                 if (t0 > 0) p.e.residual = {dW, lddw, 0};  // the pieces before
                 err = run(p, s);
             }

@@ -6,21 +6,14 @@
 #include <cstdint>
 
 #include "../../include/gemm_f32_fused.h"
+#include "device_common.h"
 #include "fused.h"
 #include "gemm_internal.h"
 
 namespace gemm_f32_impl {
 namespace fused {
 
-typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));  // 16 bytes at any word
-typedef float float2u __attribute__((ext_vector_type(2), aligned(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float float2u __attribute__((ext_vector_type(2), aligned(4)));  // 8 bytes at any word
 
 constexpr float kRootHalf = 0.70710678118654752440f;
 constexpr float kRoot2OverPi = 0.79788456080286535588f;
@@ -70,6 +63,30 @@ __device__ __forceinline__ float slope(int kind, float z) {
         }
         default: return 1.0f;
     }
+}
+
+// The three bf16 parts of four values x = h + m + l, rounded to nearest each:
+// h takes 8 of the 24 bits, m 8 of the at most 16 left, and what is then left
+// has no more than 8, so the sum is exact (down to bf16's least value, 2^-133).
+struct Parts {
+    u32x2 p[3];
+};
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+__device__ __forceinline__ Parts split4(float x0, float x1, float x2, float x3) {
+    Parts r;
+    float x[4] = {x0, x1, x2, x3};
+#pragma unroll
+    for (int c = 0; c < 3; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t v = pack_bf16(x[2 * i], x[2 * i + 1]);
+            r.p[c][i] = v;
+            x[2 * i] -= __builtin_bit_cast(float, v << 16);
+            x[2 * i + 1] -= __builtin_bit_cast(float, v & 0xffff0000u);
+        }
+    return r;
 }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }

@@ -125,8 +125,17 @@ hipError_t launch_probabilities(const Loss &l, hipStream_t stream) {
     return hipGetLastError();
 }
 
+namespace {
+// The tiles' loads count bytes from a tile's first element in 32 bits: 256 rows
+// of k, or 16 k of rows.
+bool narrow_operand(int64_t ld, bool k_contiguous) {
+    return k_contiguous ? ld <= (int64_t{1} << 22) - 64 : ld <= int64_t{1} << 25;
+}
+}  // namespace
+
 hipError_t launch_product(const Product &asked, hipStream_t stream) {
     Product p = asked;
+    p.narrow = narrow_operand(p.a.ld, !p.ta) && narrow_operand(p.b.ld, p.tb);
     const Choice c = choose(p.batch, p.M, p.N, p.K, p.splits);
     p.splits = c.splits;
     const hipError_t err = p.ta ? (p.tb ? launch_tile_tt(p, c.tile, stream) : launch_tile_tn(p, c.tile, stream))

@@ -37,146 +37,375 @@ __device__ __forceinline__ float element(const float *p, int64_t ld, int row, in
     return KC ? p[row * ld + k] : p[k * ld + row];
 }
 
+// A thread's share of the stages of one operand: E elements, 4 consecutive k of E / 4
+// rows.  Where k is contiguous (KC) these are 16-byte loads, 4 lanes a row;
+// where rows are, E / 4 neighbouring rows at 4 k.  Every address stays inside
+// the operand: rows past its end repeat the last ones, which then are written
+// to LDS where those belong.
+template <int ROWS, int E, int THREADS, bool KC>
+struct Share {
+    static_assert(ROWS * kStage == E * THREADS, "");
+    static constexpr int kUnits = E / 4;  // of 4 k of a row each
+    const char *base;   // of the operand's tile at k = 0
+    uint32_t off[KC ? kUnits : 4];
+    int lds[kUnits];    // byte in a plane
+    int64_t step;       // bytes a stage
+    float v[E];
+
+    __device__ __forceinline__ Share(const float *p, int64_t ld, int rows, bool more, int tid) {
+        if constexpr (KC) {
+            base = reinterpret_cast<const char *>(p);
+            step = kStage * 4;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int o = tid + u * THREADS, q = o & 3, place = o >> 2;
+                off[u] = static_cast<uint32_t>(min(row_at(place), rows - 1)) * static_cast<uint32_t>(ld * 4) + 16 * q;
+                lds[u] = (q >> 1) * ROWS * 16 + place * 16 + (q & 1) * 8;
+            }
+        } else {
+            constexpr int kLanes = ROWS / kUnits;
+            const int j = tid % kLanes, q = tid / kLanes;
+            // a lone last row is loaded with the one before the tile
+            const int back = rows < kUnits && more ? kUnits - rows : 0;
+            const int r = min(kUnits * j, rows - kUnits + back);
+            base = reinterpret_cast<const char *>(p - back);
+            step = kStage * 4 * ld;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                off[i] = static_cast<uint32_t>(4 * q + i) * static_cast<uint32_t>(ld * 4) + 4 * r;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+                lds[u] = (q >> 1) * ROWS * 16 + place_of_row((r - back + u + ROWS) % ROWS) * 16 + (q & 1) * 8;
+        }
+    }
+    __device__ __forceinline__ void load(int stage) {
+        const char *at = base + stage * step;
+        if constexpr (KC) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const f32x4 x = *reinterpret_cast<const float4u *>(at + off[u]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * u + i] = x[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kUnits == 2) {
+                    const f32x2 x = *reinterpret_cast<const float2u *>(at + off[i]);
+                    v[i] = x[0], v[4 + i] = x[1];
+                } else {
+                    v[i] = *reinterpret_cast<const float *>(at + off[i]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void put(int u, char *planes) const {
+        const Parts s = split4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+            *reinterpret_cast<u32x2 *>(planes + c * (2 * ROWS * 16) + lds[u]) = s.p[c];
+    }
+};
+
+// Tiles of a CU, for the registers that a wavefront may take.
+constexpr int per_cu(int fm) { return fm == 4 ? 1 : fm == 2 ? 2 : 3; }
+
 template <int WM, int WN, int FM, bool TA, bool TB>
-__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Product p, int tiles_m, int tiles_n,
-                                                             int64_t tiles, int len) {
+__global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product p, int tiles_m, int tiles_n,
+                                                                        int64_t first_tile, int len) {
     using T = Tile<WM, WN, FM>;
     constexpr int BM = T::BM, BN = T::BN, kThreads = T::kThreads;
-    __shared__ __align__(16) float xs[kStage][BM];
-    __shared__ __align__(16) float ys[kStage][BN];
+    constexpr int kPlanesA = 3 * 2 * BM * 16, kBuffer = kPlanesA + 3 * 2 * BN * 16;
+    constexpr int kRowOut = 68;  // floats: 64 of a row of results, 16 bytes apart from the next one's banks
+    static_assert(kBuffer >= (BM + BN) * kStage * 4, "");
+    static_assert(2 * kBuffer >= T::kWaves * 32 * kRowOut * 4, "");
+    __shared__ __align__(1024) char memory[2 * kBuffer];
+    auto &xs = *reinterpret_cast<float(*)[kStage][BM]>(memory);
+    auto &ys = *reinterpret_cast<float(*)[kStage][BN]>(memory + BM * kStage * 4);
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
-    const int64_t per = static_cast<int64_t>(tiles_m) * tiles_n;
-    for (int64_t id = xcd_remap(blockIdx.x, gridDim.x); id < tiles; id += gridDim.x) {
-        const int64_t slice = id / per, b = slice / p.splits;
-        int tm, tn;
-        grouped_tile(static_cast<int>(id - slice * per), tiles_m, tiles_n, 8, tm, tn);
-        const int m0 = tm * BM, n0 = tn * BN;
-        const int k0 = static_cast<int>(slice - b * p.splits) * len;
-        const int k1 = static_cast<int>(min(static_cast<int64_t>(k0) + len, static_cast<int64_t>(p.K)));
-        const float *A = p.a.p + b * p.a.stride + (TA ? m0 : m0 * p.a.ld);
-        const float *B = p.b.p + b * p.b.stride + (TB ? n0 * p.b.ld : n0);
-        const int rows = p.M - m0, cols = p.N - n0;
+    const int64_t per = static_cast<int64_t>(tiles_m) * tiles_n, id = first_tile + xcd_remap(blockIdx.x, gridDim.x);
+    const int64_t slice = id / per, b = slice / p.splits;
+    int tm, tn;
+    grouped_tile(static_cast<int>(id - slice * per), tiles_m, tiles_n, 8, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int k0 = static_cast<int>(slice - b * p.splits) * len;
+    const int k1 = max(k0, static_cast<int>(min(static_cast<int64_t>(k0) + len, static_cast<int64_t>(p.K))));
+    const float *A = p.a.p + b * p.a.stride + (TA ? m0 : m0 * p.a.ld);
+    const float *B = p.b.p + b * p.b.stride + (TB ? n0 * p.b.ld : n0);
+    const int rows = p.M - m0, cols = p.N - n0;
 
-        f32x16 acc[FM][2];
-        auto clear = [&]() {
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) acc[i][f] = f32x16{};
-        };
-
-        // FP32 multiplies: any shape, any value, one stage at a time.
-        auto general = [&](int first, int last, const int64_t *skip) {
-            for (int k = first; k < last; k += kStage) {
-                __syncthreads();
-                for (int o = tid; o < BM * kStage; o += kThreads) {
-                    const int r = TA ? o % BM : o / kStage, q = TA ? o / BM : o % kStage;
-                    float v = element<!TA>(A, p.a.ld, r, rows, k + q, last);
-                    if (skip != nullptr && k + q < last && skip[k + q] == p.ignore_k) v = 0.0f;
-                    xs[q][place_of_row(r)] = v;
-                }
-                for (int o = tid; o < BN * kStage; o += kThreads) {
-                    const int r = TB ? o / kStage : o % BN, q = TB ? o % kStage : o / BN;
-                    float v = element<TB>(B, p.b.ld, r, cols, k + q, last);
-                    if (skip != nullptr && k + q < last && skip[k + q] == p.ignore_k) v = 0.0f;
-                    ys[q][place_of_row(r)] = v;
-                }
-                __syncthreads();
-#pragma unroll
-                for (int q = 0; q < kStage; q += 2) {
-                    float y[2];
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) y[f] = ys[q + half][64 * wn + 32 * f + col];
-#pragma unroll
-                    for (int i = 0; i < FM; ++i) {
-                        const float x = xs[q + half][32 * (FM * wm + i) + col];
-#pragma unroll
-                        for (int f = 0; f < 2; ++f)
-                            acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, y[f], acc[i][f], 0, 0, 0);
-                    }
-                }
-            }
-            __syncthreads();
-        };
-
-        clear();
-        general(k0, k1, p.target_k);
-
-        // ---- results: a lane has two neighbouring columns of FM * 16 rows ----
-        const int n = n0 + 64 * wn + 4 * (col & 15) + 2 * (col >> 4);
-        // row r of block i, from the wavefront's first
-        auto row_of = [&](int i, int r) {
-            return row_at(32 * (FM * wm + i) + (r & 3) + 8 * (r >> 2) + 4 * half);
-        };
-        auto put = [&](float *dst, int64_t at, float v0, float v1) {
-            if (n + 1 < p.N)
-                *reinterpret_cast<float2u *>(dst + at) = float2u{v0, v1};
-            else
-                dst[at] = v0;
-        };
-        auto get = [&](const float *src, int64_t at) {
-            return n + 1 < p.N ? *reinterpret_cast<const float2u *>(src + at) : float2u{src[at], 0.0f};
-        };
-        if (p.mode != kStore) {
-            const int group = tn * WN + wn;
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int m = m0 + row_of(i, r);
-                    const float v0 = n < p.N ? acc[i][0][r] : -__builtin_inff();
-                    const float v1 = n + 1 < p.N ? acc[i][1][r] : -__builtin_inff();
-                    float top = fmaxf(v0, v1);
-#pragma unroll
-                    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-                    const float base = top == -__builtin_inff() ? 0.0f : top;
-                    float s = expf(v0 - base) + expf(v1 - base);
-#pragma unroll
-                    for (int d = 1; d < 32; d *= 2) s += __shfl_xor(s, d);
-                    if (m < p.M) {
-                        if (n0 + 64 * wn < p.N && col == 0)
-                            p.stats[static_cast<int64_t>(m) * p.groups + group] = stat2{top, s};
-                        const int64_t t = p.target[m] - n;
-                        if (t == 0 && n < p.N) p.at_target[m] = v0;
-                        if (t == 1 && n + 1 < p.N) p.at_target[m] = v1;
-                        if (p.mode == kStoreStats && n < p.N) put(p.c.p, m * p.c.ld + n, v0, v1);
-                    }
-                }
-            continue;
-        }
-        if (n >= p.N) continue;
-        if (p.splits > 1) {
-            float *W = p.slices + slice * p.M * p.N;
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t m = m0 + row_of(i, r);
-                    if (m < p.M) put(W, m * p.N + n, acc[i][0][r], acc[i][1][r]);
-                }
-            continue;
-        }
-        float2u bias{0.0f, 0.0f};
-        if (p.e.bias.p != nullptr) bias = get(p.e.bias.p + b * p.e.bias.stride, n);
-        float *C = p.c.p + b * p.c.stride, *Z = p.e.pre.p + b * p.e.pre.stride;
-        const float *R = p.e.residual.p + b * p.e.residual.stride;
+    f32x16 acc[FM][2];
+    auto clear = [&]() {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t m = m0 + row_of(i, r);
-                if (m >= p.M) continue;
-                const float z0 = acc[i][0][r] + bias[0], z1 = acc[i][1][r] + bias[1];
-                if (p.e.pre.p != nullptr) put(Z, m * p.e.pre.ld + n, z0, z1);
-                float v0 = activate(p.e.activation, z0), v1 = activate(p.e.activation, z1);
-                if (p.e.residual.p != nullptr) {
-                    const float2u q = get(R, m * p.e.residual.ld + n);
-                    v0 += q[0], v1 += q[1];
-                }
-                put(C, m * p.c.ld + n, v0, v1);
+            for (int f = 0; f < 2; ++f) acc[i][f] = f32x16{};
+    };
+
+    // FP32 multiplies: any shape, any value, one stage at a time.
+    auto general = [&](int first, int last, const int64_t *skip) {
+        for (int k = first; k < last; k += kStage) {
+            __syncthreads();
+#pragma unroll 1
+            for (int o = tid; o < BM * kStage; o += kThreads) {
+                const int r = TA ? o % BM : o / kStage, q = TA ? o / BM : o % kStage;
+                float v = element<!TA>(A, p.a.ld, r, rows, k + q, last);
+                if (skip != nullptr && k + q < last && skip[k + q] == p.ignore) v = 0.0f;
+                xs[q][place_of_row(r)] = v;
             }
+#pragma unroll 1
+            for (int o = tid; o < BN * kStage; o += kThreads) {
+                const int r = TB ? o / kStage : o % BN, q = TB ? o % kStage : o / BN;
+                float v = element<TB>(B, p.b.ld, r, cols, k + q, last);
+                if (skip != nullptr && k + q < last && skip[k + q] == p.ignore) v = 0.0f;
+                ys[q][place_of_row(r)] = v;
+            }
+            __syncthreads();
+#pragma unroll 2
+            for (int q = 0; q < kStage; q += 2) {
+                float y[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) y[f] = ys[q + half][64 * wn + 32 * f + col];
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    const float x = xs[q + half][32 * (FM * wm + i) + col];
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, y[f], acc[i][f], 0, 0, 0);
+                }
+            }
+        }
+        __syncthreads();
+    };
+
+            // Whole stages on the bf16 units.  A stage runs in 6 phases, a part of A
+            // times a part of B each.  Under a phase's products the next phase's
+            // operands are read from LDS, and the next stage's values, loaded into registers a
+            // stage ago, are split and written to the other buffer and their
+            // registers loaded again.  The one barrier lies before the last phase, under
+            // which the next stage's first operands are read.
+            auto quick = [&](int first, int last) {
+                Share<BM, BM * kStage / kThreads, kThreads, !TA> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid);
+                Share<BN, BN * kStage / kThreads, kThreads, TB> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid);
+                constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
+                const int stages = (last - first) / kStage;
+                u32x4 x[2][FM], y[3][2];  // parts of A by turns; the parts of B
+                const int ra = half * BM * 16 + (32 * FM * wm + col) * 16;
+                const int rb = kPlanesA + half * BN * 16 + (64 * wn + col) * 16;
+                auto fetch_a = [&](int set, int part, const char *from) {
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+                        x[set][i] = *reinterpret_cast<const u32x4 *>(from + part * (2 * BM * 16) + ra + 32 * 16 * i);
+                };
+                auto fetch_b = [&](int part, const char *from) {
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+                        y[part][f] = *reinterpret_cast<const u32x4 *>(from + part * (2 * BN * 16) + rb + 32 * 16 * f);
+                };
+                auto multiply = [&](int set, int part) {
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int f = i & 1 ? 1 - k : k;
+                            acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                __builtin_bit_cast(bf16x8, x[set][i]), __builtin_bit_cast(bf16x8, y[part][f]), acc[i][f], 0, 0, 0);
+                        }
+                    // between two matrix instructions: an LDS read, some of the
+                    // splitting, and its writes and loads
+#pragma unroll
+                    for (int k = 0; k < FM * 2; ++k) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                    }
+                    // the sums so far are used here, so their instructions stay ahead
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) asm volatile("" : "+v"(acc[i][f]));
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                // Set P of x holds l of A at the start, 1 - P at the end.
+                auto stage = [&](auto pc, int s, const char *from, char *to) {
+                    constexpr int P = decltype(pc)::value, Q = 1 - P;
+                    const int next = min(s + 2, stages - 1);  // past the end: loaded again, not used
+                    fetch_a(Q, 1, from);
+                    sa.put(0, to);
+                    multiply(P, 0);  // l h
+                    fetch_b(1, from);
+                    if constexpr (kUa > 1) sa.put(1, to);
+                    sa.load(next);
+                    multiply(Q, 0);  // m h
+                    fetch_a(P, 0, from);
+                    sb.put(0, to + kPlanesA);
+                    multiply(Q, 1);  // m m
+                    fetch_b(2, from);
+                    if constexpr (kUb > 1) sb.put(1, to + kPlanesA);
+                    sb.load(next);
+                    multiply(P, 1);  // h m
+                    multiply(P, 0);  // h h
+                    wait_older<63>();  // LDS accesses alone
+                    barrier_only();
+                    fetch_a(Q, 2, to);
+                    fetch_b(0, to);
+                    multiply(P, 2);  // h l
+                };
+                constexpr std::integral_constant<int, 0> p0;
+                constexpr std::integral_constant<int, 1> p1;
+                char *even = memory, *odd = memory + kBuffer;
+                sa.load(0), sb.load(0);
+#pragma unroll
+                for (int u = 0; u < kUa; ++u) sa.put(u, even);
+#pragma unroll
+                for (int u = 0; u < kUb; ++u) sb.put(u, even + kPlanesA);
+                sa.load(min(1, stages - 1)), sb.load(min(1, stages - 1));
+                wait_older<63>();
+                barrier_only();
+                fetch_a(0, 2, even);
+                fetch_b(0, even);
+                int s = 0;
+                for (; s + 1 < stages; s += 2) {
+                    stage(p0, s, even, odd);
+                    stage(p1, s + 1, odd, even);
+                }
+                if (s < stages) stage(p0, s, even, odd);
+            };
+
+    // The results of a block of 32 x 64 by way of LDS, so that a lane has 4
+    // neighbouring columns of a row and the code below is there once: `use` gets
+    // the row and column of the tile and the 4 values.
+    float *out = reinterpret_cast<float *>(memory) + wave * 32 * kRowOut;
+    auto each = [&](auto use) {
+#pragma unroll 1
+        for (int i = 0; i < FM; ++i) {
+            auto dump = [&](auto ic) {
+                constexpr int I = decltype(ic)::value;
+                if constexpr (I < FM)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        *reinterpret_cast<f32x2 *>(out + ((r & 3) + 8 * (r >> 2) + 4 * half) * kRowOut +
+                                                   4 * (col & 15) + 2 * (col >> 4)) = f32x2{acc[I][0][r], acc[I][1][r]};
+            };
+            if (i == 0) dump(std::integral_constant<int, 0>{});
+            if (i == 1) dump(std::integral_constant<int, 1>{});
+            if (i == 2) dump(std::integral_constant<int, 2>{});
+            if (i == 3) dump(std::integral_constant<int, 3>{});
+            wait_older<63>();
+#pragma unroll 1
+            for (int q = lane >> 4; q < 32; q += 4)
+                use(row_at(32 * (FM * wm + i) + q), 64 * wn + 4 * (lane & 15),
+                    *reinterpret_cast<const f32x4 *>(out + q * kRowOut + 4 * (lane & 15)));
+            wait_older<63>();
+        }
+    };
+    // Whether a sum that counts is infinite or NaN (an infinity's parts are NaN).
+    auto odd = [&]() {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) t = fmaf(acc[i][f][r], 0.0f, t);
+        bool found = false;
+        if (__ballot(t != 0.0f))  // NaN too
+            each([&](int r, int c, f32x4 v) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (r < rows && c + e < cols && !finite(v[e]) && (p.mode == kStore || p.target[m0 + r] != p.ignore))
+                        found = true;
+            });
+        return found;
+    };
+
+    clear();
+    // a lone row of an operand whose rows are contiguous has no neighbour to be loaded with
+    const bool lone = (TA && FM > 1 && p.M < 2) || (!TB && p.N < 2);
+    const int whole = p.narrow && !lone ? k0 + (k1 - k0) / kStage * kStage : k0;
+    bool quickly = whole > k0;
+    if (quickly) quick(k0, whole);
+    for (int from = whole;; from = k0) {
+        if (from < k1) general(from, k1, p.target_k);
+        if (!quickly) break;
+        quickly = false;
+        if (!__syncthreads_or(odd())) break;
+        clear();
+    }
+
+    // ---- results ----
+    auto put = [&](float *dst, int c, f32x4 v) {
+        if (c + 3 < cols) {
+            *reinterpret_cast<float4u *>(dst + c) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (c + e < cols) dst[c + e] = v[e];
+        }
+    };
+    auto get = [&](const float *src, int c) {
+        f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
+        if (c + 3 < cols) {
+            v = *reinterpret_cast<const float4u *>(src + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (c + e < cols) v[e] = src[c + e];
+        }
+        return v;
+    };
+    if (p.mode != kStore) {
+        each([&](int r, int c, f32x4 v) {
+            float top = -__builtin_inff(), s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = c + e < cols ? fmaxf(top, v[e]) : top;
+#pragma unroll
+            for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            const float base = top == -__builtin_inff() ? 0.0f : top;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s += c + e < cols ? expf(v[e] - base) : 0.0f;
+#pragma unroll
+            for (int d = 1; d < 16; d *= 2) s += __shfl_xor(s, d);
+            if (r < rows && c < cols) {
+                const int64_t m = m0 + r;
+                if ((lane & 15) == 0) p.stats[m * p.groups + (n0 + c) / 64] = stat2{top, s};
+                const int64_t t = p.target[m] - n0 - c;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t == e && c + e < cols) p.at_target[m] = v[e];
+                if (p.mode == kStoreStats) put(p.c.p + m * p.c.ld + n0, c, v);
+            }
+        });
+    } else if (p.splits > 1) {
+        float *W = p.slices + (slice * p.M + m0) * p.N + n0;
+        each([&](int r, int c, f32x4 v) {
+            if (r < rows && c < cols) put(W + static_cast<int64_t>(r) * p.N, c, v);
+        });
+    } else {
+        float *C = p.c.p + b * p.c.stride + m0 * p.c.ld + n0;
+        float *Z = p.e.pre.p != nullptr ? p.e.pre.p + b * p.e.pre.stride + m0 * p.e.pre.ld + n0 : nullptr;
+        const float *R = p.e.residual.p != nullptr ? p.e.residual.p + b * p.e.residual.stride + m0 * p.e.residual.ld + n0
+                                                   : nullptr;
+        const int c = 64 * wn + 4 * (lane & 15);
+        const f32x4 bias = p.e.bias.p != nullptr ? get(p.e.bias.p + b * p.e.bias.stride + n0, c)
+                                                 : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        each([&](int r, int, f32x4 v) {
+            if (r >= rows || c >= cols) return;
+            if (p.e.bias.p != nullptr) v += bias;
+            if (Z != nullptr) put(Z + r * p.e.pre.ld, c, v);
+            if (p.e.activation != GEMM_F32_ACT_NONE)
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                    const float y = activate(p.e.activation, v[0]);
+                    v = f32x4{v[1], v[2], v[3], y};
+                }
+            if (R != nullptr) v += get(R + r * p.e.residual.ld, c);
+            put(C + r * p.c.ld, c, v);
+        });
     }
 }
 
@@ -187,15 +416,20 @@ hipError_t launch_one(const Product &p, hipStream_t stream) {
     const int64_t tiles = static_cast<int64_t>(tm) * tn * p.batch * p.splits;
     // whole stages a slice
     const int len = static_cast<int>(div_up(div_up(p.K, kStage), p.splits)) * kStage;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 21));
-    tile_kernel<WM, WN, FM, TA, TB><<<grid, T::kThreads, 0, stream>>>(p, tm, tn, tiles, len);
-    return hipGetLastError();
+    for (int64_t t = 0; t < tiles; t += 1 << 21) {  // (a launch's threads are counted in 32 bits)
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles - t, 1 << 21));
+        tile_kernel<WM, WN, FM, TA, TB><<<grid, T::kThreads, 0, stream>>>(p, tm, tn, t, len);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 template <bool TA, bool TB>
 hipError_t launch_tile(const Product &p, int tile, hipStream_t stream) {
-    (void)tile;
-    return launch_one<2, 2, 1, TA, TB>(p, stream);
+    return tile == 0   ? launch_one<2, 4, 4, TA, TB>(p, stream)
+           : tile == 1 ? launch_one<2, 2, 2, TA, TB>(p, stream)
+                       : launch_one<2, 2, 1, TA, TB>(p, stream);
 }
 
 }  // namespace fused

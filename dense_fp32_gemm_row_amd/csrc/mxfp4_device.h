@@ -5,42 +5,18 @@
 
 #include <cstdint>
 
+#include "device_common.h"
 #include "gemm_internal.h"
 #include "mxfp4.h"
 
 namespace gemm_f32_impl {
 namespace mx {
 
-typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));  // 16 bytes at any word
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
 // The conversion instructions take a scale as a float and use its exponent
 // byte alone: 0 is 2^-127 and 255 NaN, as in the format.
 __device__ __forceinline__ float scale_of(uint32_t e) { return __builtin_bit_cast(float, e << 23); }
 
 typedef __attribute__((address_space(3))) void *lptr_t;
-
-// Waits until at most N of this wavefront's most recent vector-memory
-// instructions and no LDS access are outstanding.  The empty asm statements
-// keep memory accesses on their side.
-template <int N>
-__device__ __forceinline__ void wait_older() {
-    static_assert(N >= 0 && N < 64, "vmcnt has 6 bits");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-    asm volatile("" ::: "memory");
-}
-__device__ __forceinline__ void barrier_only() {
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 constexpr int kStream = 2;  // cache policy of buffer stores: non-temporal
 

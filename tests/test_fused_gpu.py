@@ -63,6 +63,35 @@ def test_product(M, N, K, ops):
     g.check()
 
 
+# whole and ragged tiles of every size: the last tile a row, a few, or all of it
+LARGE = [(3584, 3840, 64), (3329, 3585, 47), (3331, 3842, 16), (3400, 3700, 130),
+         (1792, 1920, 64), (1665, 1793, 47), (1667, 1922, 33), (1700, 1900, 400)]
+
+
+@pytest.mark.parametrize("ops", ["NN", "NT", "TN", "TT"])
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_products(M, N, K, ops):
+    A, B = stored(1, M, K, ops[0], 1), stored(2, K, N, ops[1], 2)
+    bias, res = rnd(3, N), stored(4, M, N, "N", 5)
+    c, z = Guarded(M, N), Guarded(M, N, 1)
+    b.gemm_fused(A, B, c.out, bias=bias, activation="gelu_tanh", residual=res, pre=z.out)
+    want = o.layer(A, B, bias, "gelu_tanh", res)
+    o.check(c.out, want["y"], want["y_tol"])
+    o.check(z.out, want["z"], want["z_tol"])
+    c.check(), z.check()
+
+
+@pytest.mark.parametrize("n,M,N,K", [(25, 700, 780, 48), (40, 260, 385, 50), (70, 100, 300, 33)])
+@pytest.mark.parametrize("ops", ["NN", "TT"])
+def test_large_batches(n, M, N, K, ops):
+    A = rnd(1, n, *((M, K) if ops[0] == "N" else (K, M)))
+    B = rnd(2, n, *((K, N) if ops[1] == "N" else (N, K)))
+    A, B = (A if ops[0] == "N" else A.transpose(1, 2)), (B if ops[1] == "N" else B.transpose(1, 2))
+    y = b.gemm_fused(A, B)
+    want = o.layer(A, B)
+    o.check(y, want["y"], want["y_tol"])
+
+
 @pytest.mark.parametrize("M,N,K", [(33, 70, 20), (130, 200, 64), (1, 257, 500), (300, 300, 300)])
 @pytest.mark.parametrize("kind", o.ACTS)
 @pytest.mark.parametrize("with_bias,with_residual,keep", [(True, True, True), (False, False, False), (True, False, True),
@@ -143,7 +172,8 @@ def test_nothing_to_sum(kind):
 SPECIAL = [math.inf, -math.inf, math.nan, 3.4028234663852886e38, -3.4028234663852886e38, 3.3961775292304e38, 1e-40, 0.0]
 
 
-@pytest.mark.parametrize("M,N,K", [(70, 130, 48), (300, 300, 70), (2, 600, 64), (130, 140, 33)])
+@pytest.mark.parametrize("M,N,K", [(70, 130, 48), (300, 300, 70), (2, 600, 64), (130, 140, 33), (3330, 3600, 40),
+                                   (1700, 1900, 50)])
 @pytest.mark.parametrize("ops", ["NN", "NT", "TN", "TT"])
 def test_values_at_the_ends_of_the_range(M, N, K, ops):
     """One special value in a row of A, against columns of B that hold zeros,
@@ -191,7 +221,7 @@ def test_whole_numbers_are_exact(M, N, K):
 @pytest.mark.parametrize("ops", ["NN", "NT", "TN", "TT"])
 @pytest.mark.parametrize("M,N,K,kind", [(1, 1, 1, "relu"), (33, 65, 40, "gelu"), (130, 90, 257, "silu"),
                                         (300, 40, 64, "gelu_tanh"), (64, 128, 33, "none"), (5, 300, 3, "relu"),
-                                        (260, 514, 130, "silu")])
+                                        (260, 514, 130, "silu"), (2000, 3400, 1801, "gelu"), (1801, 1700, 1902, "relu")])
 def test_grad(M, N, K, kind, ops):
     A, B = stored(1, M, K, ops[0], 2), stored(2, K, N, ops[1], 1)
     dC, z = stored(3, M, N, "N", 4), stored(4, M, N, "N", 1, scale=2.0)
@@ -276,7 +306,8 @@ def tokens(T, V, K, seed=0, ignore=-100, scale=2.0):
 
 
 LOSS_SHAPES = [(1, 1, 1), (1, 2, 5), (2, 64, 16), (3, 1000, 40), (64, 128, 32), (65, 129, 33), (100, 777, 65),
-               (130, 64, 64), (1, 5000, 300), (17, 63, 8), (300, 2049, 100), (5, 1, 7), (257, 300, 48), (16, 4096, 64)]
+               (130, 64, 64), (1, 5000, 300), (17, 63, 8), (300, 2049, 100), (5, 1, 7), (257, 300, 48), (16, 4096, 64),
+               (1700, 2000, 72), (3340, 3700, 50), (2000, 9001, 1800)]
 
 
 @pytest.mark.parametrize("T,V,K", LOSS_SHAPES)
