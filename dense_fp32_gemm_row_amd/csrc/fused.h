@@ -30,6 +30,12 @@ struct Epilogue {
     Result pre;        // p null: none
 };
 
+// Of one row of op(A) (column of op(B)), or a block of its k: the largest exponent field,
+// how many values are not zero, and the sum of their exponent fields.
+struct RowStat {
+    int top, count, sum, unused;
+};
+
 // What the tile kernel does with a tile's sums.
 enum Mode : int {  // of a product
     kStore = 0,       // the epilogue (or raw slices), stored
@@ -46,8 +52,13 @@ struct Product {
     Epilogue e;
     Result c;
     bool narrow;    // rows of a tile span less than 2^32 bytes 
+    float *space;   // product_space() bytes, or null
+    // set by launch_product:
     float *slices;  // partial sums [batch][split][M][N], or null
     int splits;     // slices of K (1: none)
+    const RowStat *row_a, *row_b;  // [block of k][batch * rows], or null: no fp16 parts
+    int blocks_a, blocks_b;
+    bool lenient;   // fp16 parts wherever a row's range allows scaling it
     // kStats, kStoreStats (no batch, no slices): stats[row * groups + column / 64];
     // at_target[row] gets the sum in column target[row], where there is one.
     Mode mode;
@@ -62,6 +73,9 @@ struct Product {
 };
 
 hipError_t launch_product(const Product &, hipStream_t);
+// Bytes of workspace that a product is quickest with; it runs with none, too.
+// `slice`: its mode is kStore.
+int64_t product_space(int64_t batch, int64_t M, int64_t N, int64_t K, bool slice);
 
 // The tile kernels, by operand form (fused_nn.hip ...); `tile` as in
 // fused_choice.h.
@@ -69,6 +83,8 @@ hipError_t launch_tile_nn(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_nt(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tn(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tt(const Product &, int tile, hipStream_t);
+
+hipError_t launch_row_stats(const Product &, hipStream_t);
 
 // C = epilogue(sum over the slices, in their order).
 hipError_t launch_sum_slices(const Product &, hipStream_t);

@@ -59,25 +59,20 @@ int check_workspace(void *workspace, int64_t bytes, int64_t need, Bytes *out) {
     return GEMM_F32_OK;
 }
 
-// Slices of K that a product takes when it may, and their bytes.
-int splits_of(int64_t batch, int64_t M, int64_t N, int64_t K) {
-    if (batch == 0 || M == 0 || N == 0 || K == 0) return 1;
-    return fused::choose(batch, M, N, K, fused::kMostSplits).splits;
-}
-int64_t slice_bytes(int64_t batch, int64_t M, int64_t N, int64_t K) {
-    const int splits = splits_of(batch, M, N, K);
-    return splits > 1 ? times(times(times(4 * splits, batch), M), N) : 0;
+// Bytes of a product's own workspace.
+int64_t space_of(int64_t batch, int64_t M, int64_t N, int64_t K, bool slice = true) {
+    if (batch == 0 || M == 0 || N == 0 || K == 0) return 0;
+    return fused::product_space(batch, M, N, K, slice);
 }
 
 fused::Product plain_product(int64_t batch, int64_t M, int64_t N, int64_t K, bool ta, fused::Operand a, bool tb,
-                             fused::Operand b, fused::Result c, float *slices) {
+                             fused::Operand b, fused::Result c, float *space) {
     fused::Product p{};
     p.batch = batch;
     p.M = static_cast<int>(M), p.N = static_cast<int>(N), p.K = static_cast<int>(K);
     p.ta = ta, p.tb = tb;
     p.a = a, p.b = b, p.c = c;
-    p.slices = slices;
-    p.splits = slices != nullptr ? splits_of(batch, M, N, K) : 1;
+    p.space = space;
     p.mode = fused::kStore;
     return p;
 }
@@ -90,11 +85,12 @@ hipError_t run(const fused::Product &p, hipStream_t s) {
 
 // ---- the parts of a gradient's workspace, in floats ----
 struct GradParts {
-    int64_t dz, partial, slices;
+    int64_t dz, partial, space;
     int blocks, rows;
-    int64_t bytes() const { return times(4, plus(plus(dz, partial), slices)); }
+    int64_t bytes() const { return times(4, plus(plus(dz, partial), space)); }
 };
-GradParts grad_parts(int64_t batch, int64_t M, int64_t N, int64_t K, int activation, bool dA, bool dB, bool dbias) {
+GradParts grad_parts(bool ta, bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, int activation, bool dA, bool dB,
+                     bool dbias) {
     GradParts g{};
     // blocks of rows of the bias gradient's first sums: enough to fill the GPU
     const int64_t strips = std::max<int64_t>(1, times(batch, div_up(N, 256)));
@@ -103,8 +99,9 @@ GradParts grad_parts(int64_t batch, int64_t M, int64_t N, int64_t K, int activat
     g.blocks = static_cast<int>(div_up(M, g.rows));
     if (activation != GEMM_F32_ACT_NONE && (dA || dB)) g.dz = times(times(batch, M), N);
     if (dbias) g.partial = times(times(batch, g.blocks), N);
-    if (dA) g.slices = slice_bytes(batch, M, K, N) / 4;
-    if (dB) g.slices = std::max(g.slices, slice_bytes(batch, K, N, M) / 4);
+    // (the sizes of the products as they are run)
+    if (dA) g.space = (ta ? space_of(batch, K, M, N) : space_of(batch, M, K, N)) / 4;
+    if (dB) g.space = std::max(g.space, (tb ? space_of(batch, N, K, M) : space_of(batch, K, N, M)) / 4);
     return g;
 }
 
@@ -115,8 +112,8 @@ int64_t stats_bytes(int64_t T, int64_t V) {  // statistics, logit at the target,
 }
 // The gradient works on `rows` tokens at a time, whose logits it holds.
 int64_t piece_bytes(int64_t rows, int64_t V) { return plus(times(times(4, rows), V), stats_bytes(rows, V)); }
-int64_t piece_slices(int64_t rows, int64_t V, int64_t K) {
-    return std::max(slice_bytes(1, rows, K, V), slice_bytes(1, V, K, rows));
+int64_t piece_space(int64_t rows, int64_t V, int64_t K) {
+    return std::max({space_of(1, rows, V, K, false), space_of(1, rows, K, V), space_of(1, V, K, rows)});
 }
 constexpr int64_t kPieceBytes = int64_t{4} << 30;
 constexpr int64_t kPieceRows = 256;
@@ -185,7 +182,7 @@ int gemm_f32_fused(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_
         rc = check_float("pre", e.pre, batch, M, N, e.ld_pre, e.stride_pre, true, &pre);
     if (rc != GEMM_F32_OK) return rc;
     if (used == 0) return GEMM_F32_OK;
-    const int64_t need = workspace != nullptr ? slice_bytes(batch, M, N, K) : 0;
+    const int64_t need = workspace != nullptr ? space_of(batch, M, N, K) : 0;
     rc = check_workspace(workspace, workspace_bytes, need, &w);
     if (rc != GEMM_F32_OK) return rc;
     // the residual may be C itself: an element is read by the thread that writes it, before
@@ -205,7 +202,7 @@ int gemm_f32_fused(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_
 
 int64_t gemm_f32_fused_workspace_size(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_t K) {
     if (!known_op(opA) || !known_op(opB) || !valid_sizes(batch, M, N, K)) return 0;
-    return slice_bytes(batch, M, N, K);
+    return space_of(batch, M, N, K);
 }
 
 int gemm_f32_fused_grad(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_t K, const float *dC,
@@ -234,14 +231,14 @@ int gemm_f32_fused_grad(int opA, int opB, int64_t batch, int64_t M, int64_t N, i
     if (rc == GEMM_F32_OK && want_bias)
         rc = check_float("dbias", dbias, batch, 1, N, std::max<int64_t>(N, 1), stride_dbias, true, &dbi);
     if (rc != GEMM_F32_OK) return rc;
-    const GradParts parts = grad_parts(batch, M, N, K, activation, want_a, want_b, want_bias);
+    const GradParts parts = grad_parts(ta, tb, batch, M, N, K, activation, want_a, want_b, want_bias);
     rc = check_workspace(workspace, workspace_bytes, parts.bytes(), &w);
     if (rc == GEMM_F32_OK) rc = check_apart({da, db, dbi, w}, {g, z, a, b});
     if (rc != GEMM_F32_OK) return rc;
     if (batch == 0) return GEMM_F32_OK;
     const bool many = batch > 1;
     float *at = static_cast<float *>(workspace);
-    float *dz = at, *partial = at + parts.dz, *slices = parts.slices ? at + parts.dz + parts.partial : nullptr;
+    float *dz = at, *partial = at + parts.dz, *space = parts.space ? at + parts.dz + parts.partial : nullptr;
     fused::Operand grad{dC, lddc, many ? stride_dC : 0};
     fused::Slope s{};
     s.batch = batch, s.M = static_cast<int>(M), s.N = static_cast<int>(N), s.activation = activation;
@@ -259,12 +256,12 @@ int gemm_f32_fused_grad(int opA, int opB, int64_t batch, int64_t M, int64_t N, i
         if (N > 0 && (want_bias || parts.dz > 0)) err = fused::launch_slope(s, q);
         // dA = dZ op(B)^T, or its transpose op(B) dZ^T
         if (err == hipSuccess && want_a)
-            err = run(ta ? plain_product(batch, K, M, N, tb, ob, true, grad, ra, slices)
-                         : plain_product(batch, M, K, N, false, grad, !tb, ob, ra, slices), q);
+            err = run(ta ? plain_product(batch, K, M, N, tb, ob, true, grad, ra, space)
+                         : plain_product(batch, M, K, N, false, grad, !tb, ob, ra, space), q);
         // dB = op(A)^T dZ, or its transpose dZ^T op(A)
         if (err == hipSuccess && want_b)
-            err = run(tb ? plain_product(batch, N, K, M, true, grad, ta, oa, rb, slices)
-                         : plain_product(batch, K, N, M, !ta, oa, false, grad, rb, slices), q);
+            err = run(tb ? plain_product(batch, N, K, M, true, grad, ta, oa, rb, space)
+                         : plain_product(batch, K, N, M, !ta, oa, false, grad, rb, space), q);
         return err;
     });
 }
@@ -272,7 +269,8 @@ int gemm_f32_fused_grad(int opA, int opB, int64_t batch, int64_t M, int64_t N, i
 int64_t gemm_f32_fused_grad_workspace_size(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_t K,
                                            int activation, int want_dA, int want_dB, int want_dbias) {
     if (!known_op(opA) || !known_op(opB) || !known_activation(activation) || !valid_sizes(batch, M, N, K)) return 0;
-    return grad_parts(batch, M, N, K, activation, want_dA, want_dB, want_dbias).bytes();
+    return grad_parts(opA == GEMM_F32_OP_T, opB == GEMM_F32_OP_T, batch, M, N, K, activation, want_dA, want_dB, want_dbias)
+        .bytes();
 }
 
 int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int64_t ldx, const float *W, int64_t ldw,
@@ -288,7 +286,8 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
     if (rc == GEMM_F32_OK) rc = check_apart({lo, ls, ws}, {x, w, t});
     if (rc != GEMM_F32_OK) return rc;
     float *at = static_cast<float *>(workspace);
-    fused::Product p = plain_product(1, T, V, K, false, {X, ldx, 0}, true, {W, ldw, 0}, {}, nullptr);
+    float *space = space_of(1, T, V, K, false) ? at + stats_bytes(T, V) / 4 : nullptr;
+    fused::Product p = plain_product(1, T, V, K, false, {X, ldx, 0}, true, {W, ldw, 0}, {}, space);
     p.mode = fused::kStats;
     p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * T), p.groups = groups_of(V);
     p.target = target, p.ignore = ignore_index;
@@ -302,7 +301,7 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
 }
 
 int64_t gemm_f32_cross_entropy_workspace_size(int64_t T, int64_t V, int64_t K) {
-    return valid_sizes(1, T, V, K) ? stats_bytes(T, V) : 0;
+    return valid_sizes(1, T, V, K) ? plus(stats_bytes(T, V), space_of(1, T, V, K, false)) : 0;
 }
 
 int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X, int64_t ldx, const float *W,
@@ -319,7 +318,7 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
     if (rc == GEMM_F32_OK && dW != nullptr) rc = check_float("dW", dW, 1, V, K, lddw, 0, true, &dw);
     if (rc != GEMM_F32_OK) return rc;
     // as many tokens at a time as the workspace holds
-    const int64_t best = piece_rows(T, V), full = plus(piece_bytes(best, V), piece_slices(best, V, K));
+    const int64_t best = piece_rows(T, V), full = plus(piece_bytes(best, V), piece_space(best, V, K));
     int64_t rows = best, bytes = full;
     const bool sliced = workspace_bytes >= full;
     if (!sliced && T > 0) {
@@ -339,13 +338,13 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
         for (int64_t t0 = 0; t0 < T && err == hipSuccess; t0 += rows) {
             const int64_t n = std::min(rows, T - t0);
             float *logits = at + 2 * n + 2 * n * groups_of(V);
-            float *slices = sliced && bytes > piece_bytes(best, V) ? at + piece_bytes(best, V) / 4 : nullptr;
-            // the last piece may be shorter, and then have more slices than there is room for
-            auto room = [&](int64_t m, int64_t k) {
-                return slices != nullptr && slice_bytes(1, m, K, k) <= full - piece_bytes(best, V) ? slices : nullptr;
+            float *space = sliced && bytes > piece_bytes(best, V) ? at + piece_bytes(best, V) / 4 : nullptr;
+            // (the last piece may be shorter, and ask for more)
+            auto room = [&](int64_t M, int64_t N, int64_t k, bool slice = true) {
+                return space != nullptr && space_of(1, M, N, k, slice) <= full - piece_bytes(best, V) ? space : nullptr;
             };
             const float *Xt = X + t0 * ldx;
-            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, V, 0}, nullptr);
+            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, V, 0}, room(n, V, K, false));
             p.mode = fused::kStoreStats;
             p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * n), p.groups = groups_of(V);
             p.target = target + t0, p.ignore = ignore_index;
@@ -358,11 +357,15 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             if (err == hipSuccess) err = fused::launch_loss(l, s);
             if (dX == nullptr && dW == nullptr) continue;
             if (err == hipSuccess) err = fused::launch_probabilities(l, s);
-            if (err == hipSuccess && dX != nullptr)
-                err = run(plain_product(1, n, K, V, false, {logits, V, 0}, false, {W, ldw, 0},
-                                        {dX + t0 * lddx, lddx, 0}, room(n, V)), s);
+            if (err == hipSuccess && dX != nullptr) {
+                p = plain_product(1, n, K, V, false, {logits, V, 0}, false, {W, ldw, 0},
+                                        {dX + t0 * lddx, lddx, 0}, room(n, K, V));
+                p.lenient = true;
+                err = run(p, s);
+            }
             if (err == hipSuccess && dW != nullptr) {
-                p = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0}, room(V, n));
+                p = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0}, room(V, K, n));
+                p.lenient = true;
                 p.target_k = target + t0, p.ignore = ignore_index;
                 if (t0 > 0) p.e.residual = {dW, lddw, 0};  // the pieces before
                 err = run(p, s);
@@ -375,7 +378,7 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
 int64_t gemm_f32_cross_entropy_grad_workspace_size(int64_t T, int64_t V, int64_t K) {
     if (!valid_sizes(1, T, V, K)) return 0;
     const int64_t rows = piece_rows(T, V);
-    return plus(piece_bytes(rows, V), piece_slices(rows, V, K));
+    return plus(piece_bytes(rows, V), piece_space(rows, V, K));
 }
 
 int64_t gemm_f32_cross_entropy_grad_workspace_least(int64_t T, int64_t V, int64_t K) {

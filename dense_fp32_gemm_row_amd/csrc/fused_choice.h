@@ -20,17 +20,26 @@ constexpr int kMostSplits = 64;
 struct Choice {
     int tile;    // index of kTiles
     int splits;  // slices of K
+    bool half;   // two fp16 parts of each value where the operands' ranges allow it
 };
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-inline Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, int most_splits) {
+// `space`: whether there is a workspace.  `slice`: whether the sums may be slices of
+// K (a row's statistics need whole ones).
+inline Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, bool space, bool slice) {
     for (int t = 0; t < kTileCount - 1; ++t)
-        if (batch * div_up(M, kTiles[t].m) * div_up(N, kTiles[t].n) >= 192) return {t, 1};
+        if (batch * div_up(M, kTiles[t].m) * div_up(N, kTiles[t].n) >= 192) return {t, 1, space && K >= 64};
     const int t = kTileCount - 1;
     const int64_t tiles = batch * div_up(M, kTiles[t].m) * div_up(N, kTiles[t].n);
-    int64_t splits = std::min<int64_t>(most_splits, std::max<int64_t>(1, std::min(512 / tiles, K / 128)));
-    return {t, static_cast<int>(splits)};
+    const int64_t splits = std::min<int64_t>(kMostSplits, std::max<int64_t>(1, std::min(512 / tiles, K / 128)));
+    return {t, space && slice ? static_cast<int>(splits) : 1, false};
+}
+
+// Blocks of k in which the statistics of `rows` rows are taken: enough of them to fill the GPU.
+inline int stat_blocks(int64_t rows, int64_t K, bool k_contiguous) {
+    const int64_t units = k_contiguous ? div_up(rows, 4) : div_up(rows, 256);
+    return static_cast<int>(std::max<int64_t>(1, std::min({int64_t{16}, div_up(2048, units), K / 256})));
 }
 
 }  // namespace fused

@@ -89,6 +89,28 @@ __device__ __forceinline__ Parts split4(float x0, float x1, float x2, float x3) 
     return r;
 }
 
+// Two fp16 parts of four values times a power of two that brings their row's
+// largest below 2^15: h has 11 bits of the 24, l 11 of the 12 and a sign that are
+// left, so h + l is off by at most 2^-23 of the value, or 2^-25, the last place of
+// fp16: 2^-40 of the row's largest.
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
+struct Halves {
+    u32x2 p[2];
+};
+__device__ __forceinline__ Halves split4_half(const float (&x)[4], float scale) {
+    Halves r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const half2v h = __builtin_convertvector(f32x2{x[2 * i] * scale, x[2 * i + 1] * scale}, half2v);
+        const half2v l = __builtin_convertvector(
+            f32x2{fmaf(x[2 * i], scale, -static_cast<float>(h[0])), fmaf(x[2 * i + 1], scale, -static_cast<float>(h[1]))}, half2v);
+        r.p[0][i] = __builtin_bit_cast(uint32_t, h);
+        r.p[1][i] = __builtin_bit_cast(uint32_t, l);
+    }
+    return r;
+}
+
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
 
 // Two running (maximum, sum of exp(x - maximum)) as one.  An empty piece is

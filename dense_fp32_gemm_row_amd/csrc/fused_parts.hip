@@ -93,6 +93,63 @@ __global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t stri
     }
 }
 
+__device__ __forceinline__ void count(RowStat &s, float x) {
+    const int bits = __builtin_bit_cast(int, x) & 0x7fffffff, e = bits >> 23;
+    s.top = max(s.top, e);
+    // a value below 2^-126 has up to 23 leading zeros in its place
+    s.count += bits != 0, s.sum += bits == 0 ? 0 : e == 0 ? -23 : e;
+}
+__device__ __forceinline__ void join(RowStat &s, int top, int n, int sum) {
+    s.top = max(s.top, top), s.count += n, s.sum += sum;
+}
+
+// One operand, `rows` rows of each of `batch` matrices, k in `blocks` blocks of `len`.
+struct StatJob {
+    Operand x;
+    bool kc;
+    int rows, K, blocks, len;
+    RowStat *out;
+    int64_t strips, units;  // workgroups: [batch][block][strip]
+};
+
+// Where k is contiguous a wavefront takes a row's block, else a workgroup 256
+// rows' (a row a thread).
+__global__ __launch_bounds__(256) void row_stats_kernel(StatJob a, StatJob b, int64_t batch) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    for (int64_t u = blockIdx.x; u < a.units + b.units; u += gridDim.x) {
+        const bool second = u >= a.units;
+        const StatJob &j = second ? b : a;
+        const int64_t w = second ? u - a.units : u, strip = w % j.strips, rest = w / j.strips;
+        const int block = static_cast<int>(rest % j.blocks);
+        const int64_t n = rest / j.blocks;
+        const int64_t k0 = static_cast<int64_t>(block) * j.len, k1 = min(k0 + j.len, static_cast<int64_t>(j.K));
+        const float *p = j.x.p + n * j.x.stride;
+        RowStat s{0, 0, 0, 0};
+        int64_t row;
+        if (j.kc) {
+            row = strip * 4 + (tid >> 6);
+            if (row >= j.rows) continue;
+            p += row * j.x.ld;
+            int64_t k = k0 + 4 * lane;
+            for (; k + 3 < k1; k += 256) {
+                const f32x4 v = *reinterpret_cast<const float4u *>(p + k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) count(s, v[e]);
+            }
+            for (; k < k1; ++k) count(s, p[k]);  // the last three at most, of one lane
+            for (int d = 1; d < 64; d *= 2) join(s, __shfl_xor(s.top, d), __shfl_xor(s.count, d), __shfl_xor(s.sum, d));
+            if (lane != 0) continue;
+        } else {
+            row = strip * 256 + tid;
+            if (row >= j.rows) continue;
+            p += row;
+#pragma unroll 8
+            for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld]);
+        }
+        j.out[(block * batch + n) * j.rows + row] = s;
+    }
+}
+
 unsigned blocks_for(int64_t n) { return static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(n, 1), 1 << 21)); }
 
 }  // namespace
@@ -133,13 +190,46 @@ bool narrow_operand(int64_t ld, bool k_contiguous) {
 }
 }  // namespace
 
+hipError_t launch_row_stats(const Product &p, hipStream_t stream) {
+    auto job = [&](const Operand &x, bool kc, int rows, int blocks, const RowStat *out) {
+        StatJob j{x, kc, rows, p.K, blocks, static_cast<int>(div_up(p.K, blocks)), const_cast<RowStat *>(out), 0, 0};
+        j.strips = div_up(rows, kc ? 4 : 256);
+        j.units = j.strips * blocks * p.batch;
+        return j;
+    };
+    const StatJob a = job(p.a, !p.ta, p.M, p.blocks_a, p.row_a), b = job(p.b, p.tb, p.N, p.blocks_b, p.row_b);
+    row_stats_kernel<<<blocks_for(a.units + b.units), 256, 0, stream>>>(a, b, p.batch);
+    return hipGetLastError();
+}
+
+int64_t product_space(int64_t batch, int64_t M, int64_t N, int64_t K, bool slice) {
+    const Choice c = choose(batch, M, N, K, true, slice);
+    const __int128 slices = c.splits > 1 ? static_cast<__int128>(4 * c.splits) * batch * M * N : 0;
+    // either form of either operand
+    const __int128 stats = c.half ? static_cast<__int128>(sizeof(RowStat)) * batch *
+                                        (std::max(stat_blocks(M, K, true), stat_blocks(M, K, false)) * M +
+                                         std::max(stat_blocks(N, K, true), stat_blocks(N, K, false)) * N)
+                                  : 0;
+    return static_cast<int64_t>(std::min<__int128>(slices + stats, __int128{1} << 61));
+}
+
 hipError_t launch_product(const Product &asked, hipStream_t stream) {
     Product p = asked;
     p.narrow = narrow_operand(p.a.ld, !p.ta) && narrow_operand(p.b.ld, p.tb);
-    const Choice c = choose(p.batch, p.M, p.N, p.K, p.splits);
+    const Choice c = choose(p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore);
     p.splits = c.splits;
-    const hipError_t err = p.ta ? (p.tb ? launch_tile_tt(p, c.tile, stream) : launch_tile_tn(p, c.tile, stream))
-                                : (p.tb ? launch_tile_nt(p, c.tile, stream) : launch_tile_nn(p, c.tile, stream));
+    p.slices = c.splits > 1 ? p.space : nullptr;
+    p.row_a = p.row_b = nullptr;
+    hipError_t err = hipSuccess;
+    if (c.half && p.narrow) {
+        p.blocks_a = stat_blocks(p.M, p.K, !p.ta), p.blocks_b = stat_blocks(p.N, p.K, p.tb);
+        p.row_a = reinterpret_cast<const RowStat *>(p.space + (c.splits > 1 ? c.splits * p.batch * p.M * p.N : 0));
+        p.row_b = p.row_a + p.blocks_a * p.batch * p.M;
+        err = launch_row_stats(p, stream);
+    }
+    if (err == hipSuccess)
+        err = p.ta ? (p.tb ? launch_tile_tt(p, c.tile, stream) : launch_tile_tn(p, c.tile, stream))
+                   : (p.tb ? launch_tile_nt(p, c.tile, stream) : launch_tile_nn(p, c.tile, stream));
     if (err != hipSuccess || p.splits == 1) return err;
     return launch_sum_slices(p, stream);
 }

@@ -37,47 +37,57 @@ __device__ __forceinline__ float element(const float *p, int64_t ld, int row, in
     return KC ? p[row * ld + k] : p[k * ld + row];
 }
 
-// A thread's share of the stages of one operand: E elements, 4 consecutive k of E / 4
-// rows.  Where k is contiguous (KC) these are 16-byte loads, 4 lanes a row;
-// where rows are, E / 4 neighbouring rows at 4 k.  Every address stays inside
-// the operand: rows past its end repeat the last ones, which then are written
-// to LDS where those belong.
-template <int ROWS, int E, int THREADS, bool KC>
+// A thread's share of the stages of one operand, STAGE k each: 4 consecutive k of
+// kUnits rows.  Where k is contiguous (KC) these are 16-byte loads, STAGE / 4
+// lanes a row; where rows are, kUnits neighbouring rows at 4 k.  Every address
+// stays inside the operand: rows past its end repeat the last ones, which then
+// are written to LDS where those belong.  HALF: in two fp16 parts, not three of
+// bf16.
+template <int ROWS, int THREADS, bool KC, int STAGE, bool HALF>
 struct Share {
-    static_assert(ROWS * kStage == E * THREADS, "");
-    static constexpr int kUnits = E / 4;  // of 4 k of a row each
+    static constexpr int E = ROWS * STAGE / THREADS;  // elements
+    static constexpr int kUnits = E / 4;
+    static constexpr int kPlane = ROWS * 16;          // 8 k of every row
+    static constexpr int kPart = STAGE / 8 * kPlane;
     const char *base;   // of the operand's tile at k = 0
-    uint32_t off[KC ? kUnits : 4];
-    int lds[kUnits];    // byte in a plane
-    int64_t step;       // bytes a stage
+    int64_t step, row;  // bytes a stage, a row of storage
+    uint32_t off[KC ? kUnits : 1];
+    int lds[KC ? 1 : kUnits];  // byte in a part
+    float scale[HALF ? kUnits : 1];
     float v[E];
 
-    __device__ __forceinline__ Share(const float *p, int64_t ld, int rows, bool more, int tid) {
+    __device__ __forceinline__ Share(const float *p, int64_t ld, int rows, bool more, int tid, const int *exponents) {
+        row = 4 * ld;
         if constexpr (KC) {
             base = reinterpret_cast<const char *>(p);
-            step = kStage * 4;
+            step = STAGE * 4;
+            const int q = tid % (STAGE / 4), place = tid / (STAGE / 4);
+            lds[0] = (q >> 1) * kPlane + place * 16 + (q & 1) * 8;
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
-                const int o = tid + u * THREADS, q = o & 3, place = o >> 2;
-                off[u] = static_cast<uint32_t>(min(row_at(place), rows - 1)) * static_cast<uint32_t>(ld * 4) + 16 * q;
-                lds[u] = (q >> 1) * ROWS * 16 + place * 16 + (q & 1) * 8;
+                const int r = row_at(place + u * (THREADS * 4 / STAGE));
+                off[u] = static_cast<uint32_t>(min(r, rows - 1)) * static_cast<uint32_t>(row) + 16 * q;
+                if constexpr (HALF) scale[u] = power(exponents[r]);
             }
         } else {
             constexpr int kLanes = ROWS / kUnits;
             const int j = tid % kLanes, q = tid / kLanes;
-            // a lone last row is loaded with the one before the tile
+            // fewer last rows than a thread loads come with some from before the tile
             const int back = rows < kUnits && more ? kUnits - rows : 0;
             const int r = min(kUnits * j, rows - kUnits + back);
             base = reinterpret_cast<const char *>(p - back);
-            step = kStage * 4 * ld;
+            step = STAGE * row;
+            off[0] = static_cast<uint32_t>(4 * q) * static_cast<uint32_t>(row) + 4 * r;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                off[i] = static_cast<uint32_t>(4 * q + i) * static_cast<uint32_t>(ld * 4) + 4 * r;
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u)
-                lds[u] = (q >> 1) * ROWS * 16 + place_of_row((r - back + u + ROWS) % ROWS) * 16 + (q & 1) * 8;
+            for (int u = 0; u < kUnits; ++u) {
+                const int at = (r - back + u + ROWS) % ROWS;
+                lds[u] = (q >> 1) * kPlane + place_of_row(at) * 16 + (q & 1) * 8;
+                if constexpr (HALF) scale[u] = power(exponents[at]);
+            }
         }
     }
+    // 2^(141 - e): values with exponent field e and less come below 2^15
+    static __device__ __forceinline__ float power(int e) { return __builtin_bit_cast(float, (268 - e) << 23); }
     __device__ __forceinline__ void load(int stage) {
         const char *at = base + stage * step;
         if constexpr (KC) {
@@ -90,20 +100,31 @@ struct Share {
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if constexpr (kUnits == 2) {
-                    const f32x2 x = *reinterpret_cast<const float2u *>(at + off[i]);
+                const char *from = at + i * row + off[0];
+                if constexpr (kUnits == 4) {
+                    const f32x4 x = *reinterpret_cast<const float4u *>(from);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) v[4 * u + i] = x[u];
+                } else if constexpr (kUnits == 2) {
+                    const f32x2 x = *reinterpret_cast<const float2u *>(from);
                     v[i] = x[0], v[4 + i] = x[1];
                 } else {
-                    v[i] = *reinterpret_cast<const float *>(at + off[i]);
+                    v[i] = *reinterpret_cast<const float *>(from);
                 }
             }
         }
     }
     __device__ __forceinline__ void put(int u, char *planes) const {
-        const Parts s = split4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        char *to = planes + (KC ? lds[0] + u * (THREADS * 4 / STAGE) * 16 : lds[KC ? 0 : u]);
+        if constexpr (HALF) {
+            const Halves s = split4_half({v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]}, scale[u]);
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
-            *reinterpret_cast<u32x2 *>(planes + c * (2 * ROWS * 16) + lds[u]) = s.p[c];
+            for (int c = 0; c < 2; ++c) *reinterpret_cast<u32x2 *>(to + c * kPart) = s.p[c];
+        } else {
+            const Parts s = split4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+#pragma unroll
+            for (int c = 0; c < 3; ++c) *reinterpret_cast<u32x2 *>(to + c * kPart) = s.p[c];
+        }
     }
 };
 
@@ -115,11 +136,16 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
                                                                         int64_t first_tile, int len) {
     using T = Tile<WM, WN, FM>;
     constexpr int BM = T::BM, BN = T::BN, kThreads = T::kThreads;
+    constexpr bool kHalf = FM > 1;  // the tiles with a loop for fp16 parts
     constexpr int kPlanesA = 3 * 2 * BM * 16, kBuffer = kPlanesA + 3 * 2 * BN * 16;
+    constexpr int kHalfA = 2 * 4 * BM * 16, kHalfBuffer = kHalfA + 2 * 4 * BN * 16;
+    constexpr int kMemory = 2 * (kHalf ? kHalfBuffer : kBuffer);
     constexpr int kRowOut = 68;  // floats: 64 of a row of results, 16 bytes apart from the next one's banks
     static_assert(kBuffer >= (BM + BN) * kStage * 4, "");
     static_assert(2 * kBuffer >= T::kWaves * 32 * kRowOut * 4, "");
-    __shared__ __align__(1024) char memory[2 * kBuffer];
+    __shared__ __align__(1024) char memory[kMemory];
+    __shared__ int exponents[kHalf ? BM + BN : 1];
+    __shared__ float worst[kHalf ? 2 * T::kWaves : 1];
     auto &xs = *reinterpret_cast<float(*)[kStage][BM]>(memory);
     auto &ys = *reinterpret_cast<float(*)[kStage][BN]>(memory + BM * kStage * 4);
 
@@ -187,8 +213,8 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
             // registers loaded again.  The one barrier lies before the last phase, under
             // which the next stage's first operands are read.
             auto quick = [&](int first, int last) {
-                Share<BM, BM * kStage / kThreads, kThreads, !TA> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid);
-                Share<BN, BN * kStage / kThreads, kThreads, TB> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid);
+                Share<BM, kThreads, !TA, kStage, false> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, nullptr);
+                Share<BN, kThreads, TB, kStage, false> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, nullptr);
                 constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
                 const int stages = (last - first) / kStage;
                 u32x4 x[2][FM], y[3][2];  // parts of A by turns; the parts of B
@@ -276,6 +302,151 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
                 if (s < stages) stage(p0, s, even, odd);
             };
 
+    // Whether two fp16 parts do: the rows' exponents for scaling, and a bound.
+    // Parts of a value are off by 2^-23 of it, or 2^-40 of its row's largest (and the
+    // product of two second parts, 2^-22 of the values' at most, is left out).
+    // The latter adds up to less than n 2^-39 a b over the n products of a cell that
+    // aren't zero, a and b the largest of its row and column; and the sum S
+    // of their |a b| is at least n a b 2^-c with c the mean over them of
+    // log2(a / |a_k|) + log2(b / |b_k|), as an arithmetic mean is at least the
+    // geometric one.  With costs (that mean over all k, zeros counting nothing)
+    // Ca and Cb and shares fa and fb of values that aren't zero, n is at least (fa
+    // + fb - 1) K and c at most (Ca + Cb) / (fa + fb - 1).  Where c <= 17 for
+    // the worst row with the worst column, all of it is below 2^-22 S.
+    auto certified = [&]() {
+        if constexpr (!kHalf) return false;
+        static_assert(!kHalf || BM + BN == kThreads, "");
+        const bool second = tid >= BM;
+        const int r = second ? tid - BM : tid, count = second ? p.N : p.M;
+        const int blocks = second ? p.blocks_b : p.blocks_a;
+        const int64_t line = p.batch * count;
+        const RowStat *from = (second ? p.row_b : p.row_a) + b * count + (second ? n0 : m0) + r;
+        float cost = 0.0f, share = 1.0f;
+        int e = 141;
+        if (r < (second ? cols : rows)) {
+            RowStat s{0, 0, 0, 0};
+            for (int q = 0; q < blocks; ++q) {
+                const RowStat t = from[q * line];
+                s.top = max(s.top, t.top), s.count += t.count, s.sum += t.sum;
+            }
+            if (s.count > 0) {  // a row of zeros is one whatever its scale
+                e = s.top;
+                const float n = static_cast<float>(p.K);
+                cost = (static_cast<float>(s.count) * static_cast<float>(e + 1) - static_cast<float>(s.sum)) / n;
+                share = static_cast<float>(s.count) / n;
+                if (p.lenient) cost = 0.0f, share = 1.0f;
+                if (e < 14 || e > 254) cost = __builtin_inff(), e = 141;
+            }
+        }
+        exponents[tid] = e;
+        for (int d = 1; d < 64; d *= 2) cost = fmaxf(cost, __shfl_xor(cost, d)), share = fminf(share, __shfl_xor(share, d));
+        if (lane == 0) worst[2 * wave] = cost, worst[2 * wave + 1] = share;
+        __syncthreads();
+        float ca = 0.0f, cb = 0.0f, fa = 1.0f, fb = 1.0f;
+        for (int w = 0; w < T::kWaves; ++w)
+            if (w < BM / 64) ca = fmaxf(ca, worst[2 * w]), fa = fminf(fa, worst[2 * w + 1]);
+            else cb = fmaxf(cb, worst[2 * w]), fb = fminf(fb, worst[2 * w + 1]);
+        const float both = fa + fb - 1.0f;
+        return both > 0.0f && ca + cb <= 17.0f * both;
+    };
+    // Whole stages of 32 k in fp16 parts, as above: per 16 k the products l h,
+    // h h and h l.
+    auto quick_half = [&](int first, auto last) {
+        constexpr int kLong = 2 * kStage;
+        Share<BM, kThreads, !TA, kLong, true> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, exponents);
+        Share<BN, kThreads, TB, kLong, true> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, exponents + BM);
+        constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
+        static_assert(kUa == 4 && kUb == 4, "");
+        const int stages = (last - first) / kLong;
+        u32x4 x[2][FM], y[3][2];
+        const int ra = half * BM * 16 + (32 * FM * wm + col) * 16;
+        const int rb = kHalfA + half * BN * 16 + (64 * wn + col) * 16;
+        auto fetch_a = [&](int set, int part, int ks, const char *from) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                x[set][i] = *reinterpret_cast<const u32x4 *>(from + (part * 4 + 2 * ks) * (BM * 16) + ra + 32 * 16 * i);
+        };
+        auto fetch_b = [&](int set, int part, int ks, const char *from) {
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+                y[set][f] = *reinterpret_cast<const u32x4 *>(from + (part * 4 + 2 * ks) * (BN * 16) + rb + 32 * 16 * f);
+        };
+        auto multiply = [&](int sx, int sy) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int f = i & 1 ? 1 - k : k;
+                    acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(half8v, x[sx][i]), __builtin_bit_cast(half8v, y[sy][f]), acc[i][f], 0, 0, 0);
+                }
+#pragma unroll
+            for (int k = 0; k < FM * 2; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) asm volatile("" : "+v"(acc[i][f]));
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto stage = [&](int s, const char *from, char *to) {
+            const int next = min(s + 2, stages - 1);  // past the end: loaded again, not used
+            fetch_a(1, 0, 0, from);
+            sa.put(0, to), sa.put(1, to);
+            multiply(0, 0);  // l h
+            fetch_b(1, 1, 0, from);
+            sa.put(2, to), sa.put(3, to);
+            sa.load(next);
+            multiply(1, 0);  // h h
+            fetch_a(0, 1, 1, from);
+            fetch_b(2, 0, 1, from);
+            sb.put(0, to + kHalfA), sb.put(1, to + kHalfA);
+            multiply(1, 1);  // h l
+            fetch_a(1, 0, 1, from);
+            sb.put(2, to + kHalfA), sb.put(3, to + kHalfA);
+            sb.load(next);
+            multiply(0, 2);  // l h
+            fetch_b(1, 1, 1, from);
+            multiply(1, 2);  // h h
+            wait_older<63>();
+            barrier_only();
+            fetch_a(0, 1, 0, to);
+            fetch_b(0, 0, 0, to);
+            multiply(1, 1);  // h l
+        };
+        char *even = memory, *odd = memory + kHalfBuffer;
+        sa.load(0), sb.load(0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sa.put(u, even), sb.put(u, even + kHalfA);
+        sa.load(min(1, stages - 1)), sb.load(min(1, stages - 1));
+        wait_older<63>();
+        barrier_only();
+        fetch_a(0, 1, 0, even);
+        fetch_b(0, 0, 0, even);
+        int s = 0;
+        for (; s + 1 < stages; s += 2) {
+            stage(s, even, odd);
+            stage(s + 1, odd, even);
+        }
+        if (s < stages) stage(s, even, odd);
+        // back to the operands' scale
+        const int en0 = exponents[BM + 64 * wn + 4 * (col & 15) + 2 * (col >> 4)];
+        const int en1 = exponents[BM + 64 * wn + 4 * (col & 15) + 2 * (col >> 4) + 1];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int em = exponents[row_at(32 * (FM * wm + i) + (r & 3) + 8 * (r >> 2) + 4 * half)] - 282;
+                acc[i][0][r] = ldexpf(acc[i][0][r], em + en0);
+                acc[i][1][r] = ldexpf(acc[i][1][r], em + en1);
+            }
+    };
+
     // The results of a block of 32 x 64 by way of LDS, so that a lane has 4
     // neighbouring columns of a row and the code below is there once: `use` gets
     // the row and column of the tile and the 4 values.
@@ -324,18 +495,32 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
     };
 
     clear();
-    // a lone row of an operand whose rows are contiguous has no neighbour to be loaded with
-    const bool lone = (TA && FM > 1 && p.M < 2) || (!TB && p.N < 2);
-    const int whole = p.narrow && !lone ? k0 + (k1 - k0) / kStage * kStage : k0;
-    bool quickly = whole > k0;
-    if (quickly) quick(k0, whole);
+    // an operand with fewer rows than a thread loads together, where they are contiguous
+    const bool few = (TA && kHalf && p.M < 4) || (!TB && p.N < 4);
+    int whole = k0;  // the end of what the stages take
+    bool check = false;
+    if (p.narrow && !few) {
+        bool half_parts = false;
+        if constexpr (kHalf)
+            if (p.row_a != nullptr && k1 - k0 >= 2 * kStage && certified()) {
+                whole = k0 + (k1 - k0) / (2 * kStage) * (2 * kStage);
+                quick_half(k0, whole);
+                half_parts = true;
+            }
+        if (!half_parts) {
+            whole = k0 + (k1 - k0) / kStage * kStage;
+            check = whole > k0;
+            if (check) quick(k0, whole);
+        }
+    }
     for (int from = whole;; from = k0) {
         if (from < k1) general(from, k1, p.target_k);
-        if (!quickly) break;
-        quickly = false;
+        if (!check) break;
+        check = false;
         if (!__syncthreads_or(odd())) break;
         clear();
     }
+    __syncthreads();
 
     // ---- results ----
     auto put = [&](float *dst, int c, f32x4 v) {

@@ -4,16 +4,22 @@
  * linear layer with bias, activation and residual, the softmax cross entropy
  * of tokens over a vocabulary, and the gradients of both.  MI355X (gfx950).
  *
- * Arithmetic: FP32 in, FP32 out, sums in FP32.  The products run on the bf16
- * matrix units: an operand's value is the sum of three bf16 values (8
- * significant bits each, 24 in all), exactly, and of the nine products of two
- * values' parts the six largest are summed; what is left out is at most 2^-23
- * of each |a b|, and 2^-26 of it as a rule.  Values below 2^-110 in magnitude
- * are held to 2^-134, not to 24 bits.  Where a product comes out infinite or NaN, its tile is computed again
- * with FP32 multiplies, so infinities, NaN and values next to the largest
- * give what gemm_f32 gives.  Few rows and small products may run on FP32 multiplies
- * throughout.  Activations and exponentials are evaluated in FP32.  Every
- * call is deterministic; the order of a sum depends on the sizes.
+ * Arithmetic: FP32 in, FP32 out, sums in FP32.  The products run on the 16-bit
+ * matrix units, a value as the sum of parts that these take:
+ *   - three bf16 parts, 24 bits, exactly (values below 2^-110 in magnitude are
+ *     held to 2^-134), of whose nine products the six largest are summed: what is left
+ *     out is at most 2^-23 of each |a b|, 2^-26 as a rule;
+ *   - in large products with a workspace, where a look at every row of op(A)
+ *     and column of op(B) finds the range for it, two fp16 parts of the value times a power of
+ *     two for its row, of whose four products three are summed.  What that
+ *     leaves out is at most 2^-21 of each |a b| (2^-24 as a rule), plus 2^-22
+ *     of the sum of |a b|.  Whole numbers up to 2^11 are held exactly.
+ * A product that comes out infinite or NaN is computed again, with its tile, by
+ * FP32 multiplies, so infinities, NaN and values next to the largest give what
+ * gemm_f32 gives.  Few rows and small products may run on FP32 multiplies
+ * throughout.  Activations and exponentials are evaluated in FP32.  Every call is
+ * deterministic; how a sum is formed depends on the sizes, and in large products on
+ * the ranges of the rows and columns that share a tile.
  *
  * Everything else is as in gemm_f32.h: row-major operands with leading
  * dimensions, device pointers aligned to 4 bytes, streams, ownership, errors

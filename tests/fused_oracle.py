@@ -27,6 +27,12 @@ def product(A, B):
     return torch.matmul(a, b), torch.matmul(a.abs(), b.abs())
 
 
+def least_tolerance(A, B):
+    """What the least place of the operands' parts amounts to (no NaN or infinities)."""
+    a, b = (torch.nan_to_num(t.double().abs(), nan=0.0, posinf=0.0) for t in (A, B))
+    return 2.0 ** -134 * (a.sum(-1)[..., :, None] + b.sum(-2)[..., None, :])
+
+
 def product_tolerance(S, K: int):
     return min(K + 16, 8 * math.sqrt(K + 16)) * U * S + K * 2.0 ** -130
 
@@ -94,7 +100,7 @@ def layer(A, B, bias=None, kind="none", residual=None):
     """{"y", "y_tol", "z", "z_tol"}"""
     z, S = product(A, B)
     K = A.shape[-1]
-    tol = product_tolerance(S, K)
+    tol = product_tolerance(S, K) + least_tolerance(A, B)
     if bias is not None:
         b = bias.double()
         b = b[:, None, :] if b.dim() == 2 else b

@@ -173,7 +173,7 @@ SPECIAL = [math.inf, -math.inf, math.nan, 3.4028234663852886e38, -3.402823466385
 
 
 @pytest.mark.parametrize("M,N,K", [(70, 130, 48), (300, 300, 70), (2, 600, 64), (130, 140, 33), (3330, 3600, 40),
-                                   (1700, 1900, 50)])
+                                   (1700, 1900, 50), (3330, 3600, 100), (1700, 1900, 96)])
 @pytest.mark.parametrize("ops", ["NN", "NT", "TN", "TT"])
 def test_values_at_the_ends_of_the_range(M, N, K, ops):
     """One special value in a row of A, against columns of B that hold zeros,
@@ -206,6 +206,76 @@ def test_scales_that_cancel_along_the_sum():
     A, B = rnd(1, 140, K) * s, rnd(2, K, 150) / s[:, None]
     want = o.layer(A, B)
     o.check(b.gemm_fused(A, B), want["y"], want["y_tol"])
+
+
+def uneven(name, M, N, K):
+    """Operands on whose ranges it depends how their values may be held."""
+    A, B = rnd(1, M, K), rnd(2, K, N)
+    if name == "along the sum":
+        s = torch.logspace(-15, 15, K, device=DEV)
+        A, B = A * s, B / s[:, None]
+    elif name == "rows":
+        A, B = A * torch.logspace(-25, 25, M, device=DEV)[:, None], B * torch.logspace(-12, 12, N, device=DEV)
+    elif name == "one large":  # met by zeros, but for one column
+        A[:, 5], B[5] = 1e20, 0.0
+        B[5, 7] = 1e-20
+    elif name == "one large each":  # met by the other's small ones
+        A[::3, 5], B[5] = 1e15, B[5] * 1e-15
+        B[9, ::5], A[:, 9] = 1e12, A[:, 9] * 1e-12
+    elif name == "outliers":
+        A[:, ::50] *= 300.0
+        B[:, ::7] *= 100.0
+    elif name == "half zeros":
+        A = A.clamp_min(0.0)
+    elif name == "zeros in both":
+        A, B = A.clamp_min(0.0), B * (rnd(3, K, N) > 0)
+    elif name == "apart":  # nothing meets: the sum is exactly zero
+        A[:, : K // 2], B[K // 2:] = 0.0, 0.0
+    elif name == "zero rows":
+        A[3::5], B[:, 2::3] = 0.0, 0.0
+    elif name == "tiny":
+        A, B = A * 1e-37, B * 1e30
+    elif name == "one row of infinities":
+        A[77] = math.inf
+    elif name == "lowest":
+        A[70, 3], B[3] = torch.finfo(torch.float32).min, 1e-30
+    return A, B
+
+
+UNEVEN = ["along the sum", "rows", "one large", "one large each", "outliers", "half zeros", "zeros in both", "apart",
+          "zero rows", "tiny", "one row of infinities", "lowest"]
+
+
+@pytest.mark.parametrize("ops", ["NN", "NT", "TN", "TT"])
+@pytest.mark.parametrize("name", UNEVEN)
+@pytest.mark.parametrize("M,N,K", [(3400, 3600, 150), (1700, 1900, 130), (130, 200, 128)])
+def test_uneven_operands(M, N, K, name, ops):
+    A, B = uneven(name, M, N, K)
+    a = A if ops[0] == "N" else A.t().contiguous().t()
+    w = B if ops[1] == "N" else B.t().contiguous().t()
+    want = o.layer(A, B)
+    top = torch.finfo(torch.float32).max
+    want["y"] = torch.where(want["y"].abs() > top, want["y"].sign() * math.inf, want["y"])
+    y = b.gemm_fused(a, w)
+    o.check(y, want["y"], torch.nan_to_num(want["y_tol"], nan=0.0, posinf=0.0))
+    if name == "apart":
+        assert not y.any()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1 << 20), (64, 64, 1 << 18), (3400, 3600, 8200)])
+@pytest.mark.parametrize("uniform", [False, True])
+def test_long_sums(M, N, K, uniform):
+    """Whether roundings fall one way would show on sums of one sign."""
+    A, B = rnd(1, M, K), rnd(2, K, N)
+    if uniform:
+        A, B = A.abs(), B.abs()
+    want = o.layer(A, B)
+    y = b.gemm_fused(A, B)
+    o.check(y, want["y"], want["y_tol"])
+    # the root of the mean square, too: sqrt(K) roundings of at most S / sqrt(3) u each
+    err = (y.double() - want["y"]).square().mean().sqrt()
+    S = o.product(A, B)[1].square().mean().sqrt()
+    assert err <= math.sqrt(K + 16) * o.U * S
 
 
 @pytest.mark.parametrize("M,N,K", [(64, 64, 64), (300, 260, 200), (1, 300, 1000)])
