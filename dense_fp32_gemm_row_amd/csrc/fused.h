@@ -84,6 +84,9 @@ hipError_t launch_tile_nt(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tn(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tt(const Product &, int tile, hipStream_t);
 
+// At most 64 rows of op(A), in tiles of 16 `columns` columns.
+hipError_t launch_rows(const Product &, int columns, hipStream_t);
+
 hipError_t launch_row_stats(const Product &, hipStream_t);
 
 // C = epilogue(sum over the slices, in their order).

@@ -13,14 +13,17 @@ struct TileSize {
 };
 constexpr TileSize kTiles[] = {{256, 256}, {128, 128}, {64, 128}};
 constexpr int kTileCount = 3;
+constexpr int kRows = 3;           // the kernel for few rows
+constexpr int kRowsMost = 64;
 
 constexpr int kStage = 16;         // k a stage
 constexpr int kMostSplits = 64;
 
 struct Choice {
-    int tile;    // index of kTiles
+    int tile;    // index of kTiles, or kRows
     int splits;  // slices of K
     bool half;   // two fp16 parts of each value where the operands' ranges allow it
+    int columns; // kRows: columns of a tile, in 16
 };
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -28,12 +31,19 @@ inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // `space`: whether there is a workspace.  `slice`: whether the sums may be slices of
 // K (a row's statistics need whole ones).
 inline Choice choose(int64_t batch, int64_t M, int64_t N, int64_t K, bool space, bool slice) {
+    // (as stored, a lane reads `columns` neighbours, so there have to be as many)
+    if (M <= kRowsMost && (!slice || N >= 4)) {
+        const int64_t columns = !slice || N >= 4 * 16 * 512 ? 4 : N >= 2 * 16 * 256 ? 2 : 1;
+        const int64_t tiles = batch * div_up(N, 16 * columns);
+        const int64_t splits = std::min<int64_t>(kMostSplits, std::max<int64_t>(1, std::min(512 / tiles, K / 1024)));
+        return {kRows, space && slice ? static_cast<int>(splits) : 1, false, static_cast<int>(columns)};
+    }
     for (int t = 0; t < kTileCount - 1; ++t)
-        if (batch * div_up(M, kTiles[t].m) * div_up(N, kTiles[t].n) >= 192) return {t, 1, space && K >= 64};
+        if (batch * div_up(M, kTiles[t].m) * div_up(N, kTiles[t].n) >= 192) return {t, 1, space && K >= 64, 0};
     const int t = kTileCount - 1;
     const int64_t tiles = batch * div_up(M, kTiles[t].m) * div_up(N, kTiles[t].n);
     const int64_t splits = std::min<int64_t>(kMostSplits, std::max<int64_t>(1, std::min(512 / tiles, K / 128)));
-    return {t, space && slice ? static_cast<int>(splits) : 1, false};
+    return {t, space && slice ? static_cast<int>(splits) : 1, false, 0};
 }
 
 // Blocks of k in which the statistics of `rows` rows are taken: enough of them to fill the GPU.

@@ -216,7 +216,8 @@ int64_t product_space(int64_t batch, int64_t M, int64_t N, int64_t K, bool slice
 hipError_t launch_product(const Product &asked, hipStream_t stream) {
     Product p = asked;
     p.narrow = narrow_operand(p.a.ld, !p.ta) && narrow_operand(p.b.ld, p.tb);
-    const Choice c = choose(p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore);
+    Choice c = choose(p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore);
+    if (c.tile == kRows && p.target_k != nullptr) c = {kTileCount - 1, 1, false, 0};  // rows look at no target
     p.splits = c.splits;
     p.slices = c.splits > 1 ? p.space : nullptr;
     p.row_a = p.row_b = nullptr;
@@ -227,7 +228,9 @@ hipError_t launch_product(const Product &asked, hipStream_t stream) {
         p.row_b = p.row_a + p.blocks_a * p.batch * p.M;
         err = launch_row_stats(p, stream);
     }
-    if (err == hipSuccess)
+    if (c.tile == kRows)
+        err = launch_rows(p, c.columns, stream);
+    else if (err == hipSuccess)
         err = p.ta ? (p.tb ? launch_tile_tt(p, c.tile, stream) : launch_tile_tn(p, c.tile, stream))
                    : (p.tb ? launch_tile_nt(p, c.tile, stream) : launch_tile_nn(p, c.tile, stream));
     if (err != hipSuccess || p.splits == 1) return err;

@@ -47,7 +47,9 @@ class Guarded:
         assert bool((rest == GUARD).all()), "written outside the output"
 
 
-SHAPES = [(1, 1, 1), (1, 2, 3), (3, 5, 7), (2, 64, 16), (64, 128, 32), (65, 129, 33), (63, 127, 31), (17, 300, 50),
+SHAPES = [(1, 4, 1), (2, 5, 4097), (16, 6, 64), (15, 2100, 200), (33, 9000, 65), (49, 16500, 70), (64, 33000, 40),
+          (7, 32801, 130), (48, 8193, 127), (17, 4, 3000),
+          (1, 1, 1), (1, 2, 3), (3, 5, 7), (2, 64, 16), (64, 128, 32), (65, 129, 33), (63, 127, 31), (17, 300, 50),
           (128, 128, 128), (129, 257, 100), (256, 256, 64), (255, 254, 253), (300, 520, 96), (1, 1000, 333),
           (5, 4, 2000), (1000, 1, 77), (260, 3, 40), (4, 4, 4), (131, 66, 17), (257, 258, 15)]
 
@@ -111,7 +113,7 @@ def test_epilogue(M, N, K, kind, with_bias, with_residual, keep):
         assert bool((z.out == GUARD).all())
 
 
-@pytest.mark.parametrize("M,N,K", [(40, 60, 30), (260, 300, 700), (1, 500, 900)])
+@pytest.mark.parametrize("M,N,K", [(40, 60, 30), (260, 300, 700), (1, 500, 900), (3, 8201, 66), (20, 33001, 40)])
 def test_residual_may_be_the_output(M, N, K):
     A, B, x = rnd(1, M, K), rnd(2, K, N), rnd(3, M, N)
     want = o.layer(A, B, None, "silu", x)
@@ -375,8 +377,11 @@ def tokens(T, V, K, seed=0, ignore=-100, scale=2.0):
     return X, W, target
 
 
-LOSS_SHAPES = [(1, 1, 1), (1, 2, 5), (2, 64, 16), (3, 1000, 40), (64, 128, 32), (65, 129, 33), (100, 777, 65),
-               (130, 64, 64), (1, 5000, 300), (17, 63, 8), (300, 2049, 100), (5, 1, 7), (257, 300, 48), (16, 4096, 64),
+LOSS_SHAPES = [(1, 4, 1), (2, 5, 4097), (16, 6, 64), (15, 2100, 200), (33, 9000, 65), (49, 16500, 70), (64, 33000, 40),
+          (7, 32801, 130), (48, 8193, 127), (17, 4, 3000),
+          (1, 1, 1), (1, 2, 5), (2, 64, 16), (3, 1000, 40), (64, 128, 32), (65, 129, 33), (100, 777, 65),
+               (130, 64, 64), (1, 5000, 300), (17, 63, 8), (300, 2049, 100), (5, 1, 7), (257, 300, 48), (16, 4096, 64), (48, 700, 90),
+               (64, 130, 1000), (33, 65, 64),
                (1700, 2000, 72), (3340, 3700, 50), (2000, 9001, 1800)]
 
 
@@ -430,7 +435,7 @@ def test_every_token_ignored():
     assert not b.cross_entropy(X, W, target)[0].any()
 
 
-@pytest.mark.parametrize("T,V,K", [(70, 200, 32), (300, 300, 64), (3, 500, 64)])
+@pytest.mark.parametrize("T,V,K", [(70, 200, 32), (300, 300, 64), (3, 500, 64), (70, 40, 32), (300, 7, 70)])
 def test_ignored_rows_may_hold_anything(T, V, K):
     """Padding of NaN, infinities and huge values takes no part; the tokens
     beside it keep their values to the last bit."""
