@@ -39,7 +39,7 @@ struct RowStat {
 // What the tile kernel does with a tile's sums.
 enum Mode : int {  // of a product
     kStore = 0,       // the epilogue (or raw slices), stored
-    kStats = 1,       // a maximum and a sum of exponentials per row and 64 columns
+    kStats = 1,       // a maximum and a sum of exponentials per row and group of columns
     kStoreStats = 2,  // both; the sums are stored as they are
 };
 
@@ -59,7 +59,7 @@ struct Product {
     const RowStat *row_a, *row_b;  // [block of k][batch * rows], or null: no fp16 parts
     int blocks_a, blocks_b;
     bool lenient;   // fp16 parts wherever a row's range allows scaling it
-    // kStats, kStoreStats (no batch, no slices): stats[row * groups + column / 64];
+    // kStats, kStoreStats (no batch, no slices): stats[row * groups + column / group_columns(M)];
     // at_target[row] gets the sum in column target[row], where there is one.
     Mode mode;
     stat2 *stats;
@@ -75,7 +75,7 @@ struct Product {
 hipError_t launch_product(const Product &, hipStream_t);
 // Bytes of workspace that a product is quickest with; it runs with none, too.
 // `slice`: its mode is kStore.
-int64_t product_space(int64_t batch, int64_t M, int64_t N, int64_t K, bool slice);
+int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool slice);
 
 // The tile kernels, by operand form (fused_nn.hip ...); `tile` as in
 // fused_choice.h.
@@ -84,8 +84,8 @@ hipError_t launch_tile_nt(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tn(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tt(const Product &, int tile, hipStream_t);
 
-// At most 64 rows of op(A), in tiles of 16 `columns` columns.
-hipError_t launch_rows(const Product &, int columns, hipStream_t);
+// At most 32 rows of op(A); `shape` as in fused_choice.h.
+hipError_t launch_rows(const Product &, int shape, hipStream_t);
 
 hipError_t launch_row_stats(const Product &, hipStream_t);
 

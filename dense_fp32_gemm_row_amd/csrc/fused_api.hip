@@ -60,9 +60,9 @@ int check_workspace(void *workspace, int64_t bytes, int64_t need, Bytes *out) {
 }
 
 // Bytes of a product's own workspace.
-int64_t space_of(int64_t batch, int64_t M, int64_t N, int64_t K, bool slice = true) {
+int64_t space_of(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool slice = true) {
     if (batch == 0 || M == 0 || N == 0 || K == 0) return 0;
-    return fused::product_space(batch, M, N, K, slice);
+    return fused::product_space(tb, batch, M, N, K, slice);
 }
 
 fused::Product plain_product(int64_t batch, int64_t M, int64_t N, int64_t K, bool ta, fused::Operand a, bool tb,
@@ -100,20 +100,24 @@ GradParts grad_parts(bool ta, bool tb, int64_t batch, int64_t M, int64_t N, int6
     if (activation != GEMM_F32_ACT_NONE && (dA || dB)) g.dz = times(times(batch, M), N);
     if (dbias) g.partial = times(times(batch, g.blocks), N);
     // (the sizes of the products as they are run)
-    if (dA) g.space = (ta ? space_of(batch, K, M, N) : space_of(batch, M, K, N)) / 4;
-    if (dB) g.space = std::max(g.space, (tb ? space_of(batch, N, K, M) : space_of(batch, K, N, M)) / 4);
+    if (dA) g.space = (ta ? space_of(true, batch, K, M, N) : space_of(!tb, batch, M, K, N)) / 4;
+    if (dB) g.space = std::max(g.space, (tb ? space_of(ta, batch, N, K, M) : space_of(false, batch, K, N, M)) / 4);
     return g;
 }
 
 // ---- the parts of a cross entropy's workspace ----
-int groups_of(int64_t V) { return static_cast<int>(div_up(V, 64)); }
+int groups_of(int64_t T, int64_t V) { return static_cast<int>(div_up(V, fused::group_columns(T))); }
 int64_t stats_bytes(int64_t T, int64_t V) {  // statistics, logit at the target, lse
-    return plus(times(times(8, T), groups_of(V)), times(8, T));
+    return plus(times(times(8, T), groups_of(T, V)), times(8, T));
 }
-// The gradient works on `rows` tokens at a time, whose logits it holds.
-int64_t piece_bytes(int64_t rows, int64_t V) { return plus(times(times(4, rows), V), stats_bytes(rows, V)); }
+// The gradient works on at most `rows` tokens at a time, whose logits it holds.  (A
+// last piece of few tokens has statistics of more groups.)
+int64_t piece_bytes(int64_t rows, int64_t V) {
+    const int64_t few = std::min<int64_t>(rows, fused::kRowsMost);
+    return plus(times(times(4, rows), V), std::max(stats_bytes(rows, V), stats_bytes(few, V)));
+}
 int64_t piece_space(int64_t rows, int64_t V, int64_t K) {
-    return std::max({space_of(1, rows, V, K, false), space_of(1, rows, K, V), space_of(1, V, K, rows)});
+    return std::max({space_of(true, 1, rows, V, K, false), space_of(false, 1, rows, K, V), space_of(false, 1, V, K, rows)});
 }
 constexpr int64_t kPieceBytes = int64_t{4} << 30;
 constexpr int64_t kPieceRows = 256;
@@ -182,7 +186,7 @@ int gemm_f32_fused(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_
         rc = check_float("pre", e.pre, batch, M, N, e.ld_pre, e.stride_pre, true, &pre);
     if (rc != GEMM_F32_OK) return rc;
     if (used == 0) return GEMM_F32_OK;
-    const int64_t need = workspace != nullptr ? space_of(batch, M, N, K) : 0;
+    const int64_t need = workspace != nullptr ? space_of(tb, batch, M, N, K) : 0;
     rc = check_workspace(workspace, workspace_bytes, need, &w);
     if (rc != GEMM_F32_OK) return rc;
     // the residual may be C itself: an element is read by the thread that writes it, before
@@ -202,7 +206,7 @@ int gemm_f32_fused(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_
 
 int64_t gemm_f32_fused_workspace_size(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_t K) {
     if (!known_op(opA) || !known_op(opB) || !valid_sizes(batch, M, N, K)) return 0;
-    return space_of(batch, M, N, K);
+    return space_of(opB == GEMM_F32_OP_T, batch, M, N, K);
 }
 
 int gemm_f32_fused_grad(int opA, int opB, int64_t batch, int64_t M, int64_t N, int64_t K, const float *dC,
@@ -286,10 +290,10 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
     if (rc == GEMM_F32_OK) rc = check_apart({lo, ls, ws}, {x, w, t});
     if (rc != GEMM_F32_OK) return rc;
     float *at = static_cast<float *>(workspace);
-    float *space = space_of(1, T, V, K, false) ? at + stats_bytes(T, V) / 4 : nullptr;
+    float *space = space_of(true, 1, T, V, K, false) ? at + stats_bytes(T, V) / 4 : nullptr;
     fused::Product p = plain_product(1, T, V, K, false, {X, ldx, 0}, true, {W, ldw, 0}, {}, space);
     p.mode = fused::kStats;
-    p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * T), p.groups = groups_of(V);
+    p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * T), p.groups = groups_of(T, V);
     p.target = target, p.ignore = ignore_index;
     fused::Loss l{};
     l.T = p.M, l.V = p.N, l.stats = p.stats, l.groups = p.groups, l.at_target = p.at_target;
@@ -301,7 +305,7 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
 }
 
 int64_t gemm_f32_cross_entropy_workspace_size(int64_t T, int64_t V, int64_t K) {
-    return valid_sizes(1, T, V, K) ? plus(stats_bytes(T, V), space_of(1, T, V, K, false)) : 0;
+    return valid_sizes(1, T, V, K) ? plus(stats_bytes(T, V), space_of(true, 1, T, V, K, false)) : 0;
 }
 
 int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X, int64_t ldx, const float *W,
@@ -337,16 +341,16 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             return run(plain_product(1, V, K, 0, true, {}, false, {}, {dW, lddw, 0}, nullptr), s);
         for (int64_t t0 = 0; t0 < T && err == hipSuccess; t0 += rows) {
             const int64_t n = std::min(rows, T - t0);
-            float *logits = at + 2 * n + 2 * n * groups_of(V);
+            float *logits = at + 2 * n + 2 * n * groups_of(n, V);
             float *space = sliced && bytes > piece_bytes(best, V) ? at + piece_bytes(best, V) / 4 : nullptr;
             // (the last piece may be shorter, and ask for more)
-            auto room = [&](int64_t M, int64_t N, int64_t k, bool slice = true) {
-                return space != nullptr && space_of(1, M, N, k, slice) <= full - piece_bytes(best, V) ? space : nullptr;
+            auto room = [&](bool tb, int64_t M, int64_t N, int64_t k, bool slice = true) {
+                return space != nullptr && space_of(tb, 1, M, N, k, slice) <= full - piece_bytes(best, V) ? space : nullptr;
             };
             const float *Xt = X + t0 * ldx;
-            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, V, 0}, room(n, V, K, false));
+            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, V, 0}, room(true, n, V, K, false));
             p.mode = fused::kStoreStats;
-            p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * n), p.groups = groups_of(V);
+            p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * n), p.groups = groups_of(n, V);
             p.target = target + t0, p.ignore = ignore_index;
             err = run(p, s);
             fused::Loss l{};
@@ -359,12 +363,12 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             if (err == hipSuccess) err = fused::launch_probabilities(l, s);
             if (err == hipSuccess && dX != nullptr) {
                 p = plain_product(1, n, K, V, false, {logits, V, 0}, false, {W, ldw, 0},
-                                        {dX + t0 * lddx, lddx, 0}, room(n, K, V));
+                                        {dX + t0 * lddx, lddx, 0}, room(false, n, K, V));
                 p.lenient = true;
                 err = run(p, s);
             }
             if (err == hipSuccess && dW != nullptr) {
-                p = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0}, room(V, K, n));
+                p = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0}, room(false, V, K, n));
                 p.lenient = true;
                 p.target_k = target + t0, p.ignore = ignore_index;
                 if (t0 > 0) p.e.residual = {dW, lddw, 0};  // the pieces before

@@ -8,16 +8,47 @@ namespace gemm_f32_impl {
 namespace fused {
 namespace {
 
-// A workgroup of 8 wavefronts holds 16 MG rows and 16 NG columns; its
-// wavefronts take steps of 64 (32) k in turn, straight from global memory, a step
-// ahead, and their sums are added in LDS in a fixed order.  In
-// v_mfma_f32_16x16x4_f32 lane l holds one k, l / 16, of row (column) l % 16; here
+// The epilogue for one sum, or its slice.
+__device__ __forceinline__ void finish(const Product &p, int64_t b, int64_t slice, int m, int n, float z) {
+    if (p.splits > 1) {
+        p.slices[(slice * p.M + m) * p.N + n] = z;
+        return;
+    }
+    if (p.e.bias.p != nullptr) z += p.e.bias.p[b * p.e.bias.stride + n];
+    if (p.e.pre.p != nullptr) p.e.pre.p[b * p.e.pre.stride + m * p.e.pre.ld + n] = z;
+    float v = activate(p.e.activation, z);
+    if (p.e.residual.p != nullptr) v += p.e.residual.p[b * p.e.residual.stride + m * p.e.residual.ld + n];
+    p.c.p[b * p.c.stride + m * p.c.ld + n] = v;
+}
+
+// One sum of 16 neighbouring columns that 16 lanes hold, all of which come here
+// together; `in`: it is one of C.
+__device__ __forceinline__ void store_cell(const Product &p, int64_t b, int64_t slice, int m, int n, float v, bool in) {
+    if (p.mode == kStore) {
+        if (in) finish(p, b, slice, m, n, v);
+        return;
+    }
+    float top = in ? v : -__builtin_inff();
+    for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    float s = in ? expf(v - (top == -__builtin_inff() ? 0.0f : top)) : 0.0f;
+    for (int d = 1; d < 16; d *= 2) s += __shfl_xor(s, d);
+    if (!in) return;
+    if (n % 16 == 0) p.stats[static_cast<int64_t>(m) * p.groups + n / 16] = stat2{top, s};
+    if (p.target[m] == n) p.at_target[m] = v;
+    if (p.mode == kStoreStats) p.c.p[m * p.c.ld + n] = v;
+}
+
+// In v_mfma_f32_16x16x4_f32 lane l holds one k, l / 16, of row (column) l % 16; here
 // lane group g = l / 16 holds k 16 u + 4 g + j of a step in instruction (u, j),
-// so its part of A, and of B where that is stored N x K (TB), is 16 bytes of a
-// row.  B stored K x N is read NG neighbouring columns at a time.
+// so its part of A is 16 bytes of a row.
+
+// B stored K x N: a workgroup of 8 wavefronts holds 16 MG rows and 16 NG
+// columns; its wavefronts take steps of 64 (32) k in turn, NG neighbouring
+// columns of a row a lane, straight from global memory, a step ahead, and their
+// sums are added in LDS in a fixed order.
 constexpr int kRowsWaves = 8;
 constexpr int quads_of(int mg, int ng) { return (mg + ng) * 4 <= 20 ? 4 : 2; }  // for two steps' registers
-template <int MG, int NG, bool TB>
+template <int MG, int NG, bool TA, bool TB>
 __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int tiles_n, int64_t tiles, int len) {
     constexpr int kQuads = quads_of(MG, NG), kStep = 16 * kQuads;
     typedef float cols_t __attribute__((ext_vector_type(NG < 2 ? 2 : NG), aligned(4)));
@@ -31,14 +62,15 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int ti
         const int k1 = max(k0, static_cast<int>(min(static_cast<int64_t>(k0) + len, static_cast<int64_t>(p.K))));
         const float *A = p.a.p + b * p.a.stride, *B = p.b.p + b * p.b.stride;
         // rows and columns past the end repeat the last ones' and are not stored
-        const float *pa[MG], *pb[TB ? NG : 1];
+        const float *pa[MG];
 #pragma unroll
         for (int m = 0; m < MG; ++m) {
             const int64_t r = min(16 * m + at, p.M - 1);
-            pa[m] = A + (p.ta ? r : r * p.a.ld);
+            pa[m] = A + (TA ? r : r * p.a.ld);
         }
         // as stored: a lane whose columns pass the end takes the last NG
         const int first = min(n0 + NG * at, p.N - NG);
+        const float *pb[TB ? NG : 1];
         if constexpr (TB) {
 #pragma unroll
             for (int c = 0; c < NG; ++c) pb[c] = B + static_cast<int64_t>(min(n0 + 16 * c + at, p.N - 1)) * p.b.ld;
@@ -49,77 +81,89 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int ti
             f32x4 a[MG][kQuads];
             f32x4 b[NG][kQuads];
         };
-        auto load = [&](int k) {
-            Step s;
-            const bool whole = k + kStep <= k1;
+        auto load = [&](int s, auto whole_) {
+            constexpr bool kWhole = decltype(whole_)::value;  // else k past k1 is zero
+            const int k = k0 + s * kStep;
+            Step x;
 #pragma unroll
             for (int u = 0; u < kQuads; ++u) {
                 const int q = k + 16 * u + 4 * group;
                 if constexpr (TB) {
 #pragma unroll
                     for (int c = 0; c < NG; ++c) {
-                        if (whole) {
-                            s.b[c][u] = *reinterpret_cast<const float4u *>(pb[c] + q);
+                        if constexpr (kWhole) {
+                            x.b[c][u] = *reinterpret_cast<const float4u *>(pb[c] + q);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) s.b[c][u][j] = q + j < k1 ? pb[c][q + j] : 0.0f;
+                            for (int j = 0; j < 4; ++j) x.b[c][u][j] = q + j < k1 ? pb[c][q + j] : 0.0f;
                         }
                     }
-                } else {
+                } else
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float *from = pb[0] + static_cast<int64_t>(whole ? q + j : min(q + j, k1 - 1)) * p.b.ld;
-                        const bool in = whole || q + j < k1;
-                        if constexpr (NG == 1) {
-                            s.b[0][u][j] = in ? *from : 0.0f;
-                        } else {
-                            const cols_t v = *reinterpret_cast<const cols_t *>(from);
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = kWhole || q + j < k1;
+                    const float *from = pb[0] + static_cast<int64_t>(in ? q + j : k1 - 1) * p.b.ld;
+                    if constexpr (NG == 1) {
+                        x.b[0][u][j] = in ? *from : 0.0f;
+                    } else {
+                        const cols_t v = *reinterpret_cast<const cols_t *>(from);
 #pragma unroll
-                            for (int c = 0; c < NG; ++c) s.b[c][u][j] = in ? v[c] : 0.0f;
-                        }
+                        for (int c = 0; c < NG; ++c) x.b[c][u][j] = in ? v[c] : 0.0f;
                     }
                 }
 #pragma unroll
                 for (int m = 0; m < MG; ++m) {
-                    if (!p.ta && whole) {
-                        s.a[m][u] = *reinterpret_cast<const float4u *>(pa[m] + q);
+                    if (kWhole && !TA) {
+                        x.a[m][u] = *reinterpret_cast<const float4u *>(pa[m] + q);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            s.a[m][u][j] = whole || q + j < k1 ? pa[m][p.ta ? (q + j) * p.a.ld : q + j] : 0.0f;
+                            x.a[m][u][j] = kWhole || q + j < k1 ? pa[m][TA ? (q + j) * p.a.ld : q + j] : 0.0f;
                     }
                 }
             }
-            return s;
+            return x;
         };
         f32x4 acc[MG][NG];
 #pragma unroll
         for (int m = 0; m < MG; ++m)
 #pragma unroll
             for (int c = 0; c < NG; ++c) acc[m][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        int k = k0 + wave * kStep;
-        if (k < k1) {
-            Step now = load(k);
-            for (;;) {
-                const int ahead = k + kRowsWaves * kStep;
-                const bool more = ahead < k1;
-                Step next;
-                if (more) next = load(ahead);
+        auto step = [&](const Step &x) {
 #pragma unroll
-                for (int u = 0; u < kQuads; ++u)
+            for (int u = 0; u < kQuads; ++u)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int m = 0; m < MG; ++m)
+                    for (int m = 0; m < MG; ++m)
 #pragma unroll
-                            for (int c = 0; c < NG; ++c)
-                                acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(now.a[m][u][j], now.b[c][u][j],
-                                                                                 acc[m][c], 0, 0, 0);
-                if (!more) break;
-                now = next;
-                k = ahead;
+                        for (int c = 0; c < NG; ++c)
+                            acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.a[m][u][j], x.b[c][u][j], acc[m][c], 0, 0, 0);
+        };
+        constexpr std::true_type all;
+        const int whole = (k1 - k0) / kStep;
+        if (wave < whole) {
+            // loads past the last step repeat it and are not used: what is on its
+            // way is known at every point
+            const int count = (whole - wave + kRowsWaves - 1) / kRowsWaves;
+            // Where rows are a power of two apart, workgroups that all start at
+            // k0 ask the same few memory channels: each starts elsewhere.
+            const int turn = TB && NG == 1 ? static_cast<int>(t % count) : 0;
+            auto turned = [&](int s) {
+                s = min(s, count - 1) + turn;
+                return wave + (s < count ? s : s - count) * kRowsWaves;
+            };
+            Step x = load(turned(0), all), y;
+            int s = 0;
+            for (; s + 1 < count; s += 2) {
+                y = load(turned(s + 1), all);
+                step(x);
+                x = load(turned(s + 2), all);
+                step(y);
             }
+            if (s < count) step(x);
         }
+        if (whole * kStep < k1 - k0 && whole % kRowsWaves == wave) step(load(whole, std::false_type{}));
 #pragma unroll
         for (int m = 0; m < MG; ++m)
 #pragma unroll
@@ -127,79 +171,163 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int ti
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sums[wave][m * NG + c][r][lane] = acc[m][c][r];
         __syncthreads();
-        // the sum of row m, column c of the tile
-        auto total = [&](int m, int c) {
+        for (int o = threadIdx.x; o < 256 * MG * NG; o += 64 * kRowsWaves) {
+            const int c = o % (16 * NG), m = o / (16 * NG);
+            // a lane that was moved back has columns that its neighbours store
+            const int wanted = TB ? n0 + c : n0 + c / NG * NG, n = TB ? wanted : min(wanted, p.N - NG) + c % NG;
             const int cell = m / 16 * NG + (TB ? c / 16 : c % NG), l = (TB ? c % 16 : c / NG) + 16 * (m % 16 / 4);
             float v = sums[0][cell][m & 3][l];
 #pragma unroll
             for (int w = 1; w < kRowsWaves; ++w) v += sums[w][cell][m & 3][l];
-            return v;
-        };
-        // Column c of the tile is column n of C; as stored, a lane that was moved back
-        // has columns that its neighbours store.
-        auto column = [&](int c) {
-            if (TB) return n0 + c < p.N ? n0 + c : -1;
-            const int wanted = n0 + c / NG * NG, n = min(wanted, p.N - NG) + c % NG;
-            return wanted < p.N && n >= wanted ? n : -1;
-        };
-        if (p.mode != kStore) {
-            // NG == 4: a wavefront a row
-            for (int m = wave; m < 16 * MG && m < p.M; m += kRowsWaves) {
-                const int n = lane < 16 * NG ? column(lane) : -1;
-                const float v = n >= 0 ? total(m, lane) : -__builtin_inff();
-                float top = v;
-                for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-                float s = n >= 0 ? expf(v - (top == -__builtin_inff() ? 0.0f : top)) : 0.0f;
-                for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-                if (lane == 0) p.stats[static_cast<int64_t>(m) * p.groups + n0 / 64] = stat2{top, s};
-                if (n >= 0 && p.target[m] == n) p.at_target[m] = v;
-                if (n >= 0 && p.mode == kStoreStats) p.c.p[m * p.c.ld + n] = v;
-            }
-        } else {
-            for (int o = threadIdx.x; o < 256 * MG * NG; o += 64 * kRowsWaves) {
-                const int c = o % (16 * NG), m = o / (16 * NG), n = column(c);
-                if (m >= p.M || n < 0) continue;
-                float z = total(m, c);
-                if (p.splits > 1) {
-                    p.slices[(slice * p.M + m) * p.N + n] = z;
-                    continue;
-                }
-                if (p.e.bias.p != nullptr) z += p.e.bias.p[b * p.e.bias.stride + n];
-                if (p.e.pre.p != nullptr) p.e.pre.p[b * p.e.pre.stride + m * p.e.pre.ld + n] = z;
-                float v = activate(p.e.activation, z);
-                if (p.e.residual.p != nullptr)
-                    v += p.e.residual.p[b * p.e.residual.stride + m * p.e.residual.ld + n];
-                p.c.p[b * p.c.stride + m * p.c.ld + n] = v;
-            }
+            store_cell(p, b, slice, m, n, v, m < p.M && wanted < p.N && n >= wanted);
         }
         __syncthreads();
     }
 }
 
-template <int MG, int NG, bool TB>
+// B stored N x K, MR (1, 2 or 4) rows of op(A): a wavefront holds 4 columns,
+// which are rows of B that it reads 1 KiB at a time, and a lane the products of
+// its 4 k; a workgroup of 4 wavefronts 16 columns.  The 64 lanes' sums are added by halves.
+template <int MR, bool TA>
+__global__ __launch_bounds__(256) void vector_kernel(Product p, int tiles_n, int64_t tiles, int len) {
+    constexpr int R = 4, kStep = 256, U = 2;  // U steps' loads on their way at once
+    __shared__ float cells[MR][16];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t slice = t / tiles_n, b = slice / p.splits;
+        const int n0 = static_cast<int>(t - slice * tiles_n) * 16;
+        const int k0 = static_cast<int>(slice - b * p.splits) * len;
+        const int k1 = max(k0, static_cast<int>(min(static_cast<int64_t>(k0) + len, static_cast<int64_t>(p.K))));
+        const float *A = p.a.p + b * p.a.stride, *B = p.b.p + b * p.b.stride;
+        // rows and columns past the end repeat the last ones' and are not stored
+        const float *row[R], *x[MR];
+#pragma unroll
+        for (int r = 0; r < R; ++r) row[r] = B + static_cast<int64_t>(min(n0 + R * wave + r, p.N - 1)) * p.b.ld;
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            const int64_t q = min(m, p.M - 1);
+            x[m] = A + (TA ? q : q * p.a.ld);
+        }
+        float acc[MR][R];
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[m][r] = 0.0f;
+        struct Step {
+            f32x4 w[R], v[MR];
+        };
+        auto load = [&](int s) {
+            const int k = k0 + s * kStep + 4 * lane;
+            Step q;
+#pragma unroll
+            for (int r = 0; r < R; ++r) q.w[r] = *reinterpret_cast<const float4u *>(row[r] + k);
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                if constexpr (!TA) {
+                    q.v[m] = *reinterpret_cast<const float4u *>(x[m] + k);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q.v[m][e] = x[m][(k + e) * p.a.ld];
+                }
+            }
+            return q;
+        };
+        auto use = [&](const Step &q) {
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][r] = fmaf(q.v[m][e], q.w[r][e], acc[m][r]);
+        };
+        const int whole = (k1 - k0) / kStep;
+        if (whole > 0) {
+            // loads past the last step repeat it and are not used: what is on its
+            // way is known at every point
+            // Where rows are a power of two apart, wavefronts that all start
+            // at k0 ask the same few memory channels: each starts elsewhere.
+            const int turn = static_cast<int>((t * 4 + wave) % whole);
+            auto turned = [&](int s) {
+                s = min(s, whole - 1) + turn;
+                return s < whole ? s : s - whole;
+            };
+            Step q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = load(turned(u));
+            int s = 0;
+            for (; s + U <= whole; s += U)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    use(q[u]);
+                    q[u] = load(turned(s + U + u));
+                }
+#pragma unroll
+            for (int u = 0; u < U - 1; ++u)
+                if (s + u < whole) use(q[u]);
+        }
+        for (int k = k0 + whole * kStep + lane; k < k1; k += 64)  // what is left of K
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                const float v = x[m][TA ? k * p.a.ld : k];
+#pragma unroll
+                for (int r = 0; r < R; ++r) acc[m][r] = fmaf(v, row[r][k], acc[m][r]);
+            }
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                for (int d = 32; d > 0; d /= 2) acc[m][r] += __shfl_xor(acc[m][r], d);
+                if (lane == 0) cells[m][R * wave + r] = acc[m][r];
+            }
+        __syncthreads();
+        const int m = threadIdx.x / 16, n = n0 + threadIdx.x % 16;
+        if (m < MR) {
+            const float v = cells[m][threadIdx.x % 16];
+            store_cell(p, b, slice, m, n, v, m < p.M && n < p.N);
+        }
+        __syncthreads();
+    }
+}
+
+template <int MR, bool TA>
+hipError_t launch_vector(const Product &p, hipStream_t stream) {
+    const int tn = static_cast<int>(div_up(p.N, 16));
+    const int64_t tiles = p.batch * p.splits * tn;
+    const int len = static_cast<int>(div_up(div_up(p.K, 256), p.splits)) * 256;
+    vector_kernel<MR, TA><<<static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20)), 256, 0, stream>>>(p, tn, tiles, len);
+    return hipGetLastError();
+}
+
+template <int MG, int NG, bool TA, bool TB>
 hipError_t launch(const Product &p, hipStream_t stream) {
     const int tn = static_cast<int>(div_up(p.N, 16 * NG));
     const int64_t tiles = p.batch * p.splits * tn;
     const int len = static_cast<int>(div_up(div_up(p.K, 64), p.splits)) * 64;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20));
-    rows_kernel<MG, NG, TB><<<grid, 64 * kRowsWaves, 0, stream>>>(p, tn, tiles, len);
+    rows_kernel<MG, NG, TA, TB><<<grid, 64 * kRowsWaves, 0, stream>>>(p, tn, tiles, len);
     return hipGetLastError();
 }
 
-template <int NG>
-hipError_t launch_columns(const Product &p, hipStream_t stream) {
-    if (p.M <= 16) return p.tb ? launch<1, NG, true>(p, stream) : launch<1, NG, false>(p, stream);
-    if (p.M <= 32) return p.tb ? launch<2, NG, true>(p, stream) : launch<2, NG, false>(p, stream);
-    if (p.M <= 48) return p.tb ? launch<3, NG, true>(p, stream) : launch<3, NG, false>(p, stream);
-    return p.tb ? launch<4, NG, true>(p, stream) : launch<4, NG, false>(p, stream);
+template <int MG, int NG>
+hipError_t launch_shape(const Product &p, hipStream_t stream) {
+    return p.ta ? (p.tb ? launch<MG, NG, true, true>(p, stream) : launch<MG, NG, true, false>(p, stream))
+                : (p.tb ? launch<MG, NG, false, true>(p, stream) : launch<MG, NG, false, false>(p, stream));
+}
+
+template <int MG>
+hipError_t launch_groups(const Product &p, int shape, hipStream_t stream) {
+    return shape == 4 ? launch_shape<MG, 4>(p, stream) : shape == 2 ? launch_shape<MG, 2>(p, stream) : launch_shape<MG, 1>(p, stream);
 }
 
 }  // namespace
 
-hipError_t launch_rows(const Product &p, int columns, hipStream_t stream) {
-    return columns == 4 ? launch_columns<4>(p, stream)
-           : columns == 2 ? launch_columns<2>(p, stream)
-                          : launch_columns<1>(p, stream);
+hipError_t launch_rows(const Product &p, int shape, hipStream_t stream) {
+    if (shape == 0)
+        return p.M == 1   ? (p.ta ? launch_vector<1, true>(p, stream) : launch_vector<1, false>(p, stream))
+               : p.M == 2 ? (p.ta ? launch_vector<2, true>(p, stream) : launch_vector<2, false>(p, stream))
+                          : (p.ta ? launch_vector<4, true>(p, stream) : launch_vector<4, false>(p, stream));
+    return p.M <= 16 ? launch_groups<1>(p, shape, stream) : launch_groups<2>(p, shape, stream);
 }
 
 }  // namespace fused

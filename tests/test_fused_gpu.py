@@ -413,15 +413,16 @@ def test_cross_entropy_grad(T, V, K, weights):
     assert alone[3] is None and torch.equal(alone[2], dX)
 
 
-@pytest.mark.parametrize("T,rows", [(300, 64), (300, 100), (600, 256), (65, 64)])
+@pytest.mark.parametrize("T,rows", [(300, 64), (300, 100), (600, 256), (65, 64), (129, 65)])
 def test_cross_entropy_grad_in_pieces(T, rows):
     """A workspace for `rows` tokens at a time."""
     V, K = 333, 50
     X, W, target = tokens(T, V, K, seed=3)
     want = o.loss_grad(X, W, target)
     least = b.gemm_f32_cross_entropy_grad_workspace_least(T, V, K)
-    space = torch.empty(least // 64 * rows // 4, device=DEV)
-    got = b.cross_entropy_grad(X, W, target, workspace=space)
+    space = torch.full((-(-least * rows // 64) // 4 + 1 + 64,), GUARD, device=DEV)
+    got = b.cross_entropy_grad(X, W, target, workspace=space[:-64])
+    assert bool((space[-64:] == GUARD).all())
     for name, t in zip(("loss", "lse", "dX", "dW"), got):
         o.check(t, *want[name], name)
 
