@@ -66,16 +66,16 @@ struct Product {
     int groups;
     const int64_t *target;
     float *at_target;
-    // Where not null, k with target_k[k] == ignore (whose factors of A are zero) take
-    // no part in a tile that is computed again because a sum came out infinite or NaN.
+    // Where not null, k with target_k[k] == ignore, whose factors of A are zero, take
+    // no part even where B holds infinities or NaN (A stored K x M, B stored K x N).
     const int64_t *target_k;
     int64_t ignore;
 };
 
 hipError_t launch_product(const Product &, hipStream_t);
 // Bytes of workspace that a product is quickest with; it runs with none, too.
-// `slice`: its mode is kStore.
-int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool slice);
+// `statistics`: its mode is not kStore.
+int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics);
 
 // The tile kernels, by operand form (fused_nn.hip ...); `tile` as in
 // fused_choice.h.
@@ -84,7 +84,7 @@ hipError_t launch_tile_nt(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tn(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tt(const Product &, int tile, hipStream_t);
 
-// At most 32 rows of op(A); `shape` as in fused_choice.h.
+// `shape` as in fused_choice.h.
 hipError_t launch_rows(const Product &, int shape, hipStream_t);
 
 hipError_t launch_row_stats(const Product &, hipStream_t);

@@ -60,9 +60,9 @@ int check_workspace(void *workspace, int64_t bytes, int64_t need, Bytes *out) {
 }
 
 // Bytes of a product's own workspace.
-int64_t space_of(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool slice = true) {
+int64_t space_of(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics = false) {
     if (batch == 0 || M == 0 || N == 0 || K == 0) return 0;
-    return fused::product_space(tb, batch, M, N, K, slice);
+    return fused::product_space(tb, batch, M, N, K, statistics);
 }
 
 fused::Product plain_product(int64_t batch, int64_t M, int64_t N, int64_t K, bool ta, fused::Operand a, bool tb,
@@ -113,11 +113,11 @@ int64_t stats_bytes(int64_t T, int64_t V) {  // statistics, logit at the target,
 // The gradient works on at most `rows` tokens at a time, whose logits it holds.  (A
 // last piece of few tokens has statistics of more groups.)
 int64_t piece_bytes(int64_t rows, int64_t V) {
-    const int64_t few = std::min<int64_t>(rows, fused::kRowsMost);
+    const int64_t few = std::min<int64_t>(rows, fused::kFineTokens);
     return plus(times(times(4, rows), V), std::max(stats_bytes(rows, V), stats_bytes(few, V)));
 }
 int64_t piece_space(int64_t rows, int64_t V, int64_t K) {
-    return std::max({space_of(true, 1, rows, V, K, false), space_of(false, 1, rows, K, V), space_of(false, 1, V, K, rows)});
+    return std::max({space_of(true, 1, rows, V, K, true), space_of(false, 1, rows, K, V), space_of(false, 1, V, K, rows)});
 }
 constexpr int64_t kPieceBytes = int64_t{4} << 30;
 constexpr int64_t kPieceRows = 256;
@@ -290,7 +290,7 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
     if (rc == GEMM_F32_OK) rc = check_apart({lo, ls, ws}, {x, w, t});
     if (rc != GEMM_F32_OK) return rc;
     float *at = static_cast<float *>(workspace);
-    float *space = space_of(true, 1, T, V, K, false) ? at + stats_bytes(T, V) / 4 : nullptr;
+    float *space = space_of(true, 1, T, V, K, true) ? at + stats_bytes(T, V) / 4 : nullptr;
     fused::Product p = plain_product(1, T, V, K, false, {X, ldx, 0}, true, {W, ldw, 0}, {}, space);
     p.mode = fused::kStats;
     p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * T), p.groups = groups_of(T, V);
@@ -305,7 +305,7 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
 }
 
 int64_t gemm_f32_cross_entropy_workspace_size(int64_t T, int64_t V, int64_t K) {
-    return valid_sizes(1, T, V, K) ? plus(stats_bytes(T, V), space_of(true, 1, T, V, K, false)) : 0;
+    return valid_sizes(1, T, V, K) ? plus(stats_bytes(T, V), space_of(true, 1, T, V, K, true)) : 0;
 }
 
 int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X, int64_t ldx, const float *W,
@@ -344,11 +344,11 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             float *logits = at + 2 * n + 2 * n * groups_of(n, V);
             float *space = sliced && bytes > piece_bytes(best, V) ? at + piece_bytes(best, V) / 4 : nullptr;
             // (the last piece may be shorter, and ask for more)
-            auto room = [&](bool tb, int64_t M, int64_t N, int64_t k, bool slice = true) {
-                return space != nullptr && space_of(tb, 1, M, N, k, slice) <= full - piece_bytes(best, V) ? space : nullptr;
+            auto room = [&](bool tb, int64_t M, int64_t N, int64_t k, bool statistics = false) {
+                return space != nullptr && space_of(tb, 1, M, N, k, statistics) <= full - piece_bytes(best, V) ? space : nullptr;
             };
             const float *Xt = X + t0 * ldx;
-            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, V, 0}, room(true, n, V, K, false));
+            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, V, 0}, room(true, n, V, K, true));
             p.mode = fused::kStoreStats;
             p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * n), p.groups = groups_of(n, V);
             p.target = target + t0, p.ignore = ignore_index;

@@ -12,44 +12,96 @@ struct TileSize {
     int m, n;
 };
 constexpr TileSize kTiles[] = {{256, 256}, {128, 128}, {64, 128}};
-constexpr int kTileCount = 3;
-constexpr int kRows = 3;           // the kernel for few rows
-constexpr int kRowsMost = 32;
+constexpr int kRows = 3;           // the kernel for few rows and small products
+constexpr int kRowsMost = 32;      // rows for which it, and only it, is taken
+// Tokens for which the cross entropy's statistics are kept by 16 columns, not 64:
+// the kernel for small products holds fewer than 64.
+constexpr int kFineTokens = 512;
 
 constexpr int kStage = 16;         // k a stage
-constexpr int kMostSplits = 64;
+constexpr int kMostSplits = 32;
 
 struct Choice {
     int tile;    // index of kTiles, or kRows
     int splits;  // slices of K
     bool half;   // two fp16 parts of each value where the operands' ranges allow it
-    // kRows: columns of a tile, in 16; 0: the kernel for up to 4 rows, B stored N x K
+    // kRows: rows and columns of a tile in 16, 16 r + c (c <= N where B is stored K x
+    // N, r <= M where A is stored K x M); 0: the kernel for up to 4 rows, B stored N x K
     int shape;
 };
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// `space`: whether there is a workspace.  `slice`: whether the sums may be slices of
-// K (a row's statistics need whole ones).
-// `tb`: B is stored N x K.
-inline Choice choose(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool space, bool slice) {
-    // (as stored, a lane reads 2 neighbours)
+// What a kernel's tile takes, in nanoseconds: `lone` a k where a CU has one of them,
+// `shared` a k of each where it has more, `fixed` besides.  Fitted to 7000 times of 210
+// products of 33 to 8192 rows (three operand forms, 70 sizes drawn evenly over their
+// logarithms): the choice is 3.7% off the best of all kernels and slices on average.
+struct Rate {
+    Choice kind;
+    int m, n;
+    double lone, shared, fixed;
+};
+constexpr Rate kRates[] = {
+    {{kRows, 1, false, 17}, 16, 16, 2.86, 2.70, 751.0},   {{kRows, 1, false, 18}, 16, 32, 4.31, 3.98, 1173.0},
+    {{kRows, 1, false, 34}, 32, 32, 6.68, 6.70, 1972.0},  {{kRows, 1, false, 36}, 32, 64, 11.1, 11.5, 2619.0},
+    {{kRows, 1, false, 66}, 64, 32, 11.0, 11.2, 2906.0},  {{2, 1, false, 0}, 64, 128, 29.4, 21.7, 3683.0},
+    {{1, 1, false, 0}, 128, 128, 35.7, 33.3, 7180.0},     {{1, 1, true, 0}, 128, 128, 26.5, 23.7, 8832.0},
+    {{0, 1, false, 0}, 256, 256, 102.5, 122.3, 26048.0},  {{0, 1, true, 0}, 256, 256, 53.2, 71.9, 32737.0},
+};
+constexpr double kCus = 256;
+constexpr double kBytesNs = 5500;                           // memory, reading
+constexpr double kSumNs = 2660, kSumBytesNs = 5700;         // adding slices
+constexpr double kStatsNs = 8870, kStatsBytesNs = 8120;     // looking at the rows' ranges
+
+inline double predicted(const Rate &r, int64_t batch, int64_t M, int64_t N, int64_t K, int64_t splits) {
+    const double tiles = static_cast<double>(batch) * div_up(M, r.m) * div_up(N, r.n) * splits / kCus;
+    const double k = static_cast<double>(div_up(K, splits)), alone = r.lone * k + r.fixed;
+    const double turns = tiles <= 6 ? static_cast<double>(static_cast<int64_t>(tiles + 0.999999)) : tiles + 0.5;
+    double t = tiles > 1 ? std::max(alone, turns * (r.shared * k + r.fixed)) : alone;
+    const double mk = static_cast<double>(M) * K, nk = static_cast<double>(N) * K, mn = static_cast<double>(M) * N;
+    t = std::max(t, 4 * batch * (mk + nk + mn) / kBytesNs);
+    if (splits > 1) t += kSumNs + 4 * batch * (splits + 1) * mn / kSumBytesNs;
+    if (r.kind.half) t += kStatsNs + 4 * batch * (mk + nk) / kStatsBytesNs;
+    return t;
+}
+
+// What the product is for: statistics of whole rows allow no slices, and of many
+// tokens only the tiles.
+enum Use { kPlain, kStatistics };
+
+// `tb`: B is stored N x K.  `space`: whether there is a workspace.
+inline Choice choose(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool space, Use use) {
+    const bool slice = space && use == kPlain;
+    // Few rows: reading B is the work, in tiles as wide as leaves enough of them (as
+    // stored, a lane reads 2 neighbours): 16 x 14336 x 4096, B transposed, 47 us with 64
+    // columns and 65 with 16, 16 x 4096 x 4096 43 and 18.
     if (M <= kRowsMost && (tb || N >= 2)) {
-        const int shape = tb ? (M <= 4 ? 0 : N >= 8192 ? 4 : 1) : N >= 2048 ? 2 : 1;
-        const int64_t tiles = batch * div_up(N, 16 * std::max(shape, 1));
+        const int c = tb ? (N >= 8192 && M > 4 ? 4 : 1) : N >= 2048 ? 2 : 1;
+        const int shape = tb && M <= 4 ? 0 : (M <= 16 ? 16 : 32) + c;
+        const int64_t tiles = batch * div_up(N, 16 * c);
         const int64_t splits = std::min<int64_t>(kMostSplits, std::max<int64_t>(1, std::min(256 / tiles, K / 1024)));
-        return {kRows, space && slice ? static_cast<int>(splits) : 1, false, shape};
+        return {kRows, slice ? static_cast<int>(splits) : 1, false, shape};
     }
-    for (int t = 0; t < kTileCount - 1; ++t)
-        if (batch * div_up(M, kTiles[t].m) * div_up(N, kTiles[t].n) >= 192) return {t, 1, space && K >= 64, 0};
-    const int t = kTileCount - 1;
-    const int64_t tiles = batch * div_up(M, kTiles[t].m) * div_up(N, kTiles[t].n);
-    const int64_t splits = std::min<int64_t>(kMostSplits, std::max<int64_t>(1, std::min(512 / tiles, K / 128)));
-    return {t, space && slice ? static_cast<int>(splits) : 1, false, 0};
+    Choice best{};
+    double least = 0;
+    for (const Rate &r : kRates) {
+        if (r.kind.half && (!space || K < 64 || K > (int64_t{1} << 22))) continue;
+        if (r.kind.tile == kRows && ((use == kStatistics && M > kFineTokens) || N < 4)) continue;
+        const int64_t tiles = batch * div_up(M, r.m) * div_up(N, r.n);
+        for (int64_t splits = 1; splits <= (slice ? kMostSplits : 1); splits *= 2) {
+            if (splits > 1 && (tiles * splits > 2048 || K < 64 * splits)) break;
+            const double t = predicted(r, batch, M, N, K, splits);
+            if (least > 0 && t >= least) continue;
+            least = t;
+            best = r.kind;
+            best.splits = static_cast<int>(splits);
+        }
+    }
+    return best;
 }
 
 // Columns of a row's piece of the cross entropy's statistics.
-inline int group_columns(int64_t M) { return M <= kRowsMost ? 16 : 64; }
+inline int group_columns(int64_t tokens) { return tokens <= kFineTokens ? 16 : 64; }
 
 // Blocks of k in which the statistics of `rows` rows are taken: enough of them to fill the GPU.
 inline int stat_blocks(int64_t rows, int64_t K, bool k_contiguous) {

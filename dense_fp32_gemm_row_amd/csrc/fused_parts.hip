@@ -202,8 +202,8 @@ hipError_t launch_row_stats(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool slice) {
-    const Choice c = choose(tb, batch, M, N, K, true, slice);
+int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics) {
+    const Choice c = choose(tb, batch, M, N, K, true, statistics ? kStatistics : kPlain);
     const __int128 slices = c.splits > 1 ? static_cast<__int128>(4 * c.splits) * batch * M * N : 0;
     // either form of either operand
     const __int128 stats = c.half ? static_cast<__int128>(sizeof(RowStat)) * batch *
@@ -216,8 +216,7 @@ int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, b
 hipError_t launch_product(const Product &asked, hipStream_t stream) {
     Product p = asked;
     p.narrow = narrow_operand(p.a.ld, !p.ta) && narrow_operand(p.b.ld, p.tb);
-    Choice c = choose(p.tb, p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore);
-    if (c.tile == kRows && p.target_k != nullptr) c = {kTileCount - 1, 1, false, 0};  // rows look at no target
+    const Choice c = choose(p.tb, p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore ? kPlain : kStatistics);
     p.splits = c.splits;
     p.slices = c.splits > 1 ? p.space : nullptr;
     p.row_a = p.row_b = nullptr;

@@ -1,4 +1,5 @@
-// The fused products with few rows of op(A): reading B is the work.
+// The fused products that are small, or have few rows of op(A), so that reading B is
+// the work.
 
 #include <type_traits>
 
@@ -38,89 +39,103 @@ __device__ __forceinline__ void store_cell(const Product &p, int64_t b, int64_t 
     if (p.mode == kStoreStats) p.c.p[m * p.c.ld + n] = v;
 }
 
-// In v_mfma_f32_16x16x4_f32 lane l holds one k, l / 16, of row (column) l % 16; here
-// lane group g = l / 16 holds k 16 u + 4 g + j of a step in instruction (u, j),
-// so its part of A is 16 bytes of a row.
-
-// B stored K x N: a workgroup of 8 wavefronts holds 16 MG rows and 16 NG
-// columns; its wavefronts take steps of 64 (32) k in turn, NG neighbouring
-// columns of a row a lane, straight from global memory, a step ahead, and their
-// sums are added in LDS in a fixed order.
+// Small products and few rows, on FP32 multiplies straight from global memory: a
+// workgroup of 8 wavefronts holds 16 MG rows and 16 NG columns; its wavefronts
+// take steps of 64 (32) k in turn, a step ahead, and their sums are added in LDS
+// in a fixed order.  In v_mfma_f32_16x16x4_f32 lane l holds one k, l / 16, of
+// row (column) l % 16; here lane group g = l / 16 holds k 16 u + 4 g + j of a step in
+// instruction (u, j).  So where k is contiguous a lane's part of a row is 16
+// bytes; where rows are, it takes MG (NG) neighbours at every k.
 constexpr int kRowsWaves = 8;
 constexpr int quads_of(int mg, int ng) { return (mg + ng) * 4 <= 20 ? 4 : 2; }  // for two steps' registers
-template <int MG, int NG, bool TA, bool TB>
-__global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int tiles_n, int64_t tiles, int len) {
+
+// One operand's share of a lane: G groups of 16 rows.
+template <int G, bool KC>
+struct Lines {
+    typedef float group_t __attribute__((ext_vector_type(G < 2 ? 2 : G), aligned(4)));
+    const float *p[KC ? G : 1];
+    int64_t ld;
+    // rows past the end repeat the last ones' and are not stored
+    __device__ __forceinline__ Lines(const Operand &x, int64_t batch, int first, int rows, int at) {
+        ld = x.ld;
+        const float *base = x.p + batch * x.stride;
+        if constexpr (KC) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) p[g] = base + static_cast<int64_t>(min(first + 16 * g + at, rows - 1)) * ld;
+        } else {
+            p[0] = base + min(first + G * at, rows - G);  // moved back from past the end
+        }
+    }
+    // Row r of the tile: its group, its place among 16, the row of the operand.
+    static __device__ __forceinline__ int group(int r) { return KC ? r / 16 : r % G; }
+    static __device__ __forceinline__ int place(int r) { return KC ? r % 16 : r / G; }
+    // -1: past the end, or a neighbour's where the lane was moved back
+    static __device__ __forceinline__ int row(int first, int r, int rows) {
+        const int wanted = KC ? first + r : first + r / G * G, got = KC ? wanted : min(wanted, rows - G) + r % G;
+        return wanted < rows && got >= wanted ? got : -1;
+    }
+    // 4 k from k on; past k1, if not WHOLE, zero, and, if SKIP, where skip[k] is `ignore`.
+    template <bool WHOLE, bool SKIP>
+    __device__ __forceinline__ void load(int k, int k1, f32x4 (&v)[G], const int64_t *skip, int64_t ignore) const {
+        if constexpr (KC) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if constexpr (WHOLE) {
+                    v[g] = *reinterpret_cast<const float4u *>(p[g] + k);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[g][j] = k + j < k1 ? p[g][k + j] : 0.0f;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bool in = WHOLE || k + j < k1;
+                const int64_t at = in ? k + j : k1 - 1;
+                const float *from = p[0] + at * ld;
+                if constexpr (SKIP) in = in && skip[at] != ignore;
+                if constexpr (G == 1) {
+                    v[0][j] = in ? *from : 0.0f;
+                } else {
+                    const group_t x = *reinterpret_cast<const group_t *>(from);
+#pragma unroll
+                    for (int g = 0; g < G; ++g) v[g][j] = in ? x[g] : 0.0f;
+                }
+            }
+        }
+    }
+};
+
+template <int MG, int NG, bool TA, bool TB, bool SKIP>
+__global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int tiles_m, int tiles_n, int64_t tiles,
+                                                               int len) {
     constexpr int kQuads = quads_of(MG, NG), kStep = 16 * kQuads;
-    typedef float cols_t __attribute__((ext_vector_type(NG < 2 ? 2 : NG), aligned(4)));
+    using LA = Lines<MG, !TA>;
+    using LB = Lines<NG, TB>;
     __shared__ __align__(16) float sums[kRowsWaves][MG * NG][4][64];
     const int lane = threadIdx.x & 63, at = lane & 15, group = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t slice = t / tiles_n, b = slice / p.splits;
-        const int n0 = static_cast<int>(t - slice * tiles_n) * 16 * NG;
+    const int64_t per = static_cast<int64_t>(tiles_m) * tiles_n;
+    for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < tiles; t += gridDim.x) {
+        const int64_t slice = t / per, b = slice / p.splits;
+        int tm, tn;
+        grouped_tile(static_cast<int>(t - slice * per), tiles_m, tiles_n, 8, tm, tn);
+        const int m0 = tm * 16 * MG, n0 = tn * 16 * NG;
         const int k0 = static_cast<int>(slice - b * p.splits) * len;
         const int k1 = max(k0, static_cast<int>(min(static_cast<int64_t>(k0) + len, static_cast<int64_t>(p.K))));
-        const float *A = p.a.p + b * p.a.stride, *B = p.b.p + b * p.b.stride;
-        // rows and columns past the end repeat the last ones' and are not stored
-        const float *pa[MG];
-#pragma unroll
-        for (int m = 0; m < MG; ++m) {
-            const int64_t r = min(16 * m + at, p.M - 1);
-            pa[m] = A + (TA ? r : r * p.a.ld);
-        }
-        // as stored: a lane whose columns pass the end takes the last NG
-        const int first = min(n0 + NG * at, p.N - NG);
-        const float *pb[TB ? NG : 1];
-        if constexpr (TB) {
-#pragma unroll
-            for (int c = 0; c < NG; ++c) pb[c] = B + static_cast<int64_t>(min(n0 + 16 * c + at, p.N - 1)) * p.b.ld;
-        } else {
-            pb[0] = B + first;
-        }
+        const LA la(p.a, b, m0, p.M, at);
+        const LB lb(p.b, b, n0, p.N, at);
         struct Step {
-            f32x4 a[MG][kQuads];
-            f32x4 b[NG][kQuads];
+            f32x4 a[kQuads][MG], b[kQuads][NG];
         };
         auto load = [&](int s, auto whole_) {
-            constexpr bool kWhole = decltype(whole_)::value;  // else k past k1 is zero
-            const int k = k0 + s * kStep;
+            constexpr bool kWhole = decltype(whole_)::value;
             Step x;
 #pragma unroll
             for (int u = 0; u < kQuads; ++u) {
-                const int q = k + 16 * u + 4 * group;
-                if constexpr (TB) {
-#pragma unroll
-                    for (int c = 0; c < NG; ++c) {
-                        if constexpr (kWhole) {
-                            x.b[c][u] = *reinterpret_cast<const float4u *>(pb[c] + q);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) x.b[c][u][j] = q + j < k1 ? pb[c][q + j] : 0.0f;
-                        }
-                    }
-                } else
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool in = kWhole || q + j < k1;
-                    const float *from = pb[0] + static_cast<int64_t>(in ? q + j : k1 - 1) * p.b.ld;
-                    if constexpr (NG == 1) {
-                        x.b[0][u][j] = in ? *from : 0.0f;
-                    } else {
-                        const cols_t v = *reinterpret_cast<const cols_t *>(from);
-#pragma unroll
-                        for (int c = 0; c < NG; ++c) x.b[c][u][j] = in ? v[c] : 0.0f;
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < MG; ++m) {
-                    if (kWhole && !TA) {
-                        x.a[m][u] = *reinterpret_cast<const float4u *>(pa[m] + q);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            x.a[m][u][j] = kWhole || q + j < k1 ? pa[m][TA ? (q + j) * p.a.ld : q + j] : 0.0f;
-                    }
-                }
+                const int k = k0 + s * kStep + 16 * u + 4 * group;
+                lb.template load<kWhole, SKIP>(k, k1, x.b[u], p.target_k, p.ignore);
+                la.template load<kWhole, false>(k, k1, x.a[u], nullptr, 0);
             }
             return x;
         };
@@ -138,7 +153,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int ti
                     for (int m = 0; m < MG; ++m)
 #pragma unroll
                         for (int c = 0; c < NG; ++c)
-                            acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.a[m][u][j], x.b[c][u][j], acc[m][c], 0, 0, 0);
+                            acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.a[u][m][j], x.b[u][c][j], acc[m][c], 0, 0, 0);
         };
         constexpr std::true_type all;
         const int whole = (k1 - k0) / kStep;
@@ -172,14 +187,13 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int ti
                 for (int r = 0; r < 4; ++r) sums[wave][m * NG + c][r][lane] = acc[m][c][r];
         __syncthreads();
         for (int o = threadIdx.x; o < 256 * MG * NG; o += 64 * kRowsWaves) {
-            const int c = o % (16 * NG), m = o / (16 * NG);
-            // a lane that was moved back has columns that its neighbours store
-            const int wanted = TB ? n0 + c : n0 + c / NG * NG, n = TB ? wanted : min(wanted, p.N - NG) + c % NG;
-            const int cell = m / 16 * NG + (TB ? c / 16 : c % NG), l = (TB ? c % 16 : c / NG) + 16 * (m % 16 / 4);
-            float v = sums[0][cell][m & 3][l];
+            const int c = o % (16 * NG), r = o / (16 * NG), q = LA::place(r);
+            const int cell = LA::group(r) * NG + LB::group(c), l = LB::place(c) + 16 * (q / 4);
+            float v = sums[0][cell][q & 3][l];
 #pragma unroll
-            for (int w = 1; w < kRowsWaves; ++w) v += sums[w][cell][m & 3][l];
-            store_cell(p, b, slice, m, n, v, m < p.M && wanted < p.N && n >= wanted);
+            for (int w = 1; w < kRowsWaves; ++w) v += sums[w][cell][q & 3][l];
+            const int m = LA::row(m0, r, p.M), n = LB::row(n0, c, p.N);
+            store_cell(p, b, slice, m, n, v, m >= 0 && n >= 0);
         }
         __syncthreads();
     }
@@ -299,25 +313,21 @@ hipError_t launch_vector(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int MG, int NG, bool TA, bool TB>
+template <int MG, int NG, bool TA, bool TB, bool SKIP = false>
 hipError_t launch(const Product &p, hipStream_t stream) {
-    const int tn = static_cast<int>(div_up(p.N, 16 * NG));
-    const int64_t tiles = p.batch * p.splits * tn;
+    const int tm = static_cast<int>(div_up(p.M, 16 * MG)), tn = static_cast<int>(div_up(p.N, 16 * NG));
+    const int64_t tiles = p.batch * p.splits * tm * tn;
     const int len = static_cast<int>(div_up(div_up(p.K, 64), p.splits)) * 64;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20));
-    rows_kernel<MG, NG, TA, TB><<<grid, 64 * kRowsWaves, 0, stream>>>(p, tn, tiles, len);
+    rows_kernel<MG, NG, TA, TB, SKIP><<<grid, 64 * kRowsWaves, 0, stream>>>(p, tm, tn, tiles, len);
     return hipGetLastError();
 }
 
 template <int MG, int NG>
-hipError_t launch_shape(const Product &p, hipStream_t stream) {
+hipError_t launch_form(const Product &p, hipStream_t stream) {
+    if (p.target_k != nullptr) return launch<MG, NG, true, false, true>(p, stream);
     return p.ta ? (p.tb ? launch<MG, NG, true, true>(p, stream) : launch<MG, NG, true, false>(p, stream))
                 : (p.tb ? launch<MG, NG, false, true>(p, stream) : launch<MG, NG, false, false>(p, stream));
-}
-
-template <int MG>
-hipError_t launch_groups(const Product &p, int shape, hipStream_t stream) {
-    return shape == 4 ? launch_shape<MG, 4>(p, stream) : shape == 2 ? launch_shape<MG, 2>(p, stream) : launch_shape<MG, 1>(p, stream);
 }
 
 }  // namespace
@@ -327,7 +337,16 @@ hipError_t launch_rows(const Product &p, int shape, hipStream_t stream) {
         return p.M == 1   ? (p.ta ? launch_vector<1, true>(p, stream) : launch_vector<1, false>(p, stream))
                : p.M == 2 ? (p.ta ? launch_vector<2, true>(p, stream) : launch_vector<2, false>(p, stream))
                           : (p.ta ? launch_vector<4, true>(p, stream) : launch_vector<4, false>(p, stream));
-    return p.M <= 16 ? launch_groups<1>(p, shape, stream) : launch_groups<2>(p, shape, stream);
+    switch (shape) {
+        case 16 + 1: return launch_form<1, 1>(p, stream);
+        case 16 + 2: return launch_form<1, 2>(p, stream);
+        case 16 + 4: return launch_form<1, 4>(p, stream);
+        case 32 + 1: return launch_form<2, 1>(p, stream);
+        case 32 + 2: return launch_form<2, 2>(p, stream);
+        case 32 + 4: return launch_form<2, 4>(p, stream);
+        case 64 + 2: return launch_form<4, 2>(p, stream);
+        default: return hipErrorInvalidConfiguration;
+    }
 }
 
 }  // namespace fused

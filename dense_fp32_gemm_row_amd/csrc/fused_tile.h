@@ -206,101 +206,101 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
         __syncthreads();
     };
 
-            // Whole stages on the bf16 units.  A stage runs in 6 phases, a part of A
-            // times a part of B each.  Under a phase's products the next phase's
-            // operands are read from LDS, and the next stage's values, loaded into registers a
-            // stage ago, are split and written to the other buffer and their
-            // registers loaded again.  The one barrier lies before the last phase, under
-            // which the next stage's first operands are read.
-            auto quick = [&](int first, int last) {
-                Share<BM, kThreads, !TA, kStage, false> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, nullptr);
-                Share<BN, kThreads, TB, kStage, false> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, nullptr);
-                constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
-                const int stages = (last - first) / kStage;
-                u32x4 x[2][FM], y[3][2];  // parts of A by turns; the parts of B
-                const int ra = half * BM * 16 + (32 * FM * wm + col) * 16;
-                const int rb = kPlanesA + half * BN * 16 + (64 * wn + col) * 16;
-                auto fetch_a = [&](int set, int part, const char *from) {
+    // Whole stages on the bf16 units.  A stage runs in 6 phases, a part of A
+    // times a part of B each.  Under a phase's products the next phase's
+    // operands are read from LDS, and the next stage's values, loaded into registers a
+    // stage ago, are split and written to the other buffer and their
+    // registers loaded again.  The one barrier lies before the last phase, under
+    // which the next stage's first operands are read.
+    auto quick = [&](int first, int last) {
+        Share<BM, kThreads, !TA, kStage, false> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, nullptr);
+        Share<BN, kThreads, TB, kStage, false> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, nullptr);
+        constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
+        const int stages = (last - first) / kStage;
+        u32x4 x[2][FM], y[3][2];  // parts of A by turns; the parts of B
+        const int ra = half * BM * 16 + (32 * FM * wm + col) * 16;
+        const int rb = kPlanesA + half * BN * 16 + (64 * wn + col) * 16;
+        auto fetch_a = [&](int set, int part, const char *from) {
 #pragma unroll
-                    for (int i = 0; i < FM; ++i)
-                        x[set][i] = *reinterpret_cast<const u32x4 *>(from + part * (2 * BM * 16) + ra + 32 * 16 * i);
-                };
-                auto fetch_b = [&](int part, const char *from) {
+            for (int i = 0; i < FM; ++i)
+                x[set][i] = *reinterpret_cast<const u32x4 *>(from + part * (2 * BM * 16) + ra + 32 * 16 * i);
+        };
+        auto fetch_b = [&](int part, const char *from) {
 #pragma unroll
-                    for (int f = 0; f < 2; ++f)
-                        y[part][f] = *reinterpret_cast<const u32x4 *>(from + part * (2 * BN * 16) + rb + 32 * 16 * f);
-                };
-                auto multiply = [&](int set, int part) {
+            for (int f = 0; f < 2; ++f)
+                y[part][f] = *reinterpret_cast<const u32x4 *>(from + part * (2 * BN * 16) + rb + 32 * 16 * f);
+        };
+        auto multiply = [&](int set, int part) {
 #pragma unroll
-                    for (int i = 0; i < FM; ++i)
+            for (int i = 0; i < FM; ++i)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int f = i & 1 ? 1 - k : k;
-                            acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                __builtin_bit_cast(bf16x8, x[set][i]), __builtin_bit_cast(bf16x8, y[part][f]), acc[i][f], 0, 0, 0);
-                        }
-                    // between two matrix instructions: an LDS read, some of the
-                    // splitting, and its writes and loads
-#pragma unroll
-                    for (int k = 0; k < FM * 2; ++k) {
-                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-                    }
-                    // the sums so far are used here, so their instructions stay ahead
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) asm volatile("" : "+v"(acc[i][f]));
-                    __builtin_amdgcn_sched_barrier(0);
-                };
-                // Set P of x holds l of A at the start, 1 - P at the end.
-                auto stage = [&](auto pc, int s, const char *from, char *to) {
-                    constexpr int P = decltype(pc)::value, Q = 1 - P;
-                    const int next = min(s + 2, stages - 1);  // past the end: loaded again, not used
-                    fetch_a(Q, 1, from);
-                    sa.put(0, to);
-                    multiply(P, 0);  // l h
-                    fetch_b(1, from);
-                    if constexpr (kUa > 1) sa.put(1, to);
-                    sa.load(next);
-                    multiply(Q, 0);  // m h
-                    fetch_a(P, 0, from);
-                    sb.put(0, to + kPlanesA);
-                    multiply(Q, 1);  // m m
-                    fetch_b(2, from);
-                    if constexpr (kUb > 1) sb.put(1, to + kPlanesA);
-                    sb.load(next);
-                    multiply(P, 1);  // h m
-                    multiply(P, 0);  // h h
-                    wait_older<63>();  // LDS accesses alone
-                    barrier_only();
-                    fetch_a(Q, 2, to);
-                    fetch_b(0, to);
-                    multiply(P, 2);  // h l
-                };
-                constexpr std::integral_constant<int, 0> p0;
-                constexpr std::integral_constant<int, 1> p1;
-                char *even = memory, *odd = memory + kBuffer;
-                sa.load(0), sb.load(0);
-#pragma unroll
-                for (int u = 0; u < kUa; ++u) sa.put(u, even);
-#pragma unroll
-                for (int u = 0; u < kUb; ++u) sb.put(u, even + kPlanesA);
-                sa.load(min(1, stages - 1)), sb.load(min(1, stages - 1));
-                wait_older<63>();
-                barrier_only();
-                fetch_a(0, 2, even);
-                fetch_b(0, even);
-                int s = 0;
-                for (; s + 1 < stages; s += 2) {
-                    stage(p0, s, even, odd);
-                    stage(p1, s + 1, odd, even);
+                for (int k = 0; k < 2; ++k) {
+                    const int f = i & 1 ? 1 - k : k;
+                    acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, x[set][i]), __builtin_bit_cast(bf16x8, y[part][f]), acc[i][f], 0, 0, 0);
                 }
-                if (s < stages) stage(p0, s, even, odd);
-            };
+            // between two matrix instructions: an LDS read, some of the
+            // splitting, and its writes and loads
+#pragma unroll
+            for (int k = 0; k < FM * 2; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+            // the sums so far are used here, so their instructions stay ahead
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) asm volatile("" : "+v"(acc[i][f]));
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // Set P of x holds l of A at the start, 1 - P at the end.
+        auto stage = [&](auto pc, int s, const char *from, char *to) {
+            constexpr int P = decltype(pc)::value, Q = 1 - P;
+            const int next = min(s + 2, stages - 1);  // past the end: loaded again, not used
+            fetch_a(Q, 1, from);
+            sa.put(0, to);
+            multiply(P, 0);  // l h
+            fetch_b(1, from);
+            if constexpr (kUa > 1) sa.put(1, to);
+            sa.load(next);
+            multiply(Q, 0);  // m h
+            fetch_a(P, 0, from);
+            sb.put(0, to + kPlanesA);
+            multiply(Q, 1);  // m m
+            fetch_b(2, from);
+            if constexpr (kUb > 1) sb.put(1, to + kPlanesA);
+            sb.load(next);
+            multiply(P, 1);  // h m
+            multiply(P, 0);  // h h
+            wait_older<63>();  // LDS accesses alone
+            barrier_only();
+            fetch_a(Q, 2, to);
+            fetch_b(0, to);
+            multiply(P, 2);  // h l
+        };
+        constexpr std::integral_constant<int, 0> p0;
+        constexpr std::integral_constant<int, 1> p1;
+        char *even = memory, *odd = memory + kBuffer;
+        sa.load(0), sb.load(0);
+#pragma unroll
+        for (int u = 0; u < kUa; ++u) sa.put(u, even);
+#pragma unroll
+        for (int u = 0; u < kUb; ++u) sb.put(u, even + kPlanesA);
+        sa.load(min(1, stages - 1)), sb.load(min(1, stages - 1));
+        wait_older<63>();
+        barrier_only();
+        fetch_a(0, 2, even);
+        fetch_b(0, even);
+        int s = 0;
+        for (; s + 1 < stages; s += 2) {
+            stage(p0, s, even, odd);
+            stage(p1, s + 1, odd, even);
+        }
+        if (s < stages) stage(p0, s, even, odd);
+    };
 
     // Whether two fp16 parts do: the rows' exponents for scaling, and a bound.
     // Parts of a value are off by 2^-23 of it, or 2^-40 of its row's largest (and the
@@ -544,20 +544,19 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
         return v;
     };
     if (p.mode != kStore) {
+        const int lanes = p.M <= kFineTokens ? 4 : 16;  // that share a piece of a row
         each([&](int r, int c, f32x4 v) {
             float top = -__builtin_inff(), s = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = c + e < cols ? fmaxf(top, v[e]) : top;
-#pragma unroll
-            for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            for (int d = 1; d < lanes; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
             const float base = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
             for (int e = 0; e < 4; ++e) s += c + e < cols ? expf(v[e] - base) : 0.0f;
-#pragma unroll
-            for (int d = 1; d < 16; d *= 2) s += __shfl_xor(s, d);
+            for (int d = 1; d < lanes; d *= 2) s += __shfl_xor(s, d);
             if (r < rows && c < cols) {
                 const int64_t m = m0 + r;
-                if ((lane & 15) == 0) p.stats[m * p.groups + (n0 + c) / 64] = stat2{top, s};
+                if ((lane & (lanes - 1)) == 0) p.stats[m * p.groups + (n0 + c) / (4 * lanes)] = stat2{top, s};
                 const int64_t t = p.target[m] - n0 - c;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)

@@ -381,7 +381,7 @@ LOSS_SHAPES = [(1, 4, 1), (2, 5, 4097), (16, 6, 64), (15, 2100, 200), (33, 9000,
           (7, 32801, 130), (48, 8193, 127), (17, 4, 3000),
           (1, 1, 1), (1, 2, 5), (2, 64, 16), (3, 1000, 40), (64, 128, 32), (65, 129, 33), (100, 777, 65),
                (130, 64, 64), (1, 5000, 300), (17, 63, 8), (300, 2049, 100), (5, 1, 7), (257, 300, 48), (16, 4096, 64), (48, 700, 90),
-               (64, 130, 1000), (33, 65, 64),
+               (64, 130, 1000), (33, 65, 64), (400, 9000, 300), (512, 20000, 700), (513, 4100, 130),
                (1700, 2000, 72), (3340, 3700, 50), (2000, 9001, 1800)]
 
 
@@ -436,7 +436,8 @@ def test_every_token_ignored():
     assert not b.cross_entropy(X, W, target)[0].any()
 
 
-@pytest.mark.parametrize("T,V,K", [(70, 200, 32), (300, 300, 64), (3, 500, 64), (70, 40, 32), (300, 7, 70)])
+@pytest.mark.parametrize("T,V,K", [(70, 200, 32), (300, 300, 64), (3, 500, 64), (70, 40, 32), (300, 7, 70),
+                                   (512, 6000, 300), (700, 2000, 1)])
 def test_ignored_rows_may_hold_anything(T, V, K):
     """Padding of NaN, infinities and huge values takes no part; the tokens
     beside it keep their values to the last bit."""
