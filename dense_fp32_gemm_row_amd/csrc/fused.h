@@ -58,7 +58,6 @@ struct Product {
     int splits;     // slices of K (1: none)
     const RowStat *row_a, *row_b;  // [block of k][batch * rows], or null: no fp16 parts
     int blocks_a, blocks_b;
-    bool lenient;   // fp16 parts wherever a row's range allows scaling it
     // kStats, kStoreStats (no batch, no slices): stats[row * groups + column / group_columns(M)];
     // at_target[row] gets the sum in column target[row], where there is one.
     Mode mode;
@@ -70,6 +69,11 @@ struct Product {
     // no part even where B holds infinities or NaN (A stored K x M, B stored K x N).
     const int64_t *target_k;
     int64_t ignore;
+    // The largest |value| of each row of op(A), as its bits, where A is the loss's
+    // gradient by the logits (no batch), or null.  Its rows have a few large
+    // values and tens of thousands of small ones, to whose sum an error of 2^-40 of the
+    // largest adds nothing that counts: fp16 parts wherever the range allows.
+    const int *top_a;
 };
 
 hipError_t launch_product(const Product &, hipStream_t);
@@ -94,6 +98,7 @@ hipError_t launch_sum_slices(const Product &, hipStream_t);
 
 // dZ = dC act'(Z), and the sums of its columns over blocks of rows; either may
 // be absent (dz.p null; partial null).
+constexpr int kSlopeBlocks = 256;
 struct Slope {
     int64_t batch;
     int M, N;
@@ -101,7 +106,7 @@ struct Slope {
     Operand dc, pre;
     Result dz;
     float *partial;  // [batch][blocks][N]
-    int blocks, rows;  // rows a block
+    int blocks, rows;  // at most kSlopeBlocks; rows a block
     Result dbias;    // ld unused
 };
 hipError_t launch_slope(const Slope &, hipStream_t);
@@ -117,6 +122,7 @@ struct Loss {
     float *loss, *lse;          // loss may be null
     const float *grad_loss;     // null: ones
     float *logits;              // launch_probabilities: T x V, in place
+    int *row_top, *column_top;  // null, or T and V: set to zero by launch_loss, to the largest |value|'s bits
 };
 hipError_t launch_loss(const Loss &, hipStream_t);
 // logits = grad_loss (exp(logits - lse) - (v == target)), zero for ignored rows

@@ -94,7 +94,7 @@ GradParts grad_parts(bool ta, bool tb, int64_t batch, int64_t M, int64_t N, int6
     GradParts g{};
     // blocks of rows of the bias gradient's first sums: enough to fill the GPU
     const int64_t strips = std::max<int64_t>(1, times(batch, div_up(N, 256)));
-    const int64_t most = std::max<int64_t>(1, 2048 / strips);
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(fused::kSlopeBlocks, 1024 / strips));
     g.rows = static_cast<int>(std::max<int64_t>(8, div_up(M, most)));
     g.blocks = static_cast<int>(div_up(M, g.rows));
     if (activation != GEMM_F32_ACT_NONE && (dA || dB)) g.dz = times(times(batch, M), N);
@@ -107,14 +107,15 @@ GradParts grad_parts(bool ta, bool tb, int64_t batch, int64_t M, int64_t N, int6
 
 // ---- the parts of a cross entropy's workspace ----
 int groups_of(int64_t T, int64_t V) { return static_cast<int>(div_up(V, fused::group_columns(T))); }
-int64_t stats_bytes(int64_t T, int64_t V) {  // statistics, logit at the target, lse
+int64_t stats_bytes(int64_t T, int64_t V) {  // logit at the target, lse, statistics
     return plus(times(times(8, T), groups_of(T, V)), times(8, T));
 }
 // The gradient works on at most `rows` tokens at a time, whose logits it holds.  (A
 // last piece of few tokens has statistics of more groups.)
 int64_t piece_bytes(int64_t rows, int64_t V) {
+    if (rows == 0) return 0;
     const int64_t few = std::min<int64_t>(rows, fused::kFineTokens);
-    return plus(times(times(4, rows), V), std::max(stats_bytes(rows, V), stats_bytes(few, V)));
+    return plus(times(times(4, rows), V) + 4 * (rows + V), std::max(stats_bytes(rows, V), stats_bytes(few, V)));
 }
 int64_t piece_space(int64_t rows, int64_t V, int64_t K) {
     return std::max({space_of(true, 1, rows, V, K, true), space_of(false, 1, rows, K, V), space_of(false, 1, V, K, rows)});
@@ -326,7 +327,8 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
     int64_t rows = best, bytes = full;
     const bool sliced = workspace_bytes >= full;
     if (!sliced && T > 0) {
-        rows = std::min(best, std::max<int64_t>(workspace_bytes, 0) / piece_bytes(1, V));
+        const int64_t one = piece_bytes(1, V), each = piece_bytes(2, V) - one;
+        rows = std::min(best, std::max<int64_t>(workspace_bytes - one, 0) / each + 1);
         if (rows > kPieceRows) rows = rows / kPieceRows * kPieceRows;
         rows = std::max(rows, piece_least(T));
         bytes = piece_bytes(rows, V);
@@ -341,7 +343,8 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             return run(plain_product(1, V, K, 0, true, {}, false, {}, {dW, lddw, 0}, nullptr), s);
         for (int64_t t0 = 0; t0 < T && err == hipSuccess; t0 += rows) {
             const int64_t n = std::min(rows, T - t0);
-            float *logits = at + 2 * n + 2 * n * groups_of(n, V);
+            int *row_top = reinterpret_cast<int *>(at) + 2 * n + 2 * n * groups_of(n, V), *column_top = row_top + n;
+            float *logits = reinterpret_cast<float *>(column_top + V);
             float *space = sliced && bytes > piece_bytes(best, V) ? at + piece_bytes(best, V) / 4 : nullptr;
             // (the last piece may be shorter, and ask for more)
             auto room = [&](bool tb, int64_t M, int64_t N, int64_t k, bool statistics = false) {
@@ -358,18 +361,19 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             l.target = p.target, l.ignore = ignore_index;
             l.loss = loss != nullptr ? loss + t0 : nullptr, l.lse = lse != nullptr ? lse + t0 : at + n;
             l.grad_loss = grad_loss != nullptr ? grad_loss + t0 : nullptr, l.logits = logits;
+            l.row_top = dX != nullptr ? row_top : nullptr, l.column_top = dW != nullptr ? column_top : nullptr;
             if (err == hipSuccess) err = fused::launch_loss(l, s);
             if (dX == nullptr && dW == nullptr) continue;
             if (err == hipSuccess) err = fused::launch_probabilities(l, s);
             if (err == hipSuccess && dX != nullptr) {
                 p = plain_product(1, n, K, V, false, {logits, V, 0}, false, {W, ldw, 0},
                                         {dX + t0 * lddx, lddx, 0}, room(false, n, K, V));
-                p.lenient = true;
+                p.top_a = row_top;
                 err = run(p, s);
             }
             if (err == hipSuccess && dW != nullptr) {
                 p = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0}, room(false, V, K, n));
-                p.lenient = true;
+                p.top_a = column_top;
                 p.target_k = target + t0, p.ignore = ignore_index;
                 if (t0 > 0) p.e.residual = {dW, lddw, 0};  // the pieces before
                 err = run(p, s);

@@ -15,27 +15,54 @@ namespace fused {
 
 typedef float float2u __attribute__((ext_vector_type(2), aligned(4)));  // 8 bytes at any word
 
-constexpr float kRootHalf = 0.70710678118654752440f;
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kRoot2OverPi = 0.79788456080286535588f;
 constexpr float kRootHalfOverPi = 0.39894228040143267794f;  // 1 / sqrt(2 pi)
 constexpr float kCubic = 0.044715f;
 
-// 1 / (1 + exp(-u)), by the exponential that cannot overflow.
-__device__ __forceinline__ float logistic(float u) {
-    const float t = expf(-fabsf(u));
-    return (u < 0.0f ? t : 1.0f) / (1.0f + t);
+// exp(x) by the hardware's power of two; results below 2^-126 are zero.
+__device__ __forceinline__ float quick_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2E); }
+
+// exp(x) for x <= 0, held below 2^-126 too.
+__device__ __forceinline__ float tail_exp(float x) {
+    const float y = x * kLog2E;
+    const bool low = y < -120.0f;
+    return __builtin_amdgcn_exp2f(low ? y + 64.0f : y) * (low ? 0x1p-64f : 1.0f);
 }
 
-// (1 + erf(z / sqrt 2)) / 2 as erfc(-z / sqrt 2) / 2: without the difference
-// of two numbers near 1 that loses the left tail.
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-z * kRootHalf); }
+// 1 / (1 + exp(-u)), by the exponential that cannot overflow.
+__device__ __forceinline__ float logistic(float u) {
+    const float t = tail_exp(-fabsf(u));
+    return (u < 0.0f ? t : 1.0f) * __builtin_amdgcn_rcpf(1.0f + t);
+}
+
+// (1 + erf(z / sqrt 2)) / 2 and e = exp(-z^2 / 2).  For z <= 0 it is e t P(t)
+// with t = 1 / (1 + 0.35 |z|), P a polynomial fitted to exp(z^2 / 2) erfc(|z| /
+// sqrt 2) / (2 t) over |z| <= 15.2 by reweighted least squares (3.3e-8 of the
+// value at most, 3e-7 with FP32's roundings): relative precision in the tail, too.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    e = tail_exp(-0.5f * z * z);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.35f, fabsf(z), 1.0f));
+    float q = -2.916558145e-02f;
+    q = fmaf(q, t, 1.440686386e-01f);
+    q = fmaf(q, t, -2.559176254e-01f);
+    q = fmaf(q, t, 1.594104647e-01f);
+    q = fmaf(q, t, -2.327564113e-02f);
+    q = fmaf(q, t, 1.055796992e-01f);
+    q = fmaf(q, t, 1.198142779e-01f);
+    q = fmaf(q, t, 1.398645026e-01f);
+    q = fmaf(q, t, 1.396212489e-01f);
+    q *= t * e;
+    return z > 0.0f ? 1.0f - q : q;
+}
 
 // Beyond these |z| the value of a tail is below FP32's range; z itself may be
 // infinite there, and 0 times it would be NaN.
 __device__ __forceinline__ float activate(int kind, float z) {
+    float e;
     switch (kind) {
         case GEMM_F32_ACT_RELU: return z < 0.0f ? 0.0f : z;
-        case GEMM_F32_ACT_GELU: return z < -15.0f ? 0.0f : z * normal_cdf(z);
+        case GEMM_F32_ACT_GELU: return z < -15.0f ? 0.0f : z * normal_cdf(z, e);
         // (1 + tanh u) / 2 is the logistic function of 2 u
         case GEMM_F32_ACT_GELU_TANH:
             return z < -15.0f ? 0.0f : z * logistic(2.0f * kRoot2OverPi * (z + kCubic * z * z * z));
@@ -49,7 +76,9 @@ __device__ __forceinline__ float slope(int kind, float z) {
         case GEMM_F32_ACT_RELU: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
         case GEMM_F32_ACT_GELU: {
             if (fabsf(z) > 15.0f) return z > 0.0f ? 1.0f : 0.0f;
-            return normal_cdf(z) + z * kRootHalfOverPi * expf(-0.5f * z * z);
+            float e;
+            const float q = normal_cdf(z, e);
+            return fmaf(z * kRootHalfOverPi, e, q);
         }
         case GEMM_F32_ACT_GELU_TANH: {
             if (fabsf(z) > 15.0f) return z > 0.0f ? 1.0f : 0.0f;
@@ -63,6 +92,27 @@ __device__ __forceinline__ float slope(int kind, float z) {
         }
         default: return 1.0f;
     }
+}
+
+// The value of a lane of the same 16 by a data-parallel move: quads turned by 1
+// and 2 lanes, rows of 16 by 4 and 8.
+template <int CONTROL>
+__device__ __forceinline__ int moved(int x) {
+    return __builtin_amdgcn_update_dpp(0, x, CONTROL, 0xf, 0xf, false);
+}
+// op over the 4 (16) lanes that share a quad (row), in every one of them.
+template <int LANES, class F>
+__device__ __forceinline__ float over_lanes(float x, F op) {
+    static_assert(LANES == 4 || LANES == 16, "");
+    auto at = [](int v) { return __builtin_bit_cast(float, v); };
+    auto of = [](float v) { return __builtin_bit_cast(int, v); };
+    x = op(x, at(moved<0xb1>(of(x))));
+    x = op(x, at(moved<0x4e>(of(x))));
+    if constexpr (LANES == 16) {
+        x = op(x, at(moved<0x124>(of(x))));
+        x = op(x, at(moved<0x128>(of(x))));
+    }
+    return x;
 }
 
 // The three bf16 parts of four values x = h + m + l, rounded to nearest each:
@@ -118,7 +168,7 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_in
 __device__ __forceinline__ void merge_stats(float &m, float &s, float m2, float s2) {
     const float top = fmaxf(m, m2);
     const float base = top == -__builtin_inff() ? 0.0f : top;
-    s = s * expf(m - base) + s2 * expf(m2 - base);
+    s = s * quick_exp(m - base) + s2 * quick_exp(m2 - base);
     m = top;
 }
 

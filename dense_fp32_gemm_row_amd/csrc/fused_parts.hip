@@ -24,41 +24,100 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t elem
     }
 }
 
-// A block of rows of 256 columns: dZ, and the columns' sums over the block.
+// 4 neighbours of a row, of which `left` are inside it.
+__device__ __forceinline__ f32x4 read4(const float *p, int64_t left) {
+    f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
+    if (left >= 4) {
+        v = *reinterpret_cast<const float4u *>(p);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) v[e] = p[e];
+    }
+    return v;
+}
+__device__ __forceinline__ void write4(float *p, int64_t left, f32x4 v) {
+    if (left >= 4) {
+        *reinterpret_cast<float4u *>(p) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) p[e] = v[e];
+    }
+}
+
+// A block of rows of 256 columns, 4 a lane, its rows shared by 4 wavefronts: dZ, and
+// the columns' sums over the block.
+template <int KIND>
 __global__ __launch_bounds__(256) void slope_kernel(Slope s, int64_t strips, int64_t units) {
+    __shared__ f32x4 sums[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t strip = u % strips, rest = u / strips, block = rest % s.blocks, b = rest / s.blocks;
-        const int64_t n = strip * 256 + threadIdx.x;
-        if (n >= s.N) continue;
+        const int64_t n = strip * 256 + 4 * lane, left = s.N - n;
         const int64_t first = block * s.rows, last = min(first + s.rows, int64_t{s.M});
-        float sum = 0.0f;
-        for (int64_t m = first; m < last; ++m) {
-            float v = s.dc.p[b * s.dc.stride + m * s.dc.ld + n];
-            if (s.activation != GEMM_F32_ACT_NONE)
-                v *= slope(s.activation, s.pre.p[b * s.pre.stride + m * s.pre.ld + n]);
-            if (s.dz.p != nullptr) s.dz.p[b * s.dz.stride + m * s.dz.ld + n] = v;
-            sum += v;
+        const float *dc = s.dc.p + b * s.dc.stride + n, *pre = s.pre.p + b * s.pre.stride + n;
+        float *dz = s.dz.p + b * s.dz.stride + n;
+        f32x4 sum{0.0f, 0.0f, 0.0f, 0.0f};
+        if (left > 0) {
+#pragma unroll 4
+            for (int64_t m = first + wave; m < last; m += 4) {
+                f32x4 v = read4(dc + m * s.dc.ld, left);
+                if constexpr (KIND != GEMM_F32_ACT_NONE) {
+                    const f32x4 z = read4(pre + m * s.pre.ld, left);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] *= slope(KIND, z[e]);
+                }
+                if (s.dz.p != nullptr) write4(dz + m * s.dz.ld, left, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += v[e];
+            }
         }
-        if (s.partial != nullptr) s.partial[(b * s.blocks + block) * s.N + n] = sum;
+        if (s.partial == nullptr) continue;
+        sums[wave][lane] = sum;
+        __syncthreads();
+        if (wave == 0 && left > 0) {
+#pragma unroll
+            for (int w = 1; w < 4; ++w)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += sums[w][lane][e];
+            write4(s.partial + (b * s.blocks + block) * s.N + n, left, sum);
+        }
+        __syncthreads();
     }
 }
 
+// The blocks' sums of 16 columns, shared by 16 threads a column.
 __global__ __launch_bounds__(256) void bias_kernel(Slope s, int64_t strips, int64_t units) {
+    __shared__ float sums[16][17];
+    const int c = threadIdx.x & 15, part = threadIdx.x >> 4;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t b = u / strips, n = (u - b * strips) * 256 + threadIdx.x;
-        if (n >= s.N) continue;
+        const int64_t b = u / strips, n = (u - b * strips) * 16 + c;
+        const float *from = s.partial + b * s.blocks * s.N + n;
         float sum = 0.0f;
-        for (int q = 0; q < s.blocks; ++q) sum += s.partial[(b * s.blocks + q) * s.N + n];
-        s.dbias.p[b * s.dbias.stride + n] = sum;
+        if (n < s.N)
+#pragma unroll 4
+            for (int q = part; q < s.blocks; q += 16) sum += from[static_cast<int64_t>(q) * s.N];
+        sums[part][c] = sum;
+        __syncthreads();
+        if (part == 0 && n < s.N) {
+            for (int q = 1; q < 16; ++q) sum += sums[q][c];
+            s.dbias.p[b * s.dbias.stride + n] = sum;
+        }
+        __syncthreads();
     }
 }
 
-// A wavefront a row: its pieces' statistics joined.
+// A workgroup a row: its pieces' statistics joined, in a fixed order.
 __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
-    const int lane = threadIdx.x & 63;
-    for (int64_t t = blockIdx.x * int64_t{4} + (threadIdx.x >> 6); t < l.T; t += gridDim.x * int64_t{4}) {
+    __shared__ float tops[4], sums[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (l.column_top != nullptr)
+        for (int64_t v = blockIdx.x * int64_t{256} + threadIdx.x; v < l.V; v += gridDim.x * int64_t{256}) l.column_top[v] = 0;
+    for (int64_t t = blockIdx.x; t < l.T; t += gridDim.x) {
         float m = -__builtin_inff(), s = 0.0f;
-        for (int g = lane; g < l.groups; g += 64) {
+#pragma unroll 4
+        for (int g = threadIdx.x; g < l.groups; g += 256) {
             const stat2 q = l.stats[t * l.groups + g];
             merge_stats(m, s, q.x, q.y);
         }
@@ -66,7 +125,10 @@ __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
             const float m2 = __shfl_xor(m, d), s2 = __shfl_xor(s, d);
             merge_stats(m, s, m2, s2);
         }
-        if (lane == 0) {
+        if (lane == 0) tops[wave] = m, sums[wave] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 4; ++w) merge_stats(m, s, tops[w], sums[w]);
             const float lse = m + logf(s);
             l.lse[t] = lse;
             if (l.loss != nullptr) {
@@ -74,22 +136,55 @@ __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
                 l.loss[t] = target == l.ignore ? 0.0f
                             : target >= 0 && target < l.V ? lse - l.at_target[t] : __builtin_nanf("");
             }
+            if (l.row_top != nullptr) l.row_top[t] = 0;
         }
+        __syncthreads();
     }
 }
 
-__global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t strips, int64_t units) {
+// `rows` rows of 1024 columns, 4 a thread.  The largest magnitudes of rows and
+// columns are found on the way (a maximum does not depend on the order).
+__global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t strips, int64_t units, int rows) {
+    const int lane = threadIdx.x & 63;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t t = u / strips, v = (u - t * strips) * 256 + threadIdx.x;
-        if (v >= l.V) continue;
-        const int64_t target = l.target[t];
-        float p = 0.0f;
-        if (target != l.ignore) {
-            const float g = l.grad_loss != nullptr ? l.grad_loss[t] : 1.0f;
-            p = g * (expf(l.logits[t * l.V + v] - l.lse[t]) - (v == target ? 1.0f : 0.0f));
-            if (target < 0 || target >= l.V) p = __builtin_nanf("");
+        const int64_t block = u / strips, v = (u - block * strips) * 1024 + 4 * threadIdx.x, left = l.V - v;
+        const int64_t first = block * rows, last = min(first + rows, static_cast<int64_t>(l.T));
+        int column[4] = {0, 0, 0, 0};
+        constexpr int kAtOnce = 4;
+        for (int64_t t0 = first; t0 < last; t0 += kAtOnce) {
+            f32x4 x[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) x[i] = read4(l.logits + min(t0 + i, last - 1) * l.V + v, left);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int64_t t = t0 + i;
+                if (t >= last) break;
+                const int64_t target = l.target[t];
+                const bool counts = target != l.ignore;
+                const float lse = l.lse[t], g = l.grad_loss != nullptr ? l.grad_loss[t] : 1.0f;
+                int row = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float p = g * (quick_exp(x[i][e] - lse) - (v + e == target ? 1.0f : 0.0f));
+                    if (target < 0 || target >= l.V) p = __builtin_nanf("");
+                    p = counts ? p : 0.0f;
+                    x[i][e] = p;
+                    const int bits = e < left ? __builtin_bit_cast(int, p) & 0x7fffffff : 0;
+                    column[e] = max(column[e], bits), row = max(row, bits);
+                }
+                write4(l.logits + t * l.V + v, left, x[i]);
+                if (l.row_top != nullptr) {
+                    row = max(row, moved<0xb1>(row)), row = max(row, moved<0x4e>(row));
+                    row = max(row, moved<0x124>(row)), row = max(row, moved<0x128>(row));
+                    row = max(row, __shfl_xor(row, 16)), row = max(row, __shfl_xor(row, 32));
+                    if (lane == 0) atomicMax(l.row_top + t, row);
+                }
+            }
         }
-        l.logits[t * l.V + v] = p;
+        if (l.column_top != nullptr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) atomicMax(l.column_top + v + e, column[e]);
     }
 }
 
@@ -162,23 +257,34 @@ hipError_t launch_sum_slices(const Product &p, hipStream_t stream) {
 
 hipError_t launch_slope(const Slope &s, hipStream_t stream) {
     const int64_t strips = div_up(s.N, 256), units = strips * s.blocks * s.batch;
-    slope_kernel<<<blocks_for(units), 256, 0, stream>>>(s, strips, units);
+    const unsigned grid = blocks_for(units);
+    switch (s.activation) {
+        case GEMM_F32_ACT_RELU: slope_kernel<GEMM_F32_ACT_RELU><<<grid, 256, 0, stream>>>(s, strips, units); break;
+        case GEMM_F32_ACT_GELU: slope_kernel<GEMM_F32_ACT_GELU><<<grid, 256, 0, stream>>>(s, strips, units); break;
+        case GEMM_F32_ACT_GELU_TANH: slope_kernel<GEMM_F32_ACT_GELU_TANH><<<grid, 256, 0, stream>>>(s, strips, units); break;
+        case GEMM_F32_ACT_SILU: slope_kernel<GEMM_F32_ACT_SILU><<<grid, 256, 0, stream>>>(s, strips, units); break;
+        default: slope_kernel<GEMM_F32_ACT_NONE><<<grid, 256, 0, stream>>>(s, strips, units);
+    }
     hipError_t err = hipGetLastError();
     if (err == hipSuccess && s.dbias.p != nullptr) {
-        bias_kernel<<<blocks_for(strips * s.batch), 256, 0, stream>>>(s, strips, strips * s.batch);
+        const int64_t lines = div_up(s.N, 16);
+        bias_kernel<<<blocks_for(lines * s.batch), 256, 0, stream>>>(s, lines, lines * s.batch);
         err = hipGetLastError();
     }
     return err;
 }
 
 hipError_t launch_loss(const Loss &l, hipStream_t stream) {
-    loss_kernel<<<blocks_for(div_up(l.T, 4)), 256, 0, stream>>>(l);
+    loss_kernel<<<blocks_for(l.T), 256, 0, stream>>>(l);
     return hipGetLastError();
 }
 
 hipError_t launch_probabilities(const Loss &l, hipStream_t stream) {
-    const int64_t strips = div_up(l.V, 256), units = strips * l.T;
-    probabilities_kernel<<<blocks_for(units), 256, 0, stream>>>(l, strips, units);
+    const int64_t strips = div_up(l.V, 1024);
+    // as many rows a workgroup as leave enough of them
+    const int rows = static_cast<int>(std::max<int64_t>(4, std::min<int64_t>(64, l.T * strips / 2048)));
+    const int64_t units = strips * div_up(l.T, rows);
+    probabilities_kernel<<<blocks_for(units), 256, 0, stream>>>(l, strips, units, rows);
     return hipGetLastError();
 }
 
@@ -197,7 +303,8 @@ hipError_t launch_row_stats(const Product &p, hipStream_t stream) {
         j.units = j.strips * blocks * p.batch;
         return j;
     };
-    const StatJob a = job(p.a, !p.ta, p.M, p.blocks_a, p.row_a), b = job(p.b, p.tb, p.N, p.blocks_b, p.row_b);
+    StatJob a = job(p.a, !p.ta, p.M, p.blocks_a, p.row_a), b = job(p.b, p.tb, p.N, p.blocks_b, p.row_b);
+    if (p.top_a != nullptr) a.units = 0;  // known
     row_stats_kernel<<<blocks_for(a.units + b.units), 256, 0, stream>>>(a, b, p.batch);
     return hipGetLastError();
 }

@@ -29,10 +29,9 @@ __device__ __forceinline__ void store_cell(const Product &p, int64_t b, int64_t 
         if (in) finish(p, b, slice, m, n, v);
         return;
     }
-    float top = in ? v : -__builtin_inff();
-    for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-    float s = in ? expf(v - (top == -__builtin_inff() ? 0.0f : top)) : 0.0f;
-    for (int d = 1; d < 16; d *= 2) s += __shfl_xor(s, d);
+    const float top = over_lanes<16>(in ? v : -__builtin_inff(), [](float a, float b) { return fmaxf(a, b); });
+    const float s = over_lanes<16>(in ? quick_exp(v - (top == -__builtin_inff() ? 0.0f : top)) : 0.0f,
+                                   [](float a, float b) { return a + b; });
     if (!in) return;
     if (n % 16 == 0) p.stats[static_cast<int64_t>(m) * p.groups + n / 16] = stat2{top, s};
     if (p.target[m] == n) p.at_target[m] = v;

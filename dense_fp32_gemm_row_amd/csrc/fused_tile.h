@@ -324,18 +324,26 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
         float cost = 0.0f, share = 1.0f;
         int e = 141;
         if (r < (second ? cols : rows)) {
-            RowStat s{0, 0, 0, 0};
-            for (int q = 0; q < blocks; ++q) {
-                const RowStat t = from[q * line];
-                s.top = max(s.top, t.top), s.count += t.count, s.sum += t.sum;
-            }
-            if (s.count > 0) {  // a row of zeros is one whatever its scale
-                e = s.top;
-                const float n = static_cast<float>(p.K);
-                cost = (static_cast<float>(s.count) * static_cast<float>(e + 1) - static_cast<float>(s.sum)) / n;
-                share = static_cast<float>(s.count) / n;
-                if (p.lenient) cost = 0.0f, share = 1.0f;
-                if (e < 14 || e > 254) cost = __builtin_inff(), e = 141;
+            if (!second && p.top_a != nullptr) {
+                // known to be probabilities less one at the target: the scale alone
+                const int top = p.top_a[m0 + r] >> 23;
+                if (top > 0) e = max(top, 14);
+                if (top > 254) cost = __builtin_inff(), e = 141;
+            } else {
+                RowStat s{0, 0, 0, 0};
+#pragma unroll 4
+                for (int q = 0; q < blocks; ++q) {
+                    const RowStat t = from[q * line];
+                    s.top = max(s.top, t.top), s.count += t.count, s.sum += t.sum;
+                }
+                if (s.count > 0) {  // a row of zeros is one whatever its scale
+                    e = s.top;
+                    const float n = static_cast<float>(p.K);
+                    cost = (static_cast<float>(s.count) * static_cast<float>(e + 1) - static_cast<float>(s.sum)) / n;
+                    share = static_cast<float>(s.count) / n;
+                    if (p.top_a != nullptr) cost = 0.0f, share = 1.0f;
+                    if (e < 14 || e > 254) cost = __builtin_inff(), e = 141;
+                }
             }
         }
         exponents[tid] = e;
@@ -502,7 +510,7 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
     if (p.narrow && !few) {
         bool half_parts = false;
         if constexpr (kHalf)
-            if (p.row_a != nullptr && k1 - k0 >= 2 * kStage && certified()) {
+            if (p.row_b != nullptr && k1 - k0 >= 2 * kStage && certified()) {
                 whole = k0 + (k1 - k0) / (2 * kStage) * (2 * kStage);
                 quick_half(k0, whole);
                 half_parts = true;
@@ -544,16 +552,19 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
         return v;
     };
     if (p.mode != kStore) {
-        const int lanes = p.M <= kFineTokens ? 4 : 16;  // that share a piece of a row
+        const bool fine = p.M <= kFineTokens;
+        const int lanes = fine ? 4 : 16;  // that share a piece of a row
         each([&](int r, int c, f32x4 v) {
             float top = -__builtin_inff(), s = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = c + e < cols ? fmaxf(top, v[e]) : top;
-            for (int d = 1; d < lanes; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            auto larger = [](float a, float b) { return fmaxf(a, b); };
+            top = fine ? over_lanes<4>(top, larger) : over_lanes<16>(top, larger);
             const float base = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s += c + e < cols ? expf(v[e] - base) : 0.0f;
-            for (int d = 1; d < lanes; d *= 2) s += __shfl_xor(s, d);
+            for (int e = 0; e < 4; ++e) s += c + e < cols ? quick_exp(v[e] - base) : 0.0f;
+            auto sum = [](float a, float b) { return a + b; };
+            s = fine ? over_lanes<4>(s, sum) : over_lanes<16>(s, sum);
             if (r < rows && c < cols) {
                 const int64_t m = m0 + r;
                 if ((lane & (lanes - 1)) == 0) p.stats[m * p.groups + (n0 + c) / (4 * lanes)] = stat2{top, s};
