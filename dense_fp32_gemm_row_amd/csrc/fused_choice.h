@@ -106,7 +106,7 @@ inline int group_columns(int64_t tokens) { return tokens <= kFineTokens ? 16 : 6
 // Blocks of k in which the statistics of `rows` rows are taken: enough of them to fill the GPU.
 inline int stat_blocks(int64_t rows, int64_t K, bool k_contiguous) {
     const int64_t units = k_contiguous ? div_up(rows, 4) : div_up(rows, 256);
-    return static_cast<int>(std::max<int64_t>(1, std::min({int64_t{k_contiguous ? 16 : 64}, div_up(1024, units), K / 256})));
+    return static_cast<int>(std::max<int64_t>(1, std::min({int64_t{k_contiguous ? 16 : 64}, div_up(1024, units), K / (k_contiguous ? 256 : 64)})));
 }
 
 }  // namespace fused

@@ -282,7 +282,7 @@ hipError_t launch_loss(const Loss &l, hipStream_t stream) {
 hipError_t launch_probabilities(const Loss &l, hipStream_t stream) {
     const int64_t strips = div_up(l.V, 1024);
     // as many rows a workgroup as leave enough of them
-    const int rows = static_cast<int>(std::max<int64_t>(4, std::min<int64_t>(64, l.T * strips / 2048)));
+    const int rows = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, l.T * strips / 1024)));
     const int64_t units = strips * div_up(l.T, rows);
     probabilities_kernel<<<blocks_for(units), 256, 0, stream>>>(l, strips, units, rows);
     return hipGetLastError();

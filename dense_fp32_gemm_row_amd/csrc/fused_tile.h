@@ -42,8 +42,8 @@ __device__ __forceinline__ float element(const float *p, int64_t ld, int row, in
 // lanes a row; where rows are, kUnits neighbouring rows at 4 k.  Every address
 // stays inside the operand: rows past its end repeat the last ones, which then
 // are written to LDS where those belong.  HALF: in two fp16 parts, not three of
-// bf16.
-template <int ROWS, int THREADS, bool KC, int STAGE, bool HALF>
+// bf16.  The values of D stages are held, or on their way.
+template <int ROWS, int THREADS, bool KC, int STAGE, bool HALF, int D = 1>
 struct Share {
     static constexpr int E = ROWS * STAGE / THREADS;  // elements
     static constexpr int kUnits = E / 4;
@@ -54,7 +54,7 @@ struct Share {
     uint32_t off[KC ? kUnits : 1];
     int lds[KC ? 1 : kUnits];  // byte in a part
     float scale[HALF ? kUnits : 1];
-    float v[E];
+    float v[D][E];
 
     __device__ __forceinline__ Share(const float *p, int64_t ld, int rows, bool more, int tid, const int *exponents) {
         row = 4 * ld;
@@ -88,14 +88,14 @@ struct Share {
     }
     // 2^(141 - e): values with exponent field e and less come below 2^15
     static __device__ __forceinline__ float power(int e) { return __builtin_bit_cast(float, (268 - e) << 23); }
-    __device__ __forceinline__ void load(int stage) {
+    __device__ __forceinline__ void load(int stage, int set = 0) {
         const char *at = base + stage * step;
         if constexpr (KC) {
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
                 const f32x4 x = *reinterpret_cast<const float4u *>(at + off[u]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[4 * u + i] = x[i];
+                for (int i = 0; i < 4; ++i) v[set][4 * u + i] = x[i];
             }
         } else {
 #pragma unroll
@@ -104,29 +104,53 @@ struct Share {
                 if constexpr (kUnits == 4) {
                     const f32x4 x = *reinterpret_cast<const float4u *>(from);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) v[4 * u + i] = x[u];
+                    for (int u = 0; u < 4; ++u) v[set][4 * u + i] = x[u];
                 } else if constexpr (kUnits == 2) {
                     const f32x2 x = *reinterpret_cast<const float2u *>(from);
-                    v[i] = x[0], v[4 + i] = x[1];
+                    v[set][i] = x[0], v[set][4 + i] = x[1];
                 } else {
-                    v[i] = *reinterpret_cast<const float *>(from);
+                    v[set][i] = *reinterpret_cast<const float *>(from);
                 }
             }
         }
     }
-    __device__ __forceinline__ void put(int u, char *planes) const {
+    __device__ __forceinline__ void put(int u, char *planes, int set = 0) const {
+        const float(&x)[E] = v[set];
         char *to = planes + (KC ? lds[0] + u * (THREADS * 4 / STAGE) * 16 : lds[KC ? 0 : u]);
         if constexpr (HALF) {
-            const Halves s = split4_half({v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]}, scale[u]);
+            const Halves s = split4_half({x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]}, scale[u]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) *reinterpret_cast<u32x2 *>(to + c * kPart) = s.p[c];
         } else {
-            const Parts s = split4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+            const Parts s = split4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
 #pragma unroll
             for (int c = 0; c < 3; ++c) *reinterpret_cast<u32x2 *>(to + c * kPart) = s.p[c];
         }
     }
 };
+
+// stage(i, s) for every s, i = s % TURN as a constant.
+template <int TURN, class F>
+__device__ __forceinline__ void turns(int stages, F stage) {
+    static_assert(TURN == 2 || TURN == 4, "");
+    constexpr std::integral_constant<int, 0> i0;
+    constexpr std::integral_constant<int, 1> i1;
+    constexpr std::integral_constant<int, 2 % TURN> i2;
+    constexpr std::integral_constant<int, 3 % TURN> i3;
+    int s = 0;
+    for (; s + TURN <= stages; s += TURN) {
+        stage(i0, s), stage(i1, s + 1);
+        if constexpr (TURN == 4) stage(i2, s + 2), stage(i3, s + 3);
+    }
+    if (s < stages) {
+        stage(i0, s);
+        if constexpr (TURN == 4)
+            if (s + 1 < stages) {
+                stage(i1, s + 1);
+                if (s + 2 < stages) stage(i2, s + 2);
+            }
+    }
+}
 
 // Tiles of a CU, for the registers that a wavefront may take.
 constexpr int per_cu(int fm) { return fm == 4 ? 1 : fm == 2 ? 2 : 3; }
@@ -138,8 +162,8 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
     constexpr int BM = T::BM, BN = T::BN, kThreads = T::kThreads;
     constexpr bool kHalf = FM > 1;  // the tiles with a loop for fp16 parts
     constexpr int kPlanesA = 3 * 2 * BM * 16, kBuffer = kPlanesA + 3 * 2 * BN * 16;
-    constexpr int kHalfA = 2 * 4 * BM * 16, kHalfBuffer = kHalfA + 2 * 4 * BN * 16;
-    constexpr int kMemory = 2 * (kHalf ? kHalfBuffer : kBuffer);
+    constexpr int kHalfA = 2 * 4 * BM * 16, kHalfBuffer = kHalfA + 2 * 4 * BN * 16;  // of 32 k
+    constexpr int kMemory = 2 * (FM == 4 ? kHalfBuffer : kBuffer);
     constexpr int kRowOut = 68;  // floats: 64 of a row of results, 16 bytes apart from the next one's banks
     static_assert(kBuffer >= (BM + BN) * kStage * 4, "");
     static_assert(2 * kBuffer >= T::kWaves * 32 * kRowOut * 4, "");
@@ -212,7 +236,7 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
     // stage ago, are split and written to the other buffer and their
     // registers loaded again.  The one barrier lies before the last phase, under
     // which the next stage's first operands are read.
-    auto quick = [&](int first, int last) {
+    auto quick = [&](int first, auto last) {
         Share<BM, kThreads, !TA, kStage, false> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, nullptr);
         Share<BN, kThreads, TB, kStage, false> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, nullptr);
         constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
@@ -357,6 +381,103 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
         const float both = fa + fb - 1.0f;
         return both > 0.0f && ca + cb <= 17.0f * both;
     };
+    // Back to the operands' scale.
+    auto unscale = [&]() {
+        const int en0 = exponents[BM + 64 * wn + 4 * (col & 15) + 2 * (col >> 4)];
+        const int en1 = exponents[BM + 64 * wn + 4 * (col & 15) + 2 * (col >> 4) + 1];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int em = exponents[row_at(32 * (FM * wm + i) + (r & 3) + 8 * (r >> 2) + 4 * half)] - 282;
+                acc[i][0][r] = ldexpf(acc[i][0][r], em + en0);
+                acc[i][1][r] = ldexpf(acc[i][1][r], em + en1);
+            }
+    };
+    // The small tiles' stages, PARTS bf16 (fp16) parts: too few products a phase to
+    // hide an LDS read, so a stage's operands are all read a stage ahead.
+    // Under the products of stage s the operands of s + 1 are read from LDS, and the values
+    // of s + 2 are split and written where those of s were.
+    auto quick_small = [&](int first, int last, auto parts) {
+        constexpr int PARTS = decltype(parts)::value, D = FM == 1 ? 4 : 2;  // stages that loads run ahead
+        constexpr bool HALF = PARTS == 2;
+        constexpr int kA = PARTS * 2 * BM * 16, kBuf = kA + PARTS * 2 * BN * 16;
+        Share<BM, kThreads, !TA, kStage, HALF, D> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, exponents);
+        Share<BN, kThreads, TB, kStage, HALF, D> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, exponents + (HALF ? BM : 0));
+        constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
+        const int stages = (last - first) / kStage;
+        u32x4 x[2][PARTS][FM], y[2][PARTS][2];
+        const int ra = half * BM * 16 + (32 * FM * wm + col) * 16;
+        const int rb = kA + half * BN * 16 + (64 * wn + col) * 16;
+        auto fetch = [&](int set, const char *from) {
+#pragma unroll
+            for (int c = PARTS - 1; c >= 0; --c) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+                    x[set][c][i] = *reinterpret_cast<const u32x4 *>(from + c * (2 * BM * 16) + ra + 32 * 16 * i);
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    y[set][c][f] = *reinterpret_cast<const u32x4 *>(from + c * (2 * BN * 16) + rb + 32 * 16 * f);
+            }
+        };
+        auto multiply = [&](int set, int ca, int cb) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    if constexpr (HALF)
+                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            __builtin_bit_cast(half8v, x[set][ca][i]), __builtin_bit_cast(half8v, y[set][cb][f]), acc[i][f], 0, 0, 0);
+                    else
+                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            __builtin_bit_cast(bf16x8, x[set][ca][i]), __builtin_bit_cast(bf16x8, y[set][cb][f]), acc[i][f], 0, 0, 0);
+        };
+        auto put = [&](char *to, int set) {
+#pragma unroll
+            for (int u = 0; u < kUa; ++u) sa.put(u, to, set);
+#pragma unroll
+            for (int u = 0; u < kUb; ++u) sb.put(u, to + kA, set);
+        };
+        auto load = [&](int s, int set) { sa.load(min(s, stages - 1), set), sb.load(min(s, stages - 1), set); };  // past the end: not used
+        auto stage = [&](auto ic, int s) {
+            constexpr int I = decltype(ic)::value, P = I % 2, S = (I + 2) % D;
+            fetch(1 - P, memory + (1 - P) * kBuf);
+            put(memory + P * kBuf, S);
+            load(s + 2 + D, S);
+            constexpr int kProducts = HALF ? 3 : 6;
+            if constexpr (!HALF) multiply(P, 2, 0), multiply(P, 0, 2), multiply(P, 1, 1);
+            multiply(P, 1, 0), multiply(P, 0, 1), multiply(P, 0, 0);
+#pragma unroll
+            for (int k = 0; k < kProducts * FM * 2; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) asm volatile("" : "+v"(acc[i][f]));
+            wait_older<63>();  // LDS accesses alone
+            barrier_only();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(d, d);
+        put(memory, 0);
+        load(D, 0);
+        put(memory + kBuf, 1);
+        load(D + 1, 1);
+        wait_older<63>();
+        barrier_only();
+        fetch(0, memory);
+        wait_older<63>();
+        barrier_only();
+        turns<D>(stages, stage);
+        if constexpr (HALF) unscale();
+    };
+
     // Whole stages of 32 k in fp16 parts, as above: per 16 k the products l h,
     // h h and h l.
     auto quick_half = [&](int first, auto last) {
@@ -442,17 +563,7 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
             stage(s + 1, odd, even);
         }
         if (s < stages) stage(s, even, odd);
-        // back to the operands' scale
-        const int en0 = exponents[BM + 64 * wn + 4 * (col & 15) + 2 * (col >> 4)];
-        const int en1 = exponents[BM + 64 * wn + 4 * (col & 15) + 2 * (col >> 4) + 1];
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int em = exponents[row_at(32 * (FM * wm + i) + (r & 3) + 8 * (r >> 2) + 4 * half)] - 282;
-                acc[i][0][r] = ldexpf(acc[i][0][r], em + en0);
-                acc[i][1][r] = ldexpf(acc[i][1][r], em + en1);
-            }
+        unscale();
     };
 
     // The results of a block of 32 x 64 by way of LDS, so that a lane has 4
@@ -509,16 +620,26 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
     bool check = false;
     if (p.narrow && !few) {
         bool half_parts = false;
+        // the large tile's fp16 stages are of 32 k
+        constexpr int kHalfStage = FM == 4 ? 2 * kStage : kStage;
         if constexpr (kHalf)
-            if (p.row_b != nullptr && k1 - k0 >= 2 * kStage && certified()) {
-                whole = k0 + (k1 - k0) / (2 * kStage) * (2 * kStage);
-                quick_half(k0, whole);
+            if (p.row_b != nullptr && k1 - k0 >= kHalfStage && certified()) {
+                whole = k0 + (k1 - k0) / kHalfStage * kHalfStage;
+                if constexpr (FM == 4)
+                    quick_half(k0, whole);
+                else
+                    quick_small(k0, whole, std::integral_constant<int, 2>{});
                 half_parts = true;
             }
         if (!half_parts) {
             whole = k0 + (k1 - k0) / kStage * kStage;
             check = whole > k0;
-            if (check) quick(k0, whole);
+            if (check) {
+                if constexpr (FM == 4)
+                    quick(k0, whole);
+                else
+                    quick_small(k0, whole, std::integral_constant<int, 3>{});
+            }
         }
     }
     for (int from = whole;; from = k0) {
