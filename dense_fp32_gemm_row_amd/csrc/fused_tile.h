@@ -37,6 +37,10 @@ __device__ __forceinline__ float element(const float *p, int64_t ld, int row, in
     return KC ? p[row * ld + k] : p[k * ld + row];
 }
 
+// Bytes from 8 k of all rows to the next 8 k of them.  A few more than those take: 16
+// lanes write 64 / STAGE rows of STAGE / 8 such planes at once, to banks of their own.
+constexpr int plane(int rows, int stage) { return rows * 16 + 1024 / stage; }
+
 // A thread's share of the stages of one operand, STAGE k each: 4 consecutive k of
 // kUnits rows.  Where k is contiguous (KC) these are 16-byte loads, STAGE / 4
 // lanes a row; where rows are, kUnits neighbouring rows at 4 k.  Every address
@@ -47,7 +51,7 @@ template <int ROWS, int THREADS, bool KC, int STAGE, bool HALF, int D = 1>
 struct Share {
     static constexpr int E = ROWS * STAGE / THREADS;  // elements
     static constexpr int kUnits = E / 4;
-    static constexpr int kPlane = ROWS * 16;          // 8 k of every row
+    static constexpr int kPlane = plane(ROWS, STAGE);  // 8 k of every row
     static constexpr int kPart = STAGE / 8 * kPlane;
     const char *base;   // of the operand's tile at k = 0
     int64_t step, row;  // bytes a stage, a row of storage
@@ -161,8 +165,10 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
     using T = Tile<WM, WN, FM>;
     constexpr int BM = T::BM, BN = T::BN, kThreads = T::kThreads;
     constexpr bool kHalf = FM > 1;  // the tiles with a loop for fp16 parts
-    constexpr int kPlanesA = 3 * 2 * BM * 16, kBuffer = kPlanesA + 3 * 2 * BN * 16;
-    constexpr int kHalfA = 2 * 4 * BM * 16, kHalfBuffer = kHalfA + 2 * 4 * BN * 16;  // of 32 k
+    constexpr int kA = plane(BM, kStage), kB = plane(BN, kStage);                        // of 16 k
+    constexpr int kLongA = plane(BM, 2 * kStage), kLongB = plane(BN, 2 * kStage);        // of 32 k
+    constexpr int kPlanesA = 3 * 2 * kA, kBuffer = kPlanesA + 3 * 2 * kB;
+    constexpr int kHalfA = 2 * 4 * kLongA, kHalfBuffer = kHalfA + 2 * 4 * kLongB;
     constexpr int kMemory = 2 * (FM == 4 ? kHalfBuffer : kBuffer);
     constexpr int kRowOut = 68;  // floats: 64 of a row of results, 16 bytes apart from the next one's banks
     static_assert(kBuffer >= (BM + BN) * kStage * 4, "");
@@ -242,17 +248,17 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
         constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
         const int stages = (last - first) / kStage;
         u32x4 x[2][FM], y[3][2];  // parts of A by turns; the parts of B
-        const int ra = half * BM * 16 + (32 * FM * wm + col) * 16;
-        const int rb = kPlanesA + half * BN * 16 + (64 * wn + col) * 16;
+        const int ra = half * kA + (32 * FM * wm + col) * 16;
+        const int rb = kPlanesA + half * kB + (64 * wn + col) * 16;
         auto fetch_a = [&](int set, int part, const char *from) {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                x[set][i] = *reinterpret_cast<const u32x4 *>(from + part * (2 * BM * 16) + ra + 32 * 16 * i);
+                x[set][i] = *reinterpret_cast<const u32x4 *>(from + part * (2 * kA) + ra + 32 * 16 * i);
         };
         auto fetch_b = [&](int part, const char *from) {
 #pragma unroll
             for (int f = 0; f < 2; ++f)
-                y[part][f] = *reinterpret_cast<const u32x4 *>(from + part * (2 * BN * 16) + rb + 32 * 16 * f);
+                y[part][f] = *reinterpret_cast<const u32x4 *>(from + part * (2 * kB) + rb + 32 * 16 * f);
         };
         auto multiply = [&](int set, int part) {
 #pragma unroll
@@ -401,23 +407,23 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
     auto quick_small = [&](int first, int last, auto parts) {
         constexpr int PARTS = decltype(parts)::value, D = FM == 1 ? 4 : 2;  // stages that loads run ahead
         constexpr bool HALF = PARTS == 2;
-        constexpr int kA = PARTS * 2 * BM * 16, kBuf = kA + PARTS * 2 * BN * 16;
+        constexpr int kAll = PARTS * 2 * kA, kBuf = kAll + PARTS * 2 * kB;
         Share<BM, kThreads, !TA, kStage, HALF, D> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, exponents);
         Share<BN, kThreads, TB, kStage, HALF, D> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, exponents + (HALF ? BM : 0));
         constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
         const int stages = (last - first) / kStage;
         u32x4 x[2][PARTS][FM], y[2][PARTS][2];
-        const int ra = half * BM * 16 + (32 * FM * wm + col) * 16;
-        const int rb = kA + half * BN * 16 + (64 * wn + col) * 16;
+        const int ra = half * kA + (32 * FM * wm + col) * 16;
+        const int rb = kAll + half * kB + (64 * wn + col) * 16;
         auto fetch = [&](int set, const char *from) {
 #pragma unroll
             for (int c = PARTS - 1; c >= 0; --c) {
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
-                    x[set][c][i] = *reinterpret_cast<const u32x4 *>(from + c * (2 * BM * 16) + ra + 32 * 16 * i);
+                    x[set][c][i] = *reinterpret_cast<const u32x4 *>(from + c * (2 * kA) + ra + 32 * 16 * i);
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
-                    y[set][c][f] = *reinterpret_cast<const u32x4 *>(from + c * (2 * BN * 16) + rb + 32 * 16 * f);
+                    y[set][c][f] = *reinterpret_cast<const u32x4 *>(from + c * (2 * kB) + rb + 32 * 16 * f);
             }
         };
         auto multiply = [&](int set, int ca, int cb) {
@@ -436,7 +442,7 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
 #pragma unroll
             for (int u = 0; u < kUa; ++u) sa.put(u, to, set);
 #pragma unroll
-            for (int u = 0; u < kUb; ++u) sb.put(u, to + kA, set);
+            for (int u = 0; u < kUb; ++u) sb.put(u, to + kAll, set);
         };
         auto load = [&](int s, int set) { sa.load(min(s, stages - 1), set), sb.load(min(s, stages - 1), set); };  // past the end: not used
         auto stage = [&](auto ic, int s) {
@@ -488,17 +494,17 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
         static_assert(kUa == 4 && kUb == 4, "");
         const int stages = (last - first) / kLong;
         u32x4 x[2][FM], y[3][2];
-        const int ra = half * BM * 16 + (32 * FM * wm + col) * 16;
-        const int rb = kHalfA + half * BN * 16 + (64 * wn + col) * 16;
+        const int ra = half * kLongA + (32 * FM * wm + col) * 16;
+        const int rb = kHalfA + half * kLongB + (64 * wn + col) * 16;
         auto fetch_a = [&](int set, int part, int ks, const char *from) {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                x[set][i] = *reinterpret_cast<const u32x4 *>(from + (part * 4 + 2 * ks) * (BM * 16) + ra + 32 * 16 * i);
+                x[set][i] = *reinterpret_cast<const u32x4 *>(from + (part * 4 + 2 * ks) * kLongA + ra + 32 * 16 * i);
         };
         auto fetch_b = [&](int set, int part, int ks, const char *from) {
 #pragma unroll
             for (int f = 0; f < 2; ++f)
-                y[set][f] = *reinterpret_cast<const u32x4 *>(from + (part * 4 + 2 * ks) * (BN * 16) + rb + 32 * 16 * f);
+                y[set][f] = *reinterpret_cast<const u32x4 *>(from + (part * 4 + 2 * ks) * kLongB + rb + 32 * 16 * f);
         };
         auto multiply = [&](int sx, int sy) {
 #pragma unroll
