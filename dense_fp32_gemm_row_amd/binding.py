@@ -784,28 +784,61 @@ def _activation(name) -> int:
         raise ValueError(f"activation {name!r} is none of {', '.join(ACTIVATIONS)}") from None
 
 
-def _sheet(t, name: str, shape, device) -> tuple[int, int, int]:
+def _laid(t, name: str) -> tuple[int, int, int, tuple]:
+    """(op, leading dimension, batch stride, shape) of a 2-D or 3-D float32
+    GPU tensor, as _float_operand (with fewer calls: these cost as much as a launch)."""
+    shape, strides = tuple(t.shape), t.stride()
+    dims = len(shape)
+    if t.dtype is not _torch.float32 or not t.is_cuda or dims not in (2, 3):
+        raise TypeError(f"{name} must be a 2-D or 3-D float32 GPU tensor")
+    rows, cols = shape[-2:]
+    rs, cs = strides[-2:]
+    bs = strides[0] if dims == 3 and shape[0] > 1 else 0
+    if cols <= 1 or cs == 1:
+        return OP_N, (rs if rows > 1 else cols or 1), bs, shape
+    if rows <= 1 or rs == 1:
+        return OP_T, cs, bs, shape
+    raise ValueError(f"{name} must be row-major or a transposed view of a row-major matrix")
+
+
+def _same_device(t, name: str, device, index: int) -> None:
+    if t.get_device() != index:
+        raise ValueError(f"{name} on {t.device}, other operands on {device}")
+
+
+def _sheet(t, name: str, shape, device, index: int) -> tuple[int, int, int]:
     """(pointer, leading dimension, batch stride) of a row-major tensor of ``shape``."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    op, ld, bs, _ = _float_operand(t, name, device)
+    op, ld, bs, got = _laid(t, name)
+    if got != shape:
+        raise ValueError(f"{name} has shape {got}, expected {shape}")
+    _same_device(t, name, device, index)
     if op != OP_N:
         raise ValueError(f"{name} must be row-major")
     return t.data_ptr(), ld, bs
 
 
-def _vector(t, name: str, shape, device) -> tuple[int, int]:
+def _vector(t, name: str, shape, device, index: int) -> tuple[int, int]:
     """(pointer, batch stride) of a float32 tensor of ``shape`` (n,) or
     (batch, n), with unit stride along the last axis."""
-    if t.dtype != _torch.float32 or not t.is_cuda:
+    if t.dtype is not _torch.float32 or not t.is_cuda:
         raise TypeError(f"{name} must be a float32 GPU tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} on {t.device}, other operands on {device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    got, strides = tuple(t.shape), t.stride()
+    if got != shape:
+        raise ValueError(f"{name} has shape {got}, expected {shape}")
+    _same_device(t, name, device, index)
+    if got[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have unit stride along its last axis")
-    return t.data_ptr(), t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else 0
+    return t.data_ptr(), strides[0] if len(got) == 2 and got[0] > 1 else 0
+
+
+def _sheet_out(out, shape, device, index: int, stream):
+    """(out, allocated if None; its pointer, leading dimension and batch stride)."""
+    if out is not None:
+        return out, *_sheet(out, "out", shape, device, index)
+    ld = shape[-1] or 1
+    bs = shape[-2] * ld
+    out = _empty(shape, (ld, 1) if len(shape) == 2 else (bs, ld, 1), _torch.float32, device, stream)
+    return out, out.data_ptr(), ld, bs
 
 
 def _space(workspace, need: int, device, stream):
@@ -821,16 +854,17 @@ def _space(workspace, need: int, device, stream):
 
 
 def _pair(A, B):
-    """Checks A and B of a product: (device, leading shape, batch, M, N, K, A's and B's (op, ld, stride))."""
+    """Checks A and B of a product: (device, its index, leading shape, batch, M, N, K, A's and B's
+    (op, ld, stride, shape))."""
     load()
-    opa, lda, sa, batch = _float_operand(A, "A")
-    device = A.device
-    opb, ldb, sb, _ = _float_operand(B, "B", device)
-    *lead, M, K = A.shape
-    *lead_b, K2, N = B.shape
-    if K != K2 or lead != lead_b:
-        raise ValueError(f"shape mismatch {tuple(A.shape)} x {tuple(B.shape)}")
-    return device, lead, batch, M, N, K, (opa, lda, sa), (opb, ldb, sb)
+    a, b = _laid(A, "A"), _laid(B, "B")
+    device, index = A.device, A.get_device()
+    _same_device(B, "B", device, index)
+    sa, sb = a[3], b[3]
+    if sa[-1] != sb[-2] or sa[:-2] != sb[:-2]:
+        raise ValueError(f"shape mismatch {sa} x {sb}")
+    lead = sa[:-2]
+    return device, index, lead, (lead[0] if lead else 1), sa[-2], sb[-1], sa[-1], a, b
 
 
 def gemm_fused(A, B, out=None, *, bias=None, activation: str = "none", residual=None, pre=None,
@@ -846,43 +880,48 @@ def gemm_fused(A, B, out=None, *, bias=None, activation: str = "none", residual=
     gemm_f32_fused_workspace_size bytes) is allocated here when the sizes call
     for one and None is given.  Enqueued on ``stream``, default torch's
     current stream; returns ``out`` without synchronising."""
-    device, lead, batch, M, N, K, (opa, lda, sa), (opb, ldb, sb) = _pair(A, B)
+    device, index, lead, batch, M, N, K, (opa, lda, sa, _), (opb, ldb, sb, _) = _pair(A, B)
     kind = _activation(activation)
     shape = (*lead, M, N)
     e = None
     if kind or bias is not None or residual is not None or pre is not None:
         e = Epilogue(kind)
         if bias is not None:
-            e.bias, e.stride_bias = _vector(bias, "bias", (batch, N) if bias.dim() == 2 and lead else (N,), device)
+            e.bias, e.stride_bias = _vector(bias, "bias", (batch, N) if bias.dim() == 2 and lead else (N,), device, index)
         if residual is not None:
-            e.residual, e.ld_residual, e.stride_residual = _sheet(residual, "residual", shape, device)
+            e.residual, e.ld_residual, e.stride_residual = _sheet(residual, "residual", shape, device, index)
         if pre is not None:
-            e.pre, e.ld_pre, e.stride_pre = _sheet(pre, "pre", shape, device)
-    lib = load()
-    out, ldc, sc, workspace, wp, wb = _mxfp4_out(
-        out, shape, device, workspace, lib.gemm_f32_fused_workspace_size(opa, opb, batch, M, N, K), stream)
+            e.pre, e.ld_pre, e.stride_pre = _sheet(pre, "pre", shape, device, index)
+        e = ctypes.byref(e)
+    lib = _LIB
+    out, cp, ldc, sc = _sheet_out(out, shape, device, index, stream)
+    wp, wb = None, 0
+    if workspace is not None or (need := lib.gemm_f32_fused_workspace_size(opa, opb, batch, M, N, K)):
+        workspace, wp, wb = _space(workspace, 0 if workspace is not None else need, device, stream)
     _run_on(device, stream, lib.gemm_f32_fused, opa, opb, batch, M, N, K, A.data_ptr(), lda, sa,
-            B.data_ptr(), ldb, sb, _matrix_arg(e), out.data_ptr(), ldc, sc, wp, wb)
+            B.data_ptr(), ldb, sb, e, cp, ldc, sc, wp, wb)
     return out
 
 
-def _like(t, op: int, want, name: str, device, stream):
-    """An output laid out as the operand ``t`` of form ``op`` (``want`` True:
+def _like(shape, op: int, want, name: str, device, index: int, stream):
+    """An output laid out as an operand of ``shape`` and form ``op`` (``want`` True:
     allocated; a tensor: that one): (tensor, pointer, leading dimension, stride)."""
     if want is None or want is False:
-        return None, None, 1 << 31, 1 << 59  # not looked at
+        return None, None, 0, 0  # not looked at
+    *lead, rows, cols = shape
+    if op == OP_T:
+        rows, cols = cols, rows
     if want is True:
-        *lead, rows, cols = t.shape
-        if op == OP_T:
-            rows, cols = cols, rows
-        ld = max(cols, 1)
-        strides = (rows * ld,) * len(lead) + (ld, 1)
-        new = _empty((*lead, rows, cols), strides, _torch.float32, device, stream)
-        return (new.transpose(-1, -2) if op == OP_T else new), new.data_ptr(), ld, (rows * ld if lead else 0)
-    if tuple(want.shape) != tuple(t.shape):
-        raise ValueError(f"{name} has shape {tuple(want.shape)}, expected {tuple(t.shape)}")
+        ld = cols or 1
+        bs = rows * ld if lead else 0
+        # (strides as a transposed view has them)
+        new = _empty(shape, (*((bs,) * len(lead)), *((1, ld) if op == OP_T else (ld, 1))), _torch.float32, device, stream)
+        return new, new.data_ptr(), ld, bs
     stored = want.transpose(-1, -2) if op == OP_T else want
-    got, ld, bs, _ = _float_operand(stored, name, device)
+    got, ld, bs, laid = _laid(stored, name)
+    if laid != (*lead, rows, cols):
+        raise ValueError(f"{name} has shape {tuple(want.shape)}, expected {shape}")
+    _same_device(want, name, device, index)
     if got != OP_N:
         raise ValueError(f"{name} must be laid out as its operand is "
                          f"({'a transposed view of a row-major matrix' if op == OP_T else 'row-major'})")
@@ -899,23 +938,25 @@ def gemm_fused_grad(dC, A, B, *, pre=None, activation: str = "none", dA=True, dB
     operand), a tensor to write, or False (not computed, None returned).  For a batch
     the gradients are per product, dbias (batch, N).  ``workspace`` (at least
     gemm_f32_fused_grad_workspace_size bytes) is allocated here when None."""
-    device, lead, batch, M, N, K, (opa, lda, sa), (opb, ldb, sb) = _pair(A, B)
+    device, index, lead, batch, M, N, K, (opa, lda, sa, shape_a), (opb, ldb, sb, shape_b) = _pair(A, B)
     kind = _activation(activation)
-    gp, ldg, sg = _sheet(dC, "dC", (*lead, M, N), device)
+    shape = (*lead, M, N)
+    gp, ldg, sg = _sheet(dC, "dC", shape, device, index)
     zp, ldz, sz = None, N or 1, 0
     if kind:
         if pre is None:
             raise ValueError(f"the gradient of {activation!r} needs pre")
-        zp, ldz, sz = _sheet(pre, "pre", (*lead, M, N), device)
-    dA, ap, ldda, sda = _like(A, opa, dA, "dA", device, stream)
-    dB, bp, lddb, sdb = _like(B, opb, dB, "dB", device, stream)
+        zp, ldz, sz = _sheet(pre, "pre", shape, device, index)
+    dA, ap, ldda, sda = _like(shape_a, opa, dA, "dA", device, index, stream)
+    dB, bp, lddb, sdb = _like(shape_b, opb, dB, "dB", device, index, stream)
+    cp, sdc = None, 0
     if dbias is None or dbias is False:
-        dbias, cp, sdc = None, None, 0
+        dbias = None
     else:
         if dbias is True:
             dbias = _empty((*lead, N), (N, 1) if lead else (1,), _torch.float32, device, stream)
-        cp, sdc = _vector(dbias, "dbias", (*lead, N), device)
-    lib = load()
+        cp, sdc = _vector(dbias, "dbias", (*lead, N), device, index)
+    lib = _LIB
     workspace, wp, wb = _space(
         workspace, lib.gemm_f32_fused_grad_workspace_size(opa, opb, batch, M, N, K, kind, ap is not None,
                                                           bp is not None, cp is not None), device, stream)
@@ -925,34 +966,34 @@ def gemm_fused_grad(dC, A, B, *, pre=None, activation: str = "none", dA=True, dB
 
 
 def _tokens(X, W, target):
-    """Checks the inputs of the cross entropy: (device, T, V, K, X's and W's leading dimension)."""
+    """Checks the inputs of the cross entropy: (device, its index, T, V, K, X's and W's leading
+    dimension)."""
     load()
-    device = X.device
     if X.dim() != 2 or W.dim() != 2:
         raise TypeError("X and W must be 2-D float32 GPU tensors")
-    opx, ldx, _, _ = _float_operand(X, "X")
-    opw, ldw, _, _ = _float_operand(W, "W", device)
+    opx, ldx, _, (T, K) = _laid(X, "X")
+    opw, ldw, _, (V, K2) = _laid(W, "W")
+    device, index = X.device, X.get_device()
+    _same_device(W, "W", device, index)
     if opx != OP_N or opw != OP_N:
         raise ValueError("X and W must be row-major")
-    T, K = X.shape
-    V, K2 = W.shape
     if K != K2:
-        raise ValueError(f"shape mismatch {tuple(X.shape)} x {tuple(W.shape)} transposed")
-    if target.dtype != _torch.int64 or not target.is_cuda:
+        raise ValueError(f"shape mismatch {(T, K)} x {(V, K2)} transposed")
+    if target.dtype is not _torch.int64 or not target.is_cuda:
         raise TypeError("target must be an int64 GPU tensor")
     if tuple(target.shape) != (T,):
         raise ValueError(f"target has shape {tuple(target.shape)}, expected {(T,)}")
-    if target.device != device:
-        raise ValueError(f"target on {target.device}, other operands on {device}")
+    _same_device(target, "target", device, index)
     if T > 1 and target.stride(0) != 1:
         raise ValueError("target must be contiguous")
-    return device, T, V, K, ldx, ldw
+    return device, index, T, V, K, ldx, ldw
 
 
-def _row_out(t, name: str, T: int, device, stream):
+def _row_out(t, name: str, T: int, device, index: int, stream):
     if t is None:
         t = _empty((T,), (1,), _torch.float32, device, stream)
-    return t, _vector(t, name, (T,), device)[0]
+        return t, t.data_ptr()
+    return t, _vector(t, name, (T,), device, index)[0]
 
 
 def cross_entropy(X, W, target, *, ignore_index: int = -100, loss=None, lse=None, workspace=None,
@@ -962,10 +1003,10 @@ def cross_entropy(X, W, target, *, ignore_index: int = -100, loss=None, lse=None
     and ``loss[t] = lse[t] - logits[t, target[t]]``, 0 where ``target[t]`` is
     ``ignore_index``; any other target outside [0, V) gives NaN.  ``loss`` and
     ``lse`` are written where given; ``workspace`` and ``stream`` as in gemm_fused."""
-    device, T, V, K, ldx, ldw = _tokens(X, W, target)
-    loss, lp = _row_out(loss, "loss", T, device, stream)
-    lse, sp = _row_out(lse, "lse", T, device, stream)
-    lib = load()
+    device, index, T, V, K, ldx, ldw = _tokens(X, W, target)
+    loss, lp = _row_out(loss, "loss", T, device, index, stream)
+    lse, sp = _row_out(lse, "lse", T, device, index, stream)
+    lib = _LIB
     workspace, wp, wb = _space(workspace, lib.gemm_f32_cross_entropy_workspace_size(T, V, K), device, stream)
     _run_on(device, stream, lib.gemm_f32_cross_entropy, T, V, K, X.data_ptr(), ldx, W.data_ptr(), ldw,
             target.data_ptr(), ignore_index, lp, sp, wp, wb)
@@ -981,13 +1022,13 @@ def cross_entropy_grad(X, W, target, grad_loss=None, *, ignore_index: int = -100
     ``workspace`` holds the logits of some tokens at a time: any size from
     gemm_f32_cross_entropy_grad_workspace_least bytes will do,
     gemm_f32_cross_entropy_grad_workspace_size (allocated when None) is quickest."""
-    device, T, V, K, ldx, ldw = _tokens(X, W, target)
-    gp = None if grad_loss is None else _vector(grad_loss, "grad_loss", (T,), device)[0]
-    loss, lp = _row_out(loss, "loss", T, device, stream)
-    lse, sp = _row_out(lse, "lse", T, device, stream)
-    dX, xp, lddx, _ = _like(X, OP_N, dX, "dX", device, stream)
-    dW, dwp, lddw, _ = _like(W, OP_N, dW, "dW", device, stream)
-    lib = load()
+    device, index, T, V, K, ldx, ldw = _tokens(X, W, target)
+    gp = None if grad_loss is None else _vector(grad_loss, "grad_loss", (T,), device, index)[0]
+    loss, lp = _row_out(loss, "loss", T, device, index, stream)
+    lse, sp = _row_out(lse, "lse", T, device, index, stream)
+    dX, xp, lddx, _ = _like((T, K), OP_N, dX, "dX", device, index, stream)
+    dW, dwp, lddw, _ = _like((V, K), OP_N, dW, "dW", device, index, stream)
+    lib = _LIB
     workspace, wp, wb = _space(workspace, lib.gemm_f32_cross_entropy_grad_workspace_size(T, V, K), device,
                                stream)
     _run_on(device, stream, lib.gemm_f32_cross_entropy_grad, T, V, K, X.data_ptr(), ldx, W.data_ptr(), ldw,

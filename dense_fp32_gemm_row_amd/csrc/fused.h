@@ -77,6 +77,10 @@ struct Product {
 };
 
 hipError_t launch_product(const Product &, hipStream_t);
+// Whether its large tiles may take fp16 parts.
+bool wants_parts(const Product &);
+// Two independent products that share their workspace.
+hipError_t launch_two(const Product &, const Product &, hipStream_t);
 // Bytes of workspace that a product is quickest with; it runs with none, too.
 // `statistics`: its mode is not kStore.
 int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics);
@@ -91,6 +95,10 @@ hipError_t launch_tile_tt(const Product &, int tile, hipStream_t);
 // `shape` as in fused_choice.h.
 hipError_t launch_rows(const Product &, int shape, hipStream_t);
 
+// Both in one launch, where both are small: whether they were (their splits are
+// set; *err is the launch's).
+bool launch_rows_pair(const Product &p, int shape_p, const Product &q, int shape_q, hipStream_t, hipError_t *err);
+
 hipError_t launch_row_stats(const Product &, hipStream_t);
 
 // C = epilogue(sum over the slices, in their order).
@@ -98,7 +106,7 @@ hipError_t launch_sum_slices(const Product &, hipStream_t);
 
 // dZ = dC act'(Z), and the sums of its columns over blocks of rows; either may
 // be absent (dz.p null; partial null).
-constexpr int kSlopeBlocks = 256;
+constexpr int kSlopeBlocks = 256;  // at most
 struct Slope {
     int64_t batch;
     int M, N;
@@ -106,7 +114,7 @@ struct Slope {
     Operand dc, pre;
     Result dz;
     float *partial;  // [batch][blocks][N]
-    int blocks, rows;  // at most kSlopeBlocks; rows a block
+    int blocks, rows;  // rows a block; of one block dbias is the sum (partial unused)
     Result dbias;    // ld unused
 };
 hipError_t launch_slope(const Slope &, hipStream_t);
@@ -127,6 +135,8 @@ struct Loss {
 hipError_t launch_loss(const Loss &, hipStream_t);
 // logits = grad_loss (exp(logits - lse) - (v == target)), zero for ignored rows
 hipError_t launch_probabilities(const Loss &, hipStream_t);
+// Both at once, for small T x V (the largest magnitudes are not found).
+hipError_t launch_loss_and_probabilities(const Loss &, hipStream_t);
 
 }  // namespace fused
 }  // namespace gemm_f32_impl

@@ -83,6 +83,12 @@ hipError_t run(const fused::Product &p, hipStream_t s) {
     return fused::launch_product(p, s);
 }
 
+hipError_t run(const fused::Product &p, const fused::Product &q, hipStream_t s) {
+    auto empty = [](const fused::Product &x) { return x.batch == 0 || x.M == 0 || x.N == 0; };
+    if (!empty(p) && !empty(q)) return fused::launch_two(p, q, s);
+    return empty(p) ? run(q, s) : run(p, s);
+}
+
 // ---- the parts of a gradient's workspace, in floats ----
 struct GradParts {
     int64_t dz, partial, space;
@@ -95,10 +101,12 @@ GradParts grad_parts(bool ta, bool tb, int64_t batch, int64_t M, int64_t N, int6
     // blocks of rows of the bias gradient's first sums: enough to fill the GPU
     const int64_t strips = std::max<int64_t>(1, times(batch, div_up(N, 256)));
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(fused::kSlopeBlocks, 1024 / strips));
-    g.rows = static_cast<int>(std::max<int64_t>(8, div_up(M, most)));
+    // a few rows of not too many columns: one block, whose sums need no second launch
+    const bool one = M <= 256 && times(times(batch, M), N) <= 1 << 18;
+    g.rows = static_cast<int>(one ? std::max<int64_t>(1, M) : std::max<int64_t>(8, div_up(M, most)));
     g.blocks = static_cast<int>(div_up(M, g.rows));
     if (activation != GEMM_F32_ACT_NONE && (dA || dB)) g.dz = times(times(batch, M), N);
-    if (dbias) g.partial = times(times(batch, g.blocks), N);
+    if (dbias && g.blocks > 1) g.partial = times(times(batch, g.blocks), N);
     // (the sizes of the products as they are run)
     if (dA) g.space = (ta ? space_of(true, batch, K, M, N) : space_of(!tb, batch, M, K, N)) / 4;
     if (dB) g.space = std::max(g.space, (tb ? space_of(ta, batch, N, K, M) : space_of(false, batch, K, N, M)) / 4);
@@ -260,13 +268,12 @@ int gemm_f32_fused_grad(int opA, int opB, int64_t batch, int64_t M, int64_t N, i
         hipError_t err = hipSuccess;
         if (N > 0 && (want_bias || parts.dz > 0)) err = fused::launch_slope(s, q);
         // dA = dZ op(B)^T, or its transpose op(B) dZ^T
-        if (err == hipSuccess && want_a)
-            err = run(ta ? plain_product(batch, K, M, N, tb, ob, true, grad, ra, space)
-                         : plain_product(batch, M, K, N, false, grad, !tb, ob, ra, space), q);
+        const fused::Product pa = ta ? plain_product(batch, K, M, N, tb, ob, true, grad, ra, space)
+                                     : plain_product(batch, M, K, N, false, grad, !tb, ob, ra, space);
         // dB = op(A)^T dZ, or its transpose dZ^T op(A)
-        if (err == hipSuccess && want_b)
-            err = run(tb ? plain_product(batch, N, K, M, true, grad, ta, oa, rb, space)
-                         : plain_product(batch, K, N, M, !ta, oa, false, grad, rb, space), q);
+        const fused::Product pb = tb ? plain_product(batch, N, K, M, true, grad, ta, oa, rb, space)
+                                     : plain_product(batch, K, N, M, !ta, oa, false, grad, rb, space);
+        if (err == hipSuccess) err = want_a && want_b ? run(pa, pb, q) : want_a ? run(pa, q) : want_b ? run(pb, q) : err;
         return err;
     });
 }
@@ -362,22 +369,28 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             l.loss = loss != nullptr ? loss + t0 : nullptr, l.lse = lse != nullptr ? lse + t0 : at + n;
             l.grad_loss = grad_loss != nullptr ? grad_loss + t0 : nullptr, l.logits = logits;
             l.row_top = dX != nullptr ? row_top : nullptr, l.column_top = dW != nullptr ? column_top : nullptr;
-            if (err == hipSuccess) err = fused::launch_loss(l, s);
-            if (dX == nullptr && dW == nullptr) continue;
-            if (err == hipSuccess) err = fused::launch_probabilities(l, s);
-            if (err == hipSuccess && dX != nullptr) {
-                p = plain_product(1, n, K, V, false, {logits, V, 0}, false, {W, ldw, 0},
-                                        {dX + t0 * lddx, lddx, 0}, room(false, n, K, V));
-                p.top_a = row_top;
-                err = run(p, s);
+            if (dX == nullptr && dW == nullptr) {
+                if (err == hipSuccess) err = fused::launch_loss(l, s);
+                continue;
             }
-            if (err == hipSuccess && dW != nullptr) {
-                p = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0}, room(false, V, K, n));
-                p.top_a = column_top;
-                p.target_k = target + t0, p.ignore = ignore_index;
-                if (t0 > 0) p.e.residual = {dW, lddw, 0};  // the pieces before
-                err = run(p, s);
+            fused::Product px = plain_product(1, n, K, V, false, {logits, V, 0}, false, {W, ldw, 0},
+                                              {dX != nullptr ? dX + t0 * lddx : nullptr, lddx, 0}, room(false, n, K, V));
+            px.top_a = row_top;
+            fused::Product pw = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0},
+                                              room(false, V, K, n));
+            pw.top_a = column_top;
+            pw.target_k = target + t0, pw.ignore = ignore_index;
+            if (t0 > 0) pw.e.residual = {dW, lddw, 0};  // the pieces before
+            // small: no fp16 parts, which want the largest magnitudes
+            if (n * V <= 1 << 18 && !fused::wants_parts(px) && !fused::wants_parts(pw)) {
+                l.row_top = l.column_top = nullptr;
+                if (err == hipSuccess) err = fused::launch_loss_and_probabilities(l, s);
+            } else {
+                if (err == hipSuccess) err = fused::launch_loss(l, s);
+                if (err == hipSuccess) err = fused::launch_probabilities(l, s);
             }
+            if (err == hipSuccess)
+                err = dX != nullptr && dW != nullptr ? run(px, pw, s) : dX != nullptr ? run(px, s) : run(pw, s);
         }
         return err;
     });

@@ -46,22 +46,23 @@ __device__ __forceinline__ void write4(float *p, int64_t left, f32x4 v) {
     }
 }
 
-// A block of rows of 256 columns, 4 a lane, its rows shared by 4 wavefronts: dZ, and
-// the columns' sums over the block.
-template <int KIND>
-__global__ __launch_bounds__(256) void slope_kernel(Slope s, int64_t strips, int64_t units) {
-    __shared__ f32x4 sums[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// A block of rows of 4 LANES columns, 4 a lane, its rows shared by WAVES wavefronts and
+// the 64 / LANES parts of each: dZ, and the columns' sums over the block.
+template <int KIND, int WAVES, int LANES>
+__global__ __launch_bounds__(64 * WAVES) void slope_kernel(Slope s, int64_t strips, int64_t units) {
+    constexpr int kParts = 64 * WAVES / LANES;
+    __shared__ f32x4 sums[kParts][LANES];
+    const int lane = threadIdx.x % LANES, part = threadIdx.x / LANES;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t strip = u % strips, rest = u / strips, block = rest % s.blocks, b = rest / s.blocks;
-        const int64_t n = strip * 256 + 4 * lane, left = s.N - n;
+        const int64_t n = strip * (4 * LANES) + 4 * lane, left = s.N - n;
         const int64_t first = block * s.rows, last = min(first + s.rows, int64_t{s.M});
         const float *dc = s.dc.p + b * s.dc.stride + n, *pre = s.pre.p + b * s.pre.stride + n;
         float *dz = s.dz.p + b * s.dz.stride + n;
         f32x4 sum{0.0f, 0.0f, 0.0f, 0.0f};
         if (left > 0) {
 #pragma unroll 4
-            for (int64_t m = first + wave; m < last; m += 4) {
+            for (int64_t m = first + part; m < last; m += kParts) {
                 f32x4 v = read4(dc + m * s.dc.ld, left);
                 if constexpr (KIND != GEMM_F32_ACT_NONE) {
                     const f32x4 z = read4(pre + m * s.pre.ld, left);
@@ -73,15 +74,16 @@ __global__ __launch_bounds__(256) void slope_kernel(Slope s, int64_t strips, int
                 for (int e = 0; e < 4; ++e) sum[e] += v[e];
             }
         }
-        if (s.partial == nullptr) continue;
-        sums[wave][lane] = sum;
+        if (s.dbias.p == nullptr) continue;
+        sums[part][lane] = sum;
         __syncthreads();
-        if (wave == 0 && left > 0) {
+        if (part == 0 && left > 0) {
 #pragma unroll
-            for (int w = 1; w < 4; ++w)
+            for (int w = 1; w < kParts; ++w)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sum[e] += sums[w][lane][e];
-            write4(s.partial + (b * s.blocks + block) * s.N + n, left, sum);
+            write4(s.blocks == 1 ? s.dbias.p + b * s.dbias.stride + n : s.partial + (b * s.blocks + block) * s.N + n, left,
+                   sum);
         }
         __syncthreads();
     }
@@ -108,7 +110,15 @@ __global__ __launch_bounds__(256) void bias_kernel(Slope s, int64_t strips, int6
     }
 }
 
-// A workgroup a row: its pieces' statistics joined, in a fixed order.
+// exp(logit - lse) - (v == target), times g.
+__device__ __forceinline__ float gradient(const Loss &l, float x, float lse, float g, int64_t v, int64_t target) {
+    const float p = g * (quick_exp(x - lse) - (v == target ? 1.0f : 0.0f));
+    return target == l.ignore ? 0.0f : target >= 0 && target < l.V ? p : __builtin_nanf("");
+}
+
+// A workgroup a row: its pieces' statistics joined, in a fixed order; with GRAD
+// the row's gradient, too.
+template <bool GRAD>
 __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
     __shared__ float tops[4], sums[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -137,8 +147,17 @@ __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
                             : target >= 0 && target < l.V ? lse - l.at_target[t] : __builtin_nanf("");
             }
             if (l.row_top != nullptr) l.row_top[t] = 0;
+            if constexpr (GRAD) tops[0] = lse;
         }
         __syncthreads();
+        if constexpr (GRAD) {
+            const float lse = tops[0], g = l.grad_loss != nullptr ? l.grad_loss[t] : 1.0f;
+            const int64_t target = l.target[t];
+            float *row = l.logits + t * l.V;
+#pragma unroll 4
+            for (int64_t v = threadIdx.x; v < l.V; v += 256) row[v] = gradient(l, row[v], lse, g, v, target);
+            __syncthreads();
+        }
     }
 }
 
@@ -160,14 +179,11 @@ __global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t stri
                 const int64_t t = t0 + i;
                 if (t >= last) break;
                 const int64_t target = l.target[t];
-                const bool counts = target != l.ignore;
                 const float lse = l.lse[t], g = l.grad_loss != nullptr ? l.grad_loss[t] : 1.0f;
                 int row = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float p = g * (quick_exp(x[i][e] - lse) - (v + e == target ? 1.0f : 0.0f));
-                    if (target < 0 || target >= l.V) p = __builtin_nanf("");
-                    p = counts ? p : 0.0f;
+                    const float p = gradient(l, x[i][e], lse, g, v + e, target);
                     x[i][e] = p;
                     const int bits = e < left ? __builtin_bit_cast(int, p) & 0x7fffffff : 0;
                     column[e] = max(column[e], bits), row = max(row, bits);
@@ -255,18 +271,29 @@ hipError_t launch_sum_slices(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_slope(const Slope &s, hipStream_t stream) {
-    const int64_t strips = div_up(s.N, 256), units = strips * s.blocks * s.batch;
-    const unsigned grid = blocks_for(units);
+template <int WAVES, int LANES>
+static void run_slope(const Slope &s, hipStream_t stream) {
+    const int64_t strips = div_up(s.N, 4 * LANES), units = strips * s.blocks * s.batch;
+    const unsigned grid = blocks_for(units), threads = 64 * WAVES;
     switch (s.activation) {
-        case GEMM_F32_ACT_RELU: slope_kernel<GEMM_F32_ACT_RELU><<<grid, 256, 0, stream>>>(s, strips, units); break;
-        case GEMM_F32_ACT_GELU: slope_kernel<GEMM_F32_ACT_GELU><<<grid, 256, 0, stream>>>(s, strips, units); break;
-        case GEMM_F32_ACT_GELU_TANH: slope_kernel<GEMM_F32_ACT_GELU_TANH><<<grid, 256, 0, stream>>>(s, strips, units); break;
-        case GEMM_F32_ACT_SILU: slope_kernel<GEMM_F32_ACT_SILU><<<grid, 256, 0, stream>>>(s, strips, units); break;
-        default: slope_kernel<GEMM_F32_ACT_NONE><<<grid, 256, 0, stream>>>(s, strips, units);
+        case GEMM_F32_ACT_RELU: slope_kernel<GEMM_F32_ACT_RELU, WAVES, LANES><<<grid, threads, 0, stream>>>(s, strips, units); break;
+        case GEMM_F32_ACT_GELU: slope_kernel<GEMM_F32_ACT_GELU, WAVES, LANES><<<grid, threads, 0, stream>>>(s, strips, units); break;
+        case GEMM_F32_ACT_GELU_TANH:
+            slope_kernel<GEMM_F32_ACT_GELU_TANH, WAVES, LANES><<<grid, threads, 0, stream>>>(s, strips, units);
+            break;
+        case GEMM_F32_ACT_SILU: slope_kernel<GEMM_F32_ACT_SILU, WAVES, LANES><<<grid, threads, 0, stream>>>(s, strips, units); break;
+        default: slope_kernel<GEMM_F32_ACT_NONE, WAVES, LANES><<<grid, threads, 0, stream>>>(s, strips, units);
     }
+}
+
+hipError_t launch_slope(const Slope &s, hipStream_t stream) {
+    // One block of rows: dbias is its sum, 16 parts of a workgroup share it.
+    if (s.blocks == 1)
+        run_slope<4, 16>(s, stream);
+    else
+        run_slope<4, 64>(s, stream);
     hipError_t err = hipGetLastError();
-    if (err == hipSuccess && s.dbias.p != nullptr) {
+    if (err == hipSuccess && s.dbias.p != nullptr && s.blocks != 1) {
         const int64_t lines = div_up(s.N, 16);
         bias_kernel<<<blocks_for(lines * s.batch), 256, 0, stream>>>(s, lines, lines * s.batch);
         err = hipGetLastError();
@@ -275,7 +302,12 @@ hipError_t launch_slope(const Slope &s, hipStream_t stream) {
 }
 
 hipError_t launch_loss(const Loss &l, hipStream_t stream) {
-    loss_kernel<<<blocks_for(l.T), 256, 0, stream>>>(l);
+    loss_kernel<false><<<blocks_for(l.T), 256, 0, stream>>>(l);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_and_probabilities(const Loss &l, hipStream_t stream) {
+    loss_kernel<true><<<blocks_for(l.T), 256, 0, stream>>>(l);
     return hipGetLastError();
 }
 
@@ -320,10 +352,30 @@ int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, b
     return static_cast<int64_t>(std::min<__int128>(slices + stats, __int128{1} << 61));
 }
 
+namespace {
+Choice choice_of(const Product &p) {
+    return choose(p.tb, p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore ? kPlain : kStatistics);
+}
+}  // namespace
+
+bool wants_parts(const Product &p) { return choice_of(p).half; }
+
+hipError_t launch_two(const Product &p, const Product &q, hipStream_t stream) {
+    const Choice c = choice_of(p), d = choice_of(q);
+    hipError_t err = hipSuccess;
+    if (c.tile == kRows && d.tile == kRows && c.splits == 1 && d.splits == 1) {
+        Product a = p, b = q;
+        a.splits = b.splits = 1;
+        if (launch_rows_pair(a, c.shape, b, d.shape, stream, &err)) return err;
+    }
+    err = launch_product(p, stream);
+    return err == hipSuccess ? launch_product(q, stream) : err;
+}
+
 hipError_t launch_product(const Product &asked, hipStream_t stream) {
     Product p = asked;
     p.narrow = narrow_operand(p.a.ld, !p.ta) && narrow_operand(p.b.ld, p.tb);
-    const Choice c = choose(p.tb, p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore ? kPlain : kStatistics);
+    const Choice c = choice_of(p);
     p.splits = c.splits;
     p.slices = c.splits > 1 ? p.space : nullptr;
     p.row_a = p.row_b = nullptr;

@@ -105,97 +105,130 @@ struct Lines {
     }
 };
 
+// How a product is laid out over workgroups.
+struct Grid {
+    int tiles_m, tiles_n, len, shape;  // k a slice
+    int64_t tiles;
+};
+constexpr int sums_bytes(int mg, int ng) { return kRowsWaves * mg * ng * 4 * 64 * 4; }
+
+// Tile t.
 template <int MG, int NG, bool TA, bool TB, bool SKIP>
-__global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, int tiles_m, int tiles_n, int64_t tiles,
-                                                               int len) {
+__device__ __forceinline__ void rows_tile(const Product &p, const Grid &g, int64_t t, float *memory) {
     constexpr int kQuads = quads_of(MG, NG), kStep = 16 * kQuads;
     using LA = Lines<MG, !TA>;
     using LB = Lines<NG, TB>;
-    __shared__ __align__(16) float sums[kRowsWaves][MG * NG][4][64];
+    auto sums = reinterpret_cast<float(*)[MG * NG][4][64]>(memory);
     const int lane = threadIdx.x & 63, at = lane & 15, group = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-    const int64_t per = static_cast<int64_t>(tiles_m) * tiles_n;
-    for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < tiles; t += gridDim.x) {
-        const int64_t slice = t / per, b = slice / p.splits;
-        int tm, tn;
-        grouped_tile(static_cast<int>(t - slice * per), tiles_m, tiles_n, 8, tm, tn);
-        const int m0 = tm * 16 * MG, n0 = tn * 16 * NG;
-        const int k0 = static_cast<int>(slice - b * p.splits) * len;
-        const int k1 = max(k0, static_cast<int>(min(static_cast<int64_t>(k0) + len, static_cast<int64_t>(p.K))));
-        const LA la(p.a, b, m0, p.M, at);
-        const LB lb(p.b, b, n0, p.N, at);
-        struct Step {
-            f32x4 a[kQuads][MG], b[kQuads][NG];
-        };
-        auto load = [&](int s, auto whole_) {
-            constexpr bool kWhole = decltype(whole_)::value;
-            Step x;
+    const int64_t per = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
+    const int64_t slice = t / per, b = slice / p.splits;
+    int tm, tn;
+    grouped_tile(static_cast<int>(t - slice * per), g.tiles_m, g.tiles_n, 8, tm, tn);
+    const int m0 = tm * 16 * MG, n0 = tn * 16 * NG;
+    const int k0 = static_cast<int>(slice - b * p.splits) * g.len;
+    const int k1 = max(k0, static_cast<int>(min(static_cast<int64_t>(k0) + g.len, static_cast<int64_t>(p.K))));
+    const LA la(p.a, b, m0, p.M, at);
+    const LB lb(p.b, b, n0, p.N, at);
+    struct Step {
+        f32x4 a[kQuads][MG], b[kQuads][NG];
+    };
+    auto load = [&](int s, auto whole_) {
+        constexpr bool kWhole = decltype(whole_)::value;
+        Step x;
 #pragma unroll
-            for (int u = 0; u < kQuads; ++u) {
-                const int k = k0 + s * kStep + 16 * u + 4 * group;
-                lb.template load<kWhole, SKIP>(k, k1, x.b[u], p.target_k, p.ignore);
-                la.template load<kWhole, false>(k, k1, x.a[u], nullptr, 0);
-            }
-            return x;
-        };
-        f32x4 acc[MG][NG];
-#pragma unroll
-        for (int m = 0; m < MG; ++m)
-#pragma unroll
-            for (int c = 0; c < NG; ++c) acc[m][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        auto step = [&](const Step &x) {
-#pragma unroll
-            for (int u = 0; u < kQuads; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int m = 0; m < MG; ++m)
-#pragma unroll
-                        for (int c = 0; c < NG; ++c)
-                            acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.a[u][m][j], x.b[u][c][j], acc[m][c], 0, 0, 0);
-        };
-        constexpr std::true_type all;
-        const int whole = (k1 - k0) / kStep;
-        if (wave < whole) {
-            // loads past the last step repeat it and are not used: what is on its
-            // way is known at every point
-            const int count = (whole - wave + kRowsWaves - 1) / kRowsWaves;
-            // Where rows are a power of two apart, workgroups that all start at
-            // k0 ask the same few memory channels: each starts elsewhere.
-            const int turn = TB && NG == 1 ? static_cast<int>(t % count) : 0;
-            auto turned = [&](int s) {
-                s = min(s, count - 1) + turn;
-                return wave + (s < count ? s : s - count) * kRowsWaves;
-            };
-            Step x = load(turned(0), all), y;
-            int s = 0;
-            for (; s + 1 < count; s += 2) {
-                y = load(turned(s + 1), all);
-                step(x);
-                x = load(turned(s + 2), all);
-                step(y);
-            }
-            if (s < count) step(x);
+        for (int u = 0; u < kQuads; ++u) {
+            const int k = k0 + s * kStep + 16 * u + 4 * group;
+            lb.template load<kWhole, SKIP>(k, k1, x.b[u], p.target_k, p.ignore);
+            la.template load<kWhole, false>(k, k1, x.a[u], nullptr, 0);
         }
-        if (whole * kStep < k1 - k0 && whole % kRowsWaves == wave) step(load(whole, std::false_type{}));
+        return x;
+    };
+    f32x4 acc[MG][NG];
 #pragma unroll
-        for (int m = 0; m < MG; ++m)
+    for (int m = 0; m < MG; ++m)
 #pragma unroll
-            for (int c = 0; c < NG; ++c)
+        for (int c = 0; c < NG; ++c) acc[m][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto step = [&](const Step &x) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sums[wave][m * NG + c][r][lane] = acc[m][c][r];
-        __syncthreads();
-        for (int o = threadIdx.x; o < 256 * MG * NG; o += 64 * kRowsWaves) {
-            const int c = o % (16 * NG), r = o / (16 * NG), q = LA::place(r);
-            const int cell = LA::group(r) * NG + LB::group(c), l = LB::place(c) + 16 * (q / 4);
-            float v = sums[0][cell][q & 3][l];
+        for (int u = 0; u < kQuads; ++u)
 #pragma unroll
-            for (int w = 1; w < kRowsWaves; ++w) v += sums[w][cell][q & 3][l];
-            const int m = LA::row(m0, r, p.M), n = LB::row(n0, c, p.N);
-            store_cell(p, b, slice, m, n, v, m >= 0 && n >= 0);
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int m = 0; m < MG; ++m)
+#pragma unroll
+                    for (int c = 0; c < NG; ++c)
+                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.a[u][m][j], x.b[u][c][j], acc[m][c], 0, 0, 0);
+    };
+    constexpr std::true_type all;
+    const int whole = (k1 - k0) / kStep;
+    if (wave < whole) {
+        // loads past the last step repeat it and are not used: what is on its
+        // way is known at every point
+        const int count = (whole - wave + kRowsWaves - 1) / kRowsWaves;
+        // Where rows are a power of two apart, workgroups that all start at
+        // k0 ask the same few memory channels: each starts elsewhere.
+        const int turn = TB && NG == 1 ? static_cast<int>(t % count) : 0;
+        auto turned = [&](int s) {
+            s = min(s, count - 1) + turn;
+            return wave + (s < count ? s : s - count) * kRowsWaves;
+        };
+        Step x = load(turned(0), all), y;
+        int s = 0;
+        for (; s + 1 < count; s += 2) {
+            y = load(turned(s + 1), all);
+            step(x);
+            x = load(turned(s + 2), all);
+            step(y);
         }
-        __syncthreads();
+        if (s < count) step(x);
     }
+    if (whole * kStep < k1 - k0 && whole % kRowsWaves == wave) step(load(whole, std::false_type{}));
+#pragma unroll
+    for (int m = 0; m < MG; ++m)
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums[wave][m * NG + c][r][lane] = acc[m][c][r];
+    __syncthreads();
+    for (int o = threadIdx.x; o < 256 * MG * NG; o += 64 * kRowsWaves) {
+        const int c = o % (16 * NG), r = o / (16 * NG), q = LA::place(r);
+        const int cell = LA::group(r) * NG + LB::group(c), l = LB::place(c) + 16 * (q / 4);
+        float v = sums[0][cell][q & 3][l];
+#pragma unroll
+        for (int w = 1; w < kRowsWaves; ++w) v += sums[w][cell][q & 3][l];
+        const int m = LA::row(m0, r, p.M), n = LB::row(n0, c, p.N);
+        store_cell(p, b, slice, m, n, v, m >= 0 && n >= 0);
+    }
+    __syncthreads();
+}
+
+template <int MG, int NG, bool TA, bool TB, bool SKIP>
+__global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Product p, Grid g) {
+    __shared__ __align__(16) float memory[sums_bytes(MG, NG) / 4];
+    for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < g.tiles; t += gridDim.x)
+        rows_tile<MG, NG, TA, TB, SKIP>(p, g, t, memory);
+}
+
+// Two small products in one launch, as a gradient has them: neither has to wait
+// for the other, and a launch takes as long as one of them.
+template <bool TA, bool TB, bool SKIP>
+__device__ __forceinline__ void any_shape(const Product &p, const Grid &g, int64_t t, float *memory) {
+    if (g.shape == 16 + 1)
+        rows_tile<1, 1, TA, TB, SKIP>(p, g, t, memory);
+    else if (g.shape == 16 + 2)
+        rows_tile<1, 2, TA, TB, SKIP>(p, g, t, memory);
+    else
+        rows_tile<2, 2, TA, TB, SKIP>(p, g, t, memory);
+}
+template <bool TA1, bool TB1, bool TA2, bool TB2, bool SKIP2>
+__global__ __launch_bounds__(64 * kRowsWaves) void pair_kernel(Product p, Grid g, Product q, Grid h) {
+    __shared__ __align__(16) float memory[sums_bytes(2, 2) / 4];
+    const int first = static_cast<int>(g.tiles), t = static_cast<int>(blockIdx.x);
+    if (t < first)
+        any_shape<TA1, TB1, false>(p, g, xcd_remap(t, first), memory);
+    else
+        any_shape<TA2, TB2, SKIP2>(q, h, xcd_remap(t - first, static_cast<int>(h.tiles)), memory);
 }
 
 // B stored N x K, MR (1, 2 or 4) rows of op(A): a wavefront holds 4 columns,
@@ -312,13 +345,21 @@ hipError_t launch_vector(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+Grid grid_of(const Product &p, int shape) {
+    const int mg = shape >> 4, ng = shape & 15;
+    Grid g{};
+    g.tiles_m = static_cast<int>(div_up(p.M, 16 * mg)), g.tiles_n = static_cast<int>(div_up(p.N, 16 * ng));
+    g.tiles = p.batch * p.splits * g.tiles_m * g.tiles_n;
+    g.len = static_cast<int>(div_up(div_up(p.K, 64), p.splits)) * 64;
+    g.shape = shape;
+    return g;
+}
+
 template <int MG, int NG, bool TA, bool TB, bool SKIP = false>
 hipError_t launch(const Product &p, hipStream_t stream) {
-    const int tm = static_cast<int>(div_up(p.M, 16 * MG)), tn = static_cast<int>(div_up(p.N, 16 * NG));
-    const int64_t tiles = p.batch * p.splits * tm * tn;
-    const int len = static_cast<int>(div_up(div_up(p.K, 64), p.splits)) * 64;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 20));
-    rows_kernel<MG, NG, TA, TB, SKIP><<<grid, 64 * kRowsWaves, 0, stream>>>(p, tm, tn, tiles, len);
+    const Grid g = grid_of(p, 16 * MG + NG);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(g.tiles, 1 << 20));
+    rows_kernel<MG, NG, TA, TB, SKIP><<<grid, 64 * kRowsWaves, 0, stream>>>(p, g);
     return hipGetLastError();
 }
 
@@ -346,6 +387,29 @@ hipError_t launch_rows(const Product &p, int shape, hipStream_t stream) {
         case 64 + 2: return launch_form<4, 2>(p, stream);
         default: return hipErrorInvalidConfiguration;
     }
+}
+
+bool launch_rows_pair(const Product &p, int shape_p, const Product &q, int shape_q, hipStream_t stream, hipError_t *err) {
+    auto taken = [](int shape) { return shape == 16 + 1 || shape == 16 + 2 || shape == 32 + 2; };
+    if (!taken(shape_p) || !taken(shape_q) || p.splits > 1 || q.splits > 1 || p.target_k != nullptr) return false;
+    const Grid g = grid_of(p, shape_p), h = grid_of(q, shape_q);
+    if (g.tiles + h.tiles > 1 << 20) return false;
+    const unsigned grid = static_cast<unsigned>(g.tiles + h.tiles), threads = 64 * kRowsWaves;
+    const int form = p.ta * 8 + p.tb * 4 + q.ta * 2 + q.tb;
+    if (q.target_k != nullptr) {
+        if (form != 2) return false;
+        pair_kernel<false, false, true, false, true><<<grid, threads, 0, stream>>>(p, g, q, h);
+    } else {
+        switch (form) {  // of gemm_f32_fused_grad's two products, by opA and opB
+            case 4 + 2: pair_kernel<false, true, true, false, false><<<grid, threads, 0, stream>>>(p, g, q, h); break;
+            case 2: pair_kernel<false, false, true, false, false><<<grid, threads, 0, stream>>>(p, g, q, h); break;
+            case 4: pair_kernel<false, true, false, false, false><<<grid, threads, 0, stream>>>(p, g, q, h); break;
+            case 8 + 4 + 2 + 1: pair_kernel<true, true, true, true, false><<<grid, threads, 0, stream>>>(p, g, q, h); break;
+            default: return false;
+        }
+    }
+    *err = hipGetLastError();
+    return true;
 }
 
 }  // namespace fused
