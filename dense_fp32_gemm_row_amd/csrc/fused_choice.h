@@ -32,21 +32,22 @@ struct Choice {
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// What a kernel's tile takes, in nanoseconds: `lone` a k where a CU has one of them,
-// `shared` a k of each where it has more, `fixed` besides.  Fitted to 7000 times of 210
-// products of 33 to 8192 rows (three operand forms, 70 sizes drawn evenly over their
-// logarithms): the choice is 3.7% off the best of all kernels and slices on average.
+// What a kernel's tile takes, in nanoseconds: `lone` a k and `fixed` besides where a
+// CU has one of them, `shared` a k and `each` besides of every one where it has more.
+// Fitted to 5600 times of 270 products of 33 to 8192 rows (three operand forms, 90 sizes
+// drawn evenly over their logarithms): the choice is 2.3% off the best of all
+// kernels and slices on average.
 struct Rate {
     Choice kind;
     int m, n;
-    double lone, shared, fixed;
+    double lone, fixed, shared, each;
 };
 constexpr Rate kRates[] = {
-    {{kRows, 1, false, 17}, 16, 16, 2.86, 2.70, 751.0},   {{kRows, 1, false, 18}, 16, 32, 4.31, 3.98, 1173.0},
-    {{kRows, 1, false, 34}, 32, 32, 6.68, 6.70, 1972.0},  {{kRows, 1, false, 36}, 32, 64, 11.1, 11.5, 2619.0},
-    {{kRows, 1, false, 66}, 64, 32, 11.0, 11.2, 2906.0},  {{2, 1, false, 0}, 64, 128, 29.4, 21.7, 3683.0},
-    {{1, 1, false, 0}, 128, 128, 35.7, 33.3, 7180.0},     {{1, 1, true, 0}, 128, 128, 26.5, 23.7, 8832.0},
-    {{0, 1, false, 0}, 256, 256, 102.5, 122.3, 26048.0},  {{0, 1, true, 0}, 256, 256, 53.2, 71.9, 32737.0},
+    {{kRows, 1, false, 17}, 16, 16, 2.6, 884, 2.8, 670},     {{kRows, 1, false, 18}, 16, 32, 4.2, 1040, 4.1, 1079},
+    {{kRows, 1, false, 34}, 32, 32, 6.6, 2167, 6.9, 1765},   {{kRows, 1, false, 36}, 32, 64, 11.5, 2310, 11.5, 2447},
+    {{kRows, 1, false, 66}, 64, 32, 11.5, 2221, 11.3, 2868}, {{2, 1, false, 0}, 64, 128, 29.2, 5210, 23.3, 3423},
+    {{1, 1, false, 0}, 128, 128, 33.0, 9106, 36.0, 5713},    {{1, 1, true, 0}, 128, 128, 31.4, 2473, 26.8, 4970},
+    {{0, 1, false, 0}, 256, 256, 96.6, 33397, 129.1, 25567}, {{0, 1, true, 0}, 256, 256, 50.8, 29554, 73.5, 30865},
 };
 constexpr double kCus = 256;
 constexpr double kBytesNs = 5500;                           // memory, reading
@@ -57,7 +58,7 @@ inline double predicted(const Rate &r, int64_t batch, int64_t M, int64_t N, int6
     const double tiles = static_cast<double>(batch) * div_up(M, r.m) * div_up(N, r.n) * splits / kCus;
     const double k = static_cast<double>(div_up(K, splits)), alone = r.lone * k + r.fixed;
     const double turns = tiles <= 6 ? static_cast<double>(static_cast<int64_t>(tiles + 0.999999)) : tiles + 0.5;
-    double t = tiles > 1 ? std::max(alone, turns * (r.shared * k + r.fixed)) : alone;
+    double t = tiles > 1 ? std::max(alone, turns * (r.shared * k + r.each)) : alone;
     const double mk = static_cast<double>(M) * K, nk = static_cast<double>(N) * K, mn = static_cast<double>(M) * N;
     t = std::max(t, 4 * batch * (mk + nk + mn) / kBytesNs);
     if (splits > 1) t += kSumNs + 4 * batch * (splits + 1) * mn / kSumBytesNs;
@@ -74,12 +75,13 @@ inline Choice choose(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bo
     const bool slice = space && use == kPlain;
     // Few rows: reading B is the work, in tiles as wide as leaves enough of them (as
     // stored, a lane reads 2 neighbours): 16 x 14336 x 4096, B transposed, 47 us with 64
-    // columns and 65 with 16, 16 x 4096 x 4096 43 and 18.
+    // columns and 65 with 16, 16 x 4096 x 4096 43 and 18; 5 x 1792 x 78080, B as stored,
+    // 119 us with 32 columns in 4 slices of K, 314 with 16 in one.
     if (M <= kRowsMost && (tb || N >= 2)) {
-        const int c = tb ? (N >= 8192 && M > 4 ? 4 : 1) : N >= 2048 ? 2 : 1;
+        const int c = tb ? (N >= 8192 && M > 4 ? 4 : 1) : N >= 1024 ? 2 : 1;
         const int shape = tb && M <= 4 ? 0 : (M <= 16 ? 16 : 32) + c;
-        const int64_t tiles = batch * div_up(N, 16 * c);
-        const int64_t splits = std::min<int64_t>(kMostSplits, std::max<int64_t>(1, std::min(256 / tiles, K / 1024)));
+        const int64_t tiles = batch * div_up(N, 16 * c), most = (tb ? 256 : 512) / tiles;
+        const int64_t splits = std::min<int64_t>(kMostSplits, std::max<int64_t>(1, std::min(most, K / 1024)));
         return {kRows, slice ? static_cast<int>(splits) : 1, false, shape};
     }
     Choice best{};
