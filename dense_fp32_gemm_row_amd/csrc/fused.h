@@ -130,6 +130,7 @@ struct Loss {
     float *loss, *lse;          // loss may be null
     const float *grad_loss;     // null: ones
     float *logits;              // launch_probabilities: T x V, in place
+    int64_t ld;
     int *row_top, *column_top;  // null, or T and V: set to zero by launch_loss, to the largest |value|'s bits
 };
 hipError_t launch_loss(const Loss &, hipStream_t);

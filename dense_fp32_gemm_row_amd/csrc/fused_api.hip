@@ -118,12 +118,15 @@ int groups_of(int64_t T, int64_t V) { return static_cast<int>(div_up(V, fused::g
 int64_t stats_bytes(int64_t T, int64_t V) {  // logit at the target, lse, statistics
     return plus(times(times(8, T), groups_of(T, V)), times(8, T));
 }
+// Logits are held in whole lines, from a line's start where the workspace begins at one.
+int64_t line(int64_t floats) { return div_up(floats, 32) * 32; }
 // The gradient works on at most `rows` tokens at a time, whose logits it holds.  (A
 // last piece of few tokens has statistics of more groups.)
 int64_t piece_bytes(int64_t rows, int64_t V) {
     if (rows == 0) return 0;
     const int64_t few = std::min<int64_t>(rows, fused::kFineTokens);
-    return plus(times(times(4, rows), V) + 4 * (rows + V), std::max(stats_bytes(rows, V), stats_bytes(few, V)));
+    return plus(times(times(4, rows), line(V)) + 4 * (rows + V + 32),
+                std::max(stats_bytes(rows, V), stats_bytes(few, V)));
 }
 int64_t piece_space(int64_t rows, int64_t V, int64_t K) {
     return std::max({space_of(true, 1, rows, V, K, true), space_of(false, 1, rows, K, V), space_of(false, 1, V, K, rows)});
@@ -132,7 +135,7 @@ constexpr int64_t kPieceBytes = int64_t{4} << 30;
 constexpr int64_t kPieceRows = 256;
 int64_t piece_rows(int64_t T, int64_t V) {
     if (T <= kPieceRows) return T;
-    int64_t rows = kPieceBytes / std::max<int64_t>(1, times(4, V)) / kPieceRows * kPieceRows;
+    int64_t rows = kPieceBytes / std::max<int64_t>(1, times(4, line(V))) / kPieceRows * kPieceRows;
     rows = std::max(rows, kPieceRows);
     if (rows >= T) return T;
     // pieces of about the same size, whole tiles
@@ -351,14 +354,15 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
         for (int64_t t0 = 0; t0 < T && err == hipSuccess; t0 += rows) {
             const int64_t n = std::min(rows, T - t0);
             int *row_top = reinterpret_cast<int *>(at) + 2 * n + 2 * n * groups_of(n, V), *column_top = row_top + n;
-            float *logits = reinterpret_cast<float *>(column_top + V);
+            float *logits = at + line(reinterpret_cast<float *>(column_top + V) - at);
+            const int64_t ldl = line(V);
             float *space = sliced && bytes > piece_bytes(best, V) ? at + piece_bytes(best, V) / 4 : nullptr;
             // (the last piece may be shorter, and ask for more)
             auto room = [&](bool tb, int64_t M, int64_t N, int64_t k, bool statistics = false) {
                 return space != nullptr && space_of(tb, 1, M, N, k, statistics) <= full - piece_bytes(best, V) ? space : nullptr;
             };
             const float *Xt = X + t0 * ldx;
-            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, V, 0}, room(true, n, V, K, true));
+            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, ldl, 0}, room(true, n, V, K, true));
             p.mode = fused::kStoreStats;
             p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * n), p.groups = groups_of(n, V);
             p.target = target + t0, p.ignore = ignore_index;
@@ -367,16 +371,16 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             l.T = p.M, l.V = p.N, l.stats = p.stats, l.groups = p.groups, l.at_target = p.at_target;
             l.target = p.target, l.ignore = ignore_index;
             l.loss = loss != nullptr ? loss + t0 : nullptr, l.lse = lse != nullptr ? lse + t0 : at + n;
-            l.grad_loss = grad_loss != nullptr ? grad_loss + t0 : nullptr, l.logits = logits;
+            l.grad_loss = grad_loss != nullptr ? grad_loss + t0 : nullptr, l.logits = logits, l.ld = ldl;
             l.row_top = dX != nullptr ? row_top : nullptr, l.column_top = dW != nullptr ? column_top : nullptr;
             if (dX == nullptr && dW == nullptr) {
                 if (err == hipSuccess) err = fused::launch_loss(l, s);
                 continue;
             }
-            fused::Product px = plain_product(1, n, K, V, false, {logits, V, 0}, false, {W, ldw, 0},
+            fused::Product px = plain_product(1, n, K, V, false, {logits, ldl, 0}, false, {W, ldw, 0},
                                               {dX != nullptr ? dX + t0 * lddx : nullptr, lddx, 0}, room(false, n, K, V));
             px.top_a = row_top;
-            fused::Product pw = plain_product(1, V, K, n, true, {logits, V, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0},
+            fused::Product pw = plain_product(1, V, K, n, true, {logits, ldl, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0},
                                               room(false, V, K, n));
             pw.top_a = column_top;
             pw.target_k = target + t0, pw.ignore = ignore_index;

@@ -153,7 +153,7 @@ __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
         if constexpr (GRAD) {
             const float lse = tops[0], g = l.grad_loss != nullptr ? l.grad_loss[t] : 1.0f;
             const int64_t target = l.target[t];
-            float *row = l.logits + t * l.V;
+            float *row = l.logits + t * l.ld;
 #pragma unroll 4
             for (int64_t v = threadIdx.x; v < l.V; v += 256) row[v] = gradient(l, row[v], lse, g, v, target);
             __syncthreads();
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t stri
         for (int64_t t0 = first; t0 < last; t0 += kAtOnce) {
             f32x4 x[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) x[i] = read4(l.logits + min(t0 + i, last - 1) * l.V + v, left);
+            for (int i = 0; i < kAtOnce; ++i) x[i] = read4(l.logits + min(t0 + i, last - 1) * l.ld + v, left);
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
                 const int64_t t = t0 + i;
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t stri
                     const int bits = e < left ? __builtin_bit_cast(int, p) & 0x7fffffff : 0;
                     column[e] = max(column[e], bits), row = max(row, bits);
                 }
-                write4(l.logits + t * l.V + v, left, x[i]);
+                write4(l.logits + t * l.ld + v, left, x[i]);
                 if (l.row_top != nullptr) {
                     row = max(row, moved<0xb1>(row)), row = max(row, moved<0x4e>(row));
                     row = max(row, moved<0x124>(row)), row = max(row, moved<0x128>(row));
