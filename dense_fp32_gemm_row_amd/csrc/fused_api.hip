@@ -372,7 +372,6 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             l.target = p.target, l.ignore = ignore_index;
             l.loss = loss != nullptr ? loss + t0 : nullptr, l.lse = lse != nullptr ? lse + t0 : at + n;
             l.grad_loss = grad_loss != nullptr ? grad_loss + t0 : nullptr, l.logits = logits, l.ld = ldl;
-            l.row_top = dX != nullptr ? row_top : nullptr, l.column_top = dW != nullptr ? column_top : nullptr;
             if (dX == nullptr && dW == nullptr) {
                 if (err == hipSuccess) err = fused::launch_loss(l, s);
                 continue;
@@ -385,9 +384,10 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             pw.top_a = column_top;
             pw.target_k = target + t0, pw.ignore = ignore_index;
             if (t0 > 0) pw.e.residual = {dW, lddw, 0};  // the pieces before
-            // small: no fp16 parts, which want the largest magnitudes
-            if (n * V <= 1 << 18 && !fused::wants_parts(px) && !fused::wants_parts(pw)) {
-                l.row_top = l.column_top = nullptr;
+            // the largest magnitudes, for fp16 parts
+            l.row_top = dX != nullptr && fused::wants_parts(px) ? row_top : nullptr;
+            l.column_top = dW != nullptr && fused::wants_parts(pw) ? column_top : nullptr;
+            if (n * V <= 1 << 18 && l.row_top == nullptr && l.column_top == nullptr) {
                 if (err == hipSuccess) err = fused::launch_loss_and_probabilities(l, s);
             } else {
                 if (err == hipSuccess) err = fused::launch_loss(l, s);
