@@ -33,7 +33,7 @@ COMMON_FLAGS = [
 SOURCES = ["mfma.hip", "mfma16.hip", "mfma_regs.hip", "api.hip", "naive.hip", "lds_tiled.hip", "regblock.hip",
            "mxfp4_api.hip", "mxfp4_convert.hip", "mxfp4_product.hip", "mxfp4_weight.hip",
            "fused_api.hip", "fused_nn.hip", "fused_nt.hip", "fused_tn.hip", "fused_tt.hip",
-           "fused_rows.hip", "fused_parts.hip"]
+           "fused_pair.hip", "fused_rows.hip", "fused_parts.hip"]
 
 
 def _compile(src: str, extra: list[str]) -> str:

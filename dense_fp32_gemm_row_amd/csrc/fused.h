@@ -79,11 +79,17 @@ struct Product {
 hipError_t launch_product(const Product &, hipStream_t);
 // Whether its large tiles may take fp16 parts.
 bool wants_parts(const Product &);
-// Two independent products that share their workspace.
-hipError_t launch_two(const Product &, const Product &, hipStream_t);
+// Two independent products; they share their workspace, of `bytes`.
+hipError_t launch_two(const Product &, const Product &, int64_t bytes, hipStream_t);
 // Bytes of workspace that a product is quickest with; it runs with none, too.
 // `statistics`: its mode is not kStore.
 int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics);
+// The same of launch_two's.
+struct Sizes {
+    bool ta, tb;
+    int64_t batch, M, N, K;
+};
+int64_t two_space(const Sizes &, const Sizes &);
 
 // The tile kernels, by operand form (fused_nn.hip ...); `tile` as in
 // fused_choice.h.
@@ -91,6 +97,9 @@ hipError_t launch_tile_nn(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_nt(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tn(const Product &, int tile, hipStream_t);
 hipError_t launch_tile_tt(const Product &, int tile, hipStream_t);
+
+// Both in one launch, in tiles of kTiles[1] or [2], p N x N or N x T and q T x N: whether they were.
+bool launch_tile_pair(const Product &p, const Product &q, int tile, hipStream_t, hipError_t *err);
 
 // `shape` as in fused_choice.h.
 hipError_t launch_rows(const Product &, int shape, hipStream_t);
@@ -103,6 +112,7 @@ hipError_t launch_row_stats(const Product &, hipStream_t);
 
 // C = epilogue(sum over the slices, in their order).
 hipError_t launch_sum_slices(const Product &, hipStream_t);
+hipError_t launch_sum_slices(const Product &, const Product &, hipStream_t);
 
 // dZ = dC act'(Z), and the sums of its columns over blocks of rows; either may
 // be absent (dz.p null; partial null).

@@ -59,10 +59,16 @@ int check_workspace(void *workspace, int64_t bytes, int64_t need, Bytes *out) {
     return GEMM_F32_OK;
 }
 
-// Bytes of a product's own workspace.
+// Bytes of a product's own workspace, and of two.
 int64_t space_of(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics = false) {
     if (batch == 0 || M == 0 || N == 0 || K == 0) return 0;
     return fused::product_space(tb, batch, M, N, K, statistics);
+}
+
+int64_t space_of(const fused::Sizes &p, const fused::Sizes &q) {
+    auto one = [](const fused::Sizes &x) { return space_of(x.tb, x.batch, x.M, x.N, x.K); };
+    auto empty = [](const fused::Sizes &x) { return x.batch == 0 || x.M == 0 || x.N == 0 || x.K == 0; };
+    return empty(p) || empty(q) ? std::max(one(p), one(q)) : fused::two_space(p, q);
 }
 
 fused::Product plain_product(int64_t batch, int64_t M, int64_t N, int64_t K, bool ta, fused::Operand a, bool tb,
@@ -83,9 +89,9 @@ hipError_t run(const fused::Product &p, hipStream_t s) {
     return fused::launch_product(p, s);
 }
 
-hipError_t run(const fused::Product &p, const fused::Product &q, hipStream_t s) {
+hipError_t run(const fused::Product &p, const fused::Product &q, int64_t bytes, hipStream_t s) {
     auto empty = [](const fused::Product &x) { return x.batch == 0 || x.M == 0 || x.N == 0; };
-    if (!empty(p) && !empty(q)) return fused::launch_two(p, q, s);
+    if (!empty(p) && !empty(q)) return fused::launch_two(p, q, bytes, s);
     return empty(p) ? run(q, s) : run(p, s);
 }
 
@@ -107,9 +113,10 @@ GradParts grad_parts(bool ta, bool tb, int64_t batch, int64_t M, int64_t N, int6
     g.blocks = static_cast<int>(div_up(M, g.rows));
     if (activation != GEMM_F32_ACT_NONE && (dA || dB)) g.dz = times(times(batch, M), N);
     if (dbias && g.blocks > 1) g.partial = times(times(batch, g.blocks), N);
-    // (the sizes of the products as they are run)
-    if (dA) g.space = (ta ? space_of(true, batch, K, M, N) : space_of(!tb, batch, M, K, N)) / 4;
-    if (dB) g.space = std::max(g.space, (tb ? space_of(ta, batch, N, K, M) : space_of(false, batch, K, N, M)) / 4);
+    // the products as they are run
+    const fused::Sizes none{}, a = ta ? fused::Sizes{tb, true, batch, K, M, N} : fused::Sizes{false, !tb, batch, M, K, N};
+    const fused::Sizes b = tb ? fused::Sizes{true, ta, batch, N, K, M} : fused::Sizes{!ta, false, batch, K, N, M};
+    g.space = space_of(dA ? a : none, dB ? b : none) / 4;
     return g;
 }
 
@@ -129,7 +136,8 @@ int64_t piece_bytes(int64_t rows, int64_t V) {
                 std::max(stats_bytes(rows, V), stats_bytes(few, V)));
 }
 int64_t piece_space(int64_t rows, int64_t V, int64_t K) {
-    return std::max({space_of(true, 1, rows, V, K, true), space_of(false, 1, rows, K, V), space_of(false, 1, V, K, rows)});
+    return std::max(space_of(true, 1, rows, V, K, true),
+                    space_of(fused::Sizes{false, false, 1, rows, K, V}, fused::Sizes{true, false, 1, V, K, rows}));
 }
 constexpr int64_t kPieceBytes = int64_t{4} << 30;
 constexpr int64_t kPieceRows = 256;
@@ -276,7 +284,7 @@ int gemm_f32_fused_grad(int opA, int opB, int64_t batch, int64_t M, int64_t N, i
         // dB = op(A)^T dZ, or its transpose dZ^T op(A)
         const fused::Product pb = tb ? plain_product(batch, N, K, M, true, grad, ta, oa, rb, space)
                                      : plain_product(batch, K, N, M, !ta, oa, false, grad, rb, space);
-        if (err == hipSuccess) err = want_a && want_b ? run(pa, pb, q) : want_a ? run(pa, q) : want_b ? run(pb, q) : err;
+        if (err == hipSuccess) err = want_a && want_b ? run(pa, pb, 4 * parts.space, q) : want_a ? run(pa, q) : want_b ? run(pb, q) : err;
         return err;
     });
 }
@@ -394,7 +402,7 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
                 if (err == hipSuccess) err = fused::launch_probabilities(l, s);
             }
             if (err == hipSuccess)
-                err = dX != nullptr && dW != nullptr ? run(px, pw, s) : dX != nullptr ? run(px, s) : run(pw, s);
+                err = dX != nullptr && dW != nullptr ? run(px, pw, px.space != nullptr ? full - piece_bytes(best, V) : 0, s) : dX != nullptr ? run(px, s) : run(pw, s);
         }
         return err;
     });

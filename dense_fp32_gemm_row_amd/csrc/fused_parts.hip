@@ -9,9 +9,9 @@ namespace fused {
 namespace {
 
 // C = epilogue(sum of slices), an element a thread, slices in order.
-__global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t elements) {
+__device__ __forceinline__ void sum_slices(const Product &p, int64_t first, int64_t step) {
     const int64_t per = static_cast<int64_t>(p.M) * p.N;
-    for (int64_t o = blockIdx.x * int64_t{256} + threadIdx.x; o < elements; o += gridDim.x * int64_t{256}) {
+    for (int64_t o = first; o < p.batch * per; o += step) {
         const int64_t b = o / per, q = o - b * per, m = q / p.N, n = q - m * p.N;
         const float *W = p.slices + b * p.splits * per + q;
         float z = W[0];
@@ -22,6 +22,16 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(Product p, int64_t elem
         if (p.e.residual.p != nullptr) v += p.e.residual.p[b * p.e.residual.stride + m * p.e.residual.ld + n];
         p.c.p[b * p.c.stride + m * p.c.ld + n] = v;
     }
+}
+__global__ __launch_bounds__(256) void sum_slices_kernel(Product p) {
+    sum_slices(p, blockIdx.x * int64_t{256} + threadIdx.x, gridDim.x * int64_t{256});
+}
+// Workgroups 0 .. first - 1 take p.
+__global__ __launch_bounds__(256) void sum_two_kernel(Product p, Product q, unsigned first) {
+    if (blockIdx.x < first)
+        sum_slices(p, blockIdx.x * int64_t{256} + threadIdx.x, first * int64_t{256});
+    else
+        sum_slices(q, (blockIdx.x - first) * int64_t{256} + threadIdx.x, (gridDim.x - first) * int64_t{256});
 }
 
 // 4 neighbours of a row, of which `left` are inside it.
@@ -282,8 +292,13 @@ unsigned blocks_for(int64_t n) { return static_cast<unsigned>(std::min<int64_t>(
 }  // namespace
 
 hipError_t launch_sum_slices(const Product &p, hipStream_t stream) {
-    const int64_t n = p.batch * p.M * p.N;
-    sum_slices_kernel<<<blocks_for(div_up(n, 256)), 256, 0, stream>>>(p, n);
+    sum_slices_kernel<<<blocks_for(div_up(p.batch * p.M * p.N, 256)), 256, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_sum_slices(const Product &p, const Product &q, hipStream_t stream) {
+    const unsigned first = blocks_for(div_up(p.batch * p.M * p.N, 256));
+    sum_two_kernel<<<first + blocks_for(div_up(q.batch * q.M * q.N, 256)), 256, 0, stream>>>(p, q, first);
     return hipGetLastError();
 }
 
@@ -357,32 +372,62 @@ hipError_t launch_row_stats(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics) {
-    const Choice c = choose(tb, batch, M, N, K, true, statistics ? kStatistics : kPlain);
-    const __int128 slices = c.splits > 1 ? static_cast<__int128>(4 * c.splits) * batch * M * N : 0;
+namespace {
+bool narrow(const Product &p) { return narrow_operand(p.a.ld, !p.ta) && narrow_operand(p.b.ld, p.tb); }
+// (at most 2^61)
+int64_t slices_bytes(const Choice &c, int64_t batch, int64_t M, int64_t N) {
+    const __int128 n = c.splits > 1 ? static_cast<__int128>(4 * c.splits) * batch * M * N : 0;
+    return static_cast<int64_t>(std::min<__int128>(n, __int128{1} << 61));
+}
+// Whether two products go into one launch of tiles.
+bool paired(const Choice &c, const Choice &d, bool ta, bool tc, bool td) {
+    return c.tile == d.tile && (c.tile == 1 || c.tile == 2) && !c.half && !d.half && !ta && tc && !td;
+}
+}  // namespace
+
+namespace {
+int64_t choice_space(const Choice &c, int64_t batch, int64_t M, int64_t N, int64_t K) {
     // either form of either operand
     const __int128 stats = c.half ? static_cast<__int128>(sizeof(RowStat)) * batch *
                                         (std::max(stat_blocks(M, K, true), stat_blocks(M, K, false)) * M +
                                          std::max(stat_blocks(N, K, true), stat_blocks(N, K, false)) * N)
                                   : 0;
-    return static_cast<int64_t>(std::min<__int128>(slices + stats, __int128{1} << 61));
+    return static_cast<int64_t>(std::min<__int128>(slices_bytes(c, batch, M, N) + stats, __int128{1} << 61));
 }
-
-namespace {
 Choice choice_of(const Product &p) {
     return choose(p.tb, p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore ? kPlain : kStatistics);
 }
 }  // namespace
 
+int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics) {
+    return choice_space(choose(tb, batch, M, N, K, true, statistics ? kStatistics : kPlain), batch, M, N, K);
+}
+
+int64_t two_space(const Sizes &p, const Sizes &q) {
+    const Choice c = choose(p.tb, p.batch, p.M, p.N, p.K, true, kPlain), d = choose(q.tb, q.batch, q.M, q.N, q.K, true, kPlain);
+    const int64_t m = choice_space(c, p.batch, p.M, p.N, p.K), n = choice_space(d, q.batch, q.M, q.N, q.K);
+    return paired(c, d, p.ta, q.ta, q.tb) ? std::min(m + n, int64_t{1} << 61) : std::max(m, n);
+}
+
 bool wants_parts(const Product &p) { return choice_of(p).half; }
 
-hipError_t launch_two(const Product &p, const Product &q, hipStream_t stream) {
+hipError_t launch_two(const Product &p, const Product &q, int64_t bytes, hipStream_t stream) {
     const Choice c = choice_of(p), d = choice_of(q);
     hipError_t err = hipSuccess;
-    if (c.tile == kRows && d.tile == kRows && c.splits == 1 && d.splits == 1) {
-        Product a = p, b = q;
-        a.splits = b.splits = 1;
-        if (launch_rows_pair(a, c.shape, b, d.shape, stream, &err)) return err;
+    Product a = p, b = q;
+    a.splits = c.splits, b.splits = d.splits;
+    if (c.tile == kRows && d.tile == kRows && c.splits == 1 && d.splits == 1 &&
+        launch_rows_pair(a, c.shape, b, d.shape, stream, &err))
+        return err;
+    const int64_t own = slices_bytes(c, p.batch, p.M, p.N);
+    if (paired(c, d, p.ta, q.ta, q.tb) && own + slices_bytes(d, q.batch, q.M, q.N) <= bytes) {
+        a.narrow = narrow(p), b.narrow = narrow(q);
+        a.slices = c.splits > 1 ? p.space : nullptr, b.slices = d.splits > 1 ? q.space + own / 4 : nullptr;
+        if (launch_tile_pair(a, b, c.tile, stream, &err)) {
+            if (err != hipSuccess || (c.splits == 1 && d.splits == 1)) return err;
+            if (c.splits > 1 && d.splits > 1) return launch_sum_slices(a, b, stream);
+            return launch_sum_slices(c.splits > 1 ? a : b, stream);
+        }
     }
     err = launch_product(p, stream);
     return err == hipSuccess ? launch_product(q, stream) : err;
@@ -390,7 +435,7 @@ hipError_t launch_two(const Product &p, const Product &q, hipStream_t stream) {
 
 hipError_t launch_product(const Product &asked, hipStream_t stream) {
     Product p = asked;
-    p.narrow = narrow_operand(p.a.ld, !p.ta) && narrow_operand(p.b.ld, p.tb);
+    p.narrow = narrow(p);
     const Choice c = choice_of(p);
     p.splits = c.splits;
     p.slices = c.splits > 1 ? p.space : nullptr;

@@ -159,29 +159,44 @@ __device__ __forceinline__ void turns(int stages, F stage) {
 // Tiles of a CU, for the registers that a wavefront may take.
 constexpr int per_cu(int fm) { return fm == 4 ? 1 : fm == 2 ? 2 : 3; }
 
-template <int WM, int WN, int FM, bool TA, bool TB>
-__global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product p, int tiles_m, int tiles_n,
-                                                                        int64_t first_tile, int len) {
+// What a tile of a workgroup takes of LDS.
+template <int WM, int WN, int FM>
+struct Room {
     using T = Tile<WM, WN, FM>;
-    constexpr int BM = T::BM, BN = T::BN, kThreads = T::kThreads;
-    constexpr bool kHalf = FM > 1;  // the tiles with a loop for fp16 parts
-    constexpr int kA = plane(BM, kStage), kB = plane(BN, kStage);                        // of 16 k
-    constexpr int kLongA = plane(BM, 2 * kStage), kLongB = plane(BN, 2 * kStage);        // of 32 k
-    constexpr int kPlanesA = 3 * 2 * kA, kBuffer = kPlanesA + 3 * 2 * kB;
-    constexpr int kHalfA = 2 * 4 * kLongA, kHalfBuffer = kHalfA + 2 * 4 * kLongB;
-    constexpr int kMemory = 2 * (FM == 4 ? kHalfBuffer : kBuffer);
-    constexpr int kRowOut = 68;  // floats: 64 of a row of results, 16 bytes apart from the next one's banks
+    static constexpr int BM = T::BM, BN = T::BN;
+    static constexpr bool kHalf = FM > 1;  // the tiles with a loop for fp16 parts
+    static constexpr int kA = plane(BM, kStage), kB = plane(BN, kStage);                      // of 16 k
+    static constexpr int kLongA = plane(BM, 2 * kStage), kLongB = plane(BN, 2 * kStage);      // of 32 k
+    static constexpr int kPlanesA = 3 * 2 * kA, kBuffer = kPlanesA + 3 * 2 * kB;
+    static constexpr int kHalfA = 2 * 4 * kLongA, kHalfBuffer = kHalfA + 2 * 4 * kLongB;
+    static constexpr int kRowOut = 68;  // floats: 64 of a row of results, 16 bytes apart from the next one's banks
     static_assert(kBuffer >= (BM + BN) * kStage * 4, "");
     static_assert(2 * kBuffer >= T::kWaves * 32 * kRowOut * 4, "");
-    __shared__ __align__(1024) char memory[kMemory];
-    __shared__ int exponents[kHalf ? BM + BN : 1];
-    __shared__ float worst[kHalf ? 2 * T::kWaves : 1];
+    alignas(128) char memory[2 * (FM == 4 ? kHalfBuffer : kBuffer)];
+    int exponents[kHalf ? BM + BN : 1];
+    float worst[kHalf ? 2 * T::kWaves : 1];
+};
+
+// Tile `id` of p's slices' tiles, `len` k a slice.
+template <int WM, int WN, int FM, bool TA, bool TB>
+__device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tiles_n, int64_t id, int len,
+                                         Room<WM, WN, FM> &room) {
+    using T = Tile<WM, WN, FM>;
+    using R = Room<WM, WN, FM>;
+    constexpr int BM = T::BM, BN = T::BN, kThreads = T::kThreads;
+    constexpr bool kHalf = R::kHalf;
+    constexpr int kA = R::kA, kB = R::kB, kLongA = R::kLongA, kLongB = R::kLongB;
+    constexpr int kPlanesA = R::kPlanesA, kBuffer = R::kBuffer, kHalfA = R::kHalfA, kHalfBuffer = R::kHalfBuffer;
+    constexpr int kRowOut = R::kRowOut;
+    char(&memory)[sizeof(room.memory)] = room.memory;
+    auto &exponents = room.exponents;
+    auto &worst = room.worst;
     auto &xs = *reinterpret_cast<float(*)[kStage][BM]>(memory);
     auto &ys = *reinterpret_cast<float(*)[kStage][BN]>(memory + BM * kStage * 4);
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
-    const int64_t per = static_cast<int64_t>(tiles_m) * tiles_n, id = first_tile + xcd_remap(blockIdx.x, gridDim.x);
+    const int64_t per = static_cast<int64_t>(tiles_m) * tiles_n;
     const int64_t slice = id / per, b = slice / p.splits;
     int tm, tn;
     grouped_tile(static_cast<int>(id - slice * per), tiles_m, tiles_n, 8, tm, tn);
@@ -732,15 +747,32 @@ __global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product 
 }
 
 template <int WM, int WN, int FM, bool TA, bool TB>
-hipError_t launch_one(const Product &p, hipStream_t stream) {
+__global__ __launch_bounds__(64 * WM * WN, per_cu(FM)) void tile_kernel(Product p, int tiles_m, int tiles_n,
+                                                                        int64_t first_tile, int len) {
+    __shared__ Room<WM, WN, FM> room;
+    one_tile<WM, WN, FM, TA, TB>(p, tiles_m, tiles_n, first_tile + xcd_remap(blockIdx.x, gridDim.x), len, room);
+}
+
+// Tiles of a product, and whole stages a slice.
+struct TileGrid {
+    int tiles_m, tiles_n, len;
+    int64_t tiles;
+};
+template <int WM, int WN, int FM>
+TileGrid tile_grid(const Product &p) {
     using T = Tile<WM, WN, FM>;
-    const int tm = static_cast<int>(div_up(p.M, T::BM)), tn = static_cast<int>(div_up(p.N, T::BN));
-    const int64_t tiles = static_cast<int64_t>(tm) * tn * p.batch * p.splits;
-    // whole stages a slice
-    const int len = static_cast<int>(div_up(div_up(p.K, kStage), p.splits)) * kStage;
-    for (int64_t t = 0; t < tiles; t += 1 << 21) {  // (a launch's threads are counted in 32 bits)
-        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles - t, 1 << 21));
-        tile_kernel<WM, WN, FM, TA, TB><<<grid, T::kThreads, 0, stream>>>(p, tm, tn, t, len);
+    TileGrid g{static_cast<int>(div_up(p.M, T::BM)), static_cast<int>(div_up(p.N, T::BN)),
+               static_cast<int>(div_up(div_up(p.K, kStage), p.splits)) * kStage, 0};
+    g.tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n * p.batch * p.splits;
+    return g;
+}
+
+template <int WM, int WN, int FM, bool TA, bool TB>
+hipError_t launch_one(const Product &p, hipStream_t stream) {
+    const TileGrid g = tile_grid<WM, WN, FM>(p);
+    for (int64_t t = 0; t < g.tiles; t += 1 << 21) {  // (a launch's threads are counted in 32 bits)
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(g.tiles - t, 1 << 21));
+        tile_kernel<WM, WN, FM, TA, TB><<<grid, 64 * WM * WN, 0, stream>>>(p, g.tiles_m, g.tiles_n, t, g.len);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
