@@ -9,11 +9,15 @@ namespace {
 template <int FM, bool TA, bool TB, bool TC, bool TD>
 __global__ __launch_bounds__(256, per_cu(FM)) void tile_pair_kernel(Product p, TileGrid g, Product q, TileGrid h) {
     __shared__ Room<2, 2, FM> room;
-    const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-    if (id < g.tiles)
-        one_tile<2, 2, FM, TA, TB>(p, g.tiles_m, g.tiles_n, id, g.len, room);
+    // The tiles with more to sum come first, and every XCD takes of both: all of
+    // 160 x 11731 x 1373 on two XCDs took 234 us with 1373 x 11731 x 160, this 102.
+    const unsigned block = blockIdx.x, mine = static_cast<unsigned>(g.tiles), other = static_cast<unsigned>(h.tiles);
+    const bool p_first = g.len >= h.len, first = block < (p_first ? mine : other);
+    const unsigned at = first ? block : block - (p_first ? mine : other);
+    if (first == p_first)
+        one_tile<2, 2, FM, TA, TB>(p, g.tiles_m, g.tiles_n, xcd_remap(at, mine), g.len, room);
     else
-        one_tile<2, 2, FM, TC, TD>(q, h.tiles_m, h.tiles_n, id - g.tiles, h.len, room);
+        one_tile<2, 2, FM, TC, TD>(q, h.tiles_m, h.tiles_n, xcd_remap(at, other), h.len, room);
 }
 
 template <int FM>

@@ -379,7 +379,9 @@ int64_t slices_bytes(const Choice &c, int64_t batch, int64_t M, int64_t N) {
     const __int128 n = c.splits > 1 ? static_cast<__int128>(4 * c.splits) * batch * M * N : 0;
     return static_cast<int64_t>(std::min<__int128>(n, __int128{1} << 61));
 }
-// Whether two products go into one launch of tiles.
+// Whether two products go into one launch of tiles: each as it would be by itself, so
+// that its values are those, too.  (1000 x 777 x 1023 and 777 x 1023 x 1000, 224 workgroups each,
+// 24 and 26 us and 6 each for their slices; together 38 and 10.)
 bool paired(const Choice &c, const Choice &d, bool ta, bool tc, bool td) {
     return c.tile == d.tile && (c.tile == 1 || c.tile == 2) && !c.half && !d.half && !ta && tc && !td;
 }
