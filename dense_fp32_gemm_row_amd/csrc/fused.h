@@ -72,7 +72,8 @@ struct Product {
     // The largest |value| of each row of op(A), as its bits, where A is the loss's
     // gradient by the logits (no batch), or null.  Its rows have a few large
     // values and tens of thousands of small ones, to whose sum an error of 2^-40 of the
-    // largest adds nothing that counts: fp16 parts wherever the range allows.
+    // largest adds nothing that counts: fp16 parts wherever its range allows, and B's values
+    // that take part are within 2^-17 of their column's largest on (geometric) average.
     const int *top_a;
 };
 

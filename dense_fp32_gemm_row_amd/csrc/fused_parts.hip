@@ -230,11 +230,12 @@ __global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t stri
     }
 }
 
-__device__ __forceinline__ void count(RowStat &s, float x) {
+__device__ __forceinline__ void count(RowStat &s, float x, bool skip = false) {
     const int bits = __builtin_bit_cast(int, x) & 0x7fffffff, e = bits >> 23;
     s.top = max(s.top, e);
     // a value below 2^-126 has up to 23 leading zeros in its place
-    s.count += bits != 0, s.sum += bits == 0 ? 0 : e == 0 ? -23 : e;
+    const bool counts = bits != 0 && !skip;
+    s.count += counts, s.sum += !counts ? 0 : e == 0 ? -23 : e;
 }
 __device__ __forceinline__ void join(RowStat &s, int top, int n, int sum) {
     s.top = max(s.top, top), s.count += n, s.sum += sum;
@@ -247,6 +248,9 @@ struct StatJob {
     int rows, K, blocks, len;
     RowStat *out;
     int64_t strips, units;  // workgroups: [batch][block][strip]
+    // not null (kc false): k with skip[k] == ignore are neither counted nor summed
+    const int64_t *skip;
+    int64_t ignore;
 };
 
 // Where k is contiguous a wavefront takes a row's block, else a workgroup 256
@@ -280,8 +284,12 @@ __global__ __launch_bounds__(256) void row_stats_kernel(StatJob a, StatJob b, in
             row = strip * 256 + tid;
             if (row >= j.rows) continue;
             p += row;
+            if (j.skip != nullptr)
 #pragma unroll 8
-            for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld]);
+                for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld], j.skip[k] == j.ignore);
+            else
+#pragma unroll 8
+                for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld]);
         }
         j.out[(block * batch + n) * j.rows + row] = s;
     }
@@ -361,13 +369,13 @@ bool narrow_operand(int64_t ld, bool k_contiguous) {
 
 hipError_t launch_row_stats(const Product &p, hipStream_t stream) {
     auto job = [&](const Operand &x, bool kc, int rows, int blocks, const RowStat *out) {
-        StatJob j{x, kc, rows, p.K, blocks, static_cast<int>(div_up(p.K, blocks)), const_cast<RowStat *>(out), 0, 0};
+        StatJob j{x, kc, rows, p.K, blocks, static_cast<int>(div_up(p.K, blocks)), const_cast<RowStat *>(out), 0, 0, nullptr, p.ignore};
         j.strips = div_up(rows, kc ? 4 : 256);
         j.units = j.strips * blocks * p.batch;
         return j;
     };
     StatJob a = job(p.a, !p.ta, p.M, p.blocks_a, p.row_a), b = job(p.b, p.tb, p.N, p.blocks_b, p.row_b);
-    if (p.top_a != nullptr) a.units = 0;  // known
+    if (p.top_a != nullptr) a.units = 0, b.skip = p.target_k;  // a: known
     row_stats_kernel<<<blocks_for(a.units + b.units), 256, 0, stream>>>(a, b, p.batch);
     return hipGetLastError();
 }

@@ -383,10 +383,10 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
                 }
                 if (s.count > 0) {  // a row of zeros is one whatever its scale
                     e = s.top;
-                    const float n = static_cast<float>(p.K);
+                    // (beside probabilities of unknown cost: over the values that take part)
+                    const float n = static_cast<float>(p.top_a != nullptr ? s.count : p.K);
                     cost = (static_cast<float>(s.count) * static_cast<float>(e + 1) - static_cast<float>(s.sum)) / n;
                     share = static_cast<float>(s.count) / n;
-                    if (p.top_a != nullptr) cost = 0.0f, share = 1.0f;
                     if (e < 14 || e > 254) cost = __builtin_inff(), e = 141;
                 }
             }

@@ -572,3 +572,155 @@ def test_a_network_learns_as_its_formulas_say():
             assert err <= 1e-4 * p.grad.abs().max()
         ws = [w1 - 0.5 * dw1.t(), w2 - 0.5 * dw2.t(), head - 0.5 * dhead]
         bias = bias - 0.5 * dbias
+
+
+# ---- large products, and what they share --------------------------------------
+
+def test_ignored_rows_out_of_scale_take_no_part():
+    """Padding many orders of magnitude above the tokens, in products large
+    enough for parts scaled by a row's largest value."""
+    T, V, K = 2048, 4096, 2048
+    X, W, target = tokens(T, V, K, seed=30)
+    target[torch.arange(T, device=DEV) % 16 != 3] = -100
+    ignored = target == -100
+    clean = torch.where(ignored[:, None], 0.0, X)
+    X = torch.where(ignored[:, None], 1e30 * clean[3].abs() + 1e30, X)
+    want = o.loss_grad(clean, W, target)
+    loss, lse, dX, dW = b.cross_entropy_grad(X, W, target)
+    o.check(loss, *want["loss"], "loss"), o.check(dX, *want["dX"], "dX"), o.check(dW, *want["dW"], "dW")
+
+
+def test_words_out_of_scale():
+    """A word that no token can take, with weights far above the others': its
+    share of dX is an exact zero."""
+    T, V, K = 2048, 4096, 2048
+    X, W, target = tokens(T, V, K, seed=31)
+    X[:, :64] = X[:, :64].abs() + 0.5
+    W[V - 1] = 0.0
+    W[V - 1, :64] = -1e9
+    target[target == V - 1] = 0
+    want = o.loss_grad(X, W[:-1], target)
+    loss, lse, dX, dW = b.cross_entropy_grad(X, W, target)
+    o.check(loss, *want["loss"], "loss"), o.check(dX, *want["dX"], "dX")
+    o.check(dW[:-1], *want["dW"], "dW")
+    assert not dW[-1].any()
+
+
+def test_pieces_of_many_tokens():
+    """Logits of more than one piece at the workspace that is quickest; the
+    oracle goes by 250 tokens.  dW is a sum of the pieces', one rounding each."""
+    T, V, K = 4000, 300_001, 24
+    X, W, target = tokens(T, V, K, seed=32)
+    loss, lse, dX, dW = b.cross_entropy_grad(X, W, target)
+    sums = [torch.zeros(V, K, dtype=torch.float64, device=DEV) for _ in range(3)]
+    for t in range(0, T, 250):
+        rows = slice(t, t + 250)
+        want = o.loss_grad(X[rows], W, target[rows])
+        for name, got in (("loss", loss), ("lse", lse), ("dX", dX)):
+            o.check(got[rows], *want[name], name)
+        sums[0] += want["dW"][0]
+        # the tolerance of a sum of 250 products covers that many roundings of its own share;
+        # a sum of T has them relative to all that came before
+        sums[1] += want["dW"][1] * math.sqrt(T / 250 + 1)
+        sums[2] += want["dW"][0].abs()
+    o.check(dW, sums[0], sums[1] + 4 * o.U * sums[2], "dW")
+
+
+@pytest.mark.parametrize("stored_as", ["in_out", "out_in"])
+@pytest.mark.parametrize("M,N,K", [(1000, 1023, 777), (160, 1373, 2000), (517, 2304, 400), (148, 1824, 1500),
+                                   (2000, 160, 700)])
+def test_gradients_that_share_a_launch(M, N, K, stored_as):
+    A, B = rnd(1, M, K), stored(2, K, N, "N" if stored_as == "in_out" else "T", 1)
+    dC = rnd(3, M, N)
+    want = o.layer_grad(dC, A, B)
+    got = b.gemm_fused_grad(dC, A, B, dbias=True)
+    for name, t in zip(("dA", "dB", "dbias"), got):
+        o.check(t, *want[name], name)
+    assert torch.equal(b.gemm_fused_grad(dC, A, B, dB=False)[0], got[0])
+    assert torch.equal(b.gemm_fused_grad(dC, A, B, dA=False)[1], got[1])
+
+
+@pytest.mark.parametrize("M,N,K,ops", [(3, 40, 70, "NT"), (20, 40, 70, "NN"), (200, 300, 64, "NN"), (200, 300, 64, "NT"),
+                                       (200, 72, 64, "TN"), (90, 300, 64, "TT")])
+def test_offsets_past_32_bits(M, N, K, ops):
+    """Rows 64 or 256 MiB apart."""
+    def far(seed, rows, cols, op):
+        r, c = (rows, cols) if op == "N" else (cols, rows)
+        ld = 2 ** 24 if r > 64 else 2 ** 26
+        wide = torch.empty(((r - 1) * ld + c,), device=DEV).as_strided((r, c), (ld, 1))
+        wide.copy_(rnd(seed, r, c))
+        return wide if op == "N" else wide.t()
+
+    A, B = far(1, M, K, ops[0]), rnd(2, K, N)
+    near = A.clone(memory_format=torch.contiguous_format)
+    want = o.layer(near, B)
+    B = B if ops[1] == "N" else B.t().contiguous().t()
+    o.check(b.gemm_fused(A, B), want["y"], want["y_tol"])
+    del A
+    B2 = far(2, K, N, ops[1])
+    want = o.layer(near, B2.clone(memory_format=torch.contiguous_format))
+    o.check(b.gemm_fused(near, B2), want["y"], want["y_tol"])
+
+
+def large_calls():
+    A, B, dC = rnd(1, 1000, 777), rnd(2, 777, 1023), rnd(3, 1000, 1023)
+    X, W, target = tokens(2048, 4096, 2048, seed=33)
+    lib = b.load()
+
+    def call(space=None, stream=None):
+        """`space(bytes)` gives a workspace."""
+        got = lambda n: space(n) if space is not None and n else None
+        y = b.gemm_fused(A, B, activation="silu", stream=stream,
+                         workspace=got(lib.gemm_f32_fused_workspace_size(0, 0, 1, 1000, 1023, 777)))
+        grads = b.gemm_fused_grad(dC, A, B, pre=y, activation="silu", dbias=True, stream=stream, workspace=got(
+            lib.gemm_f32_fused_grad_workspace_size(0, 0, 1, 1000, 1023, 777, 4, 1, 1, 1)))
+        loss = b.cross_entropy(X, W, target, stream=stream,
+                               workspace=got(lib.gemm_f32_cross_entropy_workspace_size(2048, 4096, 2048)))
+        return [y, *grads, *loss, *b.cross_entropy_grad(X, W, target, stream=stream, workspace=got(
+            lib.gemm_f32_cross_entropy_grad_workspace_size(2048, 4096, 2048)))]
+
+    return call
+
+
+def test_workspaces_start_anywhere():
+    """4-byte aligned, of exactly the bytes asked for, holding NaN."""
+    call = large_calls()
+    kept = []
+
+    def space(n):
+        kept.append(torch.full((n // 4 + 2,), math.nan, device=DEV))
+        kept[-1][0] = kept[-1][-1] = GUARD
+        return kept[-1][1:-1]
+
+    first, got = call(), call(space)
+    assert all(torch.equal(a, c) for a, c in zip(first, got))
+    assert all(t[0] == GUARD and t[-1] == GUARD for t in kept) and len(kept) == 4
+
+
+def test_calls_at_once():
+    """Two streams, a workspace for each call, several rounds."""
+    call = large_calls()
+    first = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[call(stream=s) for s in streams] for _ in range(3)]
+    torch.cuda.synchronize()
+    for pair in outs:
+        for got in pair:
+            assert all(torch.equal(a, c) for a, c in zip(first, got))
+
+
+def test_large_calls_captured_and_replayed():
+    call = large_calls()
+    first = call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call()
+    for _ in range(3):
+        for t in outs:
+            t.fill_(GUARD)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(first, outs))
+        assert all(torch.equal(a, c) for a, c in zip(first, call()))
