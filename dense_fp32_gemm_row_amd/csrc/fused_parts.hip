@@ -8,32 +8,6 @@ namespace gemm_f32_impl {
 namespace fused {
 namespace {
 
-// C = epilogue(sum of slices), an element a thread, slices in order.
-__device__ __forceinline__ void sum_slices(const Product &p, int64_t first, int64_t step) {
-    const int64_t per = static_cast<int64_t>(p.M) * p.N;
-    for (int64_t o = first; o < p.batch * per; o += step) {
-        const int64_t b = o / per, q = o - b * per, m = q / p.N, n = q - m * p.N;
-        const float *W = p.slices + b * p.splits * per + q;
-        float z = W[0];
-        for (int s = 1; s < p.splits; ++s) z += W[s * per];
-        if (p.e.bias.p != nullptr) z += p.e.bias.p[b * p.e.bias.stride + n];
-        if (p.e.pre.p != nullptr) p.e.pre.p[b * p.e.pre.stride + m * p.e.pre.ld + n] = z;
-        float v = activate(p.e.activation, z);
-        if (p.e.residual.p != nullptr) v += p.e.residual.p[b * p.e.residual.stride + m * p.e.residual.ld + n];
-        p.c.p[b * p.c.stride + m * p.c.ld + n] = v;
-    }
-}
-__global__ __launch_bounds__(256) void sum_slices_kernel(Product p) {
-    sum_slices(p, blockIdx.x * int64_t{256} + threadIdx.x, gridDim.x * int64_t{256});
-}
-// Workgroups 0 .. first - 1 take p.
-__global__ __launch_bounds__(256) void sum_two_kernel(Product p, Product q, unsigned first) {
-    if (blockIdx.x < first)
-        sum_slices(p, blockIdx.x * int64_t{256} + threadIdx.x, first * int64_t{256});
-    else
-        sum_slices(q, (blockIdx.x - first) * int64_t{256} + threadIdx.x, (gridDim.x - first) * int64_t{256});
-}
-
 // 4 neighbours of a row, of which `left` are inside it.
 __device__ __forceinline__ f32x4 read4(const float *p, int64_t left) {
     f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
@@ -54,6 +28,39 @@ __device__ __forceinline__ void write4(float *p, int64_t left, f32x4 v) {
         for (int e = 0; e < 3; ++e)
             if (e < left) p[e] = v[e];
     }
+}
+
+// C = epilogue(sum of slices), 4 neighbours of a row a thread, slices in order.
+__device__ __forceinline__ void sum_slices(const Product &p, int64_t block, int64_t blocks) {
+    const int64_t per = static_cast<int64_t>(p.M) * p.N, rows = p.batch * p.M;
+    const unsigned strips = (static_cast<unsigned>(p.N) + 3) / 4;
+    for (int64_t o = block * 256; o < rows * strips; o += blocks * 256) {
+        const int64_t first = o / strips;  // the workgroup's first row: of all, by 64 bits, the others by 32
+        const unsigned at = static_cast<unsigned>(o - first * strips) + threadIdx.x;
+        const int64_t row = first + at / strips;
+        if (row >= rows) break;
+        const int64_t b = p.batch == 1 ? 0 : row / p.M, m = row - b * p.M, n = 4 * static_cast<int64_t>(at % strips);
+        const int64_t left = p.N - n;
+        const float *W = p.slices + b * p.splits * per + m * p.N + n;
+        f32x4 z = read4(W, left);
+#pragma unroll 4
+        for (int s = 1; s < p.splits; ++s) z += read4(W + s * per, left);
+        if (p.e.bias.p != nullptr) z += read4(p.e.bias.p + b * p.e.bias.stride + n, left);
+        if (p.e.pre.p != nullptr) write4(p.e.pre.p + b * p.e.pre.stride + m * p.e.pre.ld + n, left, z);
+        if (p.e.activation != GEMM_F32_ACT_NONE)
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) z = f32x4{z[1], z[2], z[3], activate(p.e.activation, z[0])};
+        if (p.e.residual.p != nullptr) z += read4(p.e.residual.p + b * p.e.residual.stride + m * p.e.residual.ld + n, left);
+        write4(p.c.p + b * p.c.stride + m * p.c.ld + n, left, z);
+    }
+}
+__global__ __launch_bounds__(256) void sum_slices_kernel(Product p) { sum_slices(p, blockIdx.x, gridDim.x); }
+// Workgroups 0 .. first - 1 take p.
+__global__ __launch_bounds__(256) void sum_two_kernel(Product p, Product q, unsigned first) {
+    if (blockIdx.x < first)
+        sum_slices(p, blockIdx.x, first);
+    else
+        sum_slices(q, blockIdx.x - first, gridDim.x - first);
 }
 
 // A block of rows of 4 LANES columns, 4 a lane, its rows shared by WAVES wavefronts and
@@ -299,14 +306,16 @@ unsigned blocks_for(int64_t n) { return static_cast<unsigned>(std::min<int64_t>(
 
 }  // namespace
 
+static unsigned sum_blocks(const Product &p) { return blocks_for(div_up(p.batch * p.M * div_up(p.N, 4), 256)); }
+
 hipError_t launch_sum_slices(const Product &p, hipStream_t stream) {
-    sum_slices_kernel<<<blocks_for(div_up(p.batch * p.M * p.N, 256)), 256, 0, stream>>>(p);
+    sum_slices_kernel<<<sum_blocks(p), 256, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 hipError_t launch_sum_slices(const Product &p, const Product &q, hipStream_t stream) {
-    const unsigned first = blocks_for(div_up(p.batch * p.M * p.N, 256));
-    sum_two_kernel<<<first + blocks_for(div_up(q.batch * q.M * q.N, 256)), 256, 0, stream>>>(p, q, first);
+    const unsigned first = sum_blocks(p);
+    sum_two_kernel<<<first + sum_blocks(q), 256, 0, stream>>>(p, q, first);
     return hipGetLastError();
 }
 
