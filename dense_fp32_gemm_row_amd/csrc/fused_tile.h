@@ -1,6 +1,21 @@
 // The tile kernel of the fused products: C = epilogue(op(A) op(B)), or the row
 // statistics of the cross entropy, for a tile of C that a workgroup holds in
 // registers.  Each operand form is compiled in a source file of its own.
+//
+// A product of FP32 values is six of bf16 parts, or three of fp16 parts, on matrix units
+// that are 16 times as quick as the FP32 ones, so 2.7 (5.3) times their rate is what the
+// arithmetic leaves; the parts are made once a workgroup, on the way into LDS.
+//   - 256 x 256, 8 wavefronts of 128 x 64, one workgroup a CU: the fewest values split and
+//     LDS reads a product.  4096 x 4096 x 4096 with bf16 parts 586 us (235 TFLOP/s), with
+//     fp16 parts 347 (396; the matrix units 72% busy at 1.73 GHz, which is what power
+//     leaves), and 26 for the rows' ranges; an FP32 library product takes 915.
+//   - 128 x 128, 4 wavefronts, two workgroups a CU, and 64 x 128, three: for fewer tiles.
+//     There splitting, LDS and the products take turns in one or two wavefronts a
+//     SIMD: 128 x 128 x k a CU in 36 ns a k, 64 x 128 x k in 23 (matrix units a third busy).
+//     1000 x 1023 x 777 in two slices of K 24 us and 5 for their sum, 37 x 4096 x 14336 in
+//     16 slices 50 (4.7 TB/s of B) and 5.
+//   - Tried: FP32 matrix instructions straight from memory in tiles of 64 x 64, 8
+//     wavefronts sharing K (1000 x 1023 x 777 27.6 us; behind these at all of 200 sizes but ten).
 #pragma once
 
 #include <type_traits>
