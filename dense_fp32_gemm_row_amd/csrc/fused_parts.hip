@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256) void sum_two_kernel(Product p, Product q, unsi
 // A block of rows of 4 LANES columns, 4 a lane, its rows shared by WAVES wavefronts and
 // the 64 / LANES parts of each: dZ, and the columns' sums over the block.  Memory bounds it
 // (4096 x 4096, GELU, 41 us, 4.9 TB/s), at 256 x 256 one chain of loads and sums in 4
-// workgroups (8.5 us, with the bias gradient; as blocks of 8 rows and a second launch 12).
+// workgroups (8.5 us, with the bias gradient, which has no launch of its own there).
 template <int KIND, int WAVES, int LANES>
 __global__ __launch_bounds__(64 * WAVES) void slope_kernel(Slope s, int64_t strips, int64_t units) {
     constexpr int kParts = 64 * WAVES / LANES;

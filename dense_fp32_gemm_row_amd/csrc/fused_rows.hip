@@ -45,8 +45,8 @@ __device__ __forceinline__ void store_cell(const Product &p, int64_t b, int64_t 
 // row (column) l % 16; here lane group g = l / 16 holds k 16 u + 4 g + j of a step in
 // instruction (u, j).  So where k is contiguous a lane's part of a row is 16
 // bytes; where rows are, it takes MG (NG) neighbours at every k.  A launch, one chain
-// of loads and the joining of 8 sums bound it at small sizes (256 x 256 x 256 4 us, of a
-// gradient both in 4.7; the 64 x 1000 x 256 logits of a loss 5.2), memory at few rows (16 x 4096 x
+// of loads and the joining of 8 sums bound it at small sizes (both products of a
+// 256 x 256 x 256 gradient 4.7 us, the 64 x 1000 x 256 logits of a loss 5.2), memory at few rows (16 x 4096 x
 // 4096, B transposed, 18 us, 3.7 TB/s).
 constexpr int kRowsWaves = 8;
 constexpr int quads_of(int mg, int ng) { return (mg + ng) * 4 <= 20 ? 4 : 2; }  // for two steps' registers
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void pair_kernel(Product p, Grid g
 // which are rows of B that it reads 1 KiB at a time, and a lane the products of
 // its 4 k; a workgroup of 4 wavefronts 16 columns.  The 64 lanes' sums are added by halves.
 // Memory bounds it: 1 x 14336 x 4096 36 to 42 us by card (5.6 to 6.5 TB/s; a copy reaches
-// 5.2), 1 x 32768 x 4096 86 (6.2).  8 columns a wavefront, and 4 steps on their way, gave nothing.
+// 5.2), 1 x 32768 x 4096 86 (6.2).
 template <int MR, bool TA>
 __global__ __launch_bounds__(256) void vector_kernel(Product p, int tiles_n, int64_t tiles, int len) {
     constexpr int R = 4, kStep = 256, U = 2;  // U steps' loads on their way at once
