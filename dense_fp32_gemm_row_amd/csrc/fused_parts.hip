@@ -284,13 +284,20 @@ __global__ __launch_bounds__(256) void row_stats_kernel(StatJob a, StatJob b, in
             row = strip * 4 + (tid >> 6);
             if (row >= j.rows) continue;
             p += row * j.x.ld;
-            int64_t k = k0 + 4 * lane;
-            for (; k + 3 < k1; k += 256) {
-                const f32x4 v = *reinterpret_cast<const float4u *>(p + k);
+            // four at once; loads past the end repeat the last one's and do not count
+            const int64_t k4 = k1 - 4;
+            if (k4 >= k0)
+                for (int64_t k = k0 + 4 * lane; k - 4 * lane <= k4; k += 1024) {
+                    f32x4 v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) count(s, v[e]);
-            }
-            for (; k < k1; ++k) count(s, p[k]);  // the last three at most, of one lane
+                    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4u *>(p + min(k + 256 * i, k4));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) count(s, k + 256 * i <= k4 ? v[i][e] : 0.0f);
+                }
+            const int64_t rest = k0 + (k1 - k0) / 4 * 4 + lane;
+            if (rest < k1) count(s, p[rest]);  // the last three at most
             for (int d = 1; d < 64; d *= 2) join(s, __shfl_xor(s.top, d), __shfl_xor(s.count, d), __shfl_xor(s.sum, d));
             if (lane != 0) continue;
         } else {
@@ -298,10 +305,10 @@ __global__ __launch_bounds__(256) void row_stats_kernel(StatJob a, StatJob b, in
             if (row >= j.rows) continue;
             p += row;
             if (j.skip != nullptr)
-#pragma unroll 8
+#pragma unroll 16
                 for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld], j.skip[k] == j.ignore);
             else
-#pragma unroll 8
+#pragma unroll 16
                 for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld]);
         }
         j.out[(block * batch + n) * j.rows + row] = s;
