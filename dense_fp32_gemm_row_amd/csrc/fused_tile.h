@@ -42,6 +42,7 @@ template <int WM, int WN, int FM>
 struct Tile {
     static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
     static constexpr int BM = 32 * FM * WM, BN = 64 * WN;
+    static constexpr bool kHalf = FM > 1;  // the tiles with a loop for fp16 parts
 };
 
 // Elements of one k range of an operand's tile, rows and k past the end zero.
@@ -179,7 +180,7 @@ template <int WM, int WN, int FM>
 struct Room {
     using T = Tile<WM, WN, FM>;
     static constexpr int BM = T::BM, BN = T::BN;
-    static constexpr bool kHalf = FM > 1;  // the tiles with a loop for fp16 parts
+    static constexpr bool kHalf = T::kHalf;
     static constexpr int kA = plane(BM, kStage), kB = plane(BN, kStage);                      // of 16 k
     static constexpr int kLongA = plane(BM, 2 * kStage), kLongB = plane(BN, 2 * kStage);      // of 32 k
     static constexpr int kPlanesA = 3 * 2 * kA, kBuffer = kPlanesA + 3 * 2 * kB;
@@ -187,7 +188,7 @@ struct Room {
     static constexpr int kRowOut = 68;  // floats: 64 of a row of results, 16 bytes apart from the next one's banks
     static_assert(kBuffer >= (BM + BN) * kStage * 4, "");
     static_assert(2 * kBuffer >= T::kWaves * 32 * kRowOut * 4, "");
-    alignas(128) char memory[2 * (FM == 4 ? kHalfBuffer : kBuffer)];
+    alignas(128) char memory[2 * (kHalf ? kHalfBuffer : kBuffer)];
     int exponents[kHalf ? BM + BN : 1];
     float worst[kHalf ? 2 * T::kWaves : 1];
 };
@@ -430,24 +431,22 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
                 acc[i][1][r] = ldexpf(acc[i][1][r], em + en1);
             }
     };
-    // The small tiles' stages, PARTS bf16 (fp16) parts: too few products a phase to
+    // The small tiles' stages in bf16 parts: too few products a phase to
     // hide an LDS read, so a stage's operands are all read a stage ahead.
     // Under the products of stage s the operands of s + 1 are read from LDS, and the values
     // of s + 2 are split and written where those of s were.
-    auto quick_small = [&](int first, int last, auto parts) {
-        constexpr int PARTS = decltype(parts)::value, D = FM == 1 ? 4 : 2;  // stages that loads run ahead
-        constexpr bool HALF = PARTS == 2;
-        constexpr int kAll = PARTS * 2 * kA, kBuf = kAll + PARTS * 2 * kB;
-        Share<BM, kThreads, !TA, kStage, HALF, D> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, exponents);
-        Share<BN, kThreads, TB, kStage, HALF, D> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, exponents + (HALF ? BM : 0));
+    auto quick_small = [&](int first, int last) {
+        constexpr int D = FM == 1 ? 4 : 2;  // stages that loads run ahead
+        Share<BM, kThreads, !TA, kStage, false, D> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, nullptr);
+        Share<BN, kThreads, TB, kStage, false, D> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, nullptr);
         constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
         const int stages = (last - first) / kStage;
-        u32x4 x[2][PARTS][FM], y[2][PARTS][2];
+        u32x4 x[2][3][FM], y[2][3][2];
         const int ra = half * kA + (32 * FM * wm + col) * 16;
-        const int rb = kAll + half * kB + (64 * wn + col) * 16;
+        const int rb = kPlanesA + half * kB + (64 * wn + col) * 16;
         auto fetch = [&](int set, const char *from) {
 #pragma unroll
-            for (int c = PARTS - 1; c >= 0; --c) {
+            for (int c = 2; c >= 0; --c) {
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
                     x[set][c][i] = *reinterpret_cast<const u32x4 *>(from + c * (2 * kA) + ra + 32 * 16 * i);
@@ -461,30 +460,25 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
-                    if constexpr (HALF)
-                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            __builtin_bit_cast(half8v, x[set][ca][i]), __builtin_bit_cast(half8v, y[set][cb][f]), acc[i][f], 0, 0, 0);
-                    else
-                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            __builtin_bit_cast(bf16x8, x[set][ca][i]), __builtin_bit_cast(bf16x8, y[set][cb][f]), acc[i][f], 0, 0, 0);
+                    acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, x[set][ca][i]), __builtin_bit_cast(bf16x8, y[set][cb][f]), acc[i][f], 0, 0, 0);
         };
         auto put = [&](char *to, int set) {
 #pragma unroll
             for (int u = 0; u < kUa; ++u) sa.put(u, to, set);
 #pragma unroll
-            for (int u = 0; u < kUb; ++u) sb.put(u, to + kAll, set);
+            for (int u = 0; u < kUb; ++u) sb.put(u, to + kPlanesA, set);
         };
         auto load = [&](int s, int set) { sa.load(min(s, stages - 1), set), sb.load(min(s, stages - 1), set); };  // past the end: not used
         auto stage = [&](auto ic, int s) {
             constexpr int I = decltype(ic)::value, P = I % 2, S = (I + 2) % D;
-            fetch(1 - P, memory + (1 - P) * kBuf);
-            put(memory + P * kBuf, S);
+            fetch(1 - P, memory + (1 - P) * kBuffer);
+            put(memory + P * kBuffer, S);
             load(s + 2 + D, S);
-            constexpr int kProducts = HALF ? 3 : 6;
-            if constexpr (!HALF) multiply(P, 2, 0), multiply(P, 0, 2), multiply(P, 1, 1);
+            multiply(P, 2, 0), multiply(P, 0, 2), multiply(P, 1, 1);
             multiply(P, 1, 0), multiply(P, 0, 1), multiply(P, 0, 0);
 #pragma unroll
-            for (int k = 0; k < kProducts * FM * 2; ++k) {
+            for (int k = 0; k < 6 * FM * 2; ++k) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
@@ -503,7 +497,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         for (int d = 0; d < D; ++d) load(d, d);
         put(memory, 0);
         load(D, 0);
-        put(memory + kBuf, 1);
+        put(memory + kBuffer, 1);
         load(D + 1, 1);
         wait_older<63>();
         barrier_only();
@@ -511,7 +505,6 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         wait_older<63>();
         barrier_only();
         turns<D>(stages, stage);
-        if constexpr (HALF) unscale();
     };
 
     // Whole stages of 32 k in fp16 parts, as above: per 16 k the products l h,
@@ -656,15 +649,11 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
     bool check = false;
     if (p.narrow && !few) {
         bool half_parts = false;
-        // the large tile's fp16 stages are of 32 k
-        constexpr int kHalfStage = FM == 4 ? 2 * kStage : kStage;
+        constexpr int kHalfStage = 2 * kStage;  // the fp16 stages are of 32 k
         if constexpr (kHalf)
             if (p.row_b != nullptr && k1 - k0 >= kHalfStage && certified()) {
                 whole = k0 + (k1 - k0) / kHalfStage * kHalfStage;
-                if constexpr (FM == 4)
-                    quick_half(k0, whole);
-                else
-                    quick_small(k0, whole, std::integral_constant<int, 2>{});
+                quick_half(k0, whole);
                 half_parts = true;
             }
         if (!half_parts) {
@@ -674,7 +663,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
                 if constexpr (FM == 4)
                     quick(k0, whole);
                 else
-                    quick_small(k0, whole, std::integral_constant<int, 3>{});
+                    quick_small(k0, whole);
             }
         }
     }
@@ -776,8 +765,9 @@ struct TileGrid {
 template <int WM, int WN, int FM>
 TileGrid tile_grid(const Product &p) {
     using T = Tile<WM, WN, FM>;
+    constexpr int kWhole = T::kHalf ? 2 * kStage : kStage;
     TileGrid g{static_cast<int>(div_up(p.M, T::BM)), static_cast<int>(div_up(p.N, T::BN)),
-               static_cast<int>(div_up(div_up(p.K, kStage), p.splits)) * kStage, 0};
+               static_cast<int>(div_up(div_up(p.K, kWhole), p.splits)) * kWhole, 0};
     g.tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n * p.batch * p.splits;
     return g;
 }
