@@ -69,8 +69,8 @@ struct Share {
     static constexpr int kUnits = E / 4;
     static constexpr int kPlane = plane(ROWS, STAGE);  // 8 k of every row
     static constexpr int kPart = STAGE / 8 * kPlane;
-    const char *base;   // of the operand's tile at k = 0
-    int64_t step, row;  // bytes a stage, a row of storage
+    const char *base;  // of the operand's tile at k = 0
+    int64_t row;       // bytes of a row of storage
     uint32_t off[KC ? kUnits : 1];
     int lds[KC ? 1 : kUnits];  // byte in a part
     float scale[HALF ? kUnits : 1];
@@ -80,7 +80,6 @@ struct Share {
         row = 4 * ld;
         if constexpr (KC) {
             base = reinterpret_cast<const char *>(p);
-            step = STAGE * 4;
             const int q = tid % (STAGE / 4), place = tid / (STAGE / 4);
             lds[0] = (q >> 1) * kPlane + place * 16 + (q & 1) * 8;
 #pragma unroll
@@ -96,7 +95,6 @@ struct Share {
             const int back = rows < kUnits && more ? kUnits - rows : 0;
             const int r = min(kUnits * j, rows - kUnits + back);
             base = reinterpret_cast<const char *>(p - back);
-            step = STAGE * row;
             off[0] = static_cast<uint32_t>(4 * q) * static_cast<uint32_t>(row) + 4 * r;
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
@@ -108,8 +106,9 @@ struct Share {
     }
     // 2^(141 - e): values with exponent field e and less come below 2^15
     static __device__ __forceinline__ float power(int e) { return __builtin_bit_cast(float, (268 - e) << 23); }
-    __device__ __forceinline__ void load(int stage, int set = 0) {
-        const char *at = base + stage * step;
+    // The STAGE k from k on.
+    __device__ __forceinline__ void load(int k, int set = 0) {
+        const char *at = base + (KC ? int64_t{4} : row) * k;
         if constexpr (KC) {
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
@@ -134,6 +133,12 @@ struct Share {
             }
         }
     }
+    // The first `drop` k are zero.
+    __device__ __forceinline__ void cut(int drop, int tid, int set = 0) {
+        const int q = KC ? tid % (STAGE / 4) : tid / (ROWS / kUnits);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[set][e] = 4 * q + e % 4 < drop ? 0.0f : v[set][e];
+    }
     __device__ __forceinline__ void put(int u, char *planes, int set = 0) const {
         const float(&x)[E] = v[set];
         char *to = planes + (KC ? lds[0] + u * (THREADS * 4 / STAGE) * 16 : lds[KC ? 0 : u]);
@@ -147,6 +152,18 @@ struct Share {
             for (int c = 0; c < 3; ++c) *reinterpret_cast<u32x2 *>(to + c * kPart) = s.p[c];
         }
     }
+};
+
+// `length` k in stages of STAGE, at least one: where K ends inside the last one, that one is the
+// last STAGE k there are, of which the first `drop` were summed before and are
+// zero in A.  Past the end it is loaded again and not used.
+template <int STAGE>
+struct Stages {
+    int length, count, drop;
+    __device__ __forceinline__ explicit Stages(int n)
+        : length(n), count((n + STAGE - 1) / STAGE), drop(count * STAGE - n) {}
+    __device__ __forceinline__ int start(int s) const { return min(s * STAGE, length - STAGE); }
+    __device__ __forceinline__ bool cuts(int s) const { return s == count - 1 && drop > 0; }
 };
 
 // stage(i, s) for every s, i = s % TURN as a constant.
@@ -267,7 +284,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         __syncthreads();
     };
 
-    // Whole stages on the bf16 units.  A stage runs in 6 phases, a part of A
+    // The stages on the bf16 units.  A stage runs in 6 phases, a part of A
     // times a part of B each.  Under a phase's products the next phase's
     // operands are read from LDS, and the next stage's values, loaded into registers a
     // stage ago, are split and written to the other buffer and their
@@ -277,7 +294,8 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         Share<BM, kThreads, !TA, kStage, false> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, nullptr);
         Share<BN, kThreads, TB, kStage, false> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, nullptr);
         constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
-        const int stages = (last - first) / kStage;
+        const Stages<kStage> all(last - first);
+        const int stages = all.count;
         u32x4 x[2][FM], y[3][2];  // parts of A by turns; the parts of B
         const int ra = half * kA + (32 * FM * wm + col) * 16;
         const int rb = kPlanesA + half * kB + (64 * wn + col) * 16;
@@ -320,7 +338,8 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         // Set P of x holds l of A at the start, 1 - P at the end.
         auto stage = [&](auto pc, int s, const char *from, char *to) {
             constexpr int P = decltype(pc)::value, Q = 1 - P;
-            const int next = min(s + 2, stages - 1);  // past the end: loaded again, not used
+            const int next = all.start(s + 2);
+            if (all.cuts(s + 1)) sa.cut(all.drop, tid);
             fetch_a(Q, 1, from);
             sa.put(0, to);
             multiply(P, 0);  // l h
@@ -350,7 +369,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         for (int u = 0; u < kUa; ++u) sa.put(u, even);
 #pragma unroll
         for (int u = 0; u < kUb; ++u) sb.put(u, even + kPlanesA);
-        sa.load(min(1, stages - 1)), sb.load(min(1, stages - 1));
+        sa.load(all.start(1)), sb.load(all.start(1));
         wait_older<63>();
         barrier_only();
         fetch_a(0, 2, even);
@@ -440,7 +459,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         Share<BM, kThreads, !TA, kStage, false, D> sa(A + (TA ? first * p.a.ld : first), p.a.ld, rows, m0 > 0, tid, nullptr);
         Share<BN, kThreads, TB, kStage, false, D> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, nullptr);
         constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
-        const int stages = (last - first) / kStage;
+        const Stages<kStage> all(last - first);
         u32x4 x[2][3][FM], y[2][3][2];
         const int ra = half * kA + (32 * FM * wm + col) * 16;
         const int rb = kPlanesA + half * kB + (64 * wn + col) * 16;
@@ -469,9 +488,10 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
 #pragma unroll
             for (int u = 0; u < kUb; ++u) sb.put(u, to + kPlanesA, set);
         };
-        auto load = [&](int s, int set) { sa.load(min(s, stages - 1), set), sb.load(min(s, stages - 1), set); };  // past the end: not used
+        auto load = [&](int s, int set) { sa.load(all.start(s), set), sb.load(all.start(s), set); };
         auto stage = [&](auto ic, int s) {
             constexpr int I = decltype(ic)::value, P = I % 2, S = (I + 2) % D;
+            if (all.cuts(s + 2)) sa.cut(all.drop, tid, S);
             fetch(1 - P, memory + (1 - P) * kBuffer);
             put(memory + P * kBuffer, S);
             load(s + 2 + D, S);
@@ -497,6 +517,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         for (int d = 0; d < D; ++d) load(d, d);
         put(memory, 0);
         load(D, 0);
+        if (all.cuts(1)) sa.cut(all.drop, tid, 1);
         put(memory + kBuffer, 1);
         load(D + 1, 1);
         wait_older<63>();
@@ -504,10 +525,10 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         fetch(0, memory);
         wait_older<63>();
         barrier_only();
-        turns<D>(stages, stage);
+        turns<D>(all.count, stage);
     };
 
-    // Whole stages of 32 k in fp16 parts, as above: per 16 k the products l h,
+    // Stages of 32 k in fp16 parts, as above: per 16 k the products l h,
     // h h and h l.
     auto quick_half = [&](int first, auto last) {
         constexpr int kLong = 2 * kStage;
@@ -515,7 +536,8 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         Share<BN, kThreads, TB, kLong, true> sb(B + (TB ? first : first * p.b.ld), p.b.ld, cols, n0 > 0, tid, exponents + BM);
         constexpr int kUa = decltype(sa)::kUnits, kUb = decltype(sb)::kUnits;
         static_assert(kUa == 4 && kUb == 4, "");
-        const int stages = (last - first) / kLong;
+        const Stages<kLong> all(last - first);
+        const int stages = all.count;
         u32x4 x[2][FM], y[3][2];
         const int ra = half * kLongA + (32 * FM * wm + col) * 16;
         const int rb = kHalfA + half * kLongB + (64 * wn + col) * 16;
@@ -553,7 +575,8 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
             __builtin_amdgcn_sched_barrier(0);
         };
         auto stage = [&](int s, const char *from, char *to) {
-            const int next = min(s + 2, stages - 1);  // past the end: loaded again, not used
+            const int next = all.start(s + 2);
+            if (all.cuts(s + 1)) sa.cut(all.drop, tid);
             fetch_a(1, 0, 0, from);
             sa.put(0, to), sa.put(1, to);
             multiply(0, 0);  // l h
@@ -581,7 +604,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         sa.load(0), sb.load(0);
 #pragma unroll
         for (int u = 0; u < 4; ++u) sa.put(u, even), sb.put(u, even + kHalfA);
-        sa.load(min(1, stages - 1)), sb.load(min(1, stages - 1));
+        sa.load(all.start(1)), sb.load(all.start(1));
         wait_older<63>();
         barrier_only();
         fetch_a(0, 1, 0, even);
@@ -649,22 +672,19 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
     bool check = false;
     if (p.narrow && !few) {
         bool half_parts = false;
-        constexpr int kHalfStage = 2 * kStage;  // the fp16 stages are of 32 k
         if constexpr (kHalf)
-            if (p.row_b != nullptr && k1 - k0 >= kHalfStage && certified()) {
-                whole = k0 + (k1 - k0) / kHalfStage * kHalfStage;
-                quick_half(k0, whole);
+            if (p.row_b != nullptr && k1 - k0 >= 2 * kStage && certified()) {
+                quick_half(k0, k1);
+                whole = k1;
                 half_parts = true;
             }
-        if (!half_parts) {
-            whole = k0 + (k1 - k0) / kStage * kStage;
-            check = whole > k0;
-            if (check) {
-                if constexpr (FM == 4)
-                    quick(k0, whole);
-                else
-                    quick_small(k0, whole);
-            }
+        if (!half_parts && k1 - k0 >= kStage) {
+            whole = k1;
+            check = true;
+            if constexpr (FM == 4)
+                quick(k0, k1);
+            else
+                quick_small(k0, k1);
         }
     }
     for (int from = whole;; from = k0) {
