@@ -724,3 +724,20 @@ def test_large_calls_captured_and_replayed():
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(first, outs))
         assert all(torch.equal(a, c) for a, c in zip(first, call()))
+
+
+@pytest.mark.parametrize("ops", ["NN", "NT", "TN", "TT"])
+@pytest.mark.parametrize("M,N", [(700, 900), (1300, 2050), (2600, 4100)])
+def test_sums_that_end_inside_a_stage(M, N, ops):
+    """Whole numbers, whose sums are exact in any order and form: a k that is
+    summed twice or left out shows.  An infinity near the end of K counts once, too."""
+    for K in (15, 16, 17, 31, 33, 47, 48, 63, 65, 100, 127, 200, 399):
+        A = stored(K, M, K, ops[0]).mul(3.0).round()
+        B = stored(K + 1, K, N, ops[1]).mul(3.0).round()
+        want = torch.matmul(A.double().contiguous(), B.double().contiguous()).float()
+        got = b.gemm_fused(A, B)
+        assert torch.equal(got, want), K
+        A[:, max(K - 20, 0)] = 1.0
+        B[max(K - 20, 0), 5] = math.inf
+        got = b.gemm_fused(A, B)
+        assert bool((got[:, 5] == math.inf).all()) and bool(torch.isfinite(got[:, 6:]).all()), K
