@@ -35,7 +35,7 @@ inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // What a kernel's tile takes, in nanoseconds: `lone` a k and `fixed` besides where a
 // CU has one of them, `shared` a k and `each` besides of every one where it has more.
 // Fitted to 5600 times of 270 products of 33 to 8192 rows (three operand forms, 90 sizes
-// drawn evenly over their logarithms): the choice is 2.3% off the best of all
+// drawn evenly over their logarithms): the choice is 2.2% off the best of all
 // kernels and slices on average.
 struct Rate {
     Choice kind;
@@ -46,7 +46,7 @@ constexpr Rate kRates[] = {
     {{kRows, 1, false, 17}, 16, 16, 2.6, 884, 2.8, 670},     {{kRows, 1, false, 18}, 16, 32, 4.2, 1040, 4.1, 1079},
     {{kRows, 1, false, 34}, 32, 32, 6.6, 2167, 6.9, 1765},   {{kRows, 1, false, 36}, 32, 64, 11.5, 2310, 11.5, 2447},
     {{kRows, 1, false, 66}, 64, 32, 11.5, 2221, 11.3, 2868}, {{2, 1, false, 0}, 64, 128, 29.2, 5210, 23.3, 3423},
-    {{1, 1, false, 0}, 128, 128, 33.0, 9106, 36.0, 5713},    {{1, 1, true, 0}, 128, 128, 31.4, 2473, 26.8, 4970},
+    {{1, 1, false, 0}, 128, 128, 33.0, 9106, 36.0, 5713},    {{1, 1, true, 0}, 128, 128, 25.0, 2473, 22.5, 4970},
     {{0, 1, false, 0}, 256, 256, 96.6, 33397, 129.1, 25567}, {{0, 1, true, 0}, 256, 256, 50.8, 29554, 73.5, 30865},
 };
 constexpr double kCus = 256;
