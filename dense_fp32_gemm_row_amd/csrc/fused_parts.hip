@@ -267,7 +267,7 @@ struct StatJob {
 
 // Where k is contiguous a wavefront takes a row's block, else a workgroup 256
 // rows' (a row a thread).  Memory bounds it: two operands of 4096 x 4096 26 us (5.2 TB/s),
-// 131072 x 2048 by columns 243 (4.4).
+// 131072 x 2048 by columns 229 (4.7).
 __global__ __launch_bounds__(256) void row_stats_kernel(StatJob a, StatJob b, int64_t batch) {
     const int tid = threadIdx.x, lane = tid & 63;
     for (int64_t u = blockIdx.x; u < a.units + b.units; u += gridDim.x) {
@@ -411,7 +411,7 @@ int64_t slices_bytes(const Choice &c, int64_t batch, int64_t M, int64_t N) {
 }
 // Whether two products go into one launch of tiles: each as it would be by itself, so
 // that its values are those, too.  (1000 x 777 x 1023 and 777 x 1023 x 1000, 224 workgroups each,
-// 24 and 26 us and 6 each for their slices; together 38 and 10.)
+// 24 and 26 us and 6 each for their slices; together 34 and 7.)
 bool paired(const Choice &c, const Choice &d, bool ta, bool tc, bool td) {
     return c.tile == d.tile && (c.tile == 1 || c.tile == 2) && !c.half && !d.half && !ta && tc && !td;
 }

@@ -9,7 +9,8 @@
 //     LDS reads a product.  4096 x 4096 x 4096 with bf16 parts 586 us (235 TFLOP/s), with
 //     fp16 parts 347 (396; the matrix units 72% busy at 1.73 GHz, which is what power
 //     leaves), and 26 for the rows' ranges; an FP32 library product takes 915.
-//   - 128 x 128, 4 wavefronts, two workgroups a CU, and 64 x 128, three: for fewer tiles.
+//   - 128 x 128, 4 wavefronts, two workgroups a CU (517 x 32000 x 1024 160 us in fp16 parts,
+//     212 TFLOP/s; with rows that are not whole lines, 32003 x 1001, 174), and 64 x 128, three: for fewer tiles.
 //     There splitting, LDS and the products take turns in one or two wavefronts a
 //     SIMD: 128 x 128 x k a CU in 36 ns a k, 64 x 128 x k in 23 (matrix units a third busy).
 //     1000 x 1023 x 777 in two slices of K 24 us and 5 for their sum, 37 x 4096 x 14336 in
