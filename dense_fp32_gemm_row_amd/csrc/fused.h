@@ -69,26 +69,19 @@ struct Product {
     // no part even where B holds infinities or NaN (A stored K x M, B stored K x N).
     const int64_t *target_k;
     int64_t ignore;
-    // The largest |value| of each row of op(A), as its bits, where A is the loss's
-    // gradient by the logits (no batch), or null.  Its rows have a few large
-    // values and tens of thousands of small ones, to whose sum an error of 2^-40 of the
-    // largest adds nothing that counts: fp16 parts wherever its range allows, and B's values
-    // that take part are within 2^-17 of their column's largest on (geometric) average.
-    const int *top_a;
+    Use use;
 };
 
 hipError_t launch_product(const Product &, hipStream_t);
-// Whether its large tiles may take fp16 parts.
-bool wants_parts(const Product &);
 // Two independent products; they share their workspace, of `bytes`.
 hipError_t launch_two(const Product &, const Product &, int64_t bytes, hipStream_t);
 // Bytes of workspace that a product is quickest with; it runs with none, too.
-// `statistics`: its mode is not kStore.
-int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics);
+int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, Use use);
 // The same of launch_two's.
 struct Sizes {
     bool ta, tb;
     int64_t batch, M, N, K;
+    Use use;
 };
 int64_t two_space(const Sizes &, const Sizes &);
 
@@ -142,12 +135,11 @@ struct Loss {
     const float *grad_loss;     // null: ones
     float *logits;              // launch_probabilities: T x V, in place
     int64_t ld;
-    int *row_top, *column_top;  // null, or T and V: set to zero by launch_loss, to the largest |value|'s bits
 };
 hipError_t launch_loss(const Loss &, hipStream_t);
 // logits = grad_loss (exp(logits - lse) - (v == target)), zero for ignored rows
 hipError_t launch_probabilities(const Loss &, hipStream_t);
-// Both at once, for small T x V (the largest magnitudes are not found).
+// Both at once, for small T x V.
 hipError_t launch_loss_and_probabilities(const Loss &, hipStream_t);
 
 }  // namespace fused

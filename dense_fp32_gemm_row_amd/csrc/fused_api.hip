@@ -60,19 +60,19 @@ int check_workspace(void *workspace, int64_t bytes, int64_t need, Bytes *out) {
 }
 
 // Bytes of a product's own workspace, and of two.
-int64_t space_of(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics = false) {
+int64_t space_of(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, fused::Use use = fused::kPlain) {
     if (batch == 0 || M == 0 || N == 0 || K == 0) return 0;
-    return fused::product_space(tb, batch, M, N, K, statistics);
+    return fused::product_space(tb, batch, M, N, K, use);
 }
 
 int64_t space_of(const fused::Sizes &p, const fused::Sizes &q) {
-    auto one = [](const fused::Sizes &x) { return space_of(x.tb, x.batch, x.M, x.N, x.K); };
+    auto one = [](const fused::Sizes &x) { return space_of(x.tb, x.batch, x.M, x.N, x.K, x.use); };
     auto empty = [](const fused::Sizes &x) { return x.batch == 0 || x.M == 0 || x.N == 0 || x.K == 0; };
     return empty(p) || empty(q) ? std::max(one(p), one(q)) : fused::two_space(p, q);
 }
 
 fused::Product plain_product(int64_t batch, int64_t M, int64_t N, int64_t K, bool ta, fused::Operand a, bool tb,
-                             fused::Operand b, fused::Result c, float *space) {
+                             fused::Operand b, fused::Result c, float *space, fused::Use use = fused::kPlain) {
     fused::Product p{};
     p.batch = batch;
     p.M = static_cast<int>(M), p.N = static_cast<int>(N), p.K = static_cast<int>(K);
@@ -80,6 +80,7 @@ fused::Product plain_product(int64_t batch, int64_t M, int64_t N, int64_t K, boo
     p.a = a, p.b = b, p.c = c;
     p.space = space;
     p.mode = fused::kStore;
+    p.use = use;
     return p;
 }
 
@@ -114,8 +115,10 @@ GradParts grad_parts(bool ta, bool tb, int64_t batch, int64_t M, int64_t N, int6
     if (activation != GEMM_F32_ACT_NONE && (dA || dB)) g.dz = times(times(batch, M), N);
     if (dbias && g.blocks > 1) g.partial = times(times(batch, g.blocks), N);
     // the products as they are run
-    const fused::Sizes none{}, a = ta ? fused::Sizes{tb, true, batch, K, M, N} : fused::Sizes{false, !tb, batch, M, K, N};
-    const fused::Sizes b = tb ? fused::Sizes{true, ta, batch, N, K, M} : fused::Sizes{!ta, false, batch, K, N, M};
+    const fused::Sizes none{}, a = ta ? fused::Sizes{tb, true, batch, K, M, N, fused::kPlain}
+                                             : fused::Sizes{false, !tb, batch, M, K, N, fused::kPlain};
+    const fused::Sizes b = tb ? fused::Sizes{true, ta, batch, N, K, M, fused::kPlain}
+                              : fused::Sizes{!ta, false, batch, K, N, M, fused::kPlain};
     g.space = space_of(dA ? a : none, dB ? b : none) / 4;
     return g;
 }
@@ -132,12 +135,13 @@ int64_t line(int64_t floats) { return div_up(floats, 32) * 32; }
 int64_t piece_bytes(int64_t rows, int64_t V) {
     if (rows == 0) return 0;
     const int64_t few = std::min<int64_t>(rows, fused::kFineTokens);
-    return plus(times(times(4, rows), line(V)) + 4 * (rows + V + 32),
+    return plus(times(times(4, rows), line(V)) + 4 * 32,
                 std::max(stats_bytes(rows, V), stats_bytes(few, V)));
 }
 int64_t piece_space(int64_t rows, int64_t V, int64_t K) {
-    return std::max(space_of(true, 1, rows, V, K, true),
-                    space_of(fused::Sizes{false, false, 1, rows, K, V}, fused::Sizes{true, false, 1, V, K, rows}));
+    return std::max(space_of(true, 1, rows, V, K, fused::kStatistics),
+                    space_of(fused::Sizes{false, false, 1, rows, K, V, fused::kProbabilities},
+                             fused::Sizes{true, false, 1, V, K, rows, fused::kProbabilities}));
 }
 constexpr int64_t kPieceBytes = int64_t{4} << 30;
 constexpr int64_t kPieceRows = 256;
@@ -309,8 +313,8 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
     if (rc == GEMM_F32_OK) rc = check_apart({lo, ls, ws}, {x, w, t});
     if (rc != GEMM_F32_OK) return rc;
     float *at = static_cast<float *>(workspace);
-    float *space = space_of(true, 1, T, V, K, true) ? at + stats_bytes(T, V) / 4 : nullptr;
-    fused::Product p = plain_product(1, T, V, K, false, {X, ldx, 0}, true, {W, ldw, 0}, {}, space);
+    float *space = space_of(true, 1, T, V, K, fused::kStatistics) ? at + stats_bytes(T, V) / 4 : nullptr;
+    fused::Product p = plain_product(1, T, V, K, false, {X, ldx, 0}, true, {W, ldw, 0}, {}, space, fused::kStatistics);
     p.mode = fused::kStats;
     p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * T), p.groups = groups_of(T, V);
     p.target = target, p.ignore = ignore_index;
@@ -324,7 +328,7 @@ int gemm_f32_cross_entropy(int64_t T, int64_t V, int64_t K, const float *X, int6
 }
 
 int64_t gemm_f32_cross_entropy_workspace_size(int64_t T, int64_t V, int64_t K) {
-    return valid_sizes(1, T, V, K) ? plus(stats_bytes(T, V), space_of(true, 1, T, V, K, true)) : 0;
+    return valid_sizes(1, T, V, K) ? plus(stats_bytes(T, V), space_of(true, 1, T, V, K, fused::kStatistics)) : 0;
 }
 
 int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X, int64_t ldx, const float *W,
@@ -361,16 +365,16 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             return run(plain_product(1, V, K, 0, true, {}, false, {}, {dW, lddw, 0}, nullptr), s);
         for (int64_t t0 = 0; t0 < T && err == hipSuccess; t0 += rows) {
             const int64_t n = std::min(rows, T - t0);
-            int *row_top = reinterpret_cast<int *>(at) + 2 * n + 2 * n * groups_of(n, V), *column_top = row_top + n;
-            float *logits = at + line(reinterpret_cast<float *>(column_top + V) - at);
+            float *logits = at + line(2 * n + 2 * n * groups_of(n, V));
             const int64_t ldl = line(V);
             float *space = sliced && bytes > piece_bytes(best, V) ? at + piece_bytes(best, V) / 4 : nullptr;
             // (the last piece may be shorter, and ask for more)
-            auto room = [&](bool tb, int64_t M, int64_t N, int64_t k, bool statistics = false) {
-                return space != nullptr && space_of(tb, 1, M, N, k, statistics) <= full - piece_bytes(best, V) ? space : nullptr;
+            auto room = [&](bool tb, int64_t M, int64_t N, int64_t k, fused::Use use) {
+                return space != nullptr && space_of(tb, 1, M, N, k, use) <= full - piece_bytes(best, V) ? space : nullptr;
             };
             const float *Xt = X + t0 * ldx;
-            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, ldl, 0}, room(true, n, V, K, true));
+            fused::Product p = plain_product(1, n, V, K, false, {Xt, ldx, 0}, true, {W, ldw, 0}, {logits, ldl, 0}, room(true, n, V, K, fused::kStatistics),
+                                             fused::kStatistics);
             p.mode = fused::kStoreStats;
             p.at_target = at, p.stats = reinterpret_cast<fused::stat2 *>(at + 2 * n), p.groups = groups_of(n, V);
             p.target = target + t0, p.ignore = ignore_index;
@@ -385,17 +389,13 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
                 continue;
             }
             fused::Product px = plain_product(1, n, K, V, false, {logits, ldl, 0}, false, {W, ldw, 0},
-                                              {dX != nullptr ? dX + t0 * lddx : nullptr, lddx, 0}, room(false, n, K, V));
-            px.top_a = row_top;
+                                              {dX != nullptr ? dX + t0 * lddx : nullptr, lddx, 0}, room(false, n, K, V, fused::kProbabilities),
+                                              fused::kProbabilities);
             fused::Product pw = plain_product(1, V, K, n, true, {logits, ldl, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0},
-                                              room(false, V, K, n));
-            pw.top_a = column_top;
+                                              room(false, V, K, n, fused::kProbabilities), fused::kProbabilities);
             pw.target_k = target + t0, pw.ignore = ignore_index;
             if (t0 > 0) pw.e.residual = {dW, lddw, 0};  // the pieces before
-            // the largest magnitudes, for fp16 parts
-            l.row_top = dX != nullptr && fused::wants_parts(px) ? row_top : nullptr;
-            l.column_top = dW != nullptr && fused::wants_parts(pw) ? column_top : nullptr;
-            if (n * V <= 1 << 18 && l.row_top == nullptr && l.column_top == nullptr) {
+            if (n * V <= 1 << 18) {
                 if (err == hipSuccess) err = fused::launch_loss_and_probabilities(l, s);
             } else {
                 if (err == hipSuccess) err = fused::launch_loss(l, s);

@@ -67,12 +67,14 @@ inline double predicted(const Rate &r, int64_t batch, int64_t M, int64_t N, int6
 }
 
 // What the product is for: statistics of whole rows allow no slices, and of many
-// tokens only the tiles.
-enum Use { kPlain, kStatistics };
+// tokens only the tiles; of the loss's probabilities, whose small values may be all that
+// counts in a gradient, next to no two fp16 parts hold enough (a word's probability of
+// 2^-17 beside its target's 1 leaves them 2^-22 of it), so they take three bf16 parts.
+enum Use { kPlain, kStatistics, kProbabilities };
 
 // `tb`: B is stored N x K.  `space`: whether there is a workspace.
 inline Choice choose(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool space, Use use) {
-    const bool slice = space && use == kPlain;
+    const bool slice = space && use != kStatistics;
     // Few rows: reading B is the work, in tiles as wide as leaves enough of them (as
     // stored, a lane reads 2 neighbours): 16 x 14336 x 4096, B transposed, 47 us with 64
     // columns and 65 with 16, 16 x 4096 x 4096 43 and 18; 5 x 1792 x 78080, B as stored,
@@ -87,7 +89,7 @@ inline Choice choose(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bo
     Choice best{};
     double least = 0;
     for (const Rate &r : kRates) {
-        if (r.kind.half && (!space || K < 64 || K > (int64_t{1} << 22))) continue;
+        if (r.kind.half && (!space || use == kProbabilities || K < 64 || K > (int64_t{1} << 22))) continue;
         if (r.kind.tile == kRows && ((use == kStatistics && M > kFineTokens) || N < 4)) continue;
         const int64_t tiles = batch * div_up(M, r.m) * div_up(N, r.n);
         for (int64_t splits = 1; splits <= (slice ? kMostSplits : 1); splits *= 2) {

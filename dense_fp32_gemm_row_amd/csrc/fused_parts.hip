@@ -144,8 +144,6 @@ template <bool GRAD>
 __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
     __shared__ float tops[4], sums[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (l.column_top != nullptr)
-        for (int64_t v = blockIdx.x * int64_t{256} + threadIdx.x; v < l.V; v += gridDim.x * int64_t{256}) l.column_top[v] = 0;
     for (int64_t t = blockIdx.x; t < l.T; t += gridDim.x) {
         float m = -__builtin_inff(), s = 0.0f;
 #pragma unroll 4
@@ -168,7 +166,6 @@ __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
                 l.loss[t] = target == l.ignore ? 0.0f
                             : target >= 0 && target < l.V ? lse - l.at_target[t] : __builtin_nanf("");
             }
-            if (l.row_top != nullptr) l.row_top[t] = 0;
             if constexpr (GRAD) tops[0] = lse;
         }
         __syncthreads();
@@ -183,19 +180,12 @@ __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
     }
 }
 
-// `rows` (at most kProbabilityRows) rows of 1024 columns, 4 a thread.  The largest
-// magnitudes of rows and columns are found on the way (a maximum does not depend on
-// the order); the workgroup's own meet in LDS first, so that an atomic takes
-// neighbours: one for a wavefront's every row on lines that all workgroups share took
-// 57 us of 517 x 32003, this 29 (4.6 TB/s; 4096 x 131072 817 us, 5.3 TB/s, a copy's).
-constexpr int kProbabilityRows = 64;
+// `rows` rows of 1024 columns, 4 a thread (4096 x 131072 817 us, 5.3 TB/s, a copy's).
 __global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t strips, int64_t units, int rows) {
-    __shared__ int tops[kProbabilityRows][4], columns[1024];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t block = u / strips, v0 = (u - block * strips) * 1024, v = v0 + 4 * threadIdx.x, left = l.V - v;
+        const int64_t block = u / strips, v = (u - block * strips) * 1024 + 4 * threadIdx.x, left = l.V - v;
+        if (left <= 0) continue;
         const int64_t first = block * rows, last = min(first + rows, static_cast<int64_t>(l.T));
-        int column[4] = {0, 0, 0, 0};
         constexpr int kAtOnce = 4;
         for (int64_t t0 = first; t0 < last; t0 += kAtOnce) {
             f32x4 x[kAtOnce];
@@ -207,47 +197,19 @@ __global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t stri
                 if (t >= last) break;
                 const int64_t target = l.target[t];
                 const float lse = l.lse[t], g = l.grad_loss != nullptr ? l.grad_loss[t] : 1.0f;
-                int row = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = gradient(l, x[i][e], lse, g, v + e, target);
-                    x[i][e] = p;
-                    const int bits = e < left ? __builtin_bit_cast(int, p) & 0x7fffffff : 0;
-                    column[e] = max(column[e], bits), row = max(row, bits);
-                }
+                for (int e = 0; e < 4; ++e) x[i][e] = gradient(l, x[i][e], lse, g, v + e, target);
                 write4(l.logits + t * l.ld + v, left, x[i]);
-                if (l.row_top != nullptr) {
-                    row = max(row, moved<0xb1>(row)), row = max(row, moved<0x4e>(row));
-                    row = max(row, moved<0x124>(row)), row = max(row, moved<0x128>(row));
-                    row = max(row, __shfl_xor(row, 16)), row = max(row, __shfl_xor(row, 32));
-                    if (lane == 0) tops[t - first][wave] = row;
-                }
             }
         }
-        if (l.column_top != nullptr)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) columns[4 * threadIdx.x + e] = column[e];
-        __syncthreads();
-        if (l.row_top != nullptr && threadIdx.x < last - first) {
-            const int *top = tops[threadIdx.x];
-            atomicMax(l.row_top + first + threadIdx.x, max(max(top[0], top[1]), max(top[2], top[3])));
-        }
-        if (l.column_top != nullptr)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = 256 * e + threadIdx.x;
-                if (v0 + c < l.V) atomicMax(l.column_top + v0 + c, columns[c]);
-            }
-        __syncthreads();
     }
 }
 
-__device__ __forceinline__ void count(RowStat &s, float x, bool skip = false) {
+__device__ __forceinline__ void count(RowStat &s, float x) {
     const int bits = __builtin_bit_cast(int, x) & 0x7fffffff, e = bits >> 23;
     s.top = max(s.top, e);
     // a value below 2^-126 has up to 23 leading zeros in its place
-    const bool counts = bits != 0 && !skip;
-    s.count += counts, s.sum += !counts ? 0 : e == 0 ? -23 : e;
+    s.count += bits != 0, s.sum += bits == 0 ? 0 : e == 0 ? -23 : e;
 }
 __device__ __forceinline__ void join(RowStat &s, int top, int n, int sum) {
     s.top = max(s.top, top), s.count += n, s.sum += sum;
@@ -260,9 +222,6 @@ struct StatJob {
     int rows, K, blocks, len;
     RowStat *out;
     int64_t strips, units;  // workgroups: [batch][block][strip]
-    // not null (kc false): k with skip[k] == ignore are neither counted nor summed
-    const int64_t *skip;
-    int64_t ignore;
 };
 
 // Where k is contiguous a wavefront takes a row's block, else a workgroup 256
@@ -304,12 +263,8 @@ __global__ __launch_bounds__(256) void row_stats_kernel(StatJob a, StatJob b, in
             row = strip * 256 + tid;
             if (row >= j.rows) continue;
             p += row;
-            if (j.skip != nullptr)
 #pragma unroll 16
-                for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld], j.skip[k] == j.ignore);
-            else
-#pragma unroll 16
-                for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld]);
+            for (int64_t k = k0; k < k1; ++k) count(s, p[k * j.x.ld]);
         }
         j.out[(block * batch + n) * j.rows + row] = s;
     }
@@ -375,7 +330,7 @@ hipError_t launch_loss_and_probabilities(const Loss &l, hipStream_t stream) {
 hipError_t launch_probabilities(const Loss &l, hipStream_t stream) {
     const int64_t strips = div_up(l.V, 1024);
     // as many rows a workgroup as leave enough of them
-    const int rows = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kProbabilityRows, l.T * strips / 1024)));
+    const int rows = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, l.T * strips / 1024)));
     const int64_t units = strips * div_up(l.T, rows);
     probabilities_kernel<<<blocks_for(units), 256, 0, stream>>>(l, strips, units, rows);
     return hipGetLastError();
@@ -391,13 +346,12 @@ bool narrow_operand(int64_t ld, bool k_contiguous) {
 
 hipError_t launch_row_stats(const Product &p, hipStream_t stream) {
     auto job = [&](const Operand &x, bool kc, int rows, int blocks, const RowStat *out) {
-        StatJob j{x, kc, rows, p.K, blocks, static_cast<int>(div_up(p.K, blocks)), const_cast<RowStat *>(out), 0, 0, nullptr, p.ignore};
+        StatJob j{x, kc, rows, p.K, blocks, static_cast<int>(div_up(p.K, blocks)), const_cast<RowStat *>(out), 0, 0};
         j.strips = div_up(rows, kc ? 4 : 256);
         j.units = j.strips * blocks * p.batch;
         return j;
     };
-    StatJob a = job(p.a, !p.ta, p.M, p.blocks_a, p.row_a), b = job(p.b, p.tb, p.N, p.blocks_b, p.row_b);
-    if (p.top_a != nullptr) a.units = 0, b.skip = p.target_k;  // a: known
+    const StatJob a = job(p.a, !p.ta, p.M, p.blocks_a, p.row_a), b = job(p.b, p.tb, p.N, p.blocks_b, p.row_b);
     row_stats_kernel<<<blocks_for(a.units + b.units), 256, 0, stream>>>(a, b, p.batch);
     return hipGetLastError();
 }
@@ -427,21 +381,19 @@ int64_t choice_space(const Choice &c, int64_t batch, int64_t M, int64_t N, int64
     return static_cast<int64_t>(std::min<__int128>(slices_bytes(c, batch, M, N) + stats, __int128{1} << 61));
 }
 Choice choice_of(const Product &p) {
-    return choose(p.tb, p.batch, p.M, p.N, p.K, p.space != nullptr, p.mode == kStore ? kPlain : kStatistics);
+    return choose(p.tb, p.batch, p.M, p.N, p.K, p.space != nullptr, p.use);
 }
 }  // namespace
 
-int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bool statistics) {
-    return choice_space(choose(tb, batch, M, N, K, true, statistics ? kStatistics : kPlain), batch, M, N, K);
+int64_t product_space(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, Use use) {
+    return choice_space(choose(tb, batch, M, N, K, true, use), batch, M, N, K);
 }
 
 int64_t two_space(const Sizes &p, const Sizes &q) {
-    const Choice c = choose(p.tb, p.batch, p.M, p.N, p.K, true, kPlain), d = choose(q.tb, q.batch, q.M, q.N, q.K, true, kPlain);
+    const Choice c = choose(p.tb, p.batch, p.M, p.N, p.K, true, p.use), d = choose(q.tb, q.batch, q.M, q.N, q.K, true, q.use);
     const int64_t m = choice_space(c, p.batch, p.M, p.N, p.K), n = choice_space(d, q.batch, q.M, q.N, q.K);
     return paired(c, d, p.ta, q.ta, q.tb) ? std::min(m + n, int64_t{1} << 61) : std::max(m, n);
 }
-
-bool wants_parts(const Product &p) { return choice_of(p).half; }
 
 hipError_t launch_two(const Product &p, const Product &q, int64_t bytes, hipStream_t stream) {
     const Choice c = choice_of(p), d = choice_of(q);

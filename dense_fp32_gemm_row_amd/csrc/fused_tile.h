@@ -405,26 +405,18 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         float cost = 0.0f, share = 1.0f;
         int e = 141;
         if (r < (second ? cols : rows)) {
-            if (!second && p.top_a != nullptr) {
-                // known to be probabilities less one at the target: the scale alone
-                const int top = p.top_a[m0 + r] >> 23;
-                if (top > 0) e = max(top, 14);
-                if (top > 254) cost = __builtin_inff(), e = 141;
-            } else {
-                RowStat s{0, 0, 0, 0};
+            RowStat s{0, 0, 0, 0};
 #pragma unroll 4
-                for (int q = 0; q < blocks; ++q) {
-                    const RowStat t = from[q * line];
-                    s.top = max(s.top, t.top), s.count += t.count, s.sum += t.sum;
-                }
-                if (s.count > 0) {  // a row of zeros is one whatever its scale
-                    e = s.top;
-                    // (beside probabilities of unknown cost: over the values that take part)
-                    const float n = static_cast<float>(p.top_a != nullptr ? s.count : p.K);
-                    cost = (static_cast<float>(s.count) * static_cast<float>(e + 1) - static_cast<float>(s.sum)) / n;
-                    share = static_cast<float>(s.count) / n;
-                    if (e < 14 || e > 254) cost = __builtin_inff(), e = 141;
-                }
+            for (int q = 0; q < blocks; ++q) {
+                const RowStat t = from[q * line];
+                s.top = max(s.top, t.top), s.count += t.count, s.sum += t.sum;
+            }
+            if (s.count > 0) {  // a row of zeros is one whatever its scale
+                e = s.top;
+                const float n = static_cast<float>(p.K);
+                cost = (static_cast<float>(s.count) * static_cast<float>(e + 1) - static_cast<float>(s.sum)) / n;
+                share = static_cast<float>(s.count) / n;
+                if (e < 14 || e > 254) cost = __builtin_inff(), e = 141;
             }
         }
         exponents[tid] = e;

@@ -13,11 +13,9 @@
  *     and column of op(B) finds the range for it, two fp16 parts of the value times a power of
  *     two for its row, of whose four products three are summed.  What that
  *     leaves out is at most 2^-21 of each |a b| (2^-24 as a rule), plus 2^-22
- *     of the sum of |a b|.  Whole numbers up to 2^11 are held exactly.  (The cross
- *     entropy's probabilities, in the products of its gradient, have any range: there
- *     a part is off by at most 2^-40 of the largest of its row or column, and the form is
- *     taken where the other factor's values lie, on geometric average, within
- *     2^-17 of their column's largest.)
+ *     of the sum of |a b|.  Whole numbers up to 2^11 are held exactly.  (Not in the
+ *     products of the cross entropy's gradient: its probabilities have any range, and small
+ *     ones beside a large one may be all that meets a value that isn't zero.)
  * A product that comes out infinite or NaN is computed again, with its tile, by
  * FP32 multiplies, so infinities, NaN and values next to the largest give what
  * gemm_f32 gives.  Few rows and small products may run on FP32 multiplies

@@ -1,0 +1,47 @@
+"""The fused operators (include/gemm_f32_fused.h) where a result hangs on small values
+beside large ones, on infinities, or on an operand of one to three columns.
+Tolerances: fused_oracle.py."""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from dense_fp32_gemm_row_amd import binding as b
+from tests import fused_oracle as o
+from tests.test_fused_gpu import DEV, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- probabilities of any size -------------------------------------------------
+
+def peaked(T, V, K, gap, seed=40):
+    """A softmax peaked to exp(-gap): token t is of class t % 16, whose word has a logit
+    of `gap`, all others' are about 1.  Every second token's target is another word, so
+    that its P is -1 there, and its hidden values, and those words' weights, are zero in half
+    of the features: gradients there are sums of the small probabilities alone."""
+    X, W = rnd(seed, T, K), rnd(seed + 1, V, K, scale=1 / math.sqrt(K))
+    t = torch.arange(T, device=DEV)
+    X[:, :16], W[:, :16] = 0.0, 0.0
+    X[t, t % 16] = 1.0
+    W[torch.arange(16), torch.arange(16)] = gap
+    g = torch.Generator(device=DEV).manual_seed(seed + 2)
+    target = torch.where(t % 2 == 0, torch.randint(16, 16 + V // 4, (T,), generator=g, device=DEV), t % 16)
+    X[::2, K // 2:] = 0.0
+    W[:16 + V // 4, K // 2:] = 0.0
+    return X, W, target
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("gap", [16.0, 24.0, 28.0])
+@pytest.mark.parametrize("T,V,K", [(2048, 4096, 2048), (700, 9001, 1030), (300, 2000, 130), (60, 1000, 96)])
+def test_small_probabilities_count(T, V, K, gap, weights):
+    X, W, target = peaked(T, V, K, gap)
+    # loss weights from 1e-9 to 1, in an order of their own
+    g = torch.logspace(-9, 0, T, device=DEV)[torch.randperm(T, generator=torch.Generator().manual_seed(3))] if weights else None
+    want = o.loss_grad(X, W, target, g)
+    for name, got in zip(("loss", "lse", "dX", "dW"), b.cross_entropy_grad(X, W, target, g)):
+        o.check(got, *want[name], name)
