@@ -63,8 +63,10 @@ struct Product {
     Mode mode;
     stat2 *stats;
     int groups;
-    const int64_t *target;
     float *at_target;
+    // Not null: rows m with target[m] == ignore take no part.  (Of kStore they are zeros
+    // whatever B holds.)
+    const int64_t *target;
     // Where not null, k with target_k[k] == ignore, whose factors of A are zero, take
     // no part even where B holds infinities or NaN (A stored K x M, B stored K x N).
     const int64_t *target_k;

@@ -46,6 +46,7 @@ __device__ __forceinline__ void sum_slices(const Product &p, int64_t block, int6
         f32x4 z = read4(W, left);
 #pragma unroll 4
         for (int s = 1; s < p.splits; ++s) z += read4(W + s * per, left);
+        if (p.target != nullptr && p.target[m] == p.ignore) z = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (p.e.bias.p != nullptr) z += read4(p.e.bias.p + b * p.e.bias.stride + n, left);
         if (p.e.pre.p != nullptr) write4(p.e.pre.p + b * p.e.pre.stride + m * p.e.pre.ld + n, left, z);
         if (p.e.activation != GEMM_F32_ACT_NONE)

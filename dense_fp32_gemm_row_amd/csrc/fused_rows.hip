@@ -15,6 +15,7 @@ __device__ __forceinline__ void finish(const Product &p, int64_t b, int64_t slic
         p.slices[(slice * p.M + m) * p.N + n] = z;
         return;
     }
+    if (p.target != nullptr && p.target[m] == p.ignore) z = 0.0f;
     if (p.e.bias.p != nullptr) z += p.e.bias.p[b * p.e.bias.stride + n];
     if (p.e.pre.p != nullptr) p.e.pre.p[b * p.e.pre.stride + m * p.e.pre.ld + n] = z;
     float v = activate(p.e.activation, z);

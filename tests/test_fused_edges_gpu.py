@@ -11,7 +11,7 @@ import torch
 
 from dense_fp32_gemm_row_amd import binding as b
 from tests import fused_oracle as o
-from tests.test_fused_gpu import DEV, rnd
+from tests.test_fused_gpu import DEV, rnd, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,35 @@ def test_small_probabilities_count(T, V, K, gap, weights):
     want = o.loss_grad(X, W, target, g)
     for name, got in zip(("loss", "lse", "dX", "dW"), b.cross_entropy_grad(X, W, target, g)):
         o.check(got, *want[name], name)
+
+
+# ---- tokens that take no part ------------------------------------------------------
+
+SIZES = [(3, 500, 64), (70, 200, 32), (300, 300, 64), (40, 9000, 65), (400, 9000, 300), (520, 40000, 40),
+         (2048, 4096, 2048)]
+
+
+@pytest.mark.parametrize("pieces", [False, True])
+@pytest.mark.parametrize("T,V,K", SIZES)
+def test_ignored_tokens_beside_masked_words(T, V, K, pieces):
+    """Words whose logits are -inf have a probability of zero.  Times their weights, of
+    which one is -inf, that is NaN, but not in an ignored token's row of dX."""
+    X, W, target = tokens(T, V, K, seed=50)
+    X[:, 0] = 1.0
+    W[10:200:7, 0] = -math.inf
+    target[target >= 0] = target[target >= 0] % 10
+    target[T // 2] = -100
+    rest = torch.ones(V, dtype=torch.bool, device=DEV)
+    rest[10:200:7] = False
+    space = None
+    if pieces:
+        space = torch.empty(-(-b.gemm_f32_cross_entropy_grad_workspace_least(T, V, K) // 4), device=DEV)
+    loss, lse, dX, dW = b.cross_entropy_grad(X, W, target, workspace=space)
+    want = o.loss_grad(X, W[rest], target)
+    ignored = target == -100
+    o.check(loss, *want["loss"], "loss"), o.check(lse, *want["lse"], "lse")
+    assert not dX[ignored].any() and bool(torch.isnan(dX[~ignored, 0]).all())
+    o.check(dX[:, 1:], *(t[:, 1:] for t in want["dX"]), "dX")
+    o.check(dW[rest], *want["dW"], "dW")
+    assert not dW[~rest].any()
+    assert torch.equal(torch.nan_to_num(b.cross_entropy_grad(X, W, target, dW=False, workspace=space)[2]), torch.nan_to_num(dX))
