@@ -163,11 +163,16 @@ __device__ __forceinline__ Halves split4_half(const float (&x)[4], float scale) 
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
 
-// Two running (maximum, sum of exp(x - maximum)) as one.  An empty piece is
-// (-inf, 0).  A maximum of +inf or NaN makes the sum NaN, as the formula does.
+// What a row's exponentials are taken relative to: its maximum, so that they and their
+// sum stay in range, but 0 where that is infinite (x - maximum would be NaN): no word at all
+// has a sum of 0, a logit of +inf one of +inf.
+__device__ __forceinline__ float base_of(float top) { return finite(top) ? top : 0.0f; }
+
+// Two running (maximum, sum of exp(x - base_of(maximum))) as one.  An empty piece is
+// (-inf, 0).  Maxima pass over NaN, which makes the sum NaN.
 __device__ __forceinline__ void merge_stats(float &m, float &s, float m2, float s2) {
     const float top = fmaxf(m, m2);
-    const float base = top == -__builtin_inff() ? 0.0f : top;
+    const float base = base_of(top);
     s = s * quick_exp(m - base) + s2 * quick_exp(m2 - base);
     m = top;
 }

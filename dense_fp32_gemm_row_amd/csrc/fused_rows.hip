@@ -31,7 +31,7 @@ __device__ __forceinline__ void store_cell(const Product &p, int64_t b, int64_t 
         return;
     }
     const float top = over_lanes<16>(in ? v : -__builtin_inff(), [](float a, float b) { return fmaxf(a, b); });
-    const float s = over_lanes<16>(in ? quick_exp(v - (top == -__builtin_inff() ? 0.0f : top)) : 0.0f,
+    const float s = over_lanes<16>(in ? quick_exp(v - base_of(top)) : 0.0f,
                                    [](float a, float b) { return a + b; });
     if (!in) return;
     if (n % 16 == 0) p.stats[static_cast<int64_t>(m) * p.groups + n / 16] = stat2{top, s};

@@ -721,7 +721,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
             for (int e = 0; e < 4; ++e) top = c + e < cols ? fmaxf(top, v[e]) : top;
             auto larger = [](float a, float b) { return fmaxf(a, b); };
             top = fine ? over_lanes<4>(top, larger) : over_lanes<16>(top, larger);
-            const float base = top == -__builtin_inff() ? 0.0f : top;
+            const float base = base_of(top);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s += c + e < cols ? quick_exp(v[e] - base) : 0.0f;
             auto sum = [](float a, float b) { return a + b; };

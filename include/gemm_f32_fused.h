@@ -146,7 +146,9 @@ int64_t gemm_f32_fused_grad_workspace_size(int opA, int opB, int64_t batch, int6
  *   target       T word numbers.  A token whose target is `ignore_index` (any
  *                value, usually negative) takes no part: its loss is 0.  Any
  *                other target outside [0, V) gives a loss of NaN.
- *   loss, lse    T floats each; either may be NULL
+ *   loss, lse    T floats each; either may be NULL.  A logit of +inf makes its
+ *                token's lse +inf, and the loss too (NaN where it is the target's); one
+ *                of -inf is no word; NaN makes both NaN.
  *   workspace    gemm_f32_cross_entropy_workspace_size bytes; less is refused
  *
  * The logits are not kept: each tile of them ends as a maximum and a sum of

@@ -77,3 +77,41 @@ def test_ignored_tokens_beside_masked_words(T, V, K, pieces):
     o.check(dW[rest], *want["dW"], "dW")
     assert not dW[~rest].any()
     assert torch.equal(torch.nan_to_num(b.cross_entropy_grad(X, W, target, dW=False, workspace=space)[2]), torch.nan_to_num(dX))
+
+
+# ---- logits past FP32's range -----------------------------------------------------
+
+@pytest.mark.parametrize("T,V,K", SIZES + [(1, 700, 40)])
+def test_logits_past_the_range(T, V, K):
+    """A logit of +inf makes its token's lse infinite, as the formula does, and its
+    loss, unless it is the target's; its probability alone is NaN.  A logit of -inf is no
+    word at all."""
+    X, W, target = tokens(T, V, K, seed=60)
+    at, word = T // 2, V // 3
+    X[:, :2], W[:, :2] = 0.0, 0.0
+    X[at, 0], W[word, 0], W[word + 1, 0] = 1e30, 1e30, -1e30
+    target[at] = word + 2
+    want = o.loss_grad(torch.where(torch.arange(T, device=DEV)[:, None] == at, 0.0, X), W, target)
+    others = torch.arange(T, device=DEV) != at
+    for loss, lse in (b.cross_entropy(X, W, target), b.cross_entropy_grad(X, W, target)[:2]):
+        assert lse[at] == math.inf and loss[at] == math.inf
+        for name, got in (("loss", loss), ("lse", lse)):
+            o.check(got[others], *(t[others] for t in want[name]), name)
+    _, _, dX, dW = b.cross_entropy_grad(X, W, target)
+    assert bool(torch.isnan(dX[at]).all()) and bool(torch.isnan(dW[word]).all())
+    o.check(dX[others], *(t[others] for t in want["dX"]), "dX")
+    # the token's own share of the other words: a probability of 0, less 1 at the target
+    share = torch.zeros(V, K, dtype=torch.float64, device=DEV)
+    share[word + 2] = -X[at].double()
+    valid = others & (target != -100)
+    tokens_left = o.loss_grad(X[others], W, target[others]) if bool(valid.any()) else {"dW": (share * 0, share * 0)}
+    value, tol = tokens_left["dW"]
+    value, tol = value + share, tol + 2 * o.U * share.abs()
+    keep = torch.arange(V, device=DEV) != word
+    o.check(dW[keep], value[keep], tol[keep], "dW")
+    target[at] = word
+    loss, lse = b.cross_entropy(X, W, target)
+    assert lse[at] == math.inf and bool(torch.isnan(loss[at]))
+    X[at, 1] = math.nan
+    loss, lse = b.cross_entropy(X, W, target)
+    assert bool(torch.isnan(lse[at])) and bool(torch.isnan(loss[at]))
