@@ -1001,8 +1001,8 @@ def cross_entropy(X, W, target, *, ignore_index: int = -100, loss=None, lse=None
     """(loss, lse) of T tokens over a vocabulary: with ``logits = X @ W.T`` (X
     T x K, W V x K, row-major float32; never kept), ``lse = logsumexp(logits, 1)``
     and ``loss[t] = lse[t] - logits[t, target[t]]``, 0 where ``target[t]`` is
-    ``ignore_index``; any other target outside [0, V) gives NaN.  ``loss`` and
-    ``lse`` are written where given; ``workspace`` and ``stream`` as in gemm_fused."""
+    ``ignore_index`` (whose ``lse`` is only defined for finite logits); any other target
+    outside [0, V) gives NaN.  ``loss`` and ``lse`` are written where given; ``workspace`` and ``stream`` as in gemm_fused."""
     device, index, T, V, K, ldx, ldw = _tokens(X, W, target)
     loss, lp = _row_out(loss, "loss", T, device, index, stream)
     lse, sp = _row_out(lse, "lse", T, device, index, stream)

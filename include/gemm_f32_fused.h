@@ -144,8 +144,11 @@ int64_t gemm_f32_fused_grad_workspace_size(int opA, int opB, int64_t batch, int6
  *   X, ldx       T x K
  *   W, ldw       V x K, V >= 1 (unless T is 0)
  *   target       T word numbers.  A token whose target is `ignore_index` (any
- *                value, usually negative) takes no part: its loss is 0.  Any
- *                other target outside [0, V) gives a loss of NaN.
+ *                value, usually negative) takes no part: its loss is 0, and its
+ *                lse is only defined where its row of X and all its logits are finite
+ *                and X and W stay below 3.38e38 (a tile is not computed again for
+ *                it: padding of any values costs nothing).  Any other target
+ *                outside [0, V) gives a loss of NaN.
  *   loss, lse    T floats each; either may be NULL.  A logit of +inf makes its
  *                token's lse +inf, and the loss too (NaN where it is the target's); one
  *                of -inf is no word; NaN makes both NaN.
