@@ -79,18 +79,22 @@ inline Choice choose(bool tb, int64_t batch, int64_t M, int64_t N, int64_t K, bo
     // stored, a lane reads 2 neighbours): 16 x 14336 x 4096, B transposed, 47 us with 64
     // columns and 65 with 16, 16 x 4096 x 4096 43 and 18; 5 x 1792 x 78080, B as stored,
     // 119 us with 32 columns in 4 slices of K, 314 with 16 in one.
-    if (M <= kRowsMost && (tb || N >= 2)) {
+    if (M <= kRowsMost) {
         const int c = tb ? (N >= 8192 && M > 4 ? 4 : 1) : N >= 1024 ? 2 : 1;
         const int shape = tb && M <= 4 ? 0 : (M <= 16 ? 16 : 32) + c;
         const int64_t tiles = batch * div_up(N, 16 * c), most = (tb ? 256 : 512) / tiles;
         const int64_t splits = std::min<int64_t>(kMostSplits, std::max<int64_t>(1, std::min(most, K / 1024)));
         return {kRows, slice ? static_cast<int>(splits) : 1, false, shape};
     }
+    // Up to 3 columns of a B stored K x N: a tile's loads take 4 neighbours, so none serves
+    // (8192 x 1 x 4096 26 us, by a tile's loop for any shape 244).  Statistics are of a B
+    // stored N x K.
+    const bool few = !tb && N < 4 && use != kStatistics;
     Choice best{};
     double least = 0;
     for (const Rate &r : kRates) {
         if (r.kind.half && (!space || use == kProbabilities || K < 64 || K > (int64_t{1} << 22))) continue;
-        if (r.kind.tile == kRows && ((use == kStatistics && M > kFineTokens) || N < 4)) continue;
+        if (r.kind.tile == kRows ? (use == kStatistics && M > kFineTokens) || (!tb && (r.kind.shape & 15) > N) : few) continue;
         const int64_t tiles = batch * div_up(M, r.m) * div_up(N, r.n);
         for (int64_t splits = 1; splits <= (slice ? kMostSplits : 1); splits *= 2) {
             if (splits > 1 && (tiles * splits > 2048 || K < 64 * splits)) break;

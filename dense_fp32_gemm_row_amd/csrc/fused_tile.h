@@ -661,11 +661,9 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
     };
 
     clear();
-    // an operand with fewer rows than a thread loads together, where they are contiguous
-    const bool few = (TA && kHalf && p.M < 4) || (!TB && p.N < 4);
     int whole = k0;  // the end of what the stages take
     bool check = false;
-    if (p.narrow && !few) {
+    if (p.narrow) {
         bool half_parts = false;
         if constexpr (kHalf)
             if (p.row_b != nullptr && k1 - k0 >= 2 * kStage && certified()) {

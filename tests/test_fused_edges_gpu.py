@@ -11,7 +11,7 @@ import torch
 
 from dense_fp32_gemm_row_amd import binding as b
 from tests import fused_oracle as o
-from tests.test_fused_gpu import DEV, rnd, tokens
+from tests.test_fused_gpu import DEV, Guarded, rnd, stored, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,51 @@ def test_logits_past_the_range(T, V, K):
     X[at, 1] = math.nan
     loss, lse = b.cross_entropy(X, W, target)
     assert bool(torch.isnan(lse[at])) and bool(torch.isnan(loss[at]))
+
+
+# ---- one to three columns --------------------------------------------------------
+
+@pytest.mark.parametrize("ops", ["NN", "TN", "NT", "TT"])
+@pytest.mark.parametrize("N", [1, 2, 3])
+@pytest.mark.parametrize("M,K", [(1, 70000), (16, 33), (31, 5), (32, 4096), (33, 17), (300, 1), (1000, 777), (8192, 4096),
+                                 (70001, 130), (3, 1 << 20)])
+def test_few_columns(M, N, K, ops):
+    A, B = stored(1, M, K, ops[0], 1), stored(2, K, N, ops[1], 2)
+    bias, res = rnd(3, N), stored(4, M, N, "N", 5)
+    c, z = Guarded(M, N), Guarded(M, N, 1)
+    b.gemm_fused(A, B, c.out, bias=bias, activation="silu", residual=res, pre=z.out)
+    want = o.layer(A, B, bias, "silu", res)
+    o.check(c.out, want["y"], want["y_tol"])
+    o.check(z.out, want["z"], want["z_tol"])
+    c.check(), z.check()
+
+
+@pytest.mark.parametrize("ops", ["NN", "TN", "NT", "TT"])
+@pytest.mark.parametrize("M,N,K", [(8192, 1, 4096), (5000, 2, 300), (4100, 3, 3), (64, 700, 1), (1, 500, 2), (2000, 1, 1)])
+def test_gradients_of_few_columns(M, N, K, ops):
+    A, B = stored(1, M, K, ops[0], 2), stored(2, K, N, ops[1], 1)
+    dC, z = rnd(3, M, N), rnd(4, M, N)
+    da, db = Guarded(M, K, op=ops[0]), Guarded(K, N, op=ops[1])
+    got = b.gemm_fused_grad(dC, A, B, pre=z, activation="gelu", dA=da.out, dB=db.out, dbias=True)
+    want = o.layer_grad(dC, A, B, z, "gelu")
+    for name, t in zip(("dA", "dB", "dbias"), got):
+        o.check(t, *want[name], name)
+    da.check(), db.check()
+
+
+@pytest.mark.parametrize("n,M,N,K", [(40, 70, 1, 33), (300, 5, 3, 64), (7, 33, 2, 2000)])
+def test_batches_of_few_columns(n, M, N, K):
+    A, B = rnd(1, n, M, K), rnd(2, n, K, N)
+    want = o.layer(A, B)
+    o.check(b.gemm_fused(A, B), want["y"], want["y_tol"])
+
+
+@pytest.mark.parametrize("T,V,K", [(3, 1, 40), (100, 1, 33), (400, 3, 2000), (513, 2, 70), (2000, 3, 300), (600, 500, 1),
+                                   (40, 3000, 2), (2100, 40, 3)])
+def test_losses_of_few_words_or_features(T, V, K):
+    X, W, target = tokens(T, V, K, seed=70)
+    want = o.loss_grad(X, W, target)
+    for name, got in zip(("loss", "lse"), b.cross_entropy(X, W, target)):
+        o.check(got, *want[name], name)
+    for name, got in zip(("loss", "lse", "dX", "dW"), b.cross_entropy_grad(X, W, target)):
+        o.check(got, *want[name], name)

@@ -68,3 +68,19 @@ def test_probabilities_take_no_fp16_parts(choose):
     # in all else as any product: what did not take them stays as it was, and slices stay allowed
     assert all(p == q for p, q in zip(plain, got) if not p[2])
     assert any(splits > 1 for _, splits, _, _ in got)
+
+
+def test_few_columns_take_a_kernel_that_serves_them(choose):
+    """The tiles load 4 neighbouring columns of a B stored K x N at once, and 4
+    neighbouring rows of an A stored K x M: no choice may count on them where there are fewer."""
+    wanted = [(use, 0, space, batch, M, N, K) for use in (PLAIN, PROBABILITIES) for space in (0, 1) for batch in (1, 50)
+              for N in (1, 2, 3) for M in (1, 2, 3, 5, 16, 31, 32, 33, 64, 1000, 8192, 131072) for K in (1, 40, 4096, 1 << 20)]
+    for want, (tile, splits, half, shape) in zip(wanted, choose(wanted)):
+        _, _, space, _, M, N, K = want
+        assert tile == ROWS and not half, (want, tile)
+        assert 1 <= (shape & 15) <= N and shape >> 4 <= max(1, (M + 15) // 16), (want, shape)
+        assert splits == 1 or (space and K >= 64 * splits), (want, splits)
+    # few rows of either form
+    wanted = [(use, tb, 1, 1, M, N, K) for use in range(3) for tb in (0, 1) for M in range(1, 33) for N in (1, 2, 3, 4, 100)
+              for K in (1, 5000) if tb or use != STATISTICS]
+    assert all(tile == ROWS for tile, _, _, _ in choose(wanted))
