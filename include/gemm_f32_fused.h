@@ -30,8 +30,8 @@
  * Nothing is allocated: workspaces are the caller's (4-byte aligned, contents
  * don't matter, owned until the work has run; calls that may overlap need one
  * each).  An output must not overlap an input, another output or the workspace, except
- * where it is said; the work runs on the stream's device.  Calls may be
- * captured into a graph.
+ * where it is said (judged by address ranges, from an operand's first byte to its last); the
+ * work runs on the stream's device.  Calls may be captured into a graph.
  */
 #ifndef GEMM_F32_FUSED_H
 #define GEMM_F32_FUSED_H
@@ -179,7 +179,8 @@ int64_t gemm_f32_cross_entropy_workspace_size(int64_t T, int64_t V, int64_t K);
  *                gemm_f32_cross_entropy_grad_workspace_size bytes are what is
  *                quickest (a few GiB at most, unless a single row's logits
  *                take more), gemm_f32_cross_entropy_grad_workspace_least the
- *                fewest that are accepted.
+ *                fewest that are accepted.  With anything less than the quickest no product
+ *                runs in slices or fp16 parts.
  *
  * An ignored token's row of P, and so of dX, is zero, and its row of X takes
  * no part in dW even where it holds infinities or NaN.  A target that is
