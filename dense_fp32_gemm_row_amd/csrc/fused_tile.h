@@ -384,10 +384,10 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
     };
 
     // Whether two fp16 parts do: the rows' exponents for scaling, and a bound.
-    // Parts of a value are off by 2^-23 of it, or 2^-40 of its row's largest (and the
-    // product of two second parts, 2^-22 of the values' at most, is left out).
+    // Parts of a value are off by 2^-23 of it, or 2^-40 of a power of two above its row's
+    // largest (and the product of two second parts, 2^-22 of the values' at most, is left out).
     // The latter adds up to less than n 2^-39 a b over the n products of a cell that
-    // aren't zero, a and b the largest of its row and column; and the sum S
+    // aren't zero, a and b those powers of two for its row and column; and the sum S
     // of their |a b| is at least n a b 2^-c with c the mean over them of
     // log2(a / |a_k|) + log2(b / |b_k|), as an arithmetic mean is at least the
     // geometric one.  With costs (that mean over all k, zeros counting nothing)

@@ -163,3 +163,17 @@ def test_losses_of_few_words_or_features(T, V, K):
         o.check(got, *want[name], name)
     for name, got in zip(("loss", "lse", "dX", "dW"), b.cross_entropy_grad(X, W, target)):
         o.check(got, *want[name], name)
+
+
+# ---- tails of the activations --------------------------------------------------------
+
+def test_gelu_keeps_relative_precision():
+    """Of z times the normal distribution, z <= 0, down to where its parts leave FP32's normal
+    range: the share is off by 20 steps (its polynomial's argument 3, times 2.3; its Horner
+    scheme 3, its coefficients 4, the exponential 2, two products, the fit 1) and by
+    the exponential's argument's, z^2 / 2 times two roundings and a constant's 0.2; then a product."""
+    z = -torch.linspace(0.001, 12.5, 40001, device=DEV)
+    y = b.gemm_fused(z[:, None], torch.ones(1, 1, device=DEV), activation="gelu")[:, 0].double()
+    d = z.double()
+    want = d * 0.5 * torch.special.erfc(-d / math.sqrt(2))
+    assert bool(((y - want).abs() <= (1.2 * d * d + 21) * o.U * want.abs()).all())
