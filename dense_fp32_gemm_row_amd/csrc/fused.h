@@ -39,8 +39,9 @@ struct RowStat {
 // What the tile kernel does with a tile's sums.
 enum Mode : int {  // of a product
     kStore = 0,       // the epilogue (or raw slices), stored
-    kStats = 1,       // a maximum and a sum of exponentials per row and group of columns
-    kStoreStats = 2,  // both; the sums are stored as they are
+    kStoreSome = 1,   // the same, but rows that take no part are zeros whatever B holds
+    kStats = 2,       // a maximum and a sum of exponentials per row and group of columns
+    kStoreStats = 3,  // both; the sums are stored as they are
 };
 
 // C = epilogue(op(A) op(B)); ta: A is stored K x M, tb: B is stored N x K.
@@ -51,7 +52,7 @@ struct Product {
     Operand a, b;
     Epilogue e;
     Result c;
-    bool narrow;    // rows of a tile span less than 2^32 bytes 
+    bool narrow;    // rows of a tile span less than 2^32 bytes
     float *space;   // product_space() bytes, or null
     // set by launch_product:
     float *slices;  // partial sums [batch][split][M][N], or null
@@ -64,9 +65,7 @@ struct Product {
     stat2 *stats;
     int groups;
     float *at_target;
-    // Not null: rows m with target[m] == ignore take no part.  (Of kStore they are zeros
-    // whatever B holds.)
-    const int64_t *target;
+    const int64_t *target;  // but for kStore: rows m with target[m] == ignore take no part
     // Where not null, k with target_k[k] == ignore, whose factors of A are zero, take
     // no part even where B holds infinities or NaN (A stored K x M, B stored K x N).
     const int64_t *target_k;
@@ -108,7 +107,7 @@ hipError_t launch_row_stats(const Product &, hipStream_t);
 
 // C = epilogue(sum over the slices, in their order).
 hipError_t launch_sum_slices(const Product &, hipStream_t);
-hipError_t launch_sum_slices(const Product &, const Product &, hipStream_t);
+hipError_t launch_sum_slices(const Product &, const Product &, hipStream_t);  // (the second's mode kStore)
 
 // dZ = dC act'(Z), and the sums of its columns over blocks of rows; either may
 // be absent (dz.p null; partial null).

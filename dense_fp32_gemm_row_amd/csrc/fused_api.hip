@@ -391,7 +391,7 @@ int gemm_f32_cross_entropy_grad(int64_t T, int64_t V, int64_t K, const float *X,
             fused::Product px = plain_product(1, n, K, V, false, {logits, ldl, 0}, false, {W, ldw, 0},
                                               {dX != nullptr ? dX + t0 * lddx : nullptr, lddx, 0}, room(false, n, K, V, fused::kProbabilities),
                                               fused::kProbabilities);
-            px.target = target + t0, px.ignore = ignore_index;
+            px.mode = fused::kStoreSome, px.target = target + t0, px.ignore = ignore_index;
             fused::Product pw = plain_product(1, V, K, n, true, {logits, ldl, 0}, false, {Xt, ldx, 0}, {dW, lddw, 0},
                                               room(false, V, K, n, fused::kProbabilities), fused::kProbabilities);
             pw.target_k = target + t0, pw.ignore = ignore_index;

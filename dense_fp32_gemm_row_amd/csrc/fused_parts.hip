@@ -32,6 +32,8 @@ __device__ __forceinline__ void write4(float *p, int64_t left, f32x4 v) {
 
 // C = epilogue(sum of slices), 4 neighbours of a row a thread, slices in order: 1000 x
 // 1023 in two slices 5 us, most of it a launch (an element a thread, 64-bit divisions: 6.5).
+// SOME: kStoreSome (a branch for it in every product's sum: 6.8 -> 7.6 us for two).
+template <bool SOME>
 __device__ __forceinline__ void sum_slices(const Product &p, int64_t block, int64_t blocks) {
     const int64_t per = static_cast<int64_t>(p.M) * p.N, rows = p.batch * p.M;
     const unsigned strips = (static_cast<unsigned>(p.N) + 3) / 4;
@@ -46,7 +48,8 @@ __device__ __forceinline__ void sum_slices(const Product &p, int64_t block, int6
         f32x4 z = read4(W, left);
 #pragma unroll 4
         for (int s = 1; s < p.splits; ++s) z += read4(W + s * per, left);
-        if (p.target != nullptr && p.target[m] == p.ignore) z = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (SOME)
+            if (p.target[m] == p.ignore) z = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (p.e.bias.p != nullptr) z += read4(p.e.bias.p + b * p.e.bias.stride + n, left);
         if (p.e.pre.p != nullptr) write4(p.e.pre.p + b * p.e.pre.stride + m * p.e.pre.ld + n, left, z);
         if (p.e.activation != GEMM_F32_ACT_NONE)
@@ -56,13 +59,17 @@ __device__ __forceinline__ void sum_slices(const Product &p, int64_t block, int6
         write4(p.c.p + b * p.c.stride + m * p.c.ld + n, left, z);
     }
 }
-__global__ __launch_bounds__(256) void sum_slices_kernel(Product p) { sum_slices(p, blockIdx.x, gridDim.x); }
+template <bool SOME>
+__global__ __launch_bounds__(256) void sum_slices_kernel(Product p) {
+    sum_slices<SOME>(p, blockIdx.x, gridDim.x);
+}
 // Workgroups 0 .. first - 1 take p.
+template <bool SOME>
 __global__ __launch_bounds__(256) void sum_two_kernel(Product p, Product q, unsigned first) {
     if (blockIdx.x < first)
-        sum_slices(p, blockIdx.x, first);
+        sum_slices<SOME>(p, blockIdx.x, first);
     else
-        sum_slices(q, blockIdx.x - first, gridDim.x - first);
+        sum_slices<false>(q, blockIdx.x - first, gridDim.x - first);
 }
 
 // A block of rows of 4 LANES columns, 4 a lane, its rows shared by WAVES wavefronts and
@@ -278,13 +285,19 @@ unsigned blocks_for(int64_t n) { return static_cast<unsigned>(std::min<int64_t>(
 static unsigned sum_blocks(const Product &p) { return blocks_for(div_up(p.batch * p.M * div_up(p.N, 4), 256)); }
 
 hipError_t launch_sum_slices(const Product &p, hipStream_t stream) {
-    sum_slices_kernel<<<sum_blocks(p), 256, 0, stream>>>(p);
+    if (p.mode == kStoreSome)
+        sum_slices_kernel<true><<<sum_blocks(p), 256, 0, stream>>>(p);
+    else
+        sum_slices_kernel<false><<<sum_blocks(p), 256, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 hipError_t launch_sum_slices(const Product &p, const Product &q, hipStream_t stream) {
     const unsigned first = sum_blocks(p);
-    sum_two_kernel<<<first + sum_blocks(q), 256, 0, stream>>>(p, q, first);
+    if (p.mode == kStoreSome)
+        sum_two_kernel<true><<<first + sum_blocks(q), 256, 0, stream>>>(p, q, first);
+    else
+        sum_two_kernel<false><<<first + sum_blocks(q), 256, 0, stream>>>(p, q, first);
     return hipGetLastError();
 }
 

@@ -15,7 +15,7 @@ __device__ __forceinline__ void finish(const Product &p, int64_t b, int64_t slic
         p.slices[(slice * p.M + m) * p.N + n] = z;
         return;
     }
-    if (p.target != nullptr && p.target[m] == p.ignore) z = 0.0f;
+    if (p.mode == kStoreSome && p.target[m] == p.ignore) z = 0.0f;
     if (p.e.bias.p != nullptr) z += p.e.bias.p[b * p.e.bias.stride + n];
     if (p.e.pre.p != nullptr) p.e.pre.p[b * p.e.pre.stride + m * p.e.pre.ld + n] = z;
     float v = activate(p.e.activation, z);
@@ -26,7 +26,7 @@ __device__ __forceinline__ void finish(const Product &p, int64_t b, int64_t slic
 // One sum of 16 neighbouring columns that 16 lanes hold, all of which come here
 // together; `in`: it is one of C.
 __device__ __forceinline__ void store_cell(const Product &p, int64_t b, int64_t slice, int m, int n, float v, bool in) {
-    if (p.mode == kStore) {
+    if (p.mode < kStats) {
         if (in) finish(p, b, slice, m, n, v);
         return;
     }

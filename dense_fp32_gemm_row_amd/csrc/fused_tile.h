@@ -654,7 +654,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
             each([&](int r, int c, f32x4 v) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (r < rows && c + e < cols && !finite(v[e]) && (p.target == nullptr || p.target[m0 + r] != p.ignore))
+                    if (r < rows && c + e < cols && !finite(v[e]) && (p.mode == kStore || p.target[m0 + r] != p.ignore))
                         found = true;
             });
         return found;
@@ -710,7 +710,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
         }
         return v;
     };
-    if (p.mode != kStore) {
+    if (p.mode >= kStats) {
         const bool fine = p.M <= kFineTokens;
         const int lanes = fine ? 4 : 16;  // that share a piece of a row
         each([&](int r, int c, f32x4 v) {
@@ -749,7 +749,7 @@ __device__ __forceinline__ void one_tile(const Product &p, int tiles_m, int tile
                                                  : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         each([&](int r, int, f32x4 v) {
             if (r >= rows || c >= cols) return;
-            if (p.target != nullptr && p.target[m0 + r] == p.ignore) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (p.mode == kStoreSome && p.target[m0 + r] == p.ignore) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             if (p.e.bias.p != nullptr) v += bias;
             if (Z != nullptr) put(Z + r * p.e.pre.ld, c, v);
             if (p.e.activation != GEMM_F32_ACT_NONE)
