@@ -188,7 +188,8 @@ __global__ __launch_bounds__(256) void loss_kernel(Loss l) {
     }
 }
 
-// `rows` rows of 1024 columns, 4 a thread (4096 x 131072 817 us, 5.3 TB/s, a copy's).
+// `rows` rows of 1024 columns, 4 a thread (4096 x 131072 841 us, 5.1 TB/s, a copy's rate;
+// 517 x 32003 28).
 __global__ __launch_bounds__(256) void probabilities_kernel(Loss l, int64_t strips, int64_t units, int rows) {
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t block = u / strips, v = (u - block * strips) * 1024 + 4 * threadIdx.x, left = l.V - v;

@@ -7,8 +7,11 @@
 // arithmetic leaves; the parts are made once a workgroup, on the way into LDS.
 //   - 256 x 256, 8 wavefronts of 128 x 64, one workgroup a CU: the fewest values split and
 //     LDS reads a product.  4096 x 4096 x 4096 with bf16 parts 586 us (235 TFLOP/s), with
-//     fp16 parts 347 (396; the matrix units 72% busy at 1.73 GHz, which is what power
-//     leaves), and 26 for the rows' ranges; an FP32 library product takes 915.
+//     fp16 parts 347 (396; the matrix units 72% busy at 1.73 GHz), and 26 for the rows'
+//     ranges; an FP32 library product takes 915.  Power holds the clock there.  At a tile's end
+//     64 of a lane's 128 sums go to scratch and back (131 KB a workgroup: one path serves the
+//     test for infinities, the sums by FP32 multiplies and the results), about 30 us a tile
+//     with the results' stores, which nothing overlaps.
 //   - 128 x 128, 4 wavefronts, two workgroups a CU (517 x 32000 x 1024 160 us in fp16 parts,
 //     212 TFLOP/s; with rows that are not whole lines, 32003 x 1001, 174), and 64 x 128, three: for fewer tiles.
 //     There splitting, LDS and the products take turns in one or two wavefronts a
