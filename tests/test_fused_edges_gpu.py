@@ -177,3 +177,55 @@ def test_gelu_keeps_relative_precision():
     d = z.double()
     want = d * 0.5 * torch.special.erfc(-d / math.sqrt(2))
     assert bool(((y - want).abs() <= (1.2 * d * d + 21) * o.U * want.abs()).all())
+
+
+# ---- both products of a loss's gradient in one launch of tiles --------------------------
+
+# in slices of V and of T, both (643 to 804 tokens), or of V alone
+SHARED = [(643, 737, 1258), (643, 2807, 209), (804, 921, 643), (33, 3508, 1573), (53, 2246, 2459)]
+
+
+@pytest.mark.parametrize("T,V,K", SHARED)
+def test_loss_gradients_that_share_a_launch(T, V, K):
+    X, W, target = tokens(T, V, K, seed=80)
+    target[-1] = 5
+    g = rnd(81, T)
+    want = o.loss_grad(X, W, target, g)
+    got = b.cross_entropy_grad(X, W, target, g)
+    for name, t in zip(("loss", "lse", "dX", "dW"), got):
+        o.check(t, *want[name], name)
+    assert torch.equal(b.cross_entropy_grad(X, W, target, g, dW=False)[2], got[2])
+    assert torch.equal(b.cross_entropy_grad(X, W, target, g, dX=False)[3], got[3])
+    # padding of anything takes no part
+    ignored = target == -100
+    X[ignored] = math.nan
+    X[1] = math.inf
+    odd = b.cross_entropy_grad(X, W, target, g)
+    assert torch.equal(odd[0], got[0]) and torch.equal(odd[2], got[2])
+    o.check(odd[3], *want["dW"], "dW")
+
+
+@pytest.mark.parametrize("T,V,K", SHARED)
+def test_masked_words_in_a_shared_launch(T, V, K):
+    test_ignored_tokens_beside_masked_words(T, V, K, False)
+
+
+@pytest.mark.parametrize("T,V,K", SHARED[:2])
+def test_a_shared_launch_captured_and_on_another_stream(T, V, K):
+    X, W, target = tokens(T, V, K, seed=82)
+    first = b.cross_entropy_grad(X, W, target)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    other = b.cross_entropy_grad(X, W, target, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(first, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = b.cross_entropy_grad(X, W, target)
+    for _ in range(3):
+        for t in outs:
+            t.fill_(12345.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(first, outs))
+        assert all(torch.equal(a, c) for a, c in zip(first, b.cross_entropy_grad(X, W, target)))
